@@ -29,7 +29,8 @@
  *    *_workspace_size(). The first 256 bytes of every workspace are a header:
  *    the caller zero-fills them once when it allocates the workspace. Byte 0
  *    holds a device error word that kernels only OR bits into (a bounded wait
- *    that ran out sets bit 0); w4a8_device_error() reads and clears it. Calls
+ *    that ran out sets bit 0, an index out of range bit 1); w4a8_device_error()
+ *    reads and clears it. Calls
  *    may keep other counters in the header; every call leaves them zero.
  *  - Stateless and thread-safe; concurrent calls must use distinct workspaces.
  */
@@ -51,7 +52,9 @@ typedef enum {
     W4A8_ERR_WORKSPACE = 4, /* ws is NULL or ws_bytes is too small             */
     W4A8_ERR_DEVICE = 5,    /* no sm_103 device, or the kernel image is absent */
     W4A8_ERR_LAUNCH = 6,    /* a CUDA launch or driver call failed             */
-    W4A8_ERR_TIMEOUT = 7    /* reported by w4a8_device_error: a bounded wait ran out */
+    W4A8_ERR_TIMEOUT = 7,   /* reported by w4a8_device_error: a bounded wait ran out */
+    W4A8_ERR_INDEX = 8      /* reported by w4a8_device_error: a page index or a length
+                               read on the device was out of range                  */
 } w4a8_status_t;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -341,6 +344,97 @@ int fp8_block_linear(const uint16_t* x_bf16, int M, int N, int K, const uint8_t*
 size_t fp8_block_linear_workspace_size(int M, int N, int K);
 
 /*
+ * The FP8 key/value cache (the KV8 of grok-1-W4A8KV8: PR #4152 config.json,
+ * quantization_config.kv_cache_scheme, min_kv_scale), shared by the three
+ * kv8_* calls:
+ *
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] u8 : E4M3 codes. Slot
+ *        s = page * page_size + offset holds one token's keys and values of
+ *        every kv head.
+ *   k_scale, v_scale fp32 : a code c of head h stands for dec(c) * scale;
+ *        scale_mode 0: one scale per head, [Hkv] (the static scheme);
+ *        scale_mode 1: one per token and head, [num_pages, Hkv, page_size].
+ *   D is 64 or 128; page_size a power of two in 16..256; num_pages >= 1 and
+ *   num_pages * page_size < 2^31; Hkv in 1..1024.
+ *   int32 and fp32 arrays of these calls need only their natural 4-byte
+ *   alignment (they are often slices of larger tables); all other pointers
+ *   16 bytes.
+ */
+
+/*
+ * kv8_write -- quantize the keys and values of T tokens into their slots.
+ *
+ *   k_bf16, v_bf16 [T, Hkv, D] bf16 : rows of Hkv*D values, k_stride and
+ *        v_stride elements apart (each >= Hkv*D and a multiple of 8: columns of
+ *        a fused projection's output are fine).
+ *   slots [T] i32 : where each token goes. A token whose slot is outside
+ *        [0, num_pages * page_size) is skipped (padding is usually -1). Two
+ *        tokens of one call must not share a slot.
+ *   scale_mode 0: k_scale, v_scale [Hkv] are read.
+ *   scale_mode 1: s = max(max|x| / 448, min_scale) over the row's finite
+ *        values, 1 where that is 0, is written for each token and head.
+ *   Codes: E4M3(x / s), fp32 division, RNE, +-448; a NaN keeps the NaN code.
+ *   Requires T >= 1, T * Hkv < 2^31, min_scale finite and >= 0.
+ *   No workspace; one kernel.
+ */
+int kv8_write(const uint16_t* k_bf16, const uint16_t* v_bf16, int T, int64_t k_stride, int64_t v_stride,
+              const int32_t* slots, int Hkv, int D, int num_pages, int page_size, int scale_mode, float min_scale,
+              uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale, void* stream);
+
+/*
+ * kv8_read -- the keys and values of T slots as bf16: x = bf16(dec(code) * s).
+ *
+ *   slots [T] i32 : a slot outside [0, num_pages * page_size) reads as zeros;
+ *        slots may repeat.
+ *   k_bf16, v_bf16 [T, Hkv, D] bf16 : out, rows k_stride and v_stride elements
+ *        apart (as for kv8_write).
+ *   Requires T >= 1, T * Hkv < 2^31. No workspace; one kernel.
+ */
+int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+             const int32_t* slots, int T, int Hkv, int D, int num_pages, int page_size, int scale_mode,
+             uint16_t* k_bf16, int64_t k_stride, uint16_t* v_bf16, int64_t v_stride, void* stream);
+
+/*
+ * kv8_prefix_attention -- decode attention (one query token per sequence) over
+ * the cache for B sequences that share their first prefix_len tokens. The
+ * prefix is read and multiplied once for the whole batch.
+ *
+ *   q_bf16 [B, Hq, D] bf16 : rows of Hq*D values q_stride elements apart (>=
+ *        Hq*D and a multiple of 8). Query head i uses kv head i / (Hq / Hkv).
+ *   prefix_pages [ceil(prefix_len / page_size)] i32 : the shared tokens'
+ *        pages, in order (NULL allowed when prefix_len is 0).
+ *   page_table [B, max_pages] i32 : the pages of each sequence's own tokens, in
+ *        order, rows table_stride elements apart (>= max_pages); entries past a
+ *        sequence's last page are not read.
+ *   suffix_lens [B] i32 : each sequence's own tokens (0 allowed). With
+ *        max_pages 0 page_table and suffix_lens may be NULL: no own tokens.
+ *   For sequence b, head i and its keys j (the prefix's, then its own):
+ *     s_j = sm_scale * sum_d q_d * k_j,d ;  logit_cap > 0: s_j = logit_cap * tanh(s_j / logit_cap)
+ *     out [B, Hq, D] bf16 = bf16(sum_j softmax(s)_j * v_j), lse [B, Hq] fp32 = log sum_j exp(s_j)
+ *   with fp32 scores, statistics and sums; the softmax weights enter the second
+ *   product in f16, relative to a running reference. A sequence without any key
+ *   has out = 0 and lse = -infinity. lse may be NULL. Cache bytes behind the
+ *   last token of a page have no influence. The same call gives the same bits.
+ *   Several query tokens of one sequence are several rows that share its pages,
+ *   each with its own length.
+ *   Requires 1 <= B <= 4096, Hq a multiple of Hkv with Hq / Hkv <= 1024,
+ *   prefix_len >= 0, max_pages >= 0, max_pages * page_size < 2^31, sm_scale
+ *   finite, logit_cap finite and >= 0.
+ *   A page index outside [0, num_pages) or a suffix length outside
+ *   [0, max_pages * page_size] touches no memory out of range; the call's
+ *   outputs are then unspecified and w4a8_device_error reports W4A8_ERR_INDEX.
+ *   ws: kv8_prefix_attention_workspace_size(...) bytes, header zeroed once.
+ */
+int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq, int Hkv, int D,
+                         const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                         int num_pages, int page_size, int scale_mode, const int32_t* prefix_pages, int prefix_len,
+                         const int32_t* page_table, int64_t table_stride, int max_pages, const int32_t* suffix_lens,
+                         float sm_scale, float logit_cap, uint16_t* out_bf16, float* lse, void* ws, size_t ws_bytes,
+                         void* stream);
+size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages,
+                                           int page_size);
+
+/*
  * w4a8_set_profile_events -- measurement hook (not part of the method). Sets,
  * for the calling host thread, up to four cudaEvent_t handles that
  * moe_w4a8_forward records on its stream: [0] before the gate_up GEMM,
@@ -365,7 +459,7 @@ int w4a8_selftest_wait_timeout(void* ws, void* stream);
  * w4a8_device_error -- read and clear the device error word of a workspace.
  * Synchronizes `stream` (the only call that does). *code_out receives
  * W4A8_OK, or W4A8_ERR_TIMEOUT when a kernel gave up on a bounded wait since
- * the last read. Returns W4A8_OK or W4A8_ERR_NULL / W4A8_ERR_LAUNCH.
+ * the last read, else W4A8_ERR_INDEX when one met an index out of range. Returns W4A8_OK or W4A8_ERR_NULL / W4A8_ERR_LAUNCH.
  */
 int w4a8_device_error(void* ws, int* code_out, void* stream);
 

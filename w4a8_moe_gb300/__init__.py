@@ -1,4 +1,5 @@
-"""W4A8 mixture-of-experts FFN and block-FP8 projection for GB300 (sm_103a).
+"""W4A8 mixture-of-experts FFN, FP8 projections and the FP8 key/value cache with
+its decode attention for GB300 (sm_103a).
 
 Thin Python binding over the C ABI in include/w4a8_moe.h: each function has
 the C entry point's name, takes torch CUDA tensors, allocates outputs and
@@ -9,6 +10,7 @@ no other implementation, and a missing library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from collections import namedtuple
@@ -22,7 +24,8 @@ __all__ = [
     "moe_route_gate_workspace_size", "fp8_linear", "fp8_linear_workspace_size",
     "moe_w4a8_forward_dynamic", "moe_w4a8_dynamic_workspace_size", "moe_w4a8_workspace_layout",
     "moe_w4a8_plan",
-    "w4a8_quantize_act_workspace_size", "RouteResult", "library_path", "W4A8Error",
+    "w4a8_quantize_act_workspace_size", "kv8_write", "kv8_read", "kv8_prefix_attention",
+    "kv8_prefix_attention_workspace_size", "RouteResult", "library_path", "W4A8Error",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -49,6 +52,7 @@ def _load():
                         "`python -m w4a8_moe_gb300.build` (or __graft_entry__.build())")
     lib = ctypes.CDLL(_LIB_PATH)
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    f32 = ctypes.c_float
     sig = {
         "w4a8_status_string": (ctypes.c_char_p, [i32]),
         "w4a8_version": (i32, []),
@@ -71,6 +75,11 @@ def _load():
         "fp8_block_linear_workspace_size": (sz, [i32, i32, i32]),
         "fp8_linear": (i32, [P, P, i32, i32, i32, P, P, P, P, sz, P]),
         "fp8_linear_workspace_size": (sz, [i32, i32, i32]),
+        "kv8_write": (i32, [P, P, i32, i64, i64, P, i32, i32, i32, i32, i32, f32, P, P, P, P, P]),
+        "kv8_read": (i32, [P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, i64, P, i64, P]),
+        "kv8_prefix_attention": (i32, [P, i64, i32, i32, i32, i32, P, P, P, P, i32, i32, i32, P, i32, P, i64, i32, P,
+                                       f32, f32, P, P, P, sz, P]),
+        "kv8_prefix_attention_workspace_size": (sz, [i32] * 7),
         "w4a8_device_error": (i32, [P, P, P]),
         "w4a8_selftest_wait_timeout": (i32, [P, P]),
         "w4a8_set_profile_events": (i32, [P, i32]),
@@ -95,6 +104,11 @@ def _ptr(t):
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(stream):
+    """What is allocated inside belongs to `stream` (the current one when None)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _u8(t):
@@ -159,6 +173,10 @@ def fp8_block_linear_workspace_size(M, N, K) -> int:
 
 def w4a8_quantize_act_workspace_size(numel) -> int:
     return int(_load().w4a8_quantize_act_workspace_size(numel))
+
+
+def kv8_prefix_attention_workspace_size(B, Hq, Hkv, D, prefix_len, max_pages, page_size) -> int:
+    return int(_load().kv8_prefix_attention_workspace_size(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
 
 
 # --------------------------------------------------------------------------- calls
@@ -303,6 +321,116 @@ def fp8_block_linear(x_bf16, w_e4m3, w_scale_inv, out=None, xq_out=None, xs_out=
                                     _ptr(None if xq_out is None else _u8(xq_out)), _ptr(xs_out),
                                     _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows3(t, what):
+    """A bf16 [rows, heads, D] tensor whose rows may lie apart -> (rows, heads, D, row stride)."""
+    _need(t.dtype == torch.bfloat16 and t.dim() == 3, f"{what} must be a bf16 [tokens, heads, D] tensor")
+    n, h, d = t.shape
+    _need(t.stride(2) == 1 and (h == 1 or t.stride(1) == d), f"{what}: each token's heads must be contiguous")
+    # a tensor of one row may report any row stride
+    return n, h, d, t.stride(0) if n > 1 else max(t.stride(0), h * d)
+
+
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a cache's four tensors -> (pages, kv heads, page size, D, scale mode)."""
+    for c, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(c.dtype in (torch.uint8, torch.float8_e4m3fn) and c.dim() == 4 and c.is_contiguous(),
+              f"{what} must be contiguous uint8 or float8_e4m3fn [pages, kv heads, page size, D]")
+    _need(k_cache.shape == v_cache.shape, "k_cache and v_cache differ in shape")
+    n, h, page, d = k_cache.shape
+    for s, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(s.dtype == torch.float32 and s.is_contiguous(), f"{what} must be contiguous float32")
+        _need(s.shape in ((h,), (n, h, page)), f"{what} must be [kv heads] or [pages, kv heads, page size]")
+    _need(k_scale.shape == v_scale.shape, "k_scale and v_scale differ in shape")
+    return n, h, page, d, int(k_scale.dim() == 3)
+
+
+def _i32(t, dim, what):
+    _need(t.dtype == torch.int32 and t.dim() == dim, f"{what} must be an int32 tensor of {dim} dimension(s)")
+    return t
+
+
+def _same_device(ref, *tensors):
+    _need(ref.is_cuda, "tensors must be on the GPU")
+    for t in tensors:
+        _need(t is None or t.device == ref.device, "tensors must be on one device")
+
+
+def kv8_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, min_scale: float = 0.0, stream=None) -> None:
+    """Quantize bf16 keys and values [T, kv heads, D] (rows may lie apart, as in a fused projection's output) into
+    slots [T] (int32; out of range: skipped) of the cache. k_scale / v_scale of shape [kv heads] are read; of shape
+    [pages, kv heads, page size] they are computed and written."""
+    n, h, page, d, mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    T, hk, dk, k_stride = _rows3(k, "k")
+    _need(k.shape == v.shape and (hk, dk) == (h, d), "k and v must be [T, kv heads, D] of the cache's heads and D")
+    v_stride = _rows3(v, "v")[3]
+    _need(_i32(slots, 1, "slots").shape[0] == T and slots.is_contiguous(), "slots must be contiguous int32 [T]")
+    _same_device(k_cache, v_cache, k_scale, v_scale, k, v, slots)
+    _check(_load().kv8_write(_ptr(k), _ptr(v), T, k_stride, v_stride, _ptr(slots), h, d, n, page, mode,
+                             float(min_scale), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                             _stream(stream)))
+
+
+def kv8_read(k_cache, v_cache, k_scale, v_scale, slots, k_out=None, v_out=None, stream=None):
+    """The cache's slots [T] (int32; out of range: zeros) as bf16 keys and values, each [T, kv heads, D]."""
+    n, h, page, d, mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    T = _i32(slots, 1, "slots").shape[0]
+    _need(slots.is_contiguous(), "slots must be contiguous")
+    with _on(stream):
+        new = dict(dtype=torch.bfloat16, device=k_cache.device)
+        k_out = k_out if k_out is not None else torch.empty(T, h, d, **new)
+        v_out = v_out if v_out is not None else torch.empty(T, h, d, **new)
+    k_stride, v_stride = _rows3(k_out, "k_out")[3], _rows3(v_out, "v_out")[3]
+    _need(k_out.shape == v_out.shape == (T, h, d), "k_out and v_out must be [T, kv heads, D]")
+    _same_device(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
+    _check(_load().kv8_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(slots), T, h, d, n, page,
+                            mode, _ptr(k_out), k_stride, _ptr(v_out), v_stride, _stream(stream)))
+    return k_out, v_out
+
+
+def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, prefix_len: int, page_table, suffix_lens,
+                         sm_scale=None, logit_cap: float = 0.0, out=None, lse=None, ws=None, stream=None):
+    """Decode attention of bf16 q [B, query heads, D] over a shared prefix (prefix_pages, the first prefix_len tokens)
+    and each sequence's own tokens (page_table [B, max pages], suffix_lens [B]); returns (bf16 out [B, query heads, D],
+    fp32 lse [B, query heads] or None). Pass `lse` (a tensor, or True to allocate one) to receive it. sm_scale defaults
+    to D ** -0.5; logit_cap 0 is no cap."""
+    n, h, page, d, mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    B, hq, dq, q_stride = _rows3(q, "q")
+    _need(dq == d, "q and the cache differ in D")
+    prefix_len = int(prefix_len)
+    if prefix_len > 0:
+        _need(_i32(prefix_pages, 1, "prefix_pages").is_contiguous() and prefix_pages.shape[0] * page >= prefix_len,
+              "prefix_pages must be contiguous and cover prefix_len tokens")
+    most = _i32(page_table, 2, "page_table").shape[1]
+    _need(page_table.shape[0] == B and (most < 2 or page_table.stride(1) == 1), "page_table must be [B, max pages]")
+    _need(_i32(suffix_lens, 1, "suffix_lens").shape[0] == B and suffix_lens.is_contiguous(),
+          "suffix_lens must be contiguous [B]")
+    with _on(stream):
+        if out is None:
+            out = torch.empty(B, hq, d, dtype=torch.bfloat16, device=q.device)
+        if lse is True:
+            lse = torch.empty(B, hq, dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = _ws(kv8_prefix_attention_workspace_size(B, hq, h, d, prefix_len, most, page), q.device)
+    _need(out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous(),
+          "out must be contiguous bf16 [B, query heads, D]")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (B, hq) and lse.is_contiguous()),
+          "lse must be contiguous float32 [B, query heads]")
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, prefix_pages if prefix_len > 0 else None, page_table,
+                 suffix_lens, out, lse, ws)
+    _check(_load().kv8_prefix_attention(
+        _ptr(q), q_stride, B, hq, h, d, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n, page, mode,
+        _ptr(prefix_pages) if prefix_len > 0 else None, prefix_len, _ptr(page_table),
+        page_table.stride(0) if B > 1 else max(page_table.stride(0), most), most, _ptr(suffix_lens),
+        float(d ** -0.5 if sm_scale is None else sm_scale), float(logit_cap), _ptr(out), _ptr(lse), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+    return out, lse
 
 
 def w4a8_set_profile_events(events) -> None:

@@ -2,10 +2,13 @@
 // encoding and kernel launches. Declarations and contracts: include/w4a8_moe.h.
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "../../include/w4a8_moe.h"
 #include "internal.h"
+#include "kv8.cuh"
+#include "ptx.cuh"
 
 namespace w4a8 {
 
@@ -68,6 +71,7 @@ int current_device(int* num_sms)
 thread_local void* g_profile_events[4] = {nullptr, nullptr, nullptr, nullptr};
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 struct Carver {
     uint8_t* base;
@@ -209,6 +213,51 @@ static size_t fp_ws(int M, int N, int K, FpWs* w, void* ws)
     return c.off;
 }
 
+// ---- FP8 key/value cache
+// log2 of a supported page size, else -1.
+static int kv8_page_shift(int page_size)
+{
+    for (int s = 4; s <= 8; ++s)
+        if (page_size == 1 << s)
+            return s;
+    return -1;
+}
+static bool kv8_cache_ok(int Hkv, int D, int num_pages, int page_size, int scale_mode)
+{
+    return Hkv >= 1 && Hkv <= 1024 && (D == 64 || D == 128) && num_pages >= 1 && kv8_page_shift(page_size) >= 0 &&
+           static_cast<int64_t>(num_pages) * page_size < (static_cast<int64_t>(1) << 31) &&
+           (scale_mode == 0 || scale_mode == 1);
+}
+static bool kv8_rows_ok(int T, int Hkv, int D, int64_t k_stride, int64_t v_stride)
+{
+    const int64_t row = static_cast<int64_t>(Hkv) * D;
+    return T >= 1 && static_cast<int64_t>(T) * Hkv < (static_cast<int64_t>(1) << 31) && k_stride >= row &&
+           v_stride >= row && k_stride % 8 == 0 && v_stride % 8 == 0;
+}
+static bool kv8_attn_ok(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size)
+{
+    return B >= 1 && B <= kKv8MaxBatch && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq % Hkv == 0 && Hq / Hkv <= 1024 &&
+           (D == 64 || D == 128) && kv8_page_shift(page_size) >= 0 && prefix_len >= 0 &&
+           prefix_len <= 0x7FFFFF00 && max_pages >= 0 &&
+           static_cast<int64_t>(max_pages) * page_size < (static_cast<int64_t>(1) << 31);
+}
+struct Kv8Ws {
+    float* part_o;
+    float2* part_ml;
+    int tiles, ptiles;
+};
+static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, Kv8Ws* w, void* ws)
+{
+    Carver c(ws);
+    const int group = Hq / Hkv, R = kv8_attn_row_tile(group);
+    w->tiles = (group + R - 1) / R;
+    w->ptiles = prefix_len ? (B * group + R - 1) / R : 0;
+    const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxCtas;
+    w->part_o = c.take<float>(slots * R * D * 4);
+    w->part_ml = c.take<float2>(slots * R * 8);
+    return c.off;
+}
+
 }  // namespace w4a8
 
 using namespace w4a8;
@@ -226,6 +275,7 @@ const char* w4a8_status_string(int status)
     case W4A8_ERR_DEVICE: return "W4A8_ERR_DEVICE: needs a compute capability 10.3 GPU";
     case W4A8_ERR_LAUNCH: return "W4A8_ERR_LAUNCH: CUDA launch or driver call failed";
     case W4A8_ERR_TIMEOUT: return "W4A8_ERR_TIMEOUT: a kernel gave up on a bounded wait";
+    case W4A8_ERR_INDEX: return "W4A8_ERR_INDEX: a page index or length read on the device was out of range";
     default: return "W4A8: unknown status";
     }
 }
@@ -624,6 +674,101 @@ int w4a8_selftest_wait_timeout(void* ws, void* stream)
                : W4A8_ERR_LAUNCH;
 }
 
+int kv8_write(const uint16_t* k_bf16, const uint16_t* v_bf16, int T, int64_t k_stride, int64_t v_stride,
+              const int32_t* slots, int Hkv, int D, int num_pages, int page_size, int scale_mode, float min_scale,
+              uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale, void* stream)
+{
+    if (!k_bf16 || !v_bf16 || !slots || !k_cache || !v_cache || !k_scale || !v_scale)
+        return W4A8_ERR_NULL;
+    if (!kv8_cache_ok(Hkv, D, num_pages, page_size, scale_mode) || !kv8_rows_ok(T, Hkv, D, k_stride, v_stride) ||
+        !std::isfinite(min_scale) || min_scale < 0.0f)
+        return W4A8_ERR_SHAPE;
+    if (!aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(slots) ||
+        !aligned4(k_scale) || !aligned4(v_scale))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    const Kv8Rows a{T, Hkv, D, num_pages * page_size, kv8_page_shift(page_size), scale_mode, min_scale, k_stride, v_stride};
+    return launch_kv8_write(a, k_bf16, v_bf16, slots, k_cache, v_cache, k_scale, v_scale,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? W4A8_OK
+               : W4A8_ERR_LAUNCH;
+}
+
+int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+             const int32_t* slots, int T, int Hkv, int D, int num_pages, int page_size, int scale_mode,
+             uint16_t* k_bf16, int64_t k_stride, uint16_t* v_bf16, int64_t v_stride, void* stream)
+{
+    if (!k_bf16 || !v_bf16 || !slots || !k_cache || !v_cache || !k_scale || !v_scale)
+        return W4A8_ERR_NULL;
+    if (!kv8_cache_ok(Hkv, D, num_pages, page_size, scale_mode) || !kv8_rows_ok(T, Hkv, D, k_stride, v_stride))
+        return W4A8_ERR_SHAPE;
+    if (!aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(slots) ||
+        !aligned4(k_scale) || !aligned4(v_scale))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    const Kv8Rows a{T, Hkv, D, num_pages * page_size, kv8_page_shift(page_size), scale_mode, 0.0f, k_stride, v_stride};
+    return launch_kv8_read(a, k_cache, v_cache, k_scale, v_scale, slots, k_bf16, v_bf16,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? W4A8_OK
+               : W4A8_ERR_LAUNCH;
+}
+
+size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages,
+                                           int page_size)
+{
+    if (!kv8_attn_ok(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
+        return 0;
+    Kv8Ws w;
+    return kv8_ws(B, Hq, Hkv, D, prefix_len, &w, nullptr);
+}
+
+int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq, int Hkv, int D,
+                         const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                         int num_pages, int page_size, int scale_mode, const int32_t* prefix_pages, int prefix_len,
+                         const int32_t* page_table, int64_t table_stride, int max_pages, const int32_t* suffix_lens,
+                         float sm_scale, float logit_cap, uint16_t* out_bf16, float* lse, void* ws, size_t ws_bytes,
+                         void* stream)
+{
+    if (!q_bf16 || !k_cache || !v_cache || !k_scale || !v_scale || !out_bf16 || (prefix_len > 0 && !prefix_pages) ||
+        (max_pages > 0 && (!page_table || !suffix_lens)))
+        return W4A8_ERR_NULL;
+    if (!kv8_cache_ok(Hkv, D, num_pages, page_size, scale_mode) ||
+        !kv8_attn_ok(B, Hq, Hkv, D, prefix_len, max_pages, page_size) ||
+        q_stride < static_cast<int64_t>(Hq) * D || q_stride % 8 != 0 || table_stride < max_pages ||
+        !std::isfinite(sm_scale) || !std::isfinite(logit_cap) || logit_cap < 0.0f)
+        return W4A8_ERR_SHAPE;
+    if (!aligned16(q_bf16) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out_bf16) ||
+        !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(prefix_pages) || !aligned4(page_table) ||
+        !aligned4(suffix_lens) || !aligned4(lse))
+        return W4A8_ERR_ALIGN;
+    if (!ws || ws_bytes < kv8_prefix_attention_workspace_size(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
+        return W4A8_ERR_WORKSPACE;
+    if (!aligned16(ws))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    Kv8Ws w;
+    kv8_ws(B, Hq, Hkv, D, prefix_len, &w, ws);
+    Kv8Attn a = {};
+    a.q = q_bf16, a.q_stride = q_stride;
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;
+    a.k_cache = k_cache, a.v_cache = v_cache, a.k_scale = k_scale, a.v_scale = v_scale;
+    a.num_pages = num_pages, a.page_shift = kv8_page_shift(page_size);
+    a.prefix_pages = prefix_pages, a.prefix_len = prefix_len;
+    a.page_table = page_table, a.table_stride = table_stride, a.max_pages = max_pages, a.lens = suffix_lens;
+    a.sm_scale = sm_scale, a.cap = logit_cap;
+    a.tiles = w.tiles, a.ptiles = w.ptiles, a.part_o = w.part_o, a.part_ml = w.part_ml;
+    a.err = static_cast<uint32_t*>(ws);
+    a.out = out_bf16, a.lse = lse;
+    return launch_kv8_attn(a, D, scale_mode, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK
+                                                                                                   : W4A8_ERR_LAUNCH;
+}
+
 int w4a8_device_error(void* ws, int* code_out, void* stream)
 {
     if (!ws || !code_out)
@@ -633,7 +778,7 @@ int w4a8_device_error(void* ws, int* code_out, void* stream)
     if (cudaMemcpyAsync(&word, ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaMemsetAsync(ws, 0, sizeof(word), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
         return W4A8_ERR_LAUNCH;
-    *code_out = (word & 1u) ? W4A8_ERR_TIMEOUT : W4A8_OK;
+    *code_out = (word & kErrBitTimeout) ? W4A8_ERR_TIMEOUT : (word & kErrBitIndex) ? W4A8_ERR_INDEX : W4A8_OK;
     return W4A8_OK;
 }
 

@@ -1,0 +1,68 @@
+// Shared pieces of the FP8 key/value cache kernels (kv8.cu, kv8_attn.cu):
+// launch parameters, the work split of the attention, E4M3 -> f16 conversion.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace w4a8 {
+
+constexpr uint32_t kErrBitIndex = 2u;  // a page index or a length was out of range
+
+// ---- cache: E4M3 codes [num_pages, Hkv, page_size, D], page_size = 1 << page_shift.
+struct Kv8Rows {            // arguments of the write and the read
+    int T, Hkv, D;
+    int num_slots;          // num_pages * page_size
+    int page_shift;
+    int per_token;          // scales: 0 one per head, 1 one per token and head
+    float min_scale;
+    int64_t k_stride, v_stride;   // elements between two tokens' rows
+};
+cudaError_t launch_kv8_write(const Kv8Rows& a, const uint16_t* k, const uint16_t* v, const int32_t* slots,
+                             uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale, cudaStream_t s);
+cudaError_t launch_kv8_read(const Kv8Rows& a, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                            const float* v_scale, const int32_t* slots, uint16_t* k, uint16_t* v, cudaStream_t s);
+
+// ---- attention
+constexpr int kKv8MaxBatch = 4096;  // the split's prefix sums live in shared memory
+constexpr int kKv8Unit = 16;        // keys per unit of the split (a unit never crosses a page)
+constexpr int kKv8MinUnits = 8;     // units a CTA gets at least: 128 keys, two per warp
+constexpr int kKv8MaxCtas = 608;    // CTAs the unit range is divided over, at most
+
+struct Kv8Attn {
+    const uint16_t* q;
+    int64_t q_stride;
+    int B, Hq, Hkv, group;
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    int num_pages, page_shift;
+    const int32_t* prefix_pages;
+    int prefix_len;
+    const int32_t* page_table;
+    int64_t table_stride;
+    int max_pages;
+    const int32_t* lens;
+    float sm_scale, cap;
+    int tiles;          // row tiles of a sequence's query heads that share a kv head
+    int ptiles;         // row tiles of the whole batch over the prefix (0: no prefix here)
+    float* part_o;      // [slot][row of the tile][D], not divided by the sum
+    float2* part_ml;    // [slot][row of the tile]: reference exponent (log2), sum
+    uint32_t* err;
+    uint16_t* out;
+    float* lse;
+    int ctas;
+};
+int kv8_attn_row_tile(int group);
+cudaError_t launch_kv8_attn(const Kv8Attn& a, int D, int per_token, int num_sms, cudaStream_t s);
+
+// Two E4M3 codes (low byte first) to two f16 values: exact for every code.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
+    return r;
+}
+
+}  // namespace w4a8

@@ -357,8 +357,9 @@ size_t fp8_block_linear_workspace_size(int M, int N, int K);
  *   D is 64 or 128; page_size a power of two in 16..256; num_pages >= 1 and
  *   num_pages * page_size < 2^31; Hkv in 1..1024.
  *   int32 and fp32 arrays of these calls need only their natural 4-byte
- *   alignment (they are often slices of larger tables); all other pointers
- *   16 bytes.
+ *   alignment (they are often slices of larger tables), except that the
+ *   attention wants scale arrays of scale_mode 1 on 16 bytes; all other
+ *   pointers 16 bytes.
  */
 
 /*
@@ -417,7 +418,7 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
  *   last token of a page have no influence. The same call gives the same bits.
  *   Several query tokens of one sequence are several rows that share its pages,
  *   each with its own length.
- *   Requires 1 <= B <= 4096, Hq a multiple of Hkv with Hq / Hkv <= 1024,
+ *   Requires 1 <= B <= 4096, Hq a multiple of Hkv, Hq <= 65535,
  *   prefix_len >= 0, max_pages >= 0, max_pages * page_size < 2^31, sm_scale
  *   finite, logit_cap finite and >= 0.
  *   A page index outside [0, num_pages) or a suffix length outside

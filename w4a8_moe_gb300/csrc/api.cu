@@ -236,7 +236,7 @@ static bool kv8_rows_ok(int T, int Hkv, int D, int64_t k_stride, int64_t v_strid
 }
 static bool kv8_attn_ok(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size)
 {
-    return B >= 1 && B <= kKv8MaxBatch && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq % Hkv == 0 && Hq / Hkv <= 1024 &&
+    return B >= 1 && B <= kKv8MaxBatch && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq <= 65535 && Hq % Hkv == 0 &&
            (D == 64 || D == 128) && kv8_page_shift(page_size) >= 0 && prefix_len >= 0 &&
            prefix_len <= 0x7FFFFF00 && max_pages >= 0 &&
            static_cast<int64_t>(max_pages) * page_size < (static_cast<int64_t>(1) << 31);
@@ -245,16 +245,24 @@ struct Kv8Ws {
     float* part_o;
     float2* part_ml;
     int tiles, ptiles;
+    Kv8Prefix prefix;   // splits 0: the prefix is not tiled
 };
 static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, Kv8Ws* w, void* ws)
 {
     Carver c(ws);
     const int group = Hq / Hkv, R = kv8_attn_row_tile(group);
     w->tiles = (group + R - 1) / R;
-    w->ptiles = prefix_len ? (B * group + R - 1) / R : 0;
+    w->prefix = {};
+    const bool tiled = prefix_len && kv8_prefix_tiled(B * group);
+    if (tiled)
+        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len);
+    w->ptiles = prefix_len && !tiled ? (B * group + R - 1) / R : 0;
     const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxCtas;
     w->part_o = c.take<float>(slots * R * D * 4);
     w->part_ml = c.take<float2>(slots * R * 8);
+    const size_t rows = static_cast<size_t>(w->prefix.splits) * B * Hq;
+    w->prefix.part_o = c.take<float>(rows * D * 4);
+    w->prefix.part_ml = c.take<float2>(rows * 8);
     return c.off;
 }
 
@@ -743,7 +751,8 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
         return W4A8_ERR_SHAPE;
     if (!aligned16(q_bf16) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out_bf16) ||
         !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(prefix_pages) || !aligned4(page_table) ||
-        !aligned4(suffix_lens) || !aligned4(lse))
+        !aligned4(suffix_lens) || !aligned4(lse) ||
+        (scale_mode == 1 && (!aligned16(k_scale) || !aligned16(v_scale))))
         return W4A8_ERR_ALIGN;
     if (!ws || ws_bytes < kv8_prefix_attention_workspace_size(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
         return W4A8_ERR_WORKSPACE;
@@ -765,7 +774,7 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
     a.tiles = w.tiles, a.ptiles = w.ptiles, a.part_o = w.part_o, a.part_ml = w.part_ml;
     a.err = static_cast<uint32_t*>(ws);
     a.out = out_bf16, a.lse = lse;
-    return launch_kv8_attn(a, D, scale_mode, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK
+    return launch_kv8_attn(a, w.prefix, D, scale_mode, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK
                                                                                                    : W4A8_ERR_LAUNCH;
 }
 

@@ -54,8 +54,22 @@ struct Kv8Attn {
     float* lse;
     int ctas;
 };
+// The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key
+// tiles); part_* [split][kv head][row] as above.
+constexpr int kKv8PrefixCtas = 152;  // SMs the plan fills
+constexpr int kKv8MaxSplits = 64;
+struct Kv8Prefix {
+    int tiles;            // 128-key tiles of the prefix
+    int row_pairs;        // pairs of 128-row tiles
+    int splits, tiles_per_split;
+    float* part_o;
+    float2* part_ml;
+};
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len);
+cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s);
+bool kv8_prefix_tiled(int rows);
 int kv8_attn_row_tile(int group);
-cudaError_t launch_kv8_attn(const Kv8Attn& a, int D, int per_token, int num_sms, cudaStream_t s);
+cudaError_t launch_kv8_attn(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s);
 
 // Two E4M3 codes (low byte first) to two f16 values: exact for every code.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair)

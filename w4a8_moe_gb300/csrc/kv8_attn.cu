@@ -26,7 +26,9 @@ constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 // The reference exponent of a row is raised only when a score passes it by
 // this much: 2^{x - m} then stays below 2^8, far inside f16, and the row's
-// accumulators are hardly ever rescaled.
+// accumulators are hardly ever rescaled. With per-token scales the f16 operand
+// is 2^{x - m} * vs, so what is compared is x + log2(the largest vs at hand):
+// m then carries the values' size too, and drops out of o / l.
 constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ float ex2(float x)
@@ -312,7 +314,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             m[t] = -INFINITY, l[t] = 0.0f;
-        float vref = 0.0f, vinv = 0.0f;   // what the value scales are taken relative to
 
         Codes<D> x;
         auto fetch = [&](int unit) {
@@ -347,6 +348,13 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
             }
             // ---- scores in log2 units; keys past the end are -inf
             const int live = len - unit * kKv8Unit;
+            float lift = 0.0f;   // log2 of the unit's largest value scale
+            if (TOK) {
+                float top = fmaxf(fmaxf(fabsf(x.vs[0]), fabsf(x.vs[1])), fmaxf(fabsf(x.vs[2]), fabsf(x.vs[3])));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                lift = fmaxf(log2f(top), -100.0f);
+            }
             bool grow = false;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -363,37 +371,19 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
                     }
                     f = t * 8 + c * 2 + (i & 1) < live ? f : -INFINITY;
                     s[t][i] = f;
-                    grow = grow || f > m[i >> 1] + kSlack;
+                    grow = grow || f + lift > m[i >> 1] + kSlack;
                 }
-            if (TOK) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    grow = grow || x.vs[i] > vref;
-            }
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 float f[NT];
-                float ratio = 1.0f;
-                if (TOK) {
-                    float top = fmaxf(fmaxf(x.vs[0], x.vs[1]), fmaxf(x.vs[2], x.vs[3]));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                    if (top > vref) {
-                        const float to = fminf(fmaxf(2.0f * top, 1e-37f), 3e38f);
-                        ratio = vref / to;
-                        vref = to;
-                        vinv = 1.0f / to;
-                    }
-                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     float top = fmaxf(fmaxf(s[0][2 * t], s[0][2 * t + 1]), fmaxf(s[1][2 * t], s[1][2 * t + 1]));
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2)) + lift;
                     const float to = fmaxf(m[t], top);
                     f[t] = to == -INFINITY ? 1.0f : ex2(m[t] - to);
                     m[t] = to;
                     l[t] *= f[t];
-                    f[t] *= ratio;
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -416,8 +406,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
                     float p0 = ex2(s[k][2 * t] - ref), p1 = ex2(s[k][2 * t + 1] - ref);
                     l[t] += p0 + p1;
                     if (TOK) {
-                        p0 *= x.vs[2 * k] * vinv;
-                        p1 *= x.vs[2 * k + 1] * vinv;
+                        p0 *= x.vs[2 * k];
+                        p1 *= x.vs[2 * k + 1];
                     }
                     pb[t][k] = pack_f16(p0, p1);
                 }
@@ -437,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
         }
 
         // ---- the warps' results, joined in a fixed order
-        const float vscale = TOK ? vref : __ldg(a.v_scale + h);
+        const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 1);
@@ -480,14 +470,22 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
     }
 }
 
-// One CTA per (sequence, kv head): adds up the pieces of its rows.
+// One CTA per (sequence, query head) adds up the pieces of its row. Warps take
+// pieces in turn, a lane D / 32 values, all loads of a warp's pieces in flight
+// together; the warps' sums are joined in a fixed order.
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(D) kv8_join_kernel(const __grid_constant__ Kv8Attn a, int R)
+__global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
+                                                                   const __grid_constant__ Kv8Prefix p, int R)
 {
-    const int b = blockIdx.x, h = blockIdx.y, d = threadIdx.x;
-    __shared__ int part[2][D / 32];
+    constexpr int V = D / 32;
+    const int b = blockIdx.x, qh = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = qh / a.group, gi = qh % a.group;
+    __shared__ int part[2][kJoinWarps];
+    __shared__ float so[kJoinWarps][D];
+    __shared__ float2 sml[kJoinWarps];
     int before = 0, all = 0;
-    for (int i = d; i < a.B; i += D) {
+    for (int i = tid; i < a.B; i += kJoinWarps * 32) {
         const int n = seq_units(a, i);
         all += n;
         before += i < b ? n : 0;
@@ -497,46 +495,100 @@ __global__ void __launch_bounds__(D) kv8_join_kernel(const __grid_constant__ Kv8
         before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
         all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
     }
-    if ((d & 31) == 0)
-        part[0][d >> 5] = before, part[1][d >> 5] = all;
+    if (lane == 0)
+        part[0][warp] = before, part[1][warp] = all;
     __syncthreads();
     before = all = 0;
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w)
+    for (int w = 0; w < kJoinWarps; ++w)
         before += part[0][w], all += part[1][w];
     const Line line = make_line(a, all);
-    const int n = seq_units(a, b);
-    for (int gi = 0; gi < a.group; ++gi) {
-        float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-        auto add = [&](int64_t first, int units, int pair, int row) {
-            if (units == 0)
-                return;
-            const int c1 = cta_of(line, first + units - 1);
-            for (int c = cta_of(line, first); c <= c1; ++c) {
-                const int64_t at = static_cast<int64_t>(pair + c) * R + row;
-                const float2 ml = a.part_ml[at];
-                const float to = fmaxf(top, ml.x);
-                const float ref = to == -INFINITY ? 0.0f : to;
-                const float f0 = ex2(top - ref), f1 = ex2(ml.x - ref);
-                acc = acc * f0 + a.part_o[at * D + d] * f1;
-                sum = sum * f0 + ml.y * f1;
-                top = to;
-            }
-        };
-        if (a.ptiles) {
-            const int r = b * a.group + gi;
-            const int pair = h * a.ptiles + r / R;
-            add(static_cast<int64_t>(pair) * line.up, line.up, pair, r % R);
-        }
-        const int j = h * a.tiles + gi / R;
-        add(line.own + static_cast<int64_t>(before) * line.hr + static_cast<int64_t>(j) * n, n,
-            line.pairs_p + b * line.hr + j, gi % R);
-        const int64_t head = static_cast<int64_t>(b) * a.Hq + h * a.group + gi;
-        const bool empty = top == -INFINITY && sum == 0.0f;
-        a.out[head * D + d] = float_to_bf16_bits(empty ? 0.0f : acc / sum);
-        if (a.lse && d == 0)
-            a.lse[head] = empty ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+
+    // the row's pieces: [0, n0) of the tiled prefix, [n0, n1) of the untiled one, [n1, n2) of its own keys
+    const int row = b * a.group + gi;
+    const int n0 = p.splits;
+    int n1 = n0, n2, c_pre = 0, c_own = 0, pair_pre = 0, pair_own = 0;
+    if (a.ptiles) {
+        pair_pre = h * a.ptiles + row / R;
+        const int64_t first = static_cast<int64_t>(pair_pre) * line.up;
+        c_pre = cta_of(line, first);
+        n1 += cta_of(line, first + line.up - 1) - c_pre + 1;
     }
+    n2 = n1;
+    const int units = seq_units(a, b);
+    if (units) {
+        const int j = h * a.tiles + gi / R;
+        pair_own = line.pairs_p + b * line.hr + j;
+        const int64_t first = line.own + static_cast<int64_t>(before) * line.hr + static_cast<int64_t>(j) * units;
+        c_own = cta_of(line, first);
+        n2 += cta_of(line, first + units - 1) - c_own + 1;
+    }
+    float top = -INFINITY, sum = 0.0f, acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        acc[i] = 0.0f;
+#pragma unroll 4
+    for (int k = warp; k < n2; k += kJoinWarps) {
+        const float* o;
+        const float2* mlp;
+        if (k < n0) {
+            const int64_t at = (static_cast<int64_t>(k) * a.Hkv + h) * a.B * a.group + row;
+            o = p.part_o + at * D;
+            mlp = p.part_ml + at;
+        } else {
+            const int64_t at = k < n1 ? static_cast<int64_t>(pair_pre + c_pre + k - n0) * R + row % R
+                                      : static_cast<int64_t>(pair_own + c_own + k - n1) * R + gi % R;
+            o = a.part_o + at * D;
+            mlp = a.part_ml + at;
+        }
+        const float2 ml = *mlp;
+        float v[V];
+        if (V == 4) {
+            const float4 w = *(reinterpret_cast<const float4*>(o) + lane);
+            v[0] = w.x, v[1] = w.y, v[V - 2] = w.z, v[V - 1] = w.w;
+        } else {
+            const float2 w = *(reinterpret_cast<const float2*>(o) + lane);
+            v[0] = w.x, v[1] = w.y;
+        }
+        const float to = fmaxf(top, ml.x);
+        const float ref = to == -INFINITY ? 0.0f : to;
+        const float f0 = ex2(top - ref), f1 = ex2(ml.x - ref);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            acc[i] = acc[i] * f0 + v[i] * f1;
+        sum = sum * f0 + ml.y * f1;
+        top = to;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        so[warp][lane * V + i] = acc[i];
+    if (lane == 0)
+        sml[warp] = make_float2(top, sum);
+    __syncthreads();
+    if (tid >= D / 2)
+        return;
+    top = sml[0].x;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w)
+        top = fmaxf(top, sml[w].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float x = 0.0f, y = 0.0f;
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = ex2(sml[w].x - ref);
+        x += so[w][2 * tid] * f;
+        y += so[w][2 * tid + 1] * f;
+        sum += sml[w].y * f;
+    }
+    const bool empty = top == -INFINITY && sum == 0.0f;
+    const int64_t head = static_cast<int64_t>(b) * a.Hq + qh;
+    x = empty ? 0.0f : x / sum;
+    y = empty ? 0.0f : y / sum;
+    *reinterpret_cast<uint32_t*>(a.out + head * D + 2 * tid) =
+        static_cast<uint32_t>(float_to_bf16_bits(x)) | (static_cast<uint32_t>(float_to_bf16_bits(y)) << 16);
+    if (a.lse && tid == 0)
+        a.lse[head] = empty ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, int NT, bool TOK>
@@ -553,26 +605,36 @@ static cudaError_t launch_pieces(const Kv8Attn& a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv8_attn(const Kv8Attn& in, int D, int per_token, int num_sms, cudaStream_t s)
+// Rows of the batch over the prefix from which the tensor-core kernel takes it.
+bool kv8_prefix_tiled(int rows) { return rows > 16; }
+
+cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s)
 {
     Kv8Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
     a.ctas = num_sms * (R == 8 ? 3 : 2);
     a.ctas = a.ctas < kKv8MaxCtas ? a.ctas : kKv8MaxCtas;
     cudaError_t e;
+    if (p.splits) {
+        e = launch_kv8_prefix(a, p, D, per_token, s);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (a.max_pages || a.ptiles) {
+        if (D == 128)
+            e = R == 8 ? (per_token ? launch_pieces<128, 1, true>(a, s) : launch_pieces<128, 1, false>(a, s))
+                       : (per_token ? launch_pieces<128, 2, true>(a, s) : launch_pieces<128, 2, false>(a, s));
+        else
+            e = R == 8 ? (per_token ? launch_pieces<64, 1, true>(a, s) : launch_pieces<64, 1, false>(a, s))
+                       : (per_token ? launch_pieces<64, 2, true>(a, s) : launch_pieces<64, 2, false>(a, s));
+        if (e != cudaSuccess)
+            return e;
+    }
+    const dim3 grid(a.B, a.Hq);
     if (D == 128)
-        e = R == 8 ? (per_token ? launch_pieces<128, 1, true>(a, s) : launch_pieces<128, 1, false>(a, s))
-                   : (per_token ? launch_pieces<128, 2, true>(a, s) : launch_pieces<128, 2, false>(a, s));
+        kv8_join_kernel<128><<<grid, kJoinWarps * 32, 0, s>>>(a, p, R);
     else
-        e = R == 8 ? (per_token ? launch_pieces<64, 1, true>(a, s) : launch_pieces<64, 1, false>(a, s))
-                   : (per_token ? launch_pieces<64, 2, true>(a, s) : launch_pieces<64, 2, false>(a, s));
-    if (e != cudaSuccess)
-        return e;
-    const dim3 grid(a.B, a.Hkv);
-    if (D == 128)
-        kv8_join_kernel<128><<<grid, 128, 0, s>>>(a, R);
-    else
-        kv8_join_kernel<64><<<grid, 64, 0, s>>>(a, R);
+        kv8_join_kernel<64><<<grid, kJoinWarps * 32, 0, s>>>(a, p, R);
     return cudaGetLastError();
 }
 

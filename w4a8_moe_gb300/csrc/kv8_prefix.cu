@@ -1,0 +1,613 @@
+// Attention of a whole batch over its shared prefix: one pass of tensor-core
+// matrix products over the prefix's pages for all sequences at once.
+//
+// "ROCm: enable trillion-parameter MoE models with INT4-FP8 single node",
+// config.json (kv_cache_scheme FP8; 48 query and 8 key/value heads).
+//
+// For kv head h the rows are all (sequence, query head of h's group), R of
+// them, and S = Q K^T, O = P V are [R, keys] and [R, D] matrix products. A CTA
+// takes 256 rows (two 128-row tiles) and a range of 128-key tiles and runs,
+// with S, P and O in tensor memory:
+//   loader    warp 12: pages -> raw codes in shared memory (bulk copies)
+//   converter warps 8-11: E4M3 -> f16 (exact), into the layouts the MMA reads
+//   issuer    warp 13: S_t = Q_t K^T, O_t += P_t V, alternating the row tiles
+//   softmax   warps 0-3 (tile 0), 4-7 (tile 1): one thread per row
+// While one tile's softmax runs, the tensor core works for the other tile.
+//
+// Numbers: q is normalized per row by a power of two and held in f16 (at most
+// 2^-25 of the row's largest element is lost, one fp32 rounding), codes are
+// exact in f16, S and O are fp32, P is rounded to f16 (2^-11 of each weight),
+// its sum is taken in fp32 before that rounding.
+#include <math.h>
+
+#include "internal.h"
+#include "kv8.cuh"
+#include "ptx.cuh"
+
+namespace w4a8 {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;        // keys per tile, rows per row tile
+constexpr int kHalf = 64;         // keys per raw slot
+constexpr int kRaw = 3;           // raw slots
+constexpr int kScaleRing = 4;     // tiles whose per-token scales are held
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;    // see kv8_attn.cu
+
+template <int D>
+struct Smem {
+    static constexpr int kOperand = kTile * D * 2;          // one f16 operand tile
+    static constexpr int kPanel = kTile * 128;              // 64 f16 columns of it
+    static constexpr int q = 0;                             // [2] row tiles
+    static constexpr int k = q + 2 * kOperand;              // [2] stages
+    static constexpr int v = k + 2 * kOperand;              // [2] stages
+    static constexpr int raw = v + 2 * kOperand;            // [kRaw] of 64 x D codes
+    static constexpr int scales = raw + kRaw * kHalf * D;   // [kScaleRing][2][128] fp32
+    static constexpr int bars = scales + kScaleRing * 2 * kTile * 4;
+    static constexpr int total = bars + 256;
+};
+// mbarriers, 8 bytes each
+enum Bar {
+    kRawFull = 0,                    // [kRaw]
+    kRawEmpty = kRawFull + kRaw,     // [kRaw]
+    kKFull = kRawEmpty + kRaw,       // [2]
+    kKEmpty = kKFull + 2,
+    kVFull = kKEmpty + 2,
+    kVEmpty = kVFull + 2,
+    kSFull = kVEmpty + 2,            // [2] row tiles
+    kPFull = kSFull + 2,             // [2]
+    kOFull = kPFull + 2,             // [2]
+    kScFull = kOFull + 2,            // [kScaleRing]
+    kBars = kScFull + kScaleRing
+};
+static_assert(kBars * 8 + 8 <= 256, "barrier area");
+
+// MMA, f16 operands, fp32 accumulators; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
+{
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+                 "r"(acc)
+                 : "memory");
+}
+// An operand whose non-contracted axis is contiguous, 128-byte swizzle: panels
+// of 64 values by all keys; 8-key groups are 1024 bytes apart, panels `panel`.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t panel)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((panel >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// Wait for this warp's tensor-memory loads; the registers they fill pass
+// through, so that no use of them can be moved ahead of the wait.
+__device__ __forceinline__ void ld_wait32(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace
+
+template <int D, bool TOK>
+__global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_constant__ Kv8Attn a,
+                                                                 const __grid_constant__ Kv8Prefix pl)
+{
+    using L = Smem<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bars = base + L::bars;
+    auto bar = [&](int i) { return bars + 8u * i; };
+    __shared__ int abort_flag;
+    __shared__ uint32_t tmem_base;
+    const volatile int* abort = &abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // CTA -> (split, row pair, head); neighbours share the head's keys
+    const int rp = blockIdx.x % pl.row_pairs;
+    const int h = (blockIdx.x / pl.row_pairs) % a.Hkv;
+    const int split = blockIdx.x / (pl.row_pairs * a.Hkv);
+    const int tile0 = split * pl.tiles_per_split;
+    const int n = min(pl.tiles - tile0, pl.tiles_per_split);
+    const int rows_all = a.B * a.group;
+    const int row0 = rp * 2 * kTile;
+    const int nt = rows_all - row0 > kTile ? 2 : 1;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < kBars; ++i) {
+            uint32_t count = 1;
+            if ((i >= kRawEmpty && i < kKFull) || (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty))
+                count = 4;          // the converter's warps
+            else if (i >= kPFull && i < kOFull)
+                count = 4;          // a tile's softmax warps
+            mbar_init(bar(i), count);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 13)
+        tmem_alloc(smem_u32(&tmem_base), 512);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    auto fail = [&]() {
+        set_error(a.err, kErrBitTimeout);
+        *const_cast<volatile int*>(&abort_flag) = 1;
+    };
+    auto wait = [&](int i, uint32_t parity) {
+        if (mbar_wait_or_abort<1000>(bar(i), parity, abort))
+            return true;
+        fail();
+        return false;
+    };
+    auto wait_warp = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(i, parity)) != 0; };
+
+    // ---- queries into shared memory, by the softmax threads: row scale c
+    const bool softmax_role = warp < 8;
+    const int t = warp >> 2;                       // row tile of a softmax thread
+    const int my_row = row0 + t * kTile + (tid & 127);
+    float c = 0.0f;
+    if (softmax_role && t < nt) {
+        uint4 raw[D / 8];
+        if (my_row < rows_all) {
+            const int b = my_row / a.group;
+            const uint16_t* src = a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + my_row % a.group) * D;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                raw[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                raw[i] = make_uint4(0, 0, 0, 0);
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = max(top, max((w[j] >> 16) & 0x7FFFu, w[j] & 0x7FFFu));
+        }
+        const int ex = static_cast<int>(top >> 7);
+        const int e = top == 0 || ex == 255 ? 0 : max(ex, 1) - 127;
+        c = ldexpf(a.sm_scale, e);
+        if (!TOK)
+            c *= __ldg(a.k_scale + h);
+        // a negative factor goes into q, so that the largest product is the largest score
+        const float down = c < 0.0f ? -ldexpf(1.0f, -e) : ldexpf(1.0f, -e);
+        c = fabsf(c);
+        c = a.cap > 0.0f ? c / a.cap : c * kLog2e;
+        const int r = tid & 127;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            uint32_t f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+            sts128(base + L::q + t * L::kOperand + (i >> 3) * L::kPanel + r * 128 + (((i & 7) ^ (r & 7)) << 4), f[0],
+                   f[1], f[2], f[3]);
+        }
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+
+    if (softmax_role) {
+        // ------------------------------------------------------------ softmax
+        if (t < nt) {
+            const uint32_t ts = tmem + (static_cast<uint32_t>(warp & 3) << 21) + t * kTile;         // S, then P
+            const uint32_t to = tmem + (static_cast<uint32_t>(warp & 3) << 21) + 2 * kTile + t * D;  // O
+            float m = -INFINITY, l = 0.0f;
+            const float capl = a.cap * kLog2e;
+            const bool capped = a.cap > 0.0f;
+            auto score = [&](float s) {   // s * c, capped: cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y}))
+                float f = s * c;
+                if (capped) {
+                    const float e = ex2(f * (2.0f * kLog2e));
+                    f = e > 1e30f ? capl : capl * (1.0f - __fdividef(2.0f, 1.0f + e));
+                }
+                return f;
+            };
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const float* ks = nullptr;
+                if (TOK) {
+                    ok = wait_warp(kScFull + i % kScaleRing, (i / kScaleRing) & 1);
+                    if (!ok)
+                        break;
+                    ks = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + L::scales) +
+                         (i % kScaleRing) * 2 * kTile;
+                }
+                const float* vs = ks + kTile;
+                const int live = a.prefix_len - (tile0 + i) * kTile;   // keys of the tile that exist (may pass 128)
+                float lift = 0.0f;   // log2 of the tile's largest value scale
+                if (TOK) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v = fmaxf(v, lane + 32 * j < live ? fabsf(vs[lane + 32 * j]) : 0.0f);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+                    lift = fmaxf(log2f(v), -100.0f);
+                }
+                ok = wait_warp(kSFull + t, i & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // the row's largest score
+                float top = -INFINITY;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t r[32];
+                    tmem_ld32(ts + ch * 32, r);
+                    ld_wait32(r);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float f = __uint_as_float(r[j]);
+                        if (TOK)
+                            f *= ks[ch * 32 + j];
+                        if (live < kTile)
+                            f = ch * 32 + j < live ? f : -INFINITY;
+                        top = fmaxf(top, f);
+                    }
+                }
+                top = score(top) + lift;
+                if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+                    const float next = fmaxf(m, top);
+                    const float f = next == -INFINITY ? 1.0f : ex2(m - next);
+                    m = next;
+                    l *= f;
+                    if (i > 0) {
+#pragma unroll
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t r[32];
+                            tmem_ld32(to + ch * 32, r);
+                            ld_wait32(r);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+                            tmem_st32(to + ch * 32, r);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t r[32], p[16];
+                    tmem_ld32(ts + ch * 32, r);
+                    ld_wait32(r);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float w[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float f = __uint_as_float(r[j + e]);
+                            if (TOK)
+                                f *= ks[ch * 32 + j + e];
+                            f = score(f);
+                            if (live < kTile)
+                                f = ch * 32 + j + e < live ? f : -INFINITY;
+                            w[e] = ex2(f - ref);
+                            l += w[e];
+                            if (TOK)
+                                w[e] *= live < kTile && ch * 32 + j + e >= live ? 0.0f : vs[ch * 32 + j + e];
+                        }
+                        p[j >> 1] = pack_f16(w[0], w[1]);
+                    }
+                    tmem_st16(ts + ch * 16, p);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(kPFull + t));
+            }
+            if (ok && wait_warp(kOFull + t, 0)) {
+                tc_fence_after();
+                const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
+                const int64_t at = (static_cast<int64_t>(split) * a.Hkv + h) * rows_all + my_row;
+#pragma unroll
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t r[32];
+                    tmem_ld32(to + ch * 32, r);
+                    ld_wait32(r);
+                    if (my_row < rows_all) {
+                        float4* dst = reinterpret_cast<float4*>(pl.part_o + at * D + ch * 32);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_float4(__uint_as_float(r[4 * j]) * vscale, __uint_as_float(r[4 * j + 1]) * vscale,
+                                                 __uint_as_float(r[4 * j + 2]) * vscale, __uint_as_float(r[4 * j + 3]) * vscale);
+                    }
+                }
+                if (my_row < rows_all)
+                    pl.part_ml[at] = make_float2(m, l);
+                tc_fence_before();
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------- converter
+        // A thread turns 16 codes into 32 bytes of f16. Eight threads cover 64
+        // bytes of an even row and the other 64 of the odd row below, so that
+        // neither the loads nor the swizzled stores collide in a bank.
+        const int ct = tid - 256;
+        const int q4 = ct & 3, odd = (ct >> 2) & 1, pr = ct >> 3;   // 16 row pairs at a time
+        bool ok = true;
+        for (int s = 0; s < 4 * n && ok; ++s) {
+            const int i = s >> 2, half = s & 1;
+            const bool is_v = (s >> 1) & 1;
+            const int slot = s % kRaw;
+            ok = wait_warp(kRawFull + slot, (s / kRaw) & 1);
+            if (ok && half == 0 && i >= 2)
+                ok = wait_warp((is_v ? kVEmpty : kKEmpty) + (i & 1), ((i >> 1) - 1) & 1);
+            if (!ok)
+                break;
+            const uint32_t src = base + L::raw + slot * kHalf * D;
+            const uint32_t dst = base + (is_v ? L::v : L::k) + (i & 1) * L::kOperand;
+            const int live = a.prefix_len - (tile0 + i) * kTile;
+            constexpr int kPasses = D / 64;
+            uint4 w[2 * kPasses];
+            auto place = [&](int x, int& row, int& c16) {
+                row = (x / kPasses) * 32 + pr * 2 + odd;
+                c16 = D == 128 ? q4 + 4 * (odd ^ (x & 1)) : q4;
+            };
+#pragma unroll
+            for (int x = 0; x < 2 * kPasses; ++x) {
+                int row, c16;
+                place(x, row, c16);
+                w[x] = lds128(src + row * D + c16 * 16);
+                if (half * kHalf + row >= live)
+                    w[x] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int x = 0; x < 2 * kPasses; ++x) {
+                int row, c16;
+                place(x, row, c16);
+                const int key = half * kHalf + row;
+                const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+                uint32_t f[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] = e4m3x2_to_f16x2(u[j] & 0xFFFFu);
+                    f[2 * j + 1] = e4m3x2_to_f16x2(u[j] >> 16);
+                }
+                const uint32_t at = dst + (c16 >> 2) * L::kPanel + key * 128;
+                const int ch = (c16 & 3) * 2;
+                sts128(at + ((ch ^ (key & 7)) << 4), f[0], f[1], f[2], f[3]);
+                sts128(at + (((ch + 1) ^ (key & 7)) << 4), f[4], f[5], f[6], f[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(kRawEmpty + slot));
+                if (half == 1)
+                    mbar_arrive(bar((is_v ? kVFull : kKFull) + (i & 1)));
+            }
+        }
+    } else if (warp == 12) {
+        // ------------------------------------------------------------- loader
+        const int ck_shift = min(a.page_shift, 6);           // keys per copy
+        const int ck = 1 << ck_shift;
+        const int chunks = kHalf >> ck_shift;
+        const int n_pages = (a.prefix_len + (1 << a.page_shift) - 1) >> a.page_shift;
+        int issued = 0;
+        for (int s = 0; s < 4 * n; ++s) {
+            const int i = s >> 2, half = s & 1;
+            const bool is_v = (s >> 1) & 1;
+            const int slot = s % kRaw;
+            const int key = (tile0 + i) * kTile + half * kHalf + lane * ck;
+            const bool mine = lane < chunks && key < a.prefix_len;
+            int page = 0;
+            if (mine) {
+                const int idx = key >> a.page_shift;
+                page = idx < n_pages ? __ldg(a.prefix_pages + idx) : -1;
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
+                    set_error(a.err, kErrBitIndex);
+                    page = 0;
+                }
+            }
+            const int copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+            bool ok = true;
+            if (lane == 0 && s >= kRaw)
+                ok = wait(kRawEmpty + slot, (s / kRaw - 1) & 1);
+            if (!__shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0))
+                break;
+            const bool with_scales = TOK && !is_v;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(kRawFull + slot), copies * ck * D);
+                if (with_scales && half == 0) {
+                    const int live = min(a.prefix_len - (tile0 + i) * kTile, kTile);
+                    mbar_arrive_expect_tx(bar(kScFull + i % kScaleRing), ((live + ck - 1) & ~(ck - 1)) * 8);
+                }
+            }
+            __syncwarp();
+            if (mine) {
+                const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + h) << a.page_shift) +
+                                    (key & ((1 << a.page_shift) - 1));
+                bulk_load(base + L::raw + slot * kHalf * D + lane * ck * D, (is_v ? a.v_cache : a.k_cache) + row * D,
+                          ck * D, bar(kRawFull + slot));
+                if (with_scales) {
+                    const uint32_t at = base + L::scales + (i % kScaleRing) * 2 * kTile * 4 + (half * kHalf + lane * ck) * 4;
+                    bulk_load(at, a.k_scale + row, ck * 4, bar(kScFull + i % kScaleRing));
+                    bulk_load(at + kTile * 4, a.v_scale + row, ck * 4, bar(kScFull + i % kScaleRing));
+                }
+            }
+            issued = s + 1;
+        }
+        // whatever happened to the other roles, the copies in flight end before
+        // the CTA does (a raw slot's copies end before its successor's begin)
+        if (lane == 0) {
+            for (int s = max(issued - kRaw, 0); s < issued; ++s) {
+                mbar_wait(bar(kRawFull + s % kRaw), (s / kRaw) & 1);
+                if (TOK)
+                    mbar_wait(bar(kScFull + (s >> 2) % kScaleRing), ((s >> 2) / kScaleRing) & 1);
+            }
+        }
+    } else if (warp == 13 && lane == 0) {
+        // ------------------------------------------------------------- issuer
+        constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
+        auto scores = [&](int tt, int i) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t off = (s >> 2) * L::kPanel + (s & 3) * 32;
+                mma_ss(tmem + tt * kTile, desc_kmajor_sw128(base + L::q + tt * L::kOperand + off),
+                       desc_kmajor_sw128(base + L::k + (i & 1) * L::kOperand + off), kIdS, s > 0);
+            }
+            umma_commit(bar(kSFull + tt));
+        };
+        bool ok = wait(kKFull, 0);
+        if (ok) {
+            tc_fence_after();
+            for (int tt = 0; tt < nt; ++tt)
+                scores(tt, 0);
+            umma_commit(bar(kKEmpty));
+        }
+        for (int i = 0; i < n && ok; ++i) {
+            ok = wait(kVFull + (i & 1), (i >> 1) & 1);
+            for (int tt = 0; tt < nt && ok; ++tt) {
+                ok = wait(kPFull + tt, i & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                    mma_ts(tmem + 2 * kTile + tt * D, tmem + tt * kTile + s * 8,
+                           desc_mnmajor_sw128(base + L::v + (i & 1) * L::kOperand + s * 2048, L::kPanel), kIdO,
+                           i > 0 || s > 0);
+                if (i + 1 < n) {
+                    if (tt == 0)
+                        ok = wait(kKFull + ((i + 1) & 1), ((i + 1) >> 1) & 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    scores(tt, i + 1);
+                } else {
+                    umma_commit(bar(kOFull + tt));
+                }
+            }
+            if (ok) {
+                umma_commit(bar(kVEmpty + (i & 1)));
+                if (i + 1 < n)
+                    umma_commit(bar(kKEmpty + ((i + 1) & 1)));
+            }
+        }
+        if (!ok) {   // what was issued ends before tensor memory is freed
+            mbar_init(bar(kBars), 1);
+            fence_mbar_init();
+            umma_commit(bar(kBars));
+            mbar_wait(bar(kBars), 0);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+        tmem_relinquish();
+    }
+}
+
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len)
+{
+    Kv8Prefix p = {};
+    p.tiles = (prefix_len + kTile - 1) / kTile;
+    p.row_pairs = (rows + 2 * kTile - 1) / (2 * kTile);
+    // Time in key tiles: waves of CTAs, each its tiles plus about three tiles'
+    // worth of start and end, plus the join's reading of every split.
+    const int64_t base = static_cast<int64_t>(Hkv) * p.row_pairs;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= p.tiles && s <= kKv8MaxSplits; ++s) {
+        const int per = (p.tiles + s - 1) / s;
+        const int splits = (p.tiles + per - 1) / per;
+        const int64_t waves = (base * splits + kKv8PrefixCtas - 1) / kKv8PrefixCtas;
+        const int64_t cost = waves * (per + 3) * 8 + splits;
+        if (cost < best) {
+            best = cost;
+            p.splits = splits;
+            p.tiles_per_split = per;
+        }
+    }
+    return p;
+}
+
+template <int D, bool TOK>
+static cudaError_t launch(const Kv8Attn& a, const Kv8Prefix& p, cudaStream_t s)
+{
+    auto kern = kv8_prefix_kernel<D, TOK>;
+    const int smem = Smem<D>::total + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    kern<<<p.splits * a.Hkv * p.row_pairs, kThreads, smem, s>>>(a, p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s)
+{
+    if (D == 128)
+        return per_token ? launch<128, true>(a, p, s) : launch<128, false>(a, p, s);
+    return per_token ? launch<64, true>(a, p, s) : launch<64, false>(a, p, s);
+}
+
+}  // namespace w4a8

@@ -323,113 +323,131 @@ def fp8_block_linear(x_bf16, w_e4m3, w_scale_inv, out=None, xq_out=None, xs_out=
     return out
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _rows3(t, what):
-    """A bf16 [rows, heads, D] tensor whose rows may lie apart -> (rows, heads, D, row stride)."""
-    _need(t.dtype == torch.bfloat16 and t.dim() == 3, f"{what} must be a bf16 [tokens, heads, D] tensor")
-    n, h, d = t.shape
-    _need(t.stride(2) == 1 and (h == 1 or t.stride(1) == d), f"{what}: each token's heads must be contiguous")
-    # a tensor of one row may report any row stride
-    return n, h, d, t.stride(0) if n > 1 else max(t.stride(0), h * d)
+# The kv8_* calls are made once per layer and decode step, where a call takes a few microseconds on the GPU, so their
+# checks are written to cost little: one test per rule, no helper objects.
+_BF16, _F32, _I32, _U8, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 
 
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks a cache's four tensors -> (pages, kv heads, page size, D, scale mode)."""
-    for c, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(c.dtype in (torch.uint8, torch.float8_e4m3fn) and c.dim() == 4 and c.is_contiguous(),
-              f"{what} must be contiguous uint8 or float8_e4m3fn [pages, kv heads, page size, D]")
-    _need(k_cache.shape == v_cache.shape, "k_cache and v_cache differ in shape")
-    n, h, page, d = k_cache.shape
-    for s, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _need(s.dtype == torch.float32 and s.is_contiguous(), f"{what} must be contiguous float32")
-        _need(s.shape in ((h,), (n, h, page)), f"{what} must be [kv heads] or [pages, kv heads, page size]")
-    _need(k_scale.shape == v_scale.shape, "k_scale and v_scale differ in shape")
-    return n, h, page, d, int(k_scale.dim() == 3)
+    """Checks a cache's four tensors -> (shape [pages, kv heads, page size, D], scale mode)."""
+    shape, scales = k_cache.shape, k_scale.shape
+    if k_cache.dtype not in (_U8, _F8) or v_cache.dtype not in (_U8, _F8) or len(shape) != 4 or v_cache.shape != shape \
+            or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous uint8 or float8_e4m3fn [pages, kv heads, page size, D]")
+    if k_scale.dtype != _F32 or v_scale.dtype != _F32 or v_scale.shape != scales \
+            or (scales != shape[1:2] and scales != shape[:3]) or not (k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("k_scale and v_scale must be contiguous float32, both [kv heads] or both [pages, kv heads, page size]")
+    return shape, 1 if len(scales) == 3 else 0
 
 
-def _i32(t, dim, what):
-    _need(t.dtype == torch.int32 and t.dim() == dim, f"{what} must be an int32 tensor of {dim} dimension(s)")
-    return t
+def _row_stride(t, shape, what):
+    """The row stride of a bf16 [rows, heads, D] tensor whose rows may lie apart."""
+    if t.dtype != _BF16 or t.shape != shape:
+        raise ValueError(f"{what} must be bf16 of shape {list(shape)}")
+    row, head, one = t.stride()
+    if one != 1 or (head != shape[2] and shape[1] != 1):
+        raise ValueError(f"{what}: each token's heads must be contiguous")
+    return row if shape[0] > 1 else shape[1] * shape[2]   # one row may report any row stride
 
 
-def _same_device(ref, *tensors):
-    _need(ref.is_cuda, "tensors must be on the GPU")
+def _on_gpu(ref, *tensors):
+    where = ref.get_device()
     for t in tensors:
-        _need(t is None or t.device == ref.device, "tensors must be on one device")
+        if t.get_device() != where:
+            raise ValueError("tensors must be on one GPU")
+    if where < 0:
+        raise ValueError("tensors must be on the GPU")
+    return where
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def kv8_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, min_scale: float = 0.0, stream=None) -> None:
     """Quantize bf16 keys and values [T, kv heads, D] (rows may lie apart, as in a fused projection's output) into
     slots [T] (int32; out of range: skipped) of the cache. k_scale / v_scale of shape [kv heads] are read; of shape
     [pages, kv heads, page size] they are computed and written."""
-    n, h, page, d, mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    T, hk, dk, k_stride = _rows3(k, "k")
-    _need(k.shape == v.shape and (hk, dk) == (h, d), "k and v must be [T, kv heads, D] of the cache's heads and D")
-    v_stride = _rows3(v, "v")[3]
-    _need(_i32(slots, 1, "slots").shape[0] == T and slots.is_contiguous(), "slots must be contiguous int32 [T]")
-    _same_device(k_cache, v_cache, k_scale, v_scale, k, v, slots)
-    _check(_load().kv8_write(_ptr(k), _ptr(v), T, k_stride, v_stride, _ptr(slots), h, d, n, page, mode,
-                             float(min_scale), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                             _stream(stream)))
+    (n, h, page, d), mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    T = slots.numel()
+    if slots.dtype != _I32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous int32 [T]")
+    k_stride, v_stride = _row_stride(k, (T, h, d), "k"), _row_stride(v, (T, h, d), "v")
+    device = _on_gpu(k_cache, v_cache, k_scale, v_scale, k, v, slots)
+    status = _load().kv8_write(k.data_ptr(), v.data_ptr(), T, k_stride, v_stride, slots.data_ptr(), h, d, n, page, mode,
+                               min_scale, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                               v_scale.data_ptr(), _raw_stream(stream, device))
+    if status:
+        _check(status)
 
 
 def kv8_read(k_cache, v_cache, k_scale, v_scale, slots, k_out=None, v_out=None, stream=None):
     """The cache's slots [T] (int32; out of range: zeros) as bf16 keys and values, each [T, kv heads, D]."""
-    n, h, page, d, mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    T = _i32(slots, 1, "slots").shape[0]
-    _need(slots.is_contiguous(), "slots must be contiguous")
-    with _on(stream):
-        new = dict(dtype=torch.bfloat16, device=k_cache.device)
-        k_out = k_out if k_out is not None else torch.empty(T, h, d, **new)
-        v_out = v_out if v_out is not None else torch.empty(T, h, d, **new)
-    k_stride, v_stride = _rows3(k_out, "k_out")[3], _rows3(v_out, "v_out")[3]
-    _need(k_out.shape == v_out.shape == (T, h, d), "k_out and v_out must be [T, kv heads, D]")
-    _same_device(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
-    _check(_load().kv8_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(slots), T, h, d, n, page,
-                            mode, _ptr(k_out), k_stride, _ptr(v_out), v_stride, _stream(stream)))
+    (n, h, page, d), mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    T = slots.numel()
+    if slots.dtype != _I32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous int32 [T]")
+    if k_out is None or v_out is None:
+        with _on(stream):
+            k_out = k_out if k_out is not None else torch.empty(T, h, d, dtype=_BF16, device=k_cache.device)
+            v_out = v_out if v_out is not None else torch.empty(T, h, d, dtype=_BF16, device=k_cache.device)
+    k_stride, v_stride = _row_stride(k_out, (T, h, d), "k_out"), _row_stride(v_out, (T, h, d), "v_out")
+    device = _on_gpu(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
+    status = _load().kv8_read(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                              slots.data_ptr(), T, h, d, n, page, mode, k_out.data_ptr(), k_stride, v_out.data_ptr(),
+                              v_stride, _raw_stream(stream, device))
+    if status:
+        _check(status)
     return k_out, v_out
 
 
 def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, prefix_len: int, page_table, suffix_lens,
                          sm_scale=None, logit_cap: float = 0.0, out=None, lse=None, ws=None, stream=None):
-    """Decode attention of bf16 q [B, query heads, D] over a shared prefix (prefix_pages, the first prefix_len tokens)
-    and each sequence's own tokens (page_table [B, max pages], suffix_lens [B]); returns (bf16 out [B, query heads, D],
-    fp32 lse [B, query heads] or None). Pass `lse` (a tensor, or True to allocate one) to receive it. sm_scale defaults
-    to D ** -0.5; logit_cap 0 is no cap."""
-    n, h, page, d, mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    B, hq, dq, q_stride = _rows3(q, "q")
-    _need(dq == d, "q and the cache differ in D")
-    prefix_len = int(prefix_len)
+    """Decode attention of bf16 q [B, query heads, D] over a shared prefix (prefix_pages, the first prefix_len tokens;
+    None with 0) and each sequence's own tokens (page_table [B, max pages], suffix_lens [B]); returns (bf16 out [B,
+    query heads, D], fp32 lse [B, query heads] or None). Pass `lse` (a tensor, or True to allocate one) to receive it.
+    sm_scale defaults to D ** -0.5; logit_cap 0 is no cap."""
+    (n, h, page, d), mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be bf16 [B, query heads, D of the cache]")
+    B, hq, _ = shape = q.shape
+    q_stride = _row_stride(q, shape, "q")
+    device = _on_gpu(q, k_cache, v_cache, k_scale, v_scale, page_table, suffix_lens)
+    pages = None
     if prefix_len > 0:
-        _need(_i32(prefix_pages, 1, "prefix_pages").is_contiguous() and prefix_pages.shape[0] * page >= prefix_len,
-              "prefix_pages must be contiguous and cover prefix_len tokens")
-    most = _i32(page_table, 2, "page_table").shape[1]
-    _need(page_table.shape[0] == B and (most < 2 or page_table.stride(1) == 1), "page_table must be [B, max pages]")
-    _need(_i32(suffix_lens, 1, "suffix_lens").shape[0] == B and suffix_lens.is_contiguous(),
-          "suffix_lens must be contiguous [B]")
-    with _on(stream):
-        if out is None:
-            out = torch.empty(B, hq, d, dtype=torch.bfloat16, device=q.device)
-        if lse is True:
-            lse = torch.empty(B, hq, dtype=torch.float32, device=q.device)
-        if ws is None:
-            ws = _ws(kv8_prefix_attention_workspace_size(B, hq, h, d, prefix_len, most, page), q.device)
-    _need(out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous(),
-          "out must be contiguous bf16 [B, query heads, D]")
-    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (B, hq) and lse.is_contiguous()),
-          "lse must be contiguous float32 [B, query heads]")
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, prefix_pages if prefix_len > 0 else None, page_table,
-                 suffix_lens, out, lse, ws)
-    _check(_load().kv8_prefix_attention(
-        _ptr(q), q_stride, B, hq, h, d, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n, page, mode,
-        _ptr(prefix_pages) if prefix_len > 0 else None, prefix_len, _ptr(page_table),
-        page_table.stride(0) if B > 1 else max(page_table.stride(0), most), most, _ptr(suffix_lens),
-        float(d ** -0.5 if sm_scale is None else sm_scale), float(logit_cap), _ptr(out), _ptr(lse), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        if prefix_pages.dtype != _I32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous() \
+                or prefix_pages.numel() * page < prefix_len:
+            raise ValueError("prefix_pages must be contiguous int32 and cover prefix_len tokens")
+        _on_gpu(q, prefix_pages)
+        pages = prefix_pages.data_ptr()
+    if page_table.dtype != _I32 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be int32 [B, max pages]")
+    most = page_table.shape[1]
+    row, one = page_table.stride()
+    if one != 1 and most > 1:
+        raise ValueError("page_table: each sequence's pages must be contiguous")
+    if suffix_lens.dtype != _I32 or suffix_lens.shape != shape[:1] or not suffix_lens.is_contiguous():
+        raise ValueError("suffix_lens must be contiguous int32 [B]")
+    if out is None or lse is True or ws is None:
+        with _on(stream):
+            out = out if out is not None else torch.empty(B, hq, d, dtype=_BF16, device=q.device)
+            lse = torch.empty(B, hq, dtype=_F32, device=q.device) if lse is True else lse
+            ws = ws if ws is not None else _ws(
+                kv8_prefix_attention_workspace_size(B, hq, h, d, prefix_len, most, page), q.device)
+    if out.dtype != _BF16 or out.shape != shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous bf16 [B, query heads, D]")
+    if lse is not None:
+        if lse.dtype != _F32 or lse.shape != shape[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 [B, query heads]")
+        _on_gpu(q, lse)
+    _on_gpu(q, out, ws)
+    status = _load().kv8_prefix_attention(
+        q.data_ptr(), q_stride, B, hq, h, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), n, page, mode, pages, prefix_len, page_table.data_ptr(), row if B > 1 else most, most,
+        suffix_lens.data_ptr(), d ** -0.5 if sm_scale is None else sm_scale, logit_cap, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream, device))
+    if status:
+        _check(status)
     return out, lse
 
 

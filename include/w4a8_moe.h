@@ -419,8 +419,8 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
  *   Several query tokens of one sequence are several rows that share its pages,
  *   each with its own length.
  *   Requires 1 <= B <= 4096, Hq a multiple of Hkv, Hq <= 65535,
- *   prefix_len >= 0, max_pages >= 0, max_pages * page_size < 2^31, sm_scale
- *   finite, logit_cap finite and >= 0.
+ *   prefix_len >= 0, max_pages >= 0, max_pages * page_size < 2^31 and times B
+ *   <= 2^34, sm_scale finite, logit_cap finite and >= 0.
  *   A page index outside [0, num_pages) or a suffix length outside
  *   [0, max_pages * page_size] touches no memory out of range; the call's
  *   outputs are then unspecified and w4a8_device_error reports W4A8_ERR_INDEX.

@@ -239,11 +239,13 @@ static bool kv8_attn_ok(int B, int Hq, int Hkv, int D, int prefix_len, int max_p
     return B >= 1 && B <= kKv8MaxBatch && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq <= 65535 && Hq % Hkv == 0 &&
            (D == 64 || D == 128) && kv8_page_shift(page_size) >= 0 && prefix_len >= 0 &&
            prefix_len <= 0x7FFFFF00 && max_pages >= 0 &&
-           static_cast<int64_t>(max_pages) * page_size < (static_cast<int64_t>(1) << 31);
+           static_cast<int64_t>(max_pages) * page_size < (static_cast<int64_t>(1) << 31) &&
+           static_cast<int64_t>(max_pages) * page_size * B <= (static_cast<int64_t>(1) << 34);
 }
 struct Kv8Ws {
     float* part_o;
     float2* part_ml;
+    int* cum;
     int tiles, ptiles;
     Kv8Prefix prefix;   // splits 0: the prefix is not tiled
 };
@@ -257,9 +259,10 @@ static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, Kv8Ws* w, vo
     if (tiled)
         w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len);
     w->ptiles = prefix_len && !tiled ? (B * group + R - 1) / R : 0;
-    const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxCtas;
+    const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxWarps;
     w->part_o = c.take<float>(slots * R * D * 4);
     w->part_ml = c.take<float2>(slots * R * 8);
+    w->cum = c.take<int>((static_cast<size_t>(B) + 1) * 4);
     const size_t rows = static_cast<size_t>(w->prefix.splits) * B * Hq;
     w->prefix.part_o = c.take<float>(rows * D * 4);
     w->prefix.part_ml = c.take<float2>(rows * 8);
@@ -771,7 +774,7 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
     a.prefix_pages = prefix_pages, a.prefix_len = prefix_len;
     a.page_table = page_table, a.table_stride = table_stride, a.max_pages = max_pages, a.lens = suffix_lens;
     a.sm_scale = sm_scale, a.cap = logit_cap;
-    a.tiles = w.tiles, a.ptiles = w.ptiles, a.part_o = w.part_o, a.part_ml = w.part_ml;
+    a.tiles = w.tiles, a.ptiles = w.ptiles, a.part_o = w.part_o, a.part_ml = w.part_ml, a.cum = w.cum;
     a.err = static_cast<uint32_t*>(ws);
     a.out = out_bf16, a.lse = lse;
     return launch_kv8_attn(a, w.prefix, D, scale_mode, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK

@@ -26,8 +26,8 @@ cudaError_t launch_kv8_read(const Kv8Rows& a, const uint8_t* k_cache, const uint
 // ---- attention
 constexpr int kKv8MaxBatch = 4096;  // the split's prefix sums live in shared memory
 constexpr int kKv8Unit = 16;        // keys per unit of the split (a unit never crosses a page)
-constexpr int kKv8MinUnits = 8;     // units a CTA gets at least: 128 keys, two per warp
-constexpr int kKv8MaxCtas = 608;    // CTAs the unit range is divided over, at most
+constexpr int kKv8MinUnits = 4;     // units a warp gets at least
+constexpr int kKv8MaxWarps = 152 * 16;   // warps the units are divided over, at most
 
 struct Kv8Attn {
     const uint16_t* q;
@@ -52,7 +52,8 @@ struct Kv8Attn {
     uint32_t* err;
     uint16_t* out;
     float* lse;
-    int ctas;
+    int warps;
+    int* cum;           // [B + 1] prefix sums of the sequences' units, left for the join
 };
 // The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key
 // tiles); part_* [split][kv head][row] as above.

@@ -22,7 +22,9 @@ namespace w4a8 {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
+constexpr int kStages = 3;   // units in flight per warp
+constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
 constexpr float kLog2e = 1.4426950408889634f;
 // The reference exponent of a row is raised only when a score passes it by
 // this much: 2^{x - m} then stays below 2^8, far inside f16, and the row's
@@ -51,19 +53,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Codes are read once: keep them out of L1.
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
     return v;
 }
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p)
+__device__ __forceinline__ uint2 lds64(uint32_t at)
 {
     uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
     return v;
 }
 
@@ -71,14 +76,14 @@ __device__ __forceinline__ uint2 ld_codes8(const uint8_t* p)
 // The split. A pair is (rows, keys): first the prefix's pairs (kv head, row
 // tile of the whole batch), then the sequences' (sequence, kv head, row tile of
 // the group). The keys of a pair are cut into units of 16, all units stand in
-// one line in pair order, and CTA c of n takes units [U c / n, U (c + 1) / n):
-// equal work however ragged the lengths are. The piece of pair p done by CTA c
-// is stored in slot p + c: along the line p + c rises with every piece, so no
+// one line in pair order, and warp w of n takes units [U w / n, U (w + 1) / n):
+// equal work however ragged the lengths are. The piece of pair p done by warp w
+// is stored in slot p + w: along the line p + w rises with every piece, so no
 // two share a slot, and a reader finds a pair's slots from U and n alone.
 // ---------------------------------------------------------------------------
 struct Line {
     int64_t U;      // units
-    int n;          // CTAs with units
+    int n;          // warps with units
     int up;         // units of a prefix pair
     int pairs_p;    // prefix pairs
     int64_t own;    // first unit of the sequences' pairs
@@ -101,72 +106,100 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
     l.own = static_cast<int64_t>(l.pairs_p) * l.up;
     l.U = l.own + seq_total * l.hr;
     const int64_t n = (l.U + kKv8MinUnits - 1) / kKv8MinUnits;
-    l.n = static_cast<int>(n < a.ctas ? n : a.ctas);
+    l.n = static_cast<int>(n < a.warps ? n : a.warps);
     return l;
 }
-__device__ __forceinline__ int64_t cta_begin(const Line& l, int c) { return l.U * c / l.n; }
-__device__ __forceinline__ int cta_of(const Line& l, int64_t u) { return static_cast<int>(((u + 1) * l.n - 1) / l.U); }
+__device__ __forceinline__ int64_t warp_begin(const Line& l, int w) { return l.U * w / l.n; }
+__device__ __forceinline__ int warp_of(const Line& l, int64_t u) { return static_cast<int>(((u + 1) * l.n - 1) / l.U); }
 
-// One unit's codes as a thread holds them: for S = Q K^T two n-tiles of 8 keys
-// (this thread: key g of each, chunk c of its D values); for O^T = V^T P^T
-// four keys (2c, 2c+1, 2c+8, 2c+9), chunk g of their D values. Neither needs
-// shared memory: which d a fragment register stands for is free as long as q
-// and o use the same order, so every thread reads contiguous bytes.
-template <int D>
-struct Codes {
-    uint4 k[2][D / 64];
-    uint32_t v[4][D / 32];
-    float ks[4], vs[4];   // scales of keys 2c, 2c+1, 2c+8, 2c+9 (per-token scales only)
+// A unit as its warp meets it, found by one lane for each of 32 units ahead.
+struct __align__(16) Unit {
+    int64_t row;    // cache row (page, head, offset) of its first key
+    int pair;
+    int live_last;  // keys that exist (1..16), and 256 where the pair ends
 };
-
-template <int D, bool TOK>
-__device__ __forceinline__ void load_unit(Codes<D>& x, const Kv8Attn& a, int h, int page, int key0, int len, int g, int c)
+__device__ __forceinline__ Unit find_unit(const Kv8Attn& a, const Line& line, const int* cum, int64_t u)
 {
-    const int off = key0 & ((1 << a.page_shift) - 1);
-    const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + h) << a.page_shift) + off;
-    const uint8_t* kb = a.k_cache + row * D;
-    const uint8_t* vb = a.v_cache + row * D;
-    const int live = len - key0;   // keys of this unit that exist (may pass 16)
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-            x.k[t][j] = t * 8 + g < live ? ld_codes16(kb + (t * 8 + g) * D + (j * 4 + c) * 16) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int key = c * 2 + (i & 1) + (i >> 1) * 8;
-        if (D == 128) {
-            const uint4 w = key < live ? ld_codes16(vb + key * D + g * 16) : make_uint4(0, 0, 0, 0);
-            x.v[i][0] = w.x, x.v[i][1] = w.y, x.v[i][D / 32 - 2] = w.z, x.v[i][D / 32 - 1] = w.w;
+    Unit x;
+    int h, len, n_pages, k;
+    const int32_t* pages;
+    bool last;
+    if (u < line.own) {
+        x.pair = static_cast<int>(u / line.up);
+        k = static_cast<int>(u - static_cast<int64_t>(x.pair) * line.up);
+        h = x.pair / a.ptiles;
+        len = a.prefix_len;
+        last = k == line.up - 1;
+        pages = a.prefix_pages;
+        n_pages = (a.prefix_len + (1 << a.page_shift) - 1) >> a.page_shift;
+    } else {
+        const int64_t rel = u - line.own;
+        int lo = 0, hi = a.B;   // the last b with cum[b] * hr <= rel
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (static_cast<int64_t>(cum[mid]) * line.hr <= rel)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const unsigned n = cum[lo + 1] - cum[lo];
+        const int64_t in = rel - static_cast<int64_t>(cum[lo]) * line.hr;
+        int j;
+        if (in <= 0xFFFFFFFFll) {
+            j = static_cast<int>(static_cast<uint32_t>(in) / n);
+            k = static_cast<int>(static_cast<uint32_t>(in) - j * n);
         } else {
-            const uint2 w = key < live ? ld_codes8(vb + key * D + g * 8) : make_uint2(0, 0);
-            x.v[i][0] = w.x, x.v[i][1] = w.y;
+            j = static_cast<int>(in / n);
+            k = static_cast<int>(in - static_cast<int64_t>(j) * n);
         }
-        if (TOK) {
-            x.ks[i] = key < live ? __ldg(a.k_scale + row + key) : 0.0f;
-            x.vs[i] = key < live ? __ldg(a.v_scale + row + key) : 0.0f;
-        }
+        h = j / a.tiles;
+        len = seq_len(a, lo);
+        last = k == static_cast<int>(n) - 1;
+        pages = a.page_table + lo * a.table_stride;
+        n_pages = a.max_pages;
+        x.pair = line.pairs_p + lo * line.hr + j;
     }
+    const int key0 = k * kKv8Unit;
+    const int idx = key0 >> a.page_shift;
+    int page = idx < n_pages ? __ldg(pages + idx) : -1;
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
+        set_error(a.err, kErrBitIndex);
+        page = 0;
+    }
+    x.row = ((static_cast<int64_t>(page) * a.Hkv + h) << a.page_shift) + (key0 & ((1 << a.page_shift) - 1));
+    x.live_last = min(len - key0, kKv8Unit) | (last ? 256 : 0);
+    return x;
 }
+
+template <int D>
+struct Ring {   // one warp's shared memory
+    static constexpr int kCodes = kKv8Unit * D;               // bytes of K or V codes of a unit
+    static constexpr int kStage = 2 * kCodes + 2 * kKv8Unit * 4;   // K, V, their scales
+    static constexpr int desc = kStages * kStage;
+    static constexpr int bars = desc + kDescs * 16;
+    static constexpr int total = (bars + kStages * 8 + 127) / 128 * 128;   // bulk copies want 16 bytes
+};
 
 }  // namespace
 
 // Row tile: 8 rows where the group fits, else 16 (two column tiles of O^T).
 int kv8_attn_row_tile(int group) { return group <= 8 ? 8 : 16; }
 
-// A CTA walks its units piece by piece. Its four warps take units in turn, each
-// with its own running reference and sums, and join them through shared memory
-// at the piece's end.
+// Every warp walks its own units, with a ring of bulk copies kStages units
+// ahead (across piece boundaries), and stores a piece's result from registers.
+// Fragments come straight from the linear copies: which d a fragment register
+// stands for is free as long as q and o use the same order, so every thread
+// reads contiguous bytes. For S = Q K^T a thread holds key g of each n-tile and
+// chunks c of its D values; for O^T = V^T P^T keys 2c, 2c+1, 2c+8, 2c+9 and
+// chunk g of their D values; P^T then needs no exchange between lanes.
 template <int D, int NT, bool TOK>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_constant__ Kv8Attn a)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(const __grid_constant__ Kv8Attn a)
 {
+    using S = Ring<D>;
     constexpr int R = 8 * NT;      // rows of a tile
     constexpr int KS = D / 16;     // k-steps of Q K^T = m-tiles of O^T
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* so = reinterpret_cast<float*>(smem);                    // [warp][row][D]
-    float* sm = so + kWarps * R * D;                               // [warp][row]
-    float* sl = sm + kWarps * R;                                   // [warp][row]
-    int* cum = reinterpret_cast<int*>(sl + kWarps * R);            // [B + 1]
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* cum = reinterpret_cast<int*>(smem + kWarps * S::total);   // [B + 1]
     __shared__ int warp_sum[kWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -191,357 +224,359 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
         int base = carry;
         for (int w = 0; w < warp; ++w)
             base += warp_sum[w];
-        if (b < a.B)
+        if (b < a.B) {
             cum[b] = base + s - n;
+            if (blockIdx.x == 0)
+                a.cum[b] = base + s - n;
+        }
         for (int w = 0; w < kWarps; ++w)
             carry += warp_sum[w];
         __syncthreads();
     }
-    if (tid == 0)
+    if (tid == 0) {
         cum[a.B] = carry;
+        if (blockIdx.x == 0)
+            a.cum[a.B] = carry;
+    }
+    const uint32_t ring = smem_u32(smem) + warp * S::total;
+    if (lane < kStages)
+        mbar_init(ring + S::bars + lane * 8, 1);
+    fence_mbar_init();
     __syncthreads();
 
     const Line line = make_line(a, carry);
-    const int cta = blockIdx.x;
-    if (cta >= line.n)
-        return;
-    int64_t u = cta_begin(line, cta);
-    const int64_t u_end = cta_begin(line, cta + 1);
+    const int me = warp * gridDim.x + blockIdx.x;   // few units: one warp on each SM before a second
+    const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
+    const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
+    Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
 
-    while (u < u_end) {
-        // ---- the piece at u
-        int h, row0, len, b = 0, pair;
-        int64_t first, last;   // the pair's units
-        const int32_t* pages;
-        int n_pages;
-        const bool prefix = u < line.own;
-        if (prefix) {
-            pair = static_cast<int>(u / line.up);
-            h = pair / a.ptiles;
-            row0 = (pair % a.ptiles) * R;
-            len = a.prefix_len;
-            first = static_cast<int64_t>(pair) * line.up;
-            last = first + line.up;
-            pages = a.prefix_pages;
-            n_pages = (a.prefix_len + (1 << a.page_shift) - 1) >> a.page_shift;
-        } else {
-            const int64_t rel = u - line.own;
-            int lo = 0, hi = a.B;   // the last b with cum[b] * hr <= rel
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (static_cast<int64_t>(cum[mid]) * line.hr <= rel)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            b = lo;
-            const int n = cum[b + 1] - cum[b];
-            const int64_t start = static_cast<int64_t>(cum[b]) * line.hr;
-            const int j = static_cast<int>((rel - start) / n);
-            h = j / a.tiles;
-            row0 = (j % a.tiles) * R;
-            len = seq_len(a, b);
-            first = line.own + start + static_cast<int64_t>(j) * n;
-            last = first + n;
-            pages = a.page_table + b * a.table_stride;
-            n_pages = a.max_pages;
-            pair = line.pairs_p + b * line.hr + j;
+    // unit i of this warp into its ring slot; batches of 32 descriptors ahead of it
+    auto issue = [&](int i) {
+        if (i >= units)
+            return;
+        if (i % 32 == 0) {
+            if (i + lane < units)
+                descs[(i + lane) % kDescs] = find_unit(a, line, cum, u_begin + i + lane);
+            __syncwarp();
         }
-        const int64_t stop = last < u_end ? last : u_end;
-        const int ua = static_cast<int>(u - first), ub = static_cast<int>(stop - first);
-        const int rows = min(R, (prefix ? a.B * a.group : a.group) - row0);
-
-        // ---- queries: f16 fragments of q * 2^-e with e from the row's largest
-        // element. bf16 has 8 significant bits and f16 11, so only elements
-        // below 2^-16 of the row's largest lose anything, and what they lose is
-        // at most 2^-25 of it: the size of one fp32 rounding of the product.
-        uint32_t qa[KS][2 * NT];
-        float qs[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int r = row0 + t * 8 + g;
-            uint4 raw[D / 32];
-            if (t * 8 + g < rows) {
-                const int qb = prefix ? r / a.group : b;
-                const int qh = h * a.group + (prefix ? r % a.group : r);
-                const uint16_t* src = a.q + qb * a.q_stride + static_cast<int64_t>(qh) * D;
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                    raw[2 * j] = __ldg(reinterpret_cast<const uint4*>(src + (j * 4 + c) * 16));
-                    raw[2 * j + 1] = __ldg(reinterpret_cast<const uint4*>(src + (j * 4 + c) * 16) + 1);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j)
-                    raw[j] = make_uint4(0, 0, 0, 0);
-            }
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = max(top, max((w[i] >> 16) & 0x7FFFu, w[i] & 0x7FFFu));
-            }
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const int ex = static_cast<int>(top >> 7);
-            const int e = top == 0 || ex == 255 ? 0 : max(ex, 1) - 127;
-            const float down = ldexpf(1.0f, -e);
-            float f = ldexpf(a.sm_scale, e);
-            if (!TOK)
-                f *= __ldg(a.k_scale + h);
-            qs[t] = a.cap > 0.0f ? f / a.cap : f * kLog2e;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {   // 8 values: two k-steps' two registers each
-                const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    qa[2 * j + (i >> 1)][(i & 1) * NT + t] =
-                        pack_f16(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
-            }
-        }
-
-        float o[KS][NT][4];
-#pragma unroll
-        for (int j = 0; j < KS; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[j][t][i] = 0.0f;
-        float m[NT], l[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            m[t] = -INFINITY, l[t] = 0.0f;
-
-        Codes<D> x;
-        auto fetch = [&](int unit) {
-            const int key0 = unit * kKv8Unit;
-            const int idx = key0 >> a.page_shift;
-            int page = idx < n_pages ? __ldg(pages + idx) : -1;
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
-                set_error(a.err, kErrBitIndex);
-                page = 0;
-            }
-            load_unit<D, TOK>(x, a, h, page, key0, len, g, c);
-        };
-        for (int unit = ua + warp; unit < ub; unit += kWarps) {
-            fetch(unit);
-            // ---- S = Q K^T
-            float s[2][4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[t][i] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                    const uint32_t w[4] = {x.k[t][j].x, x.k[t][j].y, x.k[t][j].z, x.k[t][j].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t b0 = e4m3x2_to_f16x2(w[i] & 0xFFFFu), b1 = e4m3x2_to_f16x2(w[i] >> 16);
-                        const uint32_t* qf = qa[j * 4 + i];
-                        mma_f16(s[t], qf[0], NT == 2 ? qf[1] : 0u, qf[NT], NT == 2 ? qf[2 * NT - 1] : 0u, b0, b1);
-                    }
-                }
-            }
-            // ---- scores in log2 units; keys past the end are -inf
-            const int live = len - unit * kKv8Unit;
-            float lift = 0.0f;   // log2 of the unit's largest value scale
+        if (lane == 0) {
+            const int64_t row = descs[i % kDescs].row;
+            const uint32_t dst = ring + (i % kStages) * S::kStage, bar = ring + S::bars + (i % kStages) * 8;
+            mbar_arrive_expect_tx(bar, TOK ? S::kStage : 2 * S::kCodes);
+            bulk_load(dst, a.k_cache + row * D, S::kCodes, bar);
+            bulk_load(dst + S::kCodes, a.v_cache + row * D, S::kCodes, bar);
             if (TOK) {
-                float top = fmaxf(fmaxf(fabsf(x.vs[0]), fabsf(x.vs[1])), fmaxf(fabsf(x.vs[2]), fabsf(x.vs[3])));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                lift = fmaxf(log2f(top), -100.0f);
+                bulk_load(dst + 2 * S::kCodes, a.k_scale + row, kKv8Unit * 4, bar);
+                bulk_load(dst + 2 * S::kCodes + kKv8Unit * 4, a.v_scale + row, kKv8Unit * 4, bar);
             }
-            bool grow = false;
+        }
+    };
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 2 * NT; ++i) {
-                    float f = s[t][i] * qs[i >> 1];
-                    if (TOK)
-                        f *= x.ks[t * 2 + (i & 1)];
-                    if (a.cap > 0.0f) {   // tanh y = 1 - 2 / (1 + e^{2y})
-                        const float e = ex2(f * (2.0f * kLog2e));
-                        f = (a.cap * kLog2e) * (1.0f - __fdividef(2.0f, 1.0f + e));
-                        if (e > 1e30f)
-                            f = a.cap * kLog2e;
-                    }
-                    f = t * 8 + c * 2 + (i & 1) < live ? f : -INFINITY;
-                    s[t][i] = f;
-                    grow = grow || f + lift > m[i >> 1] + kSlack;
-                }
-            if (__any_sync(0xFFFFFFFFu, grow)) {
-                float f[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float top = fmaxf(fmaxf(s[0][2 * t], s[0][2 * t + 1]), fmaxf(s[1][2 * t], s[1][2 * t + 1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2)) + lift;
-                    const float to = fmaxf(m[t], top);
-                    f[t] = to == -INFINITY ? 1.0f : ex2(m[t] - to);
-                    m[t] = to;
-                    l[t] *= f[t];
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const float f0 = __shfl_sync(0xFFFFFFFFu, f[t], c * 8);
-                    const float f1 = __shfl_sync(0xFFFFFFFFu, f[t], c * 8 + 4);
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) {
-                        o[j][t][0] *= f0, o[j][t][1] *= f1;
-                        o[j][t][2] *= f0, o[j][t][3] *= f1;
-                    }
-                }
+    for (int i = 0; i < kStages; ++i)
+        issue(i);
+
+    uint32_t qa[KS][2 * NT];
+    float qs[NT], o[KS][NT][4], m[NT], l[NT];
+    int rows = 0, h = 0;
+    bool fresh = true;
+    for (int i = 0; i < units; ++i) {
+        const int pair = descs[i % kDescs].pair, live_last = descs[i % kDescs].live_last;
+        const int live = live_last & 255;
+        if (fresh) {
+            // ---- a new piece. Queries: f16 fragments of q * 2^-e with e from
+            // the row's largest element. bf16 has 8 significant bits and f16
+            // 11, so only elements below 2^-16 of the row's largest lose
+            // anything, and what they lose is at most 2^-25 of it: the size of
+            // one fp32 rounding of the product.
+            int b = 0, row0;
+            const bool prefix = pair < line.pairs_p;
+            if (prefix) {
+                h = pair / a.ptiles;
+                row0 = (pair % a.ptiles) * R;
+                rows = min(R, a.B * a.group - row0);
+            } else {
+                b = (pair - line.pairs_p) / line.hr;
+                const int j = (pair - line.pairs_p) % line.hr;
+                h = j / a.tiles;
+                row0 = (j % a.tiles) * R;
+                rows = min(R, a.group - row0);
             }
-            // ---- P^T and O^T += V^T P^T
-            uint32_t pb[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const float ref = m[t] == -INFINITY ? 0.0f : m[t];
+                const int r = row0 + t * 8 + g;
+                uint4 raw[D / 32];
+                if (t * 8 + g < rows) {
+                    const int qb = prefix ? r / a.group : b;
+                    const int qh = h * a.group + (prefix ? r % a.group : r);
+                    const uint16_t* src = a.q + qb * a.q_stride + static_cast<int64_t>(qh) * D;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float p0 = ex2(s[k][2 * t] - ref), p1 = ex2(s[k][2 * t + 1] - ref);
-                    l[t] += p0 + p1;
-                    if (TOK) {
-                        p0 *= x.vs[2 * k];
-                        p1 *= x.vs[2 * k + 1];
+                    for (int j = 0; j < D / 64; ++j) {
+                        raw[2 * j] = __ldg(reinterpret_cast<const uint4*>(src + (j * 4 + c) * 16));
+                        raw[2 * j + 1] = __ldg(reinterpret_cast<const uint4*>(src + (j * 4 + c) * 16) + 1);
                     }
-                    pb[t][k] = pack_f16(p0, p1);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j)
+                        raw[j] = make_uint4(0, 0, 0, 0);
                 }
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top = max(top, max((w[e] >> 16) & 0x7FFFu, w[e] & 0x7FFFu));
+                }
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const int ex = static_cast<int>(top >> 7);
+                const int e = top == 0 || ex == 255 ? 0 : max(ex, 1) - 127;
+                const float down = ldexpf(1.0f, -e);
+                float f = ldexpf(a.sm_scale, e);
+                if (!TOK)
+                    f *= __ldg(a.k_scale + h);
+                qs[t] = a.cap > 0.0f ? f / a.cap : f * kLog2e;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {   // 8 values: two k-steps' two registers each
+                    const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        qa[2 * j + (k >> 1)][(k & 1) * NT + t] =
+                            pack_f16(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+                }
+                m[t] = -INFINITY;
+                l[t] = 0.0f;
             }
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w)
+            for (int j = 0; j < KS; ++j)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t sel = half ? 0x7362u : 0x5140u;
-                    const uint32_t lo = prmt(x.v[0][w], x.v[1][w], sel), hi = prmt(x.v[2][w], x.v[3][w], sel);
-                    const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xFFFFu), a1 = e4m3x2_to_f16x2(lo >> 16);
-                    const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xFFFFu), a3 = e4m3x2_to_f16x2(hi >> 16);
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        mma_f16(o[w * 2 + half][t], a0, a1, a2, a3, pb[t][0], pb[t][1]);
-                }
+                    for (int k = 0; k < 4; ++k)
+                        o[j][t][k] = 0.0f;
+            fresh = false;
         }
 
-        // ---- the warps' results, joined in a fixed order
-        const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
+        // ---- the unit's codes into registers, and its slot to the next copy
+        const uint32_t at = ring + (i % kStages) * S::kStage;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(ring + S::bars + (i % kStages) * 8, (i / kStages) & 1))) {
+            set_error(a.err, kErrBitTimeout);
+            for (int j = i + 1; j < min(i + kStages, units); ++j)   // copies in flight end before the warp does
+                mbar_wait(ring + S::bars + (j % kStages) * 8, (j / kStages) & 1);
+            break;
+        }
+        uint4 xk[2][D / 64];
+        uint32_t xv[4][D / 32];
+        float ks[4], vs[4];   // scales of keys 2c, 2c+1, 2c+8, 2c+9
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+                xk[t][j] = lds128(at + (t * 8 + g) * D + (j * 4 + c) * 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int key = c * 2 + (k & 1) + (k >> 1) * 8;
+            if (D == 128) {
+                const uint4 w = lds128(at + S::kCodes + key * D + g * 16);
+                xv[k][0] = w.x, xv[k][1] = w.y, xv[k][D / 32 - 2] = w.z, xv[k][D / 32 - 1] = w.w;
+            } else {
+                const uint2 w = lds64(at + S::kCodes + key * D + g * 8);
+                xv[k][0] = w.x, xv[k][1] = w.y;
+            }
+        }
+        if (TOK) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint2 w = lds64(at + 2 * S::kCodes + (k * 8 + c * 2) * 4);
+                const uint2 z = lds64(at + 2 * S::kCodes + (kKv8Unit + k * 8 + c * 2) * 4);
+                ks[2 * k] = __uint_as_float(w.x), ks[2 * k + 1] = __uint_as_float(w.y);
+                vs[2 * k] = __uint_as_float(z.x), vs[2 * k + 1] = __uint_as_float(z.y);
+            }
+        }
+        if (live < kKv8Unit) {   // what lies behind the last key may be no number
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (c * 2 + (k & 1) + (k >> 1) * 8 >= live) {
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w)
+                        xv[k][w] = 0;
+                    if (TOK)
+                        ks[k] = 0.0f, vs[k] = 0.0f;
+                }
+            }
+        }
+        __syncwarp();
+        issue(i + kStages);
+
+        // ---- S = Q K^T
+        float s[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                s[t][k] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const uint32_t w[4] = {xk[t][j].x, xk[t][j].y, xk[t][j].z, xk[t][j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t b0 = e4m3x2_to_f16x2(w[k] & 0xFFFFu), b1 = e4m3x2_to_f16x2(w[k] >> 16);
+                    const uint32_t* qf = qa[j * 4 + k];
+                    mma_f16(s[t], qf[0], NT == 2 ? qf[1] : 0u, qf[NT], NT == 2 ? qf[2 * NT - 1] : 0u, b0, b1);
+                }
+            }
+        }
+        // ---- scores in log2 units; keys past the end are -inf
+        float lift = 0.0f;   // log2 of the unit's largest value scale
+        if (TOK) {
+            float top = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            lift = fmaxf(log2f(top), -100.0f);
+        }
+        bool grow = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 2 * NT; ++k) {
+                float f = s[t][k] * qs[k >> 1];
+                if (TOK)
+                    f *= ks[t * 2 + (k & 1)];
+                if (a.cap > 0.0f) {   // tanh y = 1 - 2 / (1 + e^{2y})
+                    const float e = ex2(f * (2.0f * kLog2e));
+                    f = e > 1e30f ? a.cap * kLog2e : (a.cap * kLog2e) * (1.0f - __fdividef(2.0f, 1.0f + e));
+                }
+                f = t * 8 + c * 2 + (k & 1) < live ? f : -INFINITY;
+                s[t][k] = f;
+                grow = grow || f + lift > m[k >> 1] + kSlack;
+            }
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float top = fmaxf(fmaxf(s[0][2 * t], s[0][2 * t + 1]), fmaxf(s[1][2 * t], s[1][2 * t + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2)) + lift;
+                const float to = fmaxf(m[t], top);
+                const float f = to == -INFINITY ? 1.0f : ex2(m[t] - to);
+                m[t] = to;
+                l[t] *= f;
+                const float f0 = __shfl_sync(0xFFFFFFFFu, f, c * 8);
+                const float f1 = __shfl_sync(0xFFFFFFFFu, f, c * 8 + 4);
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    o[j][t][0] *= f0, o[j][t][1] *= f1;
+                    o[j][t][2] *= f0, o[j][t][3] *= f1;
+                }
+            }
+        }
+        // ---- P^T and O^T += V^T P^T
+        uint32_t pb[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 1);
-            l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 2);
-            if (c == 0) {
-                sm[warp * R + t * 8 + g] = m[t];
-                sl[warp * R + t * 8 + g] = l[t];
-            }
+            const float ref = m[t] == -INFINITY ? 0.0f : m[t];
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                float* dst = so + (warp * R + t * 8 + c * 2) * D + g * (D / 8) + 2 * j;
-                *reinterpret_cast<float2*>(dst) = make_float2(o[j][t][0] * vscale, o[j][t][2] * vscale);
-                *reinterpret_cast<float2*>(dst + D) = make_float2(o[j][t][1] * vscale, o[j][t][3] * vscale);
+            for (int k = 0; k < 2; ++k) {
+                float p0 = ex2(s[k][2 * t] - ref), p1 = ex2(s[k][2 * t + 1] - ref);
+                l[t] += p0 + p1;
+                if (TOK) {
+                    p0 *= vs[2 * k];
+                    p1 *= vs[2 * k + 1];
+                }
+                pb[t][k] = pack_f16(p0, p1);
             }
         }
-        __syncthreads();
-        const int64_t slot = pair + cta;
-        for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
-            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-            float top = sm[r];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w)
-                top = fmaxf(top, sm[w * R + r]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            float4 acc = make_float4(0, 0, 0, 0);
-            float sum = 0.0f;
+        for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(sm[w * R + r] - ref);
-                const float4 v = *reinterpret_cast<const float4*>(so + (w * R + r) * D + d);
-                acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
-                sum += sl[w * R + r] * f;
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t sel = half ? 0x7362u : 0x5140u;
+                const uint32_t lo = prmt(xv[0][w], xv[1][w], sel), hi = prmt(xv[2][w], xv[3][w], sel);
+                const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xFFFFu), a1 = e4m3x2_to_f16x2(lo >> 16);
+                const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xFFFFu), a3 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    mma_f16(o[w * 2 + half][t], a0, a1, a2, a3, pb[t][0], pb[t][1]);
             }
-            *reinterpret_cast<float4*>(a.part_o + (slot * R + r) * D + d) = acc;
-            if (d == 0)
-                a.part_ml[slot * R + r] = make_float2(top, sum);
+
+        // ---- the piece ends with its pair or with the warp's units
+        if ((live_last & 256) || i + 1 == units) {
+            const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
+            const int64_t slot = static_cast<int64_t>(pair) + me;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 1);
+                l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 2);
+                if (c == 0 && t * 8 + g < rows)
+                    a.part_ml[slot * R + t * 8 + g] = make_float2(m[t], l[t]);
+                float* dst = a.part_o + (slot * R + t * 8 + c * 2) * D + g * (D / 8);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (t * 8 + c * 2 + e < rows) {
+#pragma unroll
+                        for (int j = 0; j < KS; j += 2)
+                            *reinterpret_cast<float4*>(dst + e * D + 2 * j) =
+                                make_float4(o[j][t][e] * vscale, o[j][t][2 + e] * vscale, o[j + 1][t][e] * vscale,
+                                            o[j + 1][t][2 + e] * vscale);
+                    }
+            }
+            fresh = true;
         }
-        __syncthreads();
-        u = stop;
     }
+    grid_dep_wait();     // the join after this kernel also reads what the one before it wrote
+    grid_dep_launch();
 }
 
-// One CTA per (sequence, query head) adds up the pieces of its row. Warps take
-// pieces in turn, a lane D / 32 values, all loads of a warp's pieces in flight
-// together; the warps' sums are joined in a fixed order.
+// Adds up the pieces of a (sequence, query head): W warps take them in turn, a
+// lane D / 32 values. W is 4 where there are few rows (each may have many
+// pieces and latency counts), 1 where the rows themselves fill the GPU.
 constexpr int kJoinWarps = 4;
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
                                                                    const __grid_constant__ Kv8Prefix p, int R)
 {
     constexpr int V = D / 32;
-    const int b = blockIdx.x, qh = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = qh / a.group, gi = qh % a.group;
-    __shared__ int part[2][kJoinWarps];
-    __shared__ float so[kJoinWarps][D];
-    __shared__ float2 sml[kJoinWarps];
-    int before = 0, all = 0;
-    for (int i = tid; i < a.B; i += kJoinWarps * 32) {
-        const int n = seq_units(a, i);
-        all += n;
-        before += i < b ? n : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-        all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-    }
-    if (lane == 0)
-        part[0][warp] = before, part[1][warp] = all;
-    __syncthreads();
-    before = all = 0;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w)
-        before += part[0][w], all += part[1][w];
-    const Line line = make_line(a, all);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int head = blockIdx.x * (kJoinWarps / W) + warp / W;   // b * Hq + query head
+    const int first_piece = warp % W;
+    grid_dep_wait();
+    if (W == 1 && head >= a.B * a.Hq)
+        return;
+    const int b = head / a.Hq, qh = head % a.Hq, h = qh / a.group, gi = qh % a.group;
 
     // the row's pieces: [0, n0) of the tiled prefix, [n0, n1) of the untiled one, [n1, n2) of its own keys
     const int row = b * a.group + gi;
     const int n0 = p.splits;
-    int n1 = n0, n2, c_pre = 0, c_own = 0, pair_pre = 0, pair_own = 0;
+    int n1 = n0, n2;
+    int64_t at_pre = 0, at_own = 0;   // the first piece's row, minus its number times R
+    const bool pieces = a.max_pages || a.ptiles;
+    const int before = pieces ? a.cum[b] : 0, units = pieces ? a.cum[b + 1] - before : 0;
+    const Line line = make_line(a, pieces ? a.cum[a.B] : 0);
     if (a.ptiles) {
-        pair_pre = h * a.ptiles + row / R;
-        const int64_t first = static_cast<int64_t>(pair_pre) * line.up;
-        c_pre = cta_of(line, first);
-        n1 += cta_of(line, first + line.up - 1) - c_pre + 1;
+        const int pair = h * a.ptiles + row / R;
+        const int64_t first = static_cast<int64_t>(pair) * line.up;
+        const int w = warp_of(line, first);
+        n1 += warp_of(line, first + line.up - 1) - w + 1;
+        at_pre = static_cast<int64_t>(pair + w - n0) * R + row % R;
     }
     n2 = n1;
-    const int units = seq_units(a, b);
     if (units) {
         const int j = h * a.tiles + gi / R;
-        pair_own = line.pairs_p + b * line.hr + j;
         const int64_t first = line.own + static_cast<int64_t>(before) * line.hr + static_cast<int64_t>(j) * units;
-        c_own = cta_of(line, first);
-        n2 += cta_of(line, first + units - 1) - c_own + 1;
+        const int w = warp_of(line, first);
+        n2 += warp_of(line, first + units - 1) - w + 1;
+        at_own = static_cast<int64_t>(line.pairs_p + b * line.hr + j + w - n1) * R + gi % R;
     }
     float top = -INFINITY, sum = 0.0f, acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
         acc[i] = 0.0f;
 #pragma unroll 4
-    for (int k = warp; k < n2; k += kJoinWarps) {
-        const float* o;
-        const float2* mlp;
-        if (k < n0) {
-            const int64_t at = (static_cast<int64_t>(k) * a.Hkv + h) * a.B * a.group + row;
-            o = p.part_o + at * D;
-            mlp = p.part_ml + at;
-        } else {
-            const int64_t at = k < n1 ? static_cast<int64_t>(pair_pre + c_pre + k - n0) * R + row % R
-                                      : static_cast<int64_t>(pair_own + c_own + k - n1) * R + gi % R;
-            o = a.part_o + at * D;
-            mlp = a.part_ml + at;
-        }
-        const float2 ml = *mlp;
+    for (int k = first_piece; k < n2; k += W) {
+        const bool tiled = k < n0;
+        const int64_t at = tiled ? (static_cast<int64_t>(k) * a.Hkv + h) * a.B * a.group + row
+                                 : (k < n1 ? at_pre : at_own) + static_cast<int64_t>(k) * R;
+        const float* o = (tiled ? p.part_o : a.part_o) + at * D;
+        const float2 ml = (tiled ? p.part_ml : a.part_ml)[at];
         float v[V];
         if (V == 4) {
             const float4 w = *(reinterpret_cast<const float4*>(o) + lane);
@@ -559,50 +594,74 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_
         sum = sum * f0 + ml.y * f1;
         top = to;
     }
+    if (W > 1) {
+        __shared__ float so[W][D];
+        __shared__ float2 sml[W];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        so[warp][lane * V + i] = acc[i];
-    if (lane == 0)
-        sml[warp] = make_float2(top, sum);
-    __syncthreads();
-    if (tid >= D / 2)
-        return;
-    top = sml[0].x;
+        for (int i = 0; i < V; ++i)
+            so[warp][lane * V + i] = acc[i];
+        if (lane == 0)
+            sml[warp] = make_float2(top, sum);
+        __syncthreads();
+        if (warp > 0)
+            return;
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w)
-        top = fmaxf(top, sml[w].x);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float x = 0.0f, y = 0.0f;
-    sum = 0.0f;
+        for (int w = 1; w < W; ++w)
+            top = fmaxf(top, sml[w].x);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = ex2(sml[w].x - ref);
-        x += so[w][2 * tid] * f;
-        y += so[w][2 * tid + 1] * f;
-        sum += sml[w].y * f;
+        for (int i = 0; i < V; ++i)
+            acc[i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = ex2(sml[w].x - ref);
+            sum += sml[w].y * f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                acc[i] += so[w][lane * V + i] * f;
+        }
     }
     const bool empty = top == -INFINITY && sum == 0.0f;
-    const int64_t head = static_cast<int64_t>(b) * a.Hq + qh;
-    x = empty ? 0.0f : x / sum;
-    y = empty ? 0.0f : y / sum;
-    *reinterpret_cast<uint32_t*>(a.out + head * D + 2 * tid) =
-        static_cast<uint32_t>(float_to_bf16_bits(x)) | (static_cast<uint32_t>(float_to_bf16_bits(y)) << 16);
-    if (a.lse && tid == 0)
+    uint32_t r[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+        r[i] = static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[2 * i] / sum)) |
+               (static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[2 * i + 1] / sum)) << 16);
+    uint16_t* dst = a.out + static_cast<int64_t>(head) * D + lane * V;
+    if (V == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[V / 2 - 1]);
+    else
+        *reinterpret_cast<uint32_t*>(dst) = r[0];
+    if (a.lse && lane == 0)
         a.lse[head] = empty ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+static int ring_smem(int D, int B) { return kWarps * (D == 128 ? Ring<128>::total : Ring<64>::total) + (B + 1) * 4; }
+
 template <int D, int NT, bool TOK>
-static cudaError_t launch_pieces(const Kv8Attn& a, cudaStream_t s)
+static cudaError_t launch_pieces(const Kv8Attn& a, bool after_prefix, cudaStream_t s)
 {
-    const int smem = (kWarps * 8 * NT * (D + 2) + a.B + 1) * 4;
+    const int smem = ring_smem(D, a.B);
     auto kern = kv8_attn_kernel<D, NT, TOK>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess)
-            return e;
-    }
-    kern<<<a.ctas, kWarps * 32, smem, s>>>(a);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    const int ctas = a.warps / kWarps;
+    if (after_prefix)
+        return launch_dependent(kern, dim3(ctas), dim3(kWarps * 32), smem, s, a);
+    kern<<<ctas, kWarps * 32, smem, s>>>(a);
     return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
+{
+    const int heads = a.B * a.Hq;
+    if (heads <= num_sms * 8)
+        return launch_dependent(kv8_join_kernel<D, kJoinWarps>, dim3(heads), dim3(kJoinWarps * 32), 0, s, a, p, R);
+    return launch_dependent(kv8_join_kernel<D, 1>, dim3((heads + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0,
+                            s, a, p, R);
 }
 
 // Rows of the batch over the prefix from which the tensor-core kernel takes it.
@@ -612,8 +671,9 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
 {
     Kv8Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
-    a.ctas = num_sms * (R == 8 ? 3 : 2);
-    a.ctas = a.ctas < kKv8MaxCtas ? a.ctas : kKv8MaxCtas;
+    const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
+    a.warps = num_sms * min(R == 8 ? 4 : 3, fit) * kWarps;
+    a.warps = a.warps < kKv8MaxWarps ? a.warps : kKv8MaxWarps;
     cudaError_t e;
     if (p.splits) {
         e = launch_kv8_prefix(a, p, D, per_token, s);
@@ -621,21 +681,17 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
             return e;
     }
     if (a.max_pages || a.ptiles) {
+        const bool after = p.splits > 0;
         if (D == 128)
-            e = R == 8 ? (per_token ? launch_pieces<128, 1, true>(a, s) : launch_pieces<128, 1, false>(a, s))
-                       : (per_token ? launch_pieces<128, 2, true>(a, s) : launch_pieces<128, 2, false>(a, s));
+            e = R == 8 ? (per_token ? launch_pieces<128, 1, true>(a, after, s) : launch_pieces<128, 1, false>(a, after, s))
+                       : (per_token ? launch_pieces<128, 2, true>(a, after, s) : launch_pieces<128, 2, false>(a, after, s));
         else
-            e = R == 8 ? (per_token ? launch_pieces<64, 1, true>(a, s) : launch_pieces<64, 1, false>(a, s))
-                       : (per_token ? launch_pieces<64, 2, true>(a, s) : launch_pieces<64, 2, false>(a, s));
+            e = R == 8 ? (per_token ? launch_pieces<64, 1, true>(a, after, s) : launch_pieces<64, 1, false>(a, after, s))
+                       : (per_token ? launch_pieces<64, 2, true>(a, after, s) : launch_pieces<64, 2, false>(a, after, s));
         if (e != cudaSuccess)
             return e;
     }
-    const dim3 grid(a.B, a.Hq);
-    if (D == 128)
-        kv8_join_kernel<128><<<grid, kJoinWarps * 32, 0, s>>>(a, p, R);
-    else
-        kv8_join_kernel<64><<<grid, kJoinWarps * 32, 0, s>>>(a, p, R);
-    return cudaGetLastError();
+    return D == 128 ? launch_join<128>(a, p, R, num_sms, s) : launch_join<64>(a, p, R, num_sms, s);
 }
 
 }  // namespace w4a8

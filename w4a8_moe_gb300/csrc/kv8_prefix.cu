@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     const int row0 = rp * 2 * kTile;
     const int nt = rows_all - row0 > kTile ? 2 : 1;
 
+    grid_dep_launch();   // the kernel after this one needs nothing of it before its own end
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < kBars; ++i) {

@@ -60,7 +60,8 @@ enum Bar {
     kPFull = kSFull + 2,             // [2]
     kOFull = kPFull + 2,             // [2]
     kScFull = kOFull + 2,            // [kScaleRing]
-    kBars = kScFull + kScaleRing
+    kQFull = kScFull + kScaleRing,
+    kBars
 };
 static_assert(kBars * 8 + 8 <= 256, "barrier area");
 
@@ -105,6 +106,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void ld_wait16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
 // Wait for this warp's tensor-memory loads; the registers they fill pass
 // through, so that no use of them can be moved ahead of the wait.
 __device__ __forceinline__ void ld_wait32(uint32_t (&r)[32])
@@ -134,10 +151,37 @@ __device__ __forceinline__ uint4 lds128(uint32_t at)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
     return v;
 }
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ float ex2(float x)
 {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
@@ -146,6 +190,37 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Two fp32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+    __device__ __forceinline__ explicit F2(uint64_t x) : v(x) {}
+    __device__ __forceinline__ float lo() const { return __uint_as_float(static_cast<uint32_t>(v)); }
+    __device__ __forceinline__ float hi() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return F2(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+    return F2(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+    return F2(r);
+}
+
+template <bool B>
+struct Const {
+    static constexpr bool value = B;
+};
 
 }  // namespace
 
@@ -182,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 count = 4;          // the converter's warps
             else if (i >= kPFull && i < kOFull)
                 count = 4;          // a tile's softmax warps
+            else if (i == kQFull)
+                count = 4 * nt;
             mbar_init(bar(i), count);
         }
         fence_mbar_init();
@@ -203,158 +280,186 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     };
     auto wait_warp = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(i, parity)) != 0; };
 
-    // ---- queries into shared memory, by the softmax threads: row scale c
-    const bool softmax_role = warp < 8;
-    const int t = warp >> 2;                       // row tile of a softmax thread
-    const int my_row = row0 + t * kTile + (tid & 127);
-    float c = 0.0f;
-    if (softmax_role && t < nt) {
-        uint4 raw[D / 8];
-        if (my_row < rows_all) {
-            const int b = my_row / a.group;
-            const uint16_t* src = a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + my_row % a.group) * D;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                raw[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                raw[i] = make_uint4(0, 0, 0, 0);
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                top = max(top, max((w[j] >> 16) & 0x7FFFu, w[j] & 0x7FFFu));
-        }
-        const int ex = static_cast<int>(top >> 7);
-        const int e = top == 0 || ex == 255 ? 0 : max(ex, 1) - 127;
-        c = ldexpf(a.sm_scale, e);
-        if (!TOK)
-            c *= __ldg(a.k_scale + h);
-        // a negative factor goes into q, so that the largest product is the largest score
-        const float down = c < 0.0f ? -ldexpf(1.0f, -e) : ldexpf(1.0f, -e);
-        c = fabsf(c);
-        c = a.cap > 0.0f ? c / a.cap : c * kLog2e;
-        const int r = tid & 127;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            uint32_t f[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                f[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
-            sts128(base + L::q + t * L::kOperand + (i >> 3) * L::kPanel + r * 128 + (((i & 7) ^ (r & 7)) << 4), f[0],
-                   f[1], f[2], f[3]);
-        }
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
+    // 512 threads start with 128 registers each; a softmax thread holds a row of 128 scores
+    if (warp < 8)
+        regs_inc<192>();
+    else
+        regs_dec<64>();
 
-    if (softmax_role) {
-        // ------------------------------------------------------------ softmax
+    if (warp < 8) {
+        const int t = warp >> 2;       // row tile
+        const int my_row = row0 + t * kTile + (tid & 127);
         if (t < nt) {
+            // -------------------------------------------------------- queries
+            // A warp stages its 32 rows, whole rows at a time; the row's scale
+            // goes to the lane that owns the row.
+            constexpr int kLanes = D / 8, kPer = 32 / kLanes, kIters = 32 / kPer;
+            const float ks_head = TOK ? 1.0f : __ldg(a.k_scale + h);
+            const bool flip = a.sm_scale * ks_head < 0.0f;
+            const int sub = lane / kLanes, ch = lane % kLanes;
+            int my_exp = 0;
+            uint4 raw[kIters];
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                const int row = row0 + t * kTile + (warp & 3) * 32 + i * kPer + sub;
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (row < rows_all) {
+                    const int b = row / a.group;
+                    const uint16_t* src = a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + row - b * a.group) * D;
+                    raw[i] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    top = max(top, max((w[j] >> 16) & 0x7FFFu, w[j] & 0x7FFFu));
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1)
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                const int ex = static_cast<int>(top >> 7);
+                const int e = top == 0 || ex == 255 ? 0 : max(ex, 1) - 127;
+                // a negative factor goes into q, so that the largest product is the largest score
+                const float down = flip ? -ldexpf(1.0f, -e) : ldexpf(1.0f, -e);
+                uint32_t f[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    f[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+                const int r = (warp & 3) * 32 + i * kPer + sub;
+                sts128(base + L::q + t * L::kOperand + (ch >> 3) * L::kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4), f[0],
+                       f[1], f[2], f[3]);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int ej = __shfl_sync(0xFFFFFFFFu, e, j * kLanes);
+                    my_exp = lane == i * kPer + j ? ej : my_exp;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(kQFull));
+            const bool capped = a.cap > 0.0f;
+            const float capl = a.cap * kLog2e;
+            float c = fabsf(ldexpf(a.sm_scale, my_exp) * ks_head);   // score = c * product
+            c = capped ? c / a.cap * (2.0f * kLog2e) : c * kLog2e;
+
+            // -------------------------------------------------------- softmax
             const uint32_t ts = tmem + (static_cast<uint32_t>(warp & 3) << 21) + t * kTile;         // S, then P
             const uint32_t to = tmem + (static_cast<uint32_t>(warp & 3) << 21) + 2 * kTile + t * D;  // O
-            float m = -INFINITY, l = 0.0f;
-            const float capl = a.cap * kLog2e;
-            const bool capped = a.cap > 0.0f;
-            auto score = [&](float s) {   // s * c, capped: cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y}))
-                float f = s * c;
-                if (capped) {
-                    const float e = ex2(f * (2.0f * kLog2e));
-                    f = e > 1e30f ? capl : capl * (1.0f - __fdividef(2.0f, 1.0f + e));
-                }
-                return f;
-            };
-            bool ok = true;
-            for (int i = 0; i < n && ok; ++i) {
-                const float* ks = nullptr;
-                if (TOK) {
-                    ok = wait_warp(kScFull + i % kScaleRing, (i / kScaleRing) & 1);
-                    if (!ok)
-                        break;
-                    ks = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + L::scales) +
-                         (i % kScaleRing) * 2 * kTile;
-                }
+            float m = -INFINITY;
+            F2 l0(0.0f, 0.0f), l1(0.0f, 0.0f);
+            const float* scales = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + L::scales);
+            // One key tile. kTail: keys past the prefix are masked.
+            auto tile = [&](int i, auto tail) {
+                constexpr bool kTail = decltype(tail)::value;
+                const float* ks = scales + (i % kScaleRing) * 2 * kTile;
                 const float* vs = ks + kTile;
-                const int live = a.prefix_len - (tile0 + i) * kTile;   // keys of the tile that exist (may pass 128)
+                const int live = a.prefix_len - (tile0 + i) * kTile;
                 float lift = 0.0f;   // log2 of the tile's largest value scale
                 if (TOK) {
                     float v = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        v = fmaxf(v, lane + 32 * j < live ? fabsf(vs[lane + 32 * j]) : 0.0f);
+                        v = fmaxf(v, kTail && lane + 32 * j >= live ? 0.0f : fabsf(vs[lane + 32 * j]));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1)
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
                     lift = fmaxf(log2f(v), -100.0f);
                 }
-                ok = wait_warp(kSFull + t, i & 1);
-                if (!ok)
-                    break;
+                if (!wait_warp(kSFull + t, i & 1))
+                    return false;
                 tc_fence_after();
-                // the row's largest score
-                float top = -INFINITY;
+                uint32_t r[4][32];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    tmem_ld32(ts + ch * 32, r[ch]);
+                float top[4];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t r[32];
-                    tmem_ld32(ts + ch * 32, r);
-                    ld_wait32(r);
+                    ld_wait32(r[ch]);
+                    if (TOK) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float f = __uint_as_float(r[j]);
-                        if (TOK)
-                            f *= ks[ch * 32 + j];
-                        if (live < kTile)
-                            f = ch * 32 + j < live ? f : -INFINITY;
-                        top = fmaxf(top, f);
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(ks + ch * 32 + j);
+                            const F2 x = mul2(F2(__uint_as_float(r[ch][j]), __uint_as_float(r[ch][j + 1])), F2(k4.x, k4.y));
+                            const F2 y = mul2(F2(__uint_as_float(r[ch][j + 2]), __uint_as_float(r[ch][j + 3])), F2(k4.z, k4.w));
+                            r[ch][j] = __float_as_uint(x.lo()), r[ch][j + 1] = __float_as_uint(x.hi());
+                            r[ch][j + 2] = __float_as_uint(y.lo()), r[ch][j + 3] = __float_as_uint(y.hi());
+                        }
                     }
+                    if (kTail) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            r[ch][j] = ch * 32 + j < live ? r[ch][j] : 0xFF800000u;
+                    }
+                    top[ch] = fmaxf(__uint_as_float(r[ch][0]), __uint_as_float(r[ch][1]));
+#pragma unroll
+                    for (int j = 2; j < 32; j += 2)
+                        top[ch] = max3(top[ch], __uint_as_float(r[ch][j]), __uint_as_float(r[ch][j + 1]));
                 }
-                top = score(top) + lift;
-                if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
-                    const float next = fmaxf(m, top);
+                // cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y})), c holding 2 log2(e) / cap
+                float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                if (capped)
+                    best = fmaf(-2.0f * capl, rcp(1.0f + ex2(best)), capl);
+                best += lift;
+                if (__any_sync(0xFFFFFFFFu, best > m + kSlack)) {
+                    const float next = fmaxf(m, best);
                     const float f = next == -INFINITY ? 1.0f : ex2(m - next);
                     m = next;
-                    l *= f;
+                    l0 = mul2(l0, F2(f, f));
+                    l1 = mul2(l1, F2(f, f));
                     if (i > 0) {
+#pragma unroll 1
+                        for (int ch = 0; ch < D / 16; ++ch) {
+                            uint32_t x[16];
+                            tmem_ld16(to + ch * 16, x);
+                            ld_wait16(x);
 #pragma unroll
-                        for (int ch = 0; ch < D / 32; ++ch) {
-                            uint32_t r[32];
-                            tmem_ld32(to + ch * 32, r);
-                            ld_wait32(r);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
-                            tmem_st32(to + ch * 32, r);
+                            for (int j = 0; j < 16; ++j)
+                                x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                            tmem_st16(to + ch * 16, x);
                         }
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
+                const F2 c2(c, c), add(capped ? capl - ref : -ref, capped ? capl - ref : -ref);
+                const F2 one(1.0f, 1.0f), two(-2.0f * capl, -2.0f * capl), zero(-0.0f, -0.0f);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t r[32], p[16];
-                    tmem_ld32(ts + ch * 32, r);
-                    ld_wait32(r);
+                    uint32_t p[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float w[2];
+                    for (int j = 0; j < 32; j += 4) {
+                        float4 v4;
+                        if (TOK)
+                            v4 = *reinterpret_cast<const float4*>(vs + ch * 32 + j);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float f = __uint_as_float(r[j + e]);
-                            if (TOK)
-                                f *= ks[ch * 32 + j + e];
-                            f = score(f);
-                            if (live < kTile)
-                                f = ch * 32 + j + e < live ? f : -INFINITY;
-                            w[e] = ex2(f - ref);
-                            l += w[e];
-                            if (TOK)
-                                w[e] *= live < kTile && ch * 32 + j + e >= live ? 0.0f : vs[ch * 32 + j + e];
+                        for (int e = 0; e < 4; e += 2) {
+                            const F2 s(__uint_as_float(r[ch][j + e]), __uint_as_float(r[ch][j + e + 1]));
+                            F2 x = fma2(s, c2, capped ? zero : add);
+                            if (capped) {
+                                x = add2(F2(ex2(x.lo()), ex2(x.hi())), one);
+                                x = fma2(F2(rcp(x.lo()), rcp(x.hi())), two, add);
+                            }
+                            float w0 = ex2(x.lo()), w1 = ex2(x.hi());
+                            if (kTail) {
+                                w0 = ch * 32 + j + e < live ? w0 : 0.0f;
+                                w1 = ch * 32 + j + e + 1 < live ? w1 : 0.0f;
+                            }
+                            F2 w(w0, w1);
+                            if (e == 0)
+                                l0 = add2(l0, w);
+                            else
+                                l1 = add2(l1, w);
+                            if (TOK) {
+                                F2 v = e == 0 ? F2(v4.x, v4.y) : F2(v4.z, v4.w);
+                                if (kTail)
+                                    v = F2(ch * 32 + j + e < live ? v.lo() : 0.0f, ch * 32 + j + e + 1 < live ? v.hi() : 0.0f);
+                                w = mul2(w, v);
+                            }
+                            p[(j + e) >> 1] = pack_f16(w.lo(), w.hi());
                         }
-                        p[j >> 1] = pack_f16(w[0], w[1]);
                     }
                     tmem_st16(ts + ch * 16, p);
                 }
@@ -363,26 +468,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(kPFull + t));
+                return true;
+            };
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                if (TOK)
+                    ok = wait_warp(kScFull + i % kScaleRing, (i / kScaleRing) & 1);
+                if (ok)
+                    ok = (tile0 + i + 1) * kTile <= a.prefix_len ? tile(i, Const<false>()) : tile(i, Const<true>());
             }
-            if (ok && wait_warp(kOFull + t, 0)) {
+            // -------------------------------------------------------- results
+            // Each thread lays its row of O in shared memory (the operands are
+            // done with once both row tiles are) and sends it off as one copy.
+            for (int x = 0; x < nt && ok; ++x)
+                ok = wait_warp(kOFull + x, 0);
+            if (ok) {
                 tc_fence_after();
                 const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
                 const int64_t at = (static_cast<int64_t>(split) * a.Hkv + h) * rows_all + my_row;
+                const uint32_t mine = base + L::k + (tid & 255) * (D * 4 + 16);
 #pragma unroll
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t r[32];
                     tmem_ld32(to + ch * 32, r);
                     ld_wait32(r);
-                    if (my_row < rows_all) {
-                        float4* dst = reinterpret_cast<float4*>(pl.part_o + at * D + ch * 32);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(__uint_as_float(r[4 * j]) * vscale, __uint_as_float(r[4 * j + 1]) * vscale,
-                                                 __uint_as_float(r[4 * j + 2]) * vscale, __uint_as_float(r[4 * j + 3]) * vscale);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        r[j] = __float_as_uint(__uint_as_float(r[j]) * vscale);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        sts128(mine + ch * 128 + j * 4, r[j], r[j + 1], r[j + 2], r[j + 3]);
                 }
-                if (my_row < rows_all)
-                    pl.part_ml[at] = make_float2(m, l);
+                fence_proxy_async_smem();
+                if (my_row < rows_all) {
+                    bulk_store(pl.part_o + at * D, mine, D * 4);
+                    bulk_commit_group();
+                    pl.part_ml[at] = make_float2(m, (l0.lo() + l0.hi()) + (l1.lo() + l1.hi()));
+                    bulk_wait_all();
+                }
                 tc_fence_before();
             }
         }
@@ -516,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             }
             umma_commit(bar(kSFull + tt));
         };
-        bool ok = wait(kKFull, 0);
+        bool ok = wait(kQFull, 0) && wait(kKFull, 0);
         if (ok) {
             tc_fence_after();
             for (int tt = 0; tt < nt; ++tt)

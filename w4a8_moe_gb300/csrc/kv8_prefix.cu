@@ -60,10 +60,11 @@ enum Bar {
     kPFull = kSFull + 2,             // [2]
     kOFull = kPFull + 2,             // [2]
     kScFull = kOFull + 2,            // [kScaleRing]
-    kQFull = kScFull + kScaleRing,
-    kBars
+    kQRaw = kScFull + kScaleRing,    // [2]
+    kQFull = kQRaw + 2,              // [2]
+    kBars = kQFull + 2
 };
-static_assert(kBars * 8 + 8 <= 256, "barrier area");
+static_assert(kBars * 8 + 16 <= 256, "barrier area");
 
 // MMA, f16 operands, fp32 accumulators; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
@@ -71,32 +72,46 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// One thread issues an MMA of 64 cycles at a time, so what it does in between
+// has to be short: descriptors are a constant high word and a low word that
+// advances by constants, and whether D is added to is a constant.
+__device__ __forceinline__ uint32_t elect_one()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                 "r"(acc)
-                 : "memory");
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+template <bool kAcc>
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                       uint32_t idesc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-                 "r"(acc)
-                 : "memory");
+    if (leader)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d), "r"(alo), "r"(ahi), "r"(blo),
+                     "r"(bhi), "r"(idesc), "n"(kAcc ? 1 : 0)
+                     : "memory");
 }
-// An operand whose non-contracted axis is contiguous, 128-byte swizzle: panels
-// of 64 values by all keys; 8-key groups are 1024 bytes apart, panels `panel`.
-__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t panel)
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi,
+                                       uint32_t idesc, uint32_t acc)
 {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((panel >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
+    if (leader)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(blo), "r"(bhi),
+                     "r"(idesc), "r"(acc)
+                     : "memory");
 }
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar)
+{
+    if (leader)
+        umma_commit(bar);
+}
+// Operands in the 128-byte swizzle: panels of 64 values (128 bytes) by all
+// rows, 8-row groups 1024 bytes apart. Contracted axis contiguous (Q, K): the
+// start advances 32 bytes per MMA inside a panel. Other axis contiguous (V):
+// panels are kPanel apart, the start advances by 16 keys, 2048 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // group stride, version, swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t panel) { return (saddr >> 4) | ((panel >> 4) << 16); }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -224,7 +239,7 @@ struct Const {
 
 }  // namespace
 
-template <int D, bool TOK>
+template <int D, bool TOK, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_constant__ Kv8Attn a,
                                                                  const __grid_constant__ Kv8Prefix pl)
 {
@@ -237,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     __shared__ uint32_t tmem_base;
     const volatile int* abort = &abort_flag;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the shuffles make warp-uniform what the issuer's instructions take from uniform registers
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     // CTA -> (split, row pair, head); neighbours share the head's keys
     const int rp = blockIdx.x % pl.row_pairs;
     const int h = (blockIdx.x / pl.row_pairs) % a.Hkv;
@@ -257,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 count = 4;          // the converter's warps
             else if (i >= kPFull && i < kOFull)
                 count = 4;          // a tile's softmax warps
-            else if (i == kQFull)
-                count = 4 * nt;
+            else if (i >= kQRaw && i < kBars)
+                count = 4;          // the same
             mbar_init(bar(i), count);
         }
         fence_mbar_init();
@@ -267,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         tmem_alloc(smem_u32(&tmem_base), 512);
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
     auto fail = [&]() {
         set_error(a.err, kErrBitTimeout);
         *const_cast<volatile int*>(&abort_flag) = 1;
@@ -291,59 +307,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         const int my_row = row0 + t * kTile + (tid & 127);
         if (t < nt) {
             // -------------------------------------------------------- queries
-            // A warp stages its 32 rows, whole rows at a time; the row's scale
-            // goes to the lane that owns the row.
-            constexpr int kLanes = D / 8, kPer = 32 / kLanes, kIters = 32 / kPer;
-            const float ks_head = TOK ? 1.0f : __ldg(a.k_scale + h);
-            const bool flip = a.sm_scale * ks_head < 0.0f;
-            const int sub = lane / kLanes, ch = lane % kLanes;
-            int my_exp = 0;
-            uint4 raw[kIters];
-#pragma unroll
-            for (int i = 0; i < kIters; ++i) {
-                const int row = row0 + t * kTile + (warp & 3) * 32 + i * kPer + sub;
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (row < rows_all) {
-                    const int b = row / a.group;
-                    const uint16_t* src = a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + row - b * a.group) * D;
-                    raw[i] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
-                }
+            // A thread owns a row: it copies it to shared memory (where later
+            // key tiles will stand, rows 16 bytes apart from a whole number of
+            // banks), finds its exponent, and writes it as an operand.
+            const uint32_t staged = base + L::k + L::kOperand + (t * kTile + (tid & 127)) * (D * 2 + 16);
+            const bool there = my_row < rows_all;
+            const int there_n = __popc(__ballot_sync(0xFFFFFFFFu, there));
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar(kQRaw + t), there_n * D * 2);
+            __syncwarp();
+            if (there) {
+                const int b = my_row / a.group;
+                bulk_load(staged, a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + my_row - b * a.group) * D, D * 2,
+                          bar(kQRaw + t));
             }
-#pragma unroll
-            for (int i = 0; i < kIters; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                uint32_t top = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    top = max(top, max((w[j] >> 16) & 0x7FFFu, w[j] & 0x7FFFu));
-#pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1)
-                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const int ex = static_cast<int>(top >> 7);
-                const int e = top == 0 || ex == 255 ? 0 : max(ex, 1) - 127;
-                // a negative factor goes into q, so that the largest product is the largest score
-                const float down = flip ? -ldexpf(1.0f, -e) : ldexpf(1.0f, -e);
+            const float ks_head = TOK ? 1.0f : __ldg(a.k_scale + h);
+            bool ok = wait_warp(kQRaw + t, 0);
+            uint32_t top = 0;
+            if (there && ok) {
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 w = lds128(staged + i * 16);
+                    // the larger magnitude of each half, side by side
+                    const uint32_t x = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
+                    top = __vmaxu2(top, __vmaxu2(x, __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+                }
+                top = max(top >> 16, top & 0xFFFFu);
+            }
+            const int ex = static_cast<int>(top >> 7);
+            const int e = top == 0 || ex == 255 ? 0 : min(max(ex, 1), 253) - 127;
+            // a negative factor goes into q, so that the largest product is the largest score
+            const float down = ((a.sm_scale < 0.0f) != (ks_head < 0.0f) ? -1.0f : 1.0f) * __int_as_float((127 - e) << 23);
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (there && ok)
+                    w = lds128(staged + i * 16);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                 uint32_t f[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    f[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
-                const int r = (warp & 3) * 32 + i * kPer + sub;
-                sts128(base + L::q + t * L::kOperand + (ch >> 3) * L::kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4), f[0],
+                    f[j] = pack_f16(__uint_as_float(u[j] << 16) * down, __uint_as_float(u[j] & 0xFFFF0000u) * down);
+                const int r = tid & 127;
+                sts128(base + L::q + t * L::kOperand + (i >> 3) * L::kPanel + r * 128 + (((i & 7) ^ (r & 7)) << 4), f[0],
                        f[1], f[2], f[3]);
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int ej = __shfl_sync(0xFFFFFFFFu, e, j * kLanes);
-                    my_exp = lane == i * kPer + j ? ej : my_exp;
-                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(bar(kQFull));
-            const bool capped = a.cap > 0.0f;
+                mbar_arrive(bar(kQFull + t));
             const float capl = a.cap * kLog2e;
-            float c = fabsf(ldexpf(a.sm_scale, my_exp) * ks_head);   // score = c * product
-            c = capped ? c / a.cap * (2.0f * kLog2e) : c * kLog2e;
+            float c = fabsf(a.sm_scale * __int_as_float((127 + e) << 23) * ks_head);   // score = c * product
+            c = CAP ? c / a.cap * (2.0f * kLog2e) : c * kLog2e;
 
             // -------------------------------------------------------- softmax
             const uint32_t ts = tmem + (static_cast<uint32_t>(warp & 3) << 21) + t * kTile;         // S, then P
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 }
                 // cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y})), c holding 2 log2(e) / cap
                 float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-                if (capped)
+                if (CAP)
                     best = fmaf(-2.0f * capl, rcp(1.0f + ex2(best)), capl);
                 best += lift;
                 if (__any_sync(0xFFFFFFFFu, best > m + kSlack)) {
@@ -424,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
-                const F2 c2(c, c), add(capped ? capl - ref : -ref, capped ? capl - ref : -ref);
+                const F2 c2(c, c), add(CAP ? capl - ref : -ref, CAP ? capl - ref : -ref);
                 const F2 one(1.0f, 1.0f), two(-2.0f * capl, -2.0f * capl), zero(-0.0f, -0.0f);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
@@ -437,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
                             const F2 s(__uint_as_float(r[ch][j + e]), __uint_as_float(r[ch][j + e + 1]));
-                            F2 x = fma2(s, c2, capped ? zero : add);
-                            if (capped) {
+                            F2 x = fma2(s, c2, CAP ? zero : add);
+                            if (CAP) {
                                 x = add2(F2(ex2(x.lo()), ex2(x.hi())), one);
                                 x = fma2(F2(rcp(x.lo()), rcp(x.hi())), two, add);
                             }
@@ -470,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     mbar_arrive(bar(kPFull + t));
                 return true;
             };
-            bool ok = true;
             for (int i = 0; i < n && ok; ++i) {
                 if (TOK)
                     ok = wait_warp(kScFull + i % kScaleRing, (i / kScaleRing) & 1);
@@ -487,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
                 const int64_t at = (static_cast<int64_t>(split) * a.Hkv + h) * rows_all + my_row;
                 const uint32_t mine = base + L::k + (tid & 255) * (D * 4 + 16);
-#pragma unroll
+#pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t r[32];
                     tmem_ld32(to + ch * 32, r);
@@ -522,6 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             const bool is_v = (s >> 1) & 1;
             const int slot = s % kRaw;
             ok = wait_warp(kRawFull + slot, (s / kRaw) & 1);
+            if (s == 2)   // until then the queries stand where V and later keys go
+                for (int x = 0; x < nt && ok; ++x)
+                    ok = wait_warp(kQFull + x, 0);
             if (ok && half == 0 && i >= 2)
                 ok = wait_warp((is_v ? kVEmpty : kKEmpty) + (i & 1), ((i >> 1) - 1) & 1);
             if (!ok)
@@ -627,55 +644,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     mbar_wait(bar(kScFull + (s >> 2) % kScaleRing), ((s >> 2) / kScaleRing) & 1);
             }
         }
-    } else if (warp == 13 && lane == 0) {
+    } else if (warp == 13) {
         // ------------------------------------------------------------- issuer
+        // The whole warp walks the loop and one elected lane issues.
+        // S_{i+1} overwrites P_i: one thread's MMAs run in order.
+        const uint32_t leader = elect_one();
         constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
-        auto scores = [&](int tt, int i) {
+        const uint32_t k_lo = desc_lo(base + L::k, 16), v_lo = desc_lo(base + L::v, L::kPanel);
+        auto scores = [&](int t, int i) {
+            const uint32_t ts = tmem + t * kTile;
+            const uint32_t q = desc_lo(base + L::q + t * L::kOperand, 16);
+            const uint32_t k = k_lo + (i & 1) * (L::kOperand >> 4);
+            mma_ss<false>(leader, ts, q, kDescHi, k, kDescHi, kIdS);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const uint32_t off = (s >> 2) * L::kPanel + (s & 3) * 32;
-                mma_ss(tmem + tt * kTile, desc_kmajor_sw128(base + L::q + tt * L::kOperand + off),
-                       desc_kmajor_sw128(base + L::k + (i & 1) * L::kOperand + off), kIdS, s > 0);
+            for (int s = 1; s < D / 16; ++s) {
+                const uint32_t off = ((s >> 2) * L::kPanel + (s & 3) * 32) >> 4;
+                mma_ss<true>(leader, ts, q + off, kDescHi, k + off, kDescHi, kIdS);
             }
-            umma_commit(bar(kSFull + tt));
+            commit(leader, bar(kSFull + t));
+            if (t == nt - 1)
+                commit(leader, bar(kKEmpty + (i & 1)));
         };
-        bool ok = wait(kQFull, 0) && wait(kKFull, 0);
-        if (ok) {
-            tc_fence_after();
-            for (int tt = 0; tt < nt; ++tt)
-                scores(tt, 0);
-            umma_commit(bar(kKEmpty));
+        bool ok = wait_warp(kKFull, 0);
+        for (int t = 0; t < nt && ok; ++t) {
+            ok = wait_warp(kQFull + t, 0);
+            if (ok) {
+                tc_fence_after();
+                scores(t, 0);
+            }
         }
         for (int i = 0; i < n && ok; ++i) {
-            ok = wait(kVFull + (i & 1), (i >> 1) & 1);
-            for (int tt = 0; tt < nt && ok; ++tt) {
-                ok = wait(kPFull + tt, i & 1);
+            const uint32_t v = v_lo + (i & 1) * (L::kOperand >> 4);
+            ok = wait_warp(kVFull + (i & 1), (i >> 1) & 1);
+            for (int t = 0; t < nt && ok; ++t) {
+                ok = wait_warp(kPFull + t, i & 1);
                 if (!ok)
                     break;
                 tc_fence_after();
+                const uint32_t to = tmem + 2 * kTile + t * D, tp = tmem + t * kTile;
 #pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
-                    mma_ts(tmem + 2 * kTile + tt * D, tmem + tt * kTile + s * 8,
-                           desc_mnmajor_sw128(base + L::v + (i & 1) * L::kOperand + s * 2048, L::kPanel), kIdO,
-                           i > 0 || s > 0);
-                if (i + 1 < n) {
-                    if (tt == 0)
-                        ok = wait(kKFull + ((i + 1) & 1), ((i + 1) >> 1) & 1);
-                    if (!ok)
-                        break;
+                    mma_ts(leader, to, tp + s * 8, v + s * (2048 >> 4), kDescHi, kIdO, s > 0 || i > 0);
+                if (t == nt - 1)
+                    commit(leader, bar(kVEmpty + (i & 1)));
+                if (i + 1 == n) {
+                    commit(leader, bar(kOFull + t));
+                } else if (t > 0 || (ok = wait_warp(kKFull + ((i + 1) & 1), ((i + 1) >> 1) & 1))) {
                     tc_fence_after();
-                    scores(tt, i + 1);
-                } else {
-                    umma_commit(bar(kOFull + tt));
+                    scores(t, i + 1);
                 }
             }
-            if (ok) {
-                umma_commit(bar(kVEmpty + (i & 1)));
-                if (i + 1 < n)
-                    umma_commit(bar(kKEmpty + ((i + 1) & 1)));
-            }
         }
-        if (!ok) {   // what was issued ends before tensor memory is freed
+        if (!ok && leader) {   // what was issued ends before tensor memory is freed
             mbar_init(bar(kBars), 1);
             fence_mbar_init();
             umma_commit(bar(kBars));
@@ -715,10 +735,10 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len)
     return p;
 }
 
-template <int D, bool TOK>
+template <int D, bool TOK, bool CAP>
 static cudaError_t launch(const Kv8Attn& a, const Kv8Prefix& p, cudaStream_t s)
 {
-    auto kern = kv8_prefix_kernel<D, TOK>;
+    auto kern = kv8_prefix_kernel<D, TOK, CAP>;
     const int smem = Smem<D>::total + 1024;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
@@ -727,11 +747,17 @@ static cudaError_t launch(const Kv8Attn& a, const Kv8Prefix& p, cudaStream_t s)
     return cudaGetLastError();
 }
 
+template <int D>
+static cudaError_t launch(const Kv8Attn& a, const Kv8Prefix& p, int per_token, cudaStream_t s)
+{
+    if (a.cap > 0.0f)
+        return per_token ? launch<D, true, true>(a, p, s) : launch<D, false, true>(a, p, s);
+    return per_token ? launch<D, true, false>(a, p, s) : launch<D, false, false>(a, p, s);
+}
+
 cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s)
 {
-    if (D == 128)
-        return per_token ? launch<128, true>(a, p, s) : launch<128, false>(a, p, s);
-    return per_token ? launch<64, true>(a, p, s) : launch<64, false>(a, p, s);
+    return D == 128 ? launch<128>(a, p, per_token, s) : launch<64>(a, p, per_token, s);
 }
 
 }  // namespace w4a8

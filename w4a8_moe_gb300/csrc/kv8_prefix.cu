@@ -9,7 +9,7 @@
 // takes 256 rows (two 128-row tiles) and a range of 128-key tiles and runs,
 // with S, P and O in tensor memory:
 //   loader    warp 12: pages -> raw codes in shared memory (bulk copies)
-//   converter warps 8-11: E4M3 -> f16 (exact), into the layouts the MMA reads
+//   converter warps 8-11, 14, 15: E4M3 -> f16 (exact), into the layouts the MMA reads
 //   issuer    warp 13: S_t = Q_t K^T, O_t += P_t V, alternating the row tiles
 //   softmax   warps 0-3 (tile 0), 4-7 (tile 1): one thread per row
 // While one tile's softmax runs, the tensor core works for the other tile.
@@ -31,7 +31,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kTile = 128;        // keys per tile, rows per row tile
 constexpr int kHalf = 64;         // keys per raw slot
-constexpr int kRaw = 3;           // raw slots
+constexpr int kStages = 3;        // f16 operand tiles, K and V in turn
+constexpr int kRaw = 7;           // raw slots
+constexpr int kPairs = 3;         // pairs of converter warps
 constexpr int kScaleRing = 4;     // tiles whose per-token scales are held
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;    // see kv8_attn.cu
@@ -41,22 +43,19 @@ struct Smem {
     static constexpr int kOperand = kTile * D * 2;          // one f16 operand tile
     static constexpr int kPanel = kTile * 128;              // 64 f16 columns of it
     static constexpr int q = 0;                             // [2] row tiles
-    static constexpr int k = q + 2 * kOperand;              // [2] stages
-    static constexpr int v = k + 2 * kOperand;              // [2] stages
-    static constexpr int raw = v + 2 * kOperand;            // [kRaw] of 64 x D codes
+    static constexpr int stage = q + 2 * kOperand;          // [kStages]: K_0, V_0, K_1, ...
+    static constexpr int raw = stage + kStages * kOperand;  // [kRaw] of 64 x D codes
     static constexpr int scales = raw + kRaw * kHalf * D;   // [kScaleRing][2][128] fp32
     static constexpr int bars = scales + kScaleRing * 2 * kTile * 4;
-    static constexpr int total = bars + 256;
+    static constexpr int total = bars + 320;
 };
 // mbarriers, 8 bytes each
 enum Bar {
     kRawFull = 0,                    // [kRaw]
     kRawEmpty = kRawFull + kRaw,     // [kRaw]
-    kKFull = kRawEmpty + kRaw,       // [2]
-    kKEmpty = kKFull + 2,
-    kVFull = kKEmpty + 2,
-    kVEmpty = kVFull + 2,
-    kSFull = kVEmpty + 2,            // [2] row tiles
+    kFull = kRawEmpty + kRaw,        // [kStages]
+    kEmpty = kFull + kStages,        // [kStages]
+    kSFull = kEmpty + kStages,       // [2] row tiles
     kPFull = kSFull + 2,             // [2]
     kOFull = kPFull + 2,             // [2]
     kScFull = kOFull + 2,            // [kScaleRing]
@@ -64,7 +63,7 @@ enum Bar {
     kQFull = kQRaw + 2,              // [2]
     kBars = kQFull + 2
 };
-static_assert(kBars * 8 + 16 <= 256, "barrier area");
+static_assert(kBars * 8 + 8 <= 320, "barrier area");
 
 // MMA, f16 operands, fp32 accumulators; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
@@ -269,8 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         abort_flag = 0;
         for (int i = 0; i < kBars; ++i) {
             uint32_t count = 1;
-            if ((i >= kRawEmpty && i < kKFull) || (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty))
-                count = 4;          // the converter's warps
+            if (i >= kRawEmpty && i < kFull)
+                count = 2;          // a pair of converter warps
+            else if (i >= kFull && i < kEmpty)
+                count = 4;          // two pairs, a half each
             else if (i >= kPFull && i < kOFull)
                 count = 4;          // a tile's softmax warps
             else if (i >= kQRaw && i < kBars)
@@ -307,10 +308,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         const int my_row = row0 + t * kTile + (tid & 127);
         if (t < nt) {
             // -------------------------------------------------------- queries
-            // A thread owns a row: it copies it to shared memory (where later
-            // key tiles will stand, rows 16 bytes apart from a whole number of
-            // banks), finds its exponent, and writes it as an operand.
-            const uint32_t staged = base + L::k + L::kOperand + (t * kTile + (tid & 127)) * (D * 2 + 16);
+            // A thread owns a row: it copies it to shared memory (where V_0 and
+            // K_1 will stand), finds its exponent, and writes it as an operand.
+            // Row r takes its 16-byte chunks in the order i ^ x r, with x r a
+            // product in GF(8): both x r and x r + r then pass through all of
+            // 0..7, so neither the reads (rows a whole number of banks apart)
+            // nor the writes (at chunk ^ r) of eight rows collide.
+            const int r = tid & 127;
+            const int turn = ((r << 1) & 4) | (((r ^ (r >> 2)) & 1) << 1) | ((r >> 2) & 1);
+            const uint32_t staged = base + L::stage + L::kOperand + (t * kTile + r) * D * 2;
             const bool there = my_row < rows_all;
             const int there_n = __popc(__ballot_sync(0xFFFFFFFFu, there));
             if (lane == 0)
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             if (there && ok) {
 #pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
-                    const uint4 w = lds128(staged + i * 16);
+                    const uint4 w = lds128(staged + (i ^ turn) * 16);
                     // the larger magnitude of each half, side by side
                     const uint32_t x = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
                     top = __vmaxu2(top, __vmaxu2(x, __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
@@ -341,16 +347,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 #pragma unroll 4
             for (int i = 0; i < D / 8; ++i) {
                 uint4 w = make_uint4(0, 0, 0, 0);
+                const int chunk = i ^ turn;
                 if (there && ok)
-                    w = lds128(staged + i * 16);
+                    w = lds128(staged + chunk * 16);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                 uint32_t f[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     f[j] = pack_f16(__uint_as_float(u[j] << 16) * down, __uint_as_float(u[j] & 0xFFFF0000u) * down);
-                const int r = tid & 127;
-                sts128(base + L::q + t * L::kOperand + (i >> 3) * L::kPanel + r * 128 + (((i & 7) ^ (r & 7)) << 4), f[0],
-                       f[1], f[2], f[3]);
+                sts128(base + L::q + t * L::kOperand + (chunk >> 3) * L::kPanel + r * 128 +
+                           (((chunk & 7) ^ (r & 7)) << 4),
+                       f[0], f[1], f[2], f[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 tc_fence_after();
                 const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
                 const int64_t at = (static_cast<int64_t>(split) * a.Hkv + h) * rows_all + my_row;
-                const uint32_t mine = base + L::k + (tid & 255) * (D * 4 + 16);
+                const uint32_t mine = base + L::stage + (tid & 255) * (D * 4 + 16);
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t r[32];
@@ -523,95 +530,106 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 tc_fence_before();
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 12 || warp >= 14) {
         // ---------------------------------------------------------- converter
-        // A thread turns 16 codes into 32 bytes of f16. Eight threads cover 64
-        // bytes of an even row and the other 64 of the odd row below, so that
-        // neither the loads nor the swizzled stores collide in a bank.
-        const int ct = tid - 256;
-        const int q4 = ct & 3, odd = (ct >> 2) & 1, pr = ct >> 3;   // 16 row pairs at a time
+        // Three pairs of warps take half tiles in turn, so that one
+        // pair's latencies pass under the others' work. A thread turns 16 codes
+        // into 32 bytes of f16; eight threads cover 64 bytes of an even row and
+        // the other 64 of the odd row below, so that neither the loads nor the
+        // swizzled stores collide in a bank.
+        const int cw = warp < 12 ? warp - 8 : warp - 10;
+        const int ct = (cw & 1) * 32 + lane;
+        const int q4 = ct & 3, odd = (ct >> 2) & 1, pr = ct >> 3;   // 8 row pairs at a time
         bool ok = true;
-        for (int s = 0; s < 4 * n && ok; ++s) {
-            const int i = s >> 2, half = s & 1;
-            const bool is_v = (s >> 1) & 1;
-            const int slot = s % kRaw;
+        for (int s = cw >> 1; s < 4 * n && ok; s += kPairs) {
+            const int j = s >> 1, half = s & 1, slot = s % kRaw, stage = j % kStages;   // j: K_0, V_0, K_1, ...
             ok = wait_warp(kRawFull + slot, (s / kRaw) & 1);
-            if (s == 2)   // until then the queries stand where V and later keys go
+            if (s >= 2 && s < 2 + kPairs)   // until then the queries stand in the later stages
                 for (int x = 0; x < nt && ok; ++x)
                     ok = wait_warp(kQFull + x, 0);
-            if (ok && half == 0 && i >= 2)
-                ok = wait_warp((is_v ? kVEmpty : kKEmpty) + (i & 1), ((i >> 1) - 1) & 1);
+            if (ok && j >= kStages)
+                ok = wait_warp(kEmpty + stage, (j / kStages - 1) & 1);
             if (!ok)
                 break;
             const uint32_t src = base + L::raw + slot * kHalf * D;
-            const uint32_t dst = base + (is_v ? L::v : L::k) + (i & 1) * L::kOperand;
-            const int live = a.prefix_len - (tile0 + i) * kTile;
-            constexpr int kPasses = D / 64;
-            uint4 w[2 * kPasses];
-            auto place = [&](int x, int& row, int& c16) {
-                row = (x / kPasses) * 32 + pr * 2 + odd;
-                c16 = D == 128 ? q4 + 4 * (odd ^ (x & 1)) : q4;
-            };
+            const uint32_t dst = base + L::stage + stage * L::kOperand;
+            const int live = a.prefix_len - (tile0 + (s >> 2)) * kTile - half * kHalf;
+            constexpr int kPasses = D / 64;      // 64-byte parts of a row
+            constexpr int kWork = 4 * kPasses;   // 16-code chunks of a thread
 #pragma unroll
-            for (int x = 0; x < 2 * kPasses; ++x) {
-                int row, c16;
-                place(x, row, c16);
-                w[x] = lds128(src + row * D + c16 * 16);
-                if (half * kHalf + row >= live)
-                    w[x] = make_uint4(0, 0, 0, 0);
-            }
+            for (int x0 = 0; x0 < kWork; x0 += 4) {
+                uint4 w[4];
+                auto place = [&](int x, int& row, int& c16) {
+                    row = (x / kPasses) * 16 + pr * 2 + odd;
+                    c16 = D == 128 ? q4 + 4 * (odd ^ (x & 1)) : q4;
+                };
 #pragma unroll
-            for (int x = 0; x < 2 * kPasses; ++x) {
-                int row, c16;
-                place(x, row, c16);
-                const int key = half * kHalf + row;
-                const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-                uint32_t f[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[2 * j] = e4m3x2_to_f16x2(u[j] & 0xFFFFu);
-                    f[2 * j + 1] = e4m3x2_to_f16x2(u[j] >> 16);
+                for (int x = 0; x < 4; ++x) {
+                    int row, c16;
+                    place(x0 + x, row, c16);
+                    w[x] = lds128(src + row * D + c16 * 16);
+                    if (row >= live)
+                        w[x] = make_uint4(0, 0, 0, 0);
                 }
-                const uint32_t at = dst + (c16 >> 2) * L::kPanel + key * 128;
-                const int ch = (c16 & 3) * 2;
-                sts128(at + ((ch ^ (key & 7)) << 4), f[0], f[1], f[2], f[3]);
-                sts128(at + (((ch + 1) ^ (key & 7)) << 4), f[4], f[5], f[6], f[7]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    int row, c16;
+                    place(x0 + x, row, c16);
+                    const int key = half * kHalf + row;
+                    const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        f[2 * y] = e4m3x2_to_f16x2(u[y] & 0xFFFFu);
+                        f[2 * y + 1] = e4m3x2_to_f16x2(u[y] >> 16);
+                    }
+                    const uint32_t at = dst + (c16 >> 2) * L::kPanel + key * 128;
+                    const int ch = (c16 & 3) * 2;
+                    sts128(at + ((ch ^ (key & 7)) << 4), f[0], f[1], f[2], f[3]);
+                    sts128(at + (((ch + 1) ^ (key & 7)) << 4), f[4], f[5], f[6], f[7]);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar(kRawEmpty + slot));
-                if (half == 1)
-                    mbar_arrive(bar((is_v ? kVFull : kKFull) + (i & 1)));
+                mbar_arrive(bar(kFull + stage));
             }
         }
     } else if (warp == 12) {
         // ------------------------------------------------------------- loader
+        // Lane 4 x + y holds the page of copy y of half tile x of the next eight
+        // (four tiles), loaded while the eight before are on their way.
         const int ck_shift = min(a.page_shift, 6);           // keys per copy
         const int ck = 1 << ck_shift;
         const int chunks = kHalf >> ck_shift;
         const int n_pages = (a.prefix_len + (1 << a.page_shift) - 1) >> a.page_shift;
-        int issued = 0;
-        for (int s = 0; s < 4 * n; ++s) {
-            const int i = s >> 2, half = s & 1;
+        auto my_key = [&](int batch) { return tile0 * kTile + (batch * 8 + (lane >> 2)) * kHalf + (lane & 3) * ck; };
+        auto my_page = [&](int batch) {
+            const int key = my_key(batch), idx = key >> a.page_shift;
+            if ((lane & 3) >= chunks || batch * 4 >= n || batch * 4 + (lane >> 3) >= n || key >= a.prefix_len)
+                return 0;
+            const int page = idx < n_pages ? __ldg(a.prefix_pages + idx) : -1;
+            if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages))
+                return page;
+            set_error(a.err, kErrBitIndex);
+            return 0;
+        };
+        int issued = 0, page = 0, next = my_page(0);
+        bool ok = true;
+        for (int s = 0; s < 4 * n && ok; ++s) {
+            const int i = s >> 2, half = s & 1, slot = s % kRaw;
             const bool is_v = (s >> 1) & 1;
-            const int slot = s % kRaw;
-            const int key = (tile0 + i) * kTile + half * kHalf + lane * ck;
-            const bool mine = lane < chunks && key < a.prefix_len;
-            int page = 0;
-            if (mine) {
-                const int idx = key >> a.page_shift;
-                page = idx < n_pages ? __ldg(a.prefix_pages + idx) : -1;
-                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
-                    set_error(a.err, kErrBitIndex);
-                    page = 0;
-                }
+            if (s % 16 == 0) {
+                page = next;
+                next = my_page(s / 16 + 1);
             }
+            const int key = my_key(s / 16);
+            const bool mine = (lane >> 2) == (i & 3) * 2 + half && (lane & 3) < chunks && key < a.prefix_len;
             const int copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-            bool ok = true;
-            if (lane == 0 && s >= kRaw)
-                ok = wait(kRawEmpty + slot, (s / kRaw - 1) & 1);
-            if (!__shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0))
+            if (s >= kRaw)
+                ok = wait_warp(kRawEmpty + slot, (s / kRaw - 1) & 1);
+            if (!ok)
                 break;
             const bool with_scales = TOK && !is_v;
             if (lane == 0) {
@@ -625,10 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             if (mine) {
                 const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + h) << a.page_shift) +
                                     (key & ((1 << a.page_shift) - 1));
-                bulk_load(base + L::raw + slot * kHalf * D + lane * ck * D, (is_v ? a.v_cache : a.k_cache) + row * D,
-                          ck * D, bar(kRawFull + slot));
+                bulk_load(base + L::raw + slot * kHalf * D + (lane & 3) * ck * D,
+                          (is_v ? a.v_cache : a.k_cache) + row * D, ck * D, bar(kRawFull + slot));
                 if (with_scales) {
-                    const uint32_t at = base + L::scales + (i % kScaleRing) * 2 * kTile * 4 + (half * kHalf + lane * ck) * 4;
+                    const uint32_t at = base + L::scales + (i % kScaleRing) * 2 * kTile * 4 +
+                                        (half * kHalf + (lane & 3) * ck) * 4;
                     bulk_load(at, a.k_scale + row, ck * 4, bar(kScFull + i % kScaleRing));
                     bulk_load(at + kTile * 4, a.v_scale + row, ck * 4, bar(kScFull + i % kScaleRing));
                 }
@@ -650,11 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         // S_{i+1} overwrites P_i: one thread's MMAs run in order.
         const uint32_t leader = elect_one();
         constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
-        const uint32_t k_lo = desc_lo(base + L::k, 16), v_lo = desc_lo(base + L::v, L::kPanel);
+        const uint32_t k_lo = desc_lo(base + L::stage, 16), v_lo = desc_lo(base + L::stage, L::kPanel);
+        constexpr uint32_t kStep = L::kOperand >> 4;
         auto scores = [&](int t, int i) {
             const uint32_t ts = tmem + t * kTile;
             const uint32_t q = desc_lo(base + L::q + t * L::kOperand, 16);
-            const uint32_t k = k_lo + (i & 1) * (L::kOperand >> 4);
+            const uint32_t k = k_lo + (2 * i % kStages) * kStep;
             mma_ss<false>(leader, ts, q, kDescHi, k, kDescHi, kIdS);
 #pragma unroll
             for (int s = 1; s < D / 16; ++s) {
@@ -663,9 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             }
             commit(leader, bar(kSFull + t));
             if (t == nt - 1)
-                commit(leader, bar(kKEmpty + (i & 1)));
+                commit(leader, bar(kEmpty + 2 * i % kStages));
         };
-        bool ok = wait_warp(kKFull, 0);
+        bool ok = wait_warp(kFull, 0);
         for (int t = 0; t < nt && ok; ++t) {
             ok = wait_warp(kQFull + t, 0);
             if (ok) {
@@ -674,8 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             }
         }
         for (int i = 0; i < n && ok; ++i) {
-            const uint32_t v = v_lo + (i & 1) * (L::kOperand >> 4);
-            ok = wait_warp(kVFull + (i & 1), (i >> 1) & 1);
+            const int jv = 2 * i + 1, jk = 2 * i + 2;
+            const uint32_t v = v_lo + (jv % kStages) * kStep;
+            ok = wait_warp(kFull + jv % kStages, (jv / kStages) & 1);
             for (int t = 0; t < nt && ok; ++t) {
                 ok = wait_warp(kPFull + t, i & 1);
                 if (!ok)
@@ -686,10 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 for (int s = 0; s < kTile / 16; ++s)
                     mma_ts(leader, to, tp + s * 8, v + s * (2048 >> 4), kDescHi, kIdO, s > 0 || i > 0);
                 if (t == nt - 1)
-                    commit(leader, bar(kVEmpty + (i & 1)));
+                    commit(leader, bar(kEmpty + jv % kStages));
                 if (i + 1 == n) {
                     commit(leader, bar(kOFull + t));
-                } else if (t > 0 || (ok = wait_warp(kKFull + ((i + 1) & 1), ((i + 1) >> 1) & 1))) {
+                } else if (t > 0 || (ok = wait_warp(kFull + jk % kStages, (jk / kStages) & 1))) {
                     tc_fence_after();
                     scores(t, i + 1);
                 }

@@ -240,6 +240,38 @@ def test_write_min_scale(lib):
     _check_write(lib, 40, 2, 128, 32, 1, min_scale=0.01)
 
 
+def test_write_scale_of_every_bf16_value(lib):
+    """The scale of a row is its largest magnitude / 448 as fp32 division has it, for all finite bf16 magnitudes."""
+    x = torch.zeros(0x7F80, 1, 64, dtype=torch.int16)
+    x[:, 0, 17] = torch.arange(0x7F80, dtype=torch.int32).to(torch.int16)
+    x = x.view(torch.bfloat16).cuda()
+    pages = 0x7F80 // 256 + 1
+    kc, vc = (torch.zeros(pages, 1, 256, 64, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(pages, 1, 256, device="cuda") for _ in range(2))
+    lib.kv8_write(x, -x, torch.arange(0x7F80, dtype=torch.int32, device="cuda"), kc, vc, ks, vs)
+    amax = x[:, 0, 17].float()
+    want = amax / torch.full_like(amax, 448.0)
+    want = torch.where(want == 0, 1.0, want)
+    for s in (ks, vs):
+        assert torch.equal(s.reshape(-1)[:0x7F80], want)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -7, 1 / 448, 0.05, 0.1, 0.3, 1.7, 3e-5, 1.9999999, 2.0 ** -61, 1e-30, 1e-39,
+                                   2.0 ** 61, 3e37])
+def test_write_code_of_every_bf16_value(lib, scale):
+    """Codes are those of the fp32 quotient, for every bf16 bit pattern, whatever shares the row with it."""
+    bits = np.arange(0x10000, dtype=np.uint16)
+    for order in (bits, np.random.default_rng(1).permutation(bits)):
+        x = torch.from_numpy(order.view(np.int16).copy()).view(torch.bfloat16).reshape(1024, 1, 64).cuda()
+        kc, vc = (torch.zeros(4, 1, 256, 64, dtype=torch.uint8, device="cuda") for _ in range(2))
+        s = torch.tensor([scale], device="cuda")
+        lib.kv8_write(x, x, torch.arange(1024, dtype=torch.int32, device="cuda"), kc, vc, s, s)
+        q = (x.float() / s[None, None]).cpu().numpy().reshape(-1)
+        want = np.where(np.isnan(q), 127, encode(q))
+        for c in (kc, vc):
+            assert codes_equal(c.cpu().numpy().reshape(-1), want.astype(np.uint8))
+
+
 @pytest.mark.parametrize("t,h,d,page,mode", [(1, 1, 64, 16, 1), (19, 5, 128, 32, 0), (333, 8, 64, 64, 1),
                                              (2049, 2, 128, 256, 0)])
 def test_read(lib, t, h, d, page, mode):

@@ -13,6 +13,8 @@ namespace w4a8 {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr float kInv448Hi = static_cast<float>(1.0 / 448.0);
+constexpr float kInv448Lo = static_cast<float>(1.0 / 448.0 - static_cast<double>(kInv448Hi));
 
 // A row is one (token, head), its keys and its values: D values each. A lane
 // takes 8 values (16 bytes of bf16) out of each half of both, so D / 16 lanes
@@ -42,39 +44,69 @@ __device__ __forceinline__ int64_t cache_row(const Kv8Rows& a, int64_t slot, int
     return ((page * a.Hkv + h) << a.page_shift) + off;
 }
 
-// E4M3(x / s) of 16 values, the quotient rounded to fp32 first (as the format's
-// definition here says). A correctly rounded fp32 division of every value is
-// most of the call's arithmetic, so the quotient is taken as q = x * (1 / s):
-// that is within 2^-22 of x / s, which changes the code only where a rounding
-// boundary of E4M3 lies that close to q. Boundaries have the low 20 bits
-// 0x80000 (4 significant bits and a half) or, below 2^-6, 0 (odd multiples of
-// 2^-10); a thread with any q within 4 units of either divides. With s a power
-// of two the product is exact and none needs it; where 1 / s could leave the
-// normal range all divide. Measured at 32768 tokens of 8 heads: see
-// kv8_write_kernel.
-__device__ __forceinline__ void encode16(const float (&x)[2][8], float s, uint32_t (&c)[2][4])
+// E4M3(x / s) of 16 values, the quotient rounded to fp32 first. A division of
+// every value would be most of the call's arithmetic; here it is q = x r with
+// r = 1 / s correctly rounded, then q + (q s - x) (-r) by two fused multiply-adds,
+// which is the correctly rounded quotient where nothing under- or overflows
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990). With 2^-60 <= s < 2^60 and finite values below 2^60 s that
+// holds for every quotient above 2^-11, and smaller ones have the code 0 either
+// way; other rows divide. The residual is taken with that sign so that a zero
+// keeps its own: q s - x is +0 for x = -0, and +0 (-r) + (-0) is -0.
+__device__ __forceinline__ void encode16(const uint4 (&raw)[2], float top, float s, uint2 (&c)[2])
 {
-    const uint32_t sb = __float_as_uint(s);
-    const bool plain = sb - 0x04000000u < 0x78000000u;   // 2^-119 <= s < 2^121
-    const bool power = (sb & 0x7FFFFFu) == 0;
-    const float r = __fdiv_rn(1.0f, s);
-    uint32_t nearest = 0x7FFFFu;
+    const float r = __frcp_rn(s);
+    const bool plain = s >= 8.6736174e-19f && s < 1.1529215e18f && top < s * 1.1529215e18f;
+    const F2 r2(-r, -r), s2(s, s);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t e[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float lo = x[i][2 * j] * r, hi = x[i][2 * j + 1] * r;
-            nearest = min(nearest, (__float_as_uint(lo) + 4u) & 0x7FFFFu);
-            nearest = min(nearest, (__float_as_uint(hi) + 4u) & 0x7FFFFu);
-            c[i][j] = cvt_e4m3x2(hi, lo);
+            const float lo = __uint_as_float(u[j] << 16), hi = __uint_as_float(u[j] & 0xFFFF0000u);
+            if (plain) {
+                const F2 x(-lo, -hi), q = mul2(x, r2);
+                const F2 t = fma2(fma2(q, s2, x), r2, q);
+                e[j] = cvt_e4m3x2(t.hi(), t.lo());
+            } else {
+                e[j] = cvt_e4m3x2(__fdiv_rn(hi, s), __fdiv_rn(lo, s));
+            }
         }
-    if (!plain || (nearest <= 8u && !power)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                c[i][j] = cvt_e4m3x2(__fdiv_rn(x[i][2 * j + 1], s), __fdiv_rn(x[i][2 * j], s));
+        c[i] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
     }
+}
+
+// The largest magnitude of 16 bf16 values, as bits: not finite from 0x7F80 on.
+__device__ __forceinline__ uint32_t top16(const uint4 (&raw)[2])
+{
+    constexpr uint32_t m = 0x7FFF7FFFu;
+    const uint32_t a = __vmaxu2(__vmaxu2(raw[0].x & m, raw[0].y & m), __vmaxu2(raw[0].z & m, raw[0].w & m));
+    const uint32_t b = __vmaxu2(__vmaxu2(raw[1].x & m, raw[1].y & m), __vmaxu2(raw[1].z & m, raw[1].w & m));
+    const uint32_t t = __vmaxu2(a, b);
+    return max(t >> 16, t & 0xFFFFu);
+}
+// The same over the finite ones.
+__device__ __forceinline__ uint32_t top16_finite(const uint4 (&raw)[2])
+{
+    uint32_t top = 0;
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t m = (u[j >> 1] >> (j & 1 ? 16 : 0)) & 0x7FFFu;
+            top = m < 0x7F80u ? max(top, m) : top;
+        }
+    }
+    return top;
+}
+// Over the lanes of a row.
+template <int L>
+__device__ __forceinline__ uint32_t row_top(uint32_t top)
+{
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    return top;
 }
 
 }  // namespace
@@ -107,42 +139,31 @@ __global__ void __launch_bounds__(kRowThreads) kv8_write_kernel(const __grid_con
     const int64_t at = ok ? cache_row(a, r.slot, r.h) : 0;
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-        float x[2][8];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t u[4] = {raw[y][i].x, raw[y][i].y, raw[y][i].z, raw[y][i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[i][2 * j] = __uint_as_float(u[j] << 16);
-                x[i][2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-            }
-        }
-        float s;
         float* scale = y ? v_scale : k_scale;
+        uint32_t top = top16(raw[y]);
+        float s;
         if (a.per_token) {
-            float amax = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float m = fabsf(x[i][j]);
-                    amax = m < __int_as_float(0x7F800000) ? fmaxf(amax, m) : amax;
-                }
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            s = fmaxf(__fdiv_rn(amax, 448.0f), a.min_scale);
+            top = row_top<L>(top);
+            uint32_t finite = top;
+            if (__any_sync(0xFFFFFFFFu, top >= 0x7F80u))
+                finite = row_top<L>(top16_finite(raw[y]));
+            // s = the row's largest / 448: its product with 1 / 448 kept in two
+            // parts rounds like the quotient (compared for every bf16 value)
+            const float amax = __uint_as_float(finite << 16);
+            s = fmaf(amax, kInv448Hi, amax * kInv448Lo);
+            if (finite < 0x1800u)   // below 2^-79 the second part may be no normal number
+                s = __fdiv_rn(amax, 448.0f);
+            s = fmaxf(s, a.min_scale);
             s = s == 0.0f ? 1.0f : s;
         } else {
             s = ok ? __ldg(scale + r.h) : 1.0f;
         }
         if (ok) {
-            uint32_t c[2][4];
-            encode16(x, s, c);
+            uint2 c[2];
+            encode16(raw[y], __uint_as_float(top << 16), s, c);
             uint2* dst = reinterpret_cast<uint2*>((y ? v_cache : k_cache) + at * D);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                dst[i * L + lane] = make_uint2(c[i][0] | (c[i][1] << 16), c[i][2] | (c[i][3] << 16));
+            dst[lane] = c[0];
+            dst[L + lane] = c[1];
             if (a.per_token && lane == 0)
                 scale[at] = s;
         }

@@ -25,7 +25,6 @@ namespace {
 constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
 constexpr int kStages = 3;   // units in flight per warp
 constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
-constexpr float kLog2e = 1.4426950408889634f;
 // The reference exponent of a row is raised only when a score passes it by
 // this much: 2^{x - m} then stays below 2^8, far inside f16, and the row's
 // accumulators are hardly ever rescaled. With per-token scales the f16 operand
@@ -33,18 +32,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 // m then carries the values' size too, and drops out of o / l.
 constexpr float kSlack = 8.0f;
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 // D[16x8] += A[16x16] B[16x8], f16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1)
@@ -52,18 +39,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t at)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t at)
 {

@@ -35,7 +35,6 @@ constexpr int kStages = 3;        // f16 operand tiles, K and V in turn
 constexpr int kRaw = 7;           // raw slots
 constexpr int kPairs = 3;         // pairs of converter warps
 constexpr int kScaleRing = 4;     // tiles whose per-token scales are held
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;    // see kv8_attn.cu
 
 template <int D>
@@ -149,21 +148,9 @@ __device__ __forceinline__ void ld_wait32(uint32_t (&r)[32])
                  :
                  : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t at)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
 }
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes)
 {
@@ -180,12 +167,6 @@ __device__ __forceinline__ void regs_dec()
 {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ float rcp(float x)
 {
     float r;
@@ -198,39 +179,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// Two fp32 operations in one instruction.
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
-    __device__ __forceinline__ explicit F2(uint64_t x) : v(x) {}
-    __device__ __forceinline__ float lo() const { return __uint_as_float(static_cast<uint32_t>(v)); }
-    __device__ __forceinline__ float hi() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-};
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return F2(r);
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-    return F2(r);
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-    return F2(r);
-}
-
 template <bool B>
 struct Const {
     static constexpr bool value = B;

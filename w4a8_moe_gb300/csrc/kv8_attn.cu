@@ -25,12 +25,13 @@ namespace {
 constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
 constexpr int kStages = 3;   // units in flight per warp
 constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
-// The reference exponent of a row is raised only when a score passes it by
-// this much: 2^{x - m} then stays below 2^8, far inside f16, and the row's
-// accumulators are hardly ever rescaled. With per-token scales the f16 operand
-// is 2^{x - m} * vs, so what is compared is x + log2(the largest vs at hand):
-// m then carries the values' size too, and drops out of o / l.
-constexpr float kSlack = 8.0f;
+// A row's reference exponent is raised only when a weight passes 2^8 under it:
+// weights then stay far inside f16 and the row's accumulators are hardly ever
+// rescaled. With per-token scales what is compared, and what goes into f16, is
+// the weight times its value's scale: the reference then carries the values'
+// size too, and drops out of o / l.
+constexpr float kMostWeight = 256.0f;
+constexpr float kLowest = -1e30f;   // the reference of a row without keys
 
 // D[16x8] += A[16x16] B[16x8], f16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -39,6 +40,20 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Thread (g, c) of an 8 x 8 matrix of f16 holds row g, columns 2c and 2c + 1:
+// the same of its transpose.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ float lds32(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t at)
 {
@@ -85,7 +100,12 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
     return l;
 }
 __device__ __forceinline__ int64_t warp_begin(const Line& l, int w) { return l.U * w / l.n; }
-__device__ __forceinline__ int warp_of(const Line& l, int64_t u) { return static_cast<int>(((u + 1) * l.n - 1) / l.U); }
+__device__ __forceinline__ int warp_of(const Line& l, int64_t u)
+{
+    if (l.U < 1 << 20)   // n < 2^12: no 64-bit division
+        return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(l.n) - 1) / static_cast<uint32_t>(l.U));
+    return static_cast<int>(((u + 1) * l.n - 1) / l.U);
+}
 
 // A unit as its warp meets it, found by one lane for each of 32 units ahead.
 struct __align__(16) Unit {
@@ -162,11 +182,14 @@ int kv8_attn_row_tile(int group) { return group <= 8 ? 8 : 16; }
 
 // Every warp walks its own units, with a ring of bulk copies kStages units
 // ahead (across piece boundaries), and stores a piece's result from registers.
-// Fragments come straight from the linear copies: which d a fragment register
-// stands for is free as long as q and o use the same order, so every thread
-// reads contiguous bytes. For S = Q K^T a thread holds key g of each n-tile and
-// chunks c of its D values; for O^T = V^T P^T keys 2c, 2c+1, 2c+8, 2c+9 and
-// chunk g of their D values; P^T then needs no exchange between lanes.
+// Both products have the rows as their N: S^T = K Q^T with 16 keys as M and
+// O^T = V^T P^T with D as M, so no MMA row is idle for groups of 8. Fragments
+// come straight from the linear copies: which d a fragment register stands for
+// is free as long as q and o use the same order, so every thread reads
+// contiguous bytes: of K keys g and g + 8, chunks c of their D values; of V keys
+// 2c, 2c+1, 2c+8, 2c+9, chunk g. P^T passes from the first product's layout to
+// the second's by an 8 x 8 transpose. A thread's rows are 2c and 2c + 1 in both,
+// so the running statistics need no exchange.
 template <int D, int NT, bool TOK>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(const __grid_constant__ Kv8Attn a)
 {
@@ -178,6 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
     __shared__ int warp_sum[kWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    grid_dep_launch();   // the join reads the lengths only until this kernel has ended
 
     // prefix sums of the sequences' units
     int carry = 0;
@@ -250,8 +274,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
     for (int i = 0; i < kStages; ++i)
         issue(i);
 
-    uint32_t qa[KS][2 * NT];
-    float qs[NT], o[KS][NT][4], m[NT], l[NT];
+    uint32_t qb[KS][NT][2];
+    float qs[NT][2], o[KS][NT][4], m[NT][2], l[NT][2];
     int rows = 0, h = 0;
     bool fresh = true;
     for (int i = 0; i < units; ++i) {
@@ -310,17 +334,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
                 float f = ldexpf(a.sm_scale, e);
                 if (!TOK)
                     f *= __ldg(a.k_scale + h);
-                qs[t] = a.cap > 0.0f ? f / a.cap : f * kLog2e;
+                f = a.cap > 0.0f ? f / a.cap * (2.0f * kLog2e) : f * kLog2e;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {   // of the rows 2c, 2c + 1
+                    qs[t][y] = __shfl_sync(0xFFFFFFFFu, f, c * 8 + y * 4);
+                    m[t][y] = kLowest;
+                    l[t][y] = 0.0f;
+                }
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {   // 8 values: two k-steps' two registers each
                     const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        qa[2 * j + (k >> 1)][(k & 1) * NT + t] =
+                        qb[2 * j + (k >> 1)][t][k & 1] =
                             pack_f16(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
                 }
-                m[t] = -INFINITY;
-                l[t] = 0.0f;
             }
 #pragma unroll
             for (int j = 0; j < KS; ++j)
@@ -342,7 +370,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
         }
         uint4 xk[2][D / 64];
         uint32_t xv[4][D / 32];
-        float ks[4], vs[4];   // scales of keys 2c, 2c+1, 2c+8, 2c+9
+        float ks[2], vs[2];   // scales of keys g, g + 8
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -361,113 +389,135 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
         }
         if (TOK) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint2 w = lds64(at + 2 * S::kCodes + (k * 8 + c * 2) * 4);
-                const uint2 z = lds64(at + 2 * S::kCodes + (kKv8Unit + k * 8 + c * 2) * 4);
-                ks[2 * k] = __uint_as_float(w.x), ks[2 * k + 1] = __uint_as_float(w.y);
-                vs[2 * k] = __uint_as_float(z.x), vs[2 * k + 1] = __uint_as_float(z.y);
+            for (int x = 0; x < 2; ++x) {
+                ks[x] = lds32(at + 2 * S::kCodes + (x * 8 + g) * 4);
+                vs[x] = lds32(at + 2 * S::kCodes + (kKv8Unit + x * 8 + g) * 4);
             }
         }
         if (live < kKv8Unit) {   // what lies behind the last key may be no number
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 4; ++k)
                 if (c * 2 + (k & 1) + (k >> 1) * 8 >= live) {
 #pragma unroll
                     for (int w = 0; w < D / 32; ++w)
                         xv[k][w] = 0;
-                    if (TOK)
-                        ks[k] = 0.0f, vs[k] = 0.0f;
                 }
-            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (TOK && x * 8 + g >= live)
+                    ks[x] = 0.0f, vs[x] = 0.0f;
         }
         __syncwarp();
         issue(i + kStages);
 
-        // ---- S = Q K^T
-        float s[2][4];
+        // ---- S^T = K Q^T: s[t][2 x + y] is key g + 8 x, row 8 t + 2c + y
+        float s[NT][4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 s[t][k] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const uint32_t w[4] = {xk[t][j].x, xk[t][j].y, xk[t][j].z, xk[t][j].w};
+        for (int j = 0; j < D / 64; ++j) {
+            const uint32_t w0[4] = {xk[0][j].x, xk[0][j].y, xk[0][j].z, xk[0][j].w};
+            const uint32_t w1[4] = {xk[1][j].x, xk[1][j].y, xk[1][j].z, xk[1][j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x4(w0[k], a0, a2);
+                e4m3x4_to_f16x4(w1[k], a1, a3);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    mma_f16(s[t], a0, a1, a2, a3, qb[j * 4 + k][t][0], qb[j * 4 + k][t][1]);
+            }
+        }
+        // ---- scores in log2 units (cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y})),
+        // qs holding 2 log2(e) / cap); keys past the end are -inf
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[t][k] *= qs[t][k & 1];
+                if (TOK)
+                    s[t][k] *= ks[k >> 1];
+            }
+        if (a.cap > 0.0f) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[t][k] = fmaf(-2.0f * kLog2e * a.cap, rcp(1.0f + ex2(s[t][k])), kLog2e * a.cap);
+        }
+        if (live < kKv8Unit) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[t][k] = (k >> 1) * 8 + g < live ? s[t][k] : -INFINITY;
+        }
+        // ---- weights under the reference as it stands; where one would come
+        // near f16's end the reference is raised and they are taken again
+        float p[NT][4];
+        auto weigh = [&]() {
+            float top = 0.0f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t b0 = e4m3x2_to_f16x2(w[k] & 0xFFFFu), b1 = e4m3x2_to_f16x2(w[k] >> 16);
-                    const uint32_t* qf = qa[j * 4 + k];
-                    mma_f16(s[t], qf[0], NT == 2 ? qf[1] : 0u, qf[NT], NT == 2 ? qf[2 * NT - 1] : 0u, b0, b1);
+                    p[t][k] = ex2(s[t][k] - m[t][k & 1]);
+                    // (the second bound holds a weight in range where its value's scale is 0)
+                    top = fmaxf(top, TOK ? p[t][k] * fmaxf(fabsf(vs[k >> 1]), 0x1p-92f) : p[t][k]);
                 }
+            return top;
+        };
+        if (__any_sync(0xFFFFFFFFu, weigh() > kMostWeight)) {
+            float lift = 0.0f;   // log2 of the unit's largest value scale
+            if (TOK) {
+                lift = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1)
+                    lift = fmaxf(lift, __shfl_xor_sync(0xFFFFFFFFu, lift, x));
+                lift = fmaxf(log2f(lift), -100.0f);
             }
-        }
-        // ---- scores in log2 units; keys past the end are -inf
-        float lift = 0.0f;   // log2 of the unit's largest value scale
-        if (TOK) {
-            float top = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            lift = fmaxf(log2f(top), -100.0f);
-        }
-        bool grow = false;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < 2 * NT; ++k) {
-                float f = s[t][k] * qs[k >> 1];
-                if (TOK)
-                    f *= ks[t * 2 + (k & 1)];
-                if (a.cap > 0.0f) {   // tanh y = 1 - 2 / (1 + e^{2y})
-                    const float e = ex2(f * (2.0f * kLog2e));
-                    f = e > 1e30f ? a.cap * kLog2e : (a.cap * kLog2e) * (1.0f - __fdividef(2.0f, 1.0f + e));
+                for (int y = 0; y < 2; ++y) {
+                    float top = fmaxf(s[t][y], s[t][2 + y]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+                    const float to = fmaxf(m[t][y], top + lift);
+                    const float f = ex2(m[t][y] - to);
+                    m[t][y] = to;
+                    l[t][y] *= f;
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) {
+                        o[j][t][y] *= f;
+                        o[j][t][2 + y] *= f;
+                    }
                 }
-                f = t * 8 + c * 2 + (k & 1) < live ? f : -INFINITY;
-                s[t][k] = f;
-                grow = grow || f + lift > m[k >> 1] + kSlack;
-            }
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float top = fmaxf(fmaxf(s[0][2 * t], s[0][2 * t + 1]), fmaxf(s[1][2 * t], s[1][2 * t + 1]));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2)) + lift;
-                const float to = fmaxf(m[t], top);
-                const float f = to == -INFINITY ? 1.0f : ex2(m[t] - to);
-                m[t] = to;
-                l[t] *= f;
-                const float f0 = __shfl_sync(0xFFFFFFFFu, f, c * 8);
-                const float f1 = __shfl_sync(0xFFFFFFFFu, f, c * 8 + 4);
-#pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    o[j][t][0] *= f0, o[j][t][1] *= f1;
-                    o[j][t][2] *= f0, o[j][t][3] *= f1;
-                }
-            }
+            weigh();
         }
         // ---- P^T and O^T += V^T P^T
         uint32_t pb[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const float ref = m[t] == -INFINITY ? 0.0f : m[t];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float p0 = ex2(s[k][2 * t] - ref), p1 = ex2(s[k][2 * t + 1] - ref);
-                l[t] += p0 + p1;
-                if (TOK) {
-                    p0 *= vs[2 * k];
-                    p1 *= vs[2 * k + 1];
-                }
-                pb[t][k] = pack_f16(p0, p1);
+            for (int x = 0; x < 2; ++x) {
+                l[t][0] += p[t][2 * x];
+                l[t][1] += p[t][2 * x + 1];
+                pb[t][x] = transpose8(TOK ? pack_f16(p[t][2 * x] * vs[x], p[t][2 * x + 1] * vs[x])
+                                          : pack_f16(p[t][2 * x], p[t][2 * x + 1]));
             }
-        }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint32_t sel = half ? 0x7362u : 0x5140u;
-                const uint32_t lo = prmt(xv[0][w], xv[1][w], sel), hi = prmt(xv[2][w], xv[3][w], sel);
-                const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xFFFFu), a1 = e4m3x2_to_f16x2(lo >> 16);
-                const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xFFFFu), a3 = e4m3x2_to_f16x2(hi >> 16);
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x4(prmt(xv[0][w], xv[1][w], sel), a0, a1);
+                e4m3x4_to_f16x4(prmt(xv[2][w], xv[3][w], sel), a2, a3);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     mma_f16(o[w * 2 + half][t], a0, a1, a2, a3, pb[t][0], pb[t][1]);
@@ -479,10 +529,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
             const int64_t slot = static_cast<int64_t>(pair) + me;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 1);
-                l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 2);
-                if (c == 0 && t * 8 + g < rows)
-                    a.part_ml[slot * R + t * 8 + g] = make_float2(m[t], l[t]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        l[t][y] += __shfl_xor_sync(0xFFFFFFFFu, l[t][y], x);
+                    if (g == 0 && t * 8 + c * 2 + y < rows)
+                        a.part_ml[slot * R + t * 8 + c * 2 + y] = make_float2(m[t][y], l[t][y]);
+                }
                 float* dst = a.part_o + (slot * R + t * 8 + c * 2) * D + g * (D / 8);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
@@ -497,14 +551,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
             fresh = true;
         }
     }
-    grid_dep_wait();     // the join after this kernel also reads what the one before it wrote
-    grid_dep_launch();
+    grid_dep_wait();   // the join after this kernel also reads what the one before it wrote
 }
 
 // Adds up the pieces of a (sequence, query head): W warps take them in turn, a
 // lane D / 32 values. W is 4 where there are few rows (each may have many
 // pieces and latency counts), 1 where the rows themselves fill the GPU.
 constexpr int kJoinWarps = 4;
+constexpr int kJoinSums = 128;   // sequences up to which a warp sums their units itself
 template <int D, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
                                                                    const __grid_constant__ Kv8Prefix p, int R)
@@ -513,19 +567,40 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int head = blockIdx.x * (kJoinWarps / W) + warp / W;   // b * Hq + query head
     const int first_piece = warp % W;
-    grid_dep_wait();
-    if (W == 1 && head >= a.B * a.Hq)
-        return;
     const int b = head / a.Hq, qh = head % a.Hq, h = qh / a.group, gi = qh % a.group;
+    // units before the sequence's and all of them: a short sum over the lengths
+    // while the kernel before is still at work, else what it left
+    const bool sum_here = a.B <= kJoinSums;
+    int before = 0, units = 0, all = 0;
+    if (sum_here) {
+        for (int i = lane; i < a.B; i += 32) {
+            const int n = seq_units(a, i);
+            all += n;
+            before += i < b ? n : 0;
+            units += i == b ? n : 0;
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) {
+            all += __shfl_xor_sync(0xFFFFFFFFu, all, x);
+            before += __shfl_xor_sync(0xFFFFFFFFu, before, x);
+            units += __shfl_xor_sync(0xFFFFFFFFu, units, x);
+        }
+    }
+    if (!sum_here) {
+        grid_dep_wait();
+        if (a.max_pages && head < a.B * a.Hq) {
+            before = a.cum[b];
+            units = a.cum[b + 1] - before;
+            all = a.cum[a.B];
+        }
+    }
+    const Line line = make_line(a, all);
 
     // the row's pieces: [0, n0) of the tiled prefix, [n0, n1) of the untiled one, [n1, n2) of its own keys
     const int row = b * a.group + gi;
     const int n0 = p.splits;
     int n1 = n0, n2;
     int64_t at_pre = 0, at_own = 0;   // the first piece's row, minus its number times R
-    const bool pieces = a.max_pages || a.ptiles;
-    const int before = pieces ? a.cum[b] : 0, units = pieces ? a.cum[b + 1] - before : 0;
-    const Line line = make_line(a, pieces ? a.cum[a.B] : 0);
     if (a.ptiles) {
         const int pair = h * a.ptiles + row / R;
         const int64_t first = static_cast<int64_t>(pair) * line.up;
@@ -541,6 +616,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_
         n2 += warp_of(line, first + units - 1) - w + 1;
         at_own = static_cast<int64_t>(line.pairs_p + b * line.hr + j + w - n1) * R + gi % R;
     }
+    if (sum_here)
+        grid_dep_wait();
+    if (W == 1 && head >= a.B * a.Hq)
+        return;
     float top = -INFINITY, sum = 0.0f, acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -597,7 +676,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_
                 acc[i] += so[w][lane * V + i] * f;
         }
     }
-    const bool empty = top == -INFINITY && sum == 0.0f;
+    const bool empty = sum == 0.0f;
     uint32_t r[V / 2];
 #pragma unroll
     for (int i = 0; i < V / 2; ++i)
@@ -647,7 +726,11 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
     Kv8Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
-    a.warps = num_sms * min(R == 8 ? 4 : 3, fit) * kWarps;
+    // A CTA of the tiled prefix takes a whole SM. Where those leave most SMs free
+    // the units go to the free ones, which then all end together.
+    const int taken = p.splits * a.Hkv * p.row_pairs;
+    const int sms = 2 * taken <= num_sms ? num_sms - taken : num_sms;
+    a.warps = sms * min(R == 8 ? 4 : 3, fit) * kWarps;
     a.warps = a.warps < kKv8MaxWarps ? a.warps : kKv8MaxWarps;
     cudaError_t e;
     if (p.splits) {

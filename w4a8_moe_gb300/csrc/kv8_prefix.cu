@@ -167,12 +167,6 @@ __device__ __forceinline__ void regs_dec()
 {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ float rcp(float x)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -527,10 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
                     uint32_t f[8];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        f[2 * y] = e4m3x2_to_f16x2(u[y] & 0xFFFFu);
-                        f[2 * y + 1] = e4m3x2_to_f16x2(u[y] >> 16);
-                    }
+                    for (int y = 0; y < 4; ++y)
+                        e4m3x4_to_f16x4(u[y], f[2 * y], f[2 * y + 1]);
                     const uint32_t at = dst + (c16 >> 2) * L::kPanel + key * 128;
                     const int ch = (c16 & 3) * 2;
                     sts128(at + ((ch ^ (key & 7)) << 4), f[0], f[1], f[2], f[3]);

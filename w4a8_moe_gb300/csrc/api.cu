@@ -249,15 +249,15 @@ struct Kv8Ws {
     int tiles, ptiles;
     Kv8Prefix prefix;   // splits 0: the prefix is not tiled
 };
-static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, Kv8Ws* w, void* ws)
+static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, Kv8Ws* w, void* ws)
 {
     Carver c(ws);
     const int group = Hq / Hkv, R = kv8_attn_row_tile(group);
     w->tiles = (group + R - 1) / R;
     w->prefix = {};
-    const bool tiled = prefix_len && kv8_prefix_tiled(B * group);
+    const bool tiled = prefix_len && kv8_prefix_tiled(Hkv, B * group, prefix_len);
     if (tiled)
-        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len);
+        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len, max_pages > 0 ? B * Hkv : 0);
     w->ptiles = prefix_len && !tiled ? (B * group + R - 1) / R : 0;
     const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxWarps;
     w->part_o = c.take<float>(slots * R * D * 4);
@@ -734,7 +734,7 @@ size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int pr
     if (!kv8_attn_ok(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
         return 0;
     Kv8Ws w;
-    return kv8_ws(B, Hq, Hkv, D, prefix_len, &w, nullptr);
+    return kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, &w, nullptr);
 }
 
 int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq, int Hkv, int D,
@@ -765,7 +765,7 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
     if (int st = current_device(&sms))
         return st;
     Kv8Ws w;
-    kv8_ws(B, Hq, Hkv, D, prefix_len, &w, ws);
+    kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, &w, ws);
     Kv8Attn a = {};
     a.q = q_bf16, a.q_stride = q_stride;
     a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;

@@ -52,7 +52,9 @@ struct Kv8Attn {
     uint32_t* err;
     uint16_t* out;
     float* lse;
-    int warps;
+    int warps;          // that the units go to, and how many units at most to how many of them
+    int free_warps;     // instead, while the tiled prefix holds the other SMs
+    int64_t free_units;
     int* cum;           // [B + 1] prefix sums of the sequences' units, left for the join
 };
 // The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key
@@ -66,9 +68,9 @@ struct Kv8Prefix {
     float* part_o;
     float2* part_ml;
 };
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len);
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int own_pairs);
 cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s);
-bool kv8_prefix_tiled(int rows);
+bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);
 int kv8_attn_row_tile(int group);
 cudaError_t launch_kv8_attn(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s);
 

@@ -96,7 +96,8 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
     l.own = static_cast<int64_t>(l.pairs_p) * l.up;
     l.U = l.own + seq_total * l.hr;
     const int64_t n = (l.U + kKv8MinUnits - 1) / kKv8MinUnits;
-    l.n = static_cast<int>(n < a.warps ? n : a.warps);
+    const int most = l.U <= a.free_units ? a.free_warps : a.warps;
+    l.n = static_cast<int>(n < most ? n : most);
     return l;
 }
 __device__ __forceinline__ int64_t warp_begin(const Line& l, int w) { return l.U * w / l.n; }
@@ -244,7 +245,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
     __syncthreads();
 
     const Line line = make_line(a, carry);
-    const int me = warp * gridDim.x + blockIdx.x;   // few units: one warp on each SM before a second
+    // few units: one warp on each SM before a second, or, while the tiled prefix
+    // holds most SMs, whole CTAs, which the free SMs take at once
+    const int me = 2 * a.free_warps < a.warps ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
     const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
     const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
     Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
@@ -555,17 +558,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
 }
 
 // Adds up the pieces of a (sequence, query head): W warps take them in turn, a
-// lane D / 32 values. W is 4 where there are few rows (each may have many
-// pieces and latency counts), 1 where the rows themselves fill the GPU.
-constexpr int kJoinWarps = 4;
+// lane D / 32 values. The fewer rows, the more warps take one: with few rows
+// each has many pieces, and only their number hides the loads' latency.
+constexpr int kJoinCta = 4;      // warps of a CTA where W < 4
 constexpr int kJoinSums = 128;   // sequences up to which a warp sums their units itself
 template <int D, int W>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
+__global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
                                                                    const __grid_constant__ Kv8Prefix p, int R)
 {
     constexpr int V = D / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int head = blockIdx.x * (kJoinWarps / W) + warp / W;   // b * Hq + query head
+    const int head = W >= kJoinCta ? blockIdx.x : blockIdx.x * (kJoinCta / W) + warp / W;   // b * Hq + query head
     const int first_piece = warp % W;
     const int b = head / a.Hq, qh = head % a.Hq, h = qh / a.group, gi = qh % a.group;
     // units before the sequence's and all of them: a short sum over the lengths
@@ -712,26 +715,41 @@ template <int D>
 static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
 {
     const int heads = a.B * a.Hq;
-    if (heads <= num_sms * 8)
-        return launch_dependent(kv8_join_kernel<D, kJoinWarps>, dim3(heads), dim3(kJoinWarps * 32), 0, s, a, p, R);
-    return launch_dependent(kv8_join_kernel<D, 1>, dim3((heads + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0,
-                            s, a, p, R);
+    if (heads <= num_sms * 4)
+        return launch_dependent(kv8_join_kernel<D, 8>, dim3(heads), dim3(8 * 32), 0, s, a, p, R);
+    if (heads <= num_sms * (p.splits >= 8 ? 32 : 8))
+        return launch_dependent(kv8_join_kernel<D, 4>, dim3(heads), dim3(4 * 32), 0, s, a, p, R);
+    return launch_dependent(kv8_join_kernel<D, 1>, dim3((heads + kJoinCta - 1) / kJoinCta), dim3(kJoinCta * 32), 0, s, a,
+                            p, R);
 }
 
-// Rows of the batch over the prefix from which the tensor-core kernel takes it.
-bool kv8_prefix_tiled(int rows) { return rows > 16; }
+// Whether the tensor-core kernel takes the prefix. It costs a third launch and
+// whole SMs; without it every 8 rows read the prefix again, from L2, at the cost
+// of a unit of a sequence's own keys. 48 query and 8 kv heads, 16 sequences of up
+// to 64 own keys, us without / with: 512 prefix tokens (3072 such units) 13.3 /
+// 13.8, 1024 15.5 / 13.9, 2048 22.6 / 14.5; one sequence of 48 query heads (6 rows)
+// 16384 tokens (8192 units) 21.7 / 19.0, 65536 47.6 / 50.8.
+bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len)
+{
+    const int64_t units = static_cast<int64_t>(Hkv) * ((rows + 7) / 8) * ((prefix_len + kKv8Unit - 1) / kKv8Unit);
+    return units > 3072;
+}
 
 cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s)
 {
     Kv8Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
-    // A CTA of the tiled prefix takes a whole SM. Where those leave most SMs free
-    // the units go to the free ones, which then all end together.
+    const int per_sm = min(R == 8 ? 4 : 3, fit) * kWarps;
+    a.warps = num_sms * per_sm;
+    // A CTA of the tiled prefix takes a whole SM. The units go to the SMs that
+    // those leave, so that they need not wait for the prefix, where they are most
+    // SMs or the units are few (16 a warp at most, some 6 us).
     const int taken = p.splits * a.Hkv * p.row_pairs;
-    const int sms = 2 * taken <= num_sms ? num_sms - taken : num_sms;
-    a.warps = sms * min(R == 8 ? 4 : 3, fit) * kWarps;
-    a.warps = a.warps < kKv8MaxWarps ? a.warps : kKv8MaxWarps;
+    a.free_warps = max(num_sms - taken, 0) * per_sm;
+    a.free_units = 2 * taken <= num_sms ? INT64_MAX : static_cast<int64_t>(a.free_warps) * 16;
+    a.warps = min(a.warps, kKv8MaxWarps);
+    a.free_warps = min(a.free_warps, kKv8MaxWarps);
     cudaError_t e;
     if (p.splits) {
         e = launch_kv8_prefix(a, p, D, per_token, s);

@@ -673,20 +673,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     }
 }
 
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len)
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int own_pairs)
 {
     Kv8Prefix p = {};
     p.tiles = (prefix_len + kTile - 1) / kTile;
     p.row_pairs = (rows + 2 * kTile - 1) / (2 * kTile);
     // Time in key tiles: waves of CTAs, each its tiles plus about three tiles'
-    // worth of start and end, plus the join's reading of every split.
+    // worth of start and end, plus the join's reading of every split. With most
+    // SMs taken and more (sequence, kv head) pairs than the others hold, pairs
+    // wait for the prefix: about four tiles' worth. 48 query heads, 4096 tokens, us
+    // with 128 / 64 CTAs: 32 sequences 24.4 / 20.8, 16 sequences 16.4 / 17.4.
     const int64_t base = static_cast<int64_t>(Hkv) * p.row_pairs;
     int64_t best = INT64_MAX;
     for (int s = 1; s <= p.tiles && s <= kKv8MaxSplits; ++s) {
         const int per = (p.tiles + s - 1) / s;
         const int splits = (p.tiles + per - 1) / per;
         const int64_t waves = (base * splits + kKv8PrefixCtas - 1) / kKv8PrefixCtas;
-        const int64_t cost = waves * (per + 3) * 8 + splits;
+        const int64_t taken = base * splits;
+        const int64_t late = 2 * taken > kKv8PrefixCtas && own_pairs > (kKv8PrefixCtas - taken) * 8 ? 4 : 0;
+        const int64_t cost = (waves * (per + 3) + late) * 8 + splits;
         if (cost < best) {
             best = cost;
             p.splits = splits;

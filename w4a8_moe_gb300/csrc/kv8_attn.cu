@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
     const Line line = make_line(a, carry);
     // few units: one warp on each SM before a second, or, while the tiled prefix
     // holds most SMs, whole CTAs, which the free SMs take at once
-    const int me = 2 * a.free_warps < a.warps ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
+    const int me = a.free_units ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
     const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
     const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
     Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
@@ -743,11 +743,15 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
     const int per_sm = min(R == 8 ? 4 : 3, fit) * kWarps;
     a.warps = num_sms * per_sm;
     // A CTA of the tiled prefix takes a whole SM. The units go to the SMs that
-    // those leave, so that they need not wait for the prefix, where they are most
-    // SMs or the units are few (16 a warp at most, some 6 us).
+    // those leave, so that they need not wait for the prefix: all units where
+    // these are most SMs, else only few units (16 a warp, some 6 us).
     const int taken = p.splits * a.Hkv * p.row_pairs;
     a.free_warps = max(num_sms - taken, 0) * per_sm;
-    a.free_units = 2 * taken <= num_sms ? INT64_MAX : static_cast<int64_t>(a.free_warps) * 16;
+    a.free_units = static_cast<int64_t>(a.free_warps) * 16;
+    if (2 * taken <= num_sms) {
+        a.warps = a.free_warps;
+        a.free_units = 0;
+    }
     a.warps = min(a.warps, kKv8MaxWarps);
     a.free_warps = min(a.free_warps, kKv8MaxWarps);
     cudaError_t e;

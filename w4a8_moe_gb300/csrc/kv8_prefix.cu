@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     bulk_store(pl.part_o + at * D, mine, D * 4);
                     bulk_commit_group();
                     pl.part_ml[at] = make_float2(m, (l0.lo() + l0.hi()) + (l1.lo() + l1.hi()));
-                    bulk_wait_all();
+                    bulk_wait_read_all();
                 }
                 tc_fence_before();
             }

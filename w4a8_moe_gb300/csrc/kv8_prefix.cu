@@ -56,7 +56,8 @@ enum Bar {
     kEmpty = kFull + kStages,        // [kStages]
     kSFull = kEmpty + kStages,       // [2] row tiles
     kPFull = kSFull + 2,             // [2]
-    kOFull = kPFull + 2,             // [2]
+    kPHalf = kPFull + 2,             // [2]
+    kOFull = kPHalf + 2,             // [2]
     kScFull = kOFull + 2,            // [kScaleRing]
     kQRaw = kScFull + kScaleRing,    // [2]
     kQFull = kQRaw + 2,              // [2]
@@ -426,6 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                         }
                     }
                     tmem_st16(ts + ch * 16, p);
+                    if (ch == 1) {   // O can take the first half of the keys
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar(kPHalf + t));
+                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -638,14 +646,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             const uint32_t v = v_lo + (jv % kStages) * kStep;
             ok = wait_warp(kFull + jv % kStages, (jv / kStages) & 1);
             for (int t = 0; t < nt && ok; ++t) {
-                ok = wait_warp(kPFull + t, i & 1);
-                if (!ok)
-                    break;
-                tc_fence_after();
                 const uint32_t to = tmem + 2 * kTile + t * D, tp = tmem + t * kTile;
 #pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    mma_ts(leader, to, tp + s * 8, v + s * (2048 >> 4), kDescHi, kIdO, s > 0 || i > 0);
+                for (int half = 0; half < 2; ++half) {
+                    ok = ok && wait_warp((half ? kPFull : kPHalf) + t, i & 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = half * 4; s < half * 4 + 4; ++s)
+                        mma_ts(leader, to, tp + s * 8, v + s * (2048 >> 4), kDescHi, kIdO, s > 0 || i > 0);
+                }
+                if (!ok)
+                    break;
                 if (t == nt - 1)
                     commit(leader, bar(kEmpty + jv % kStages));
                 if (i + 1 == n) {

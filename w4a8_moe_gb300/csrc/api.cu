@@ -249,7 +249,8 @@ struct Kv8Ws {
     int tiles, ptiles;
     Kv8Prefix prefix;   // splits 0: the prefix is not tiled
 };
-static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, Kv8Ws* w, void* ws)
+static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size, Kv8Ws* w,
+                     void* ws)
 {
     Carver c(ws);
     const int group = Hq / Hkv, R = kv8_attn_row_tile(group);
@@ -257,13 +258,14 @@ static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_page
     w->prefix = {};
     const bool tiled = prefix_len && kv8_prefix_tiled(Hkv, B * group, prefix_len);
     if (tiled)
-        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len, max_pages > 0 ? B * Hkv : 0);
+        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len, D,
+                                    static_cast<int64_t>(B) * max_pages * page_size);
     w->ptiles = prefix_len && !tiled ? (B * group + R - 1) / R : 0;
     const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxWarps;
     w->part_o = c.take<float>(slots * R * D * 4);
     w->part_ml = c.take<float2>(slots * R * 8);
     w->cum = c.take<int>((static_cast<size_t>(B) + 1) * 4);
-    const size_t rows = static_cast<size_t>(w->prefix.splits) * B * Hq;
+    const size_t rows = tiled ? static_cast<size_t>(kv8_prefix_most_splits(Hkv, B * group, prefix_len)) * B * Hq : 0;
     w->prefix.part_o = c.take<float>(rows * D * 4);
     w->prefix.part_ml = c.take<float2>(rows * 8);
     return c.off;
@@ -734,7 +736,7 @@ size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int pr
     if (!kv8_attn_ok(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
         return 0;
     Kv8Ws w;
-    return kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, &w, nullptr);
+    return kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, &w, nullptr);
 }
 
 int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq, int Hkv, int D,
@@ -765,7 +767,7 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
     if (int st = current_device(&sms))
         return st;
     Kv8Ws w;
-    kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, &w, ws);
+    kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, &w, ws);
     Kv8Attn a = {};
     a.q = q_bf16, a.q_stride = q_stride;
     a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;

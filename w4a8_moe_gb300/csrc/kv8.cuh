@@ -65,10 +65,12 @@ struct Kv8Prefix {
     int tiles;            // 128-key tiles of the prefix
     int row_pairs;        // pairs of 128-row tiles
     int splits, tiles_per_split;
+    float us;             // about how long it takes
     float* part_o;
     float2* part_ml;
 };
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int own_pairs);
+int kv8_prefix_most_splits(int Hkv, int rows, int prefix_len);
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, int64_t own_max);
 cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s);
 bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);
 int kv8_attn_row_tile(int group);

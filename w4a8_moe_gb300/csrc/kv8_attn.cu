@@ -96,7 +96,7 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
     l.own = static_cast<int64_t>(l.pairs_p) * l.up;
     l.U = l.own + seq_total * l.hr;
     const int64_t n = (l.U + kKv8MinUnits - 1) / kKv8MinUnits;
-    const int most = l.U <= a.free_units ? a.free_warps : a.warps;
+    const int most = l.U <= a.free_units ? a.free_warps : a.warps;   // (no prefix CTAs: the same)
     l.n = static_cast<int>(n < most ? n : most);
     return l;
 }
@@ -245,9 +245,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
     __syncthreads();
 
     const Line line = make_line(a, carry);
-    // few units: one warp on each SM before a second, or, while the tiled prefix
-    // holds most SMs, whole CTAs, which the free SMs take at once
-    const int me = a.free_units ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
+    // Few units: one warp on each SM before a second. Units for the SMs that the
+    // tiled prefix leaves go to the first CTAs, which those take at once; with
+    // more, warp order is CTA order.
+    const int first = a.free_warps / kWarps;
+    const bool spread = line.U <= a.free_units || a.free_warps == a.warps;
+    int me = spread ? warp * first + static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kWarps + warp;
+    if (spread && blockIdx.x >= first)
+        me = line.n;
     const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
     const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
     Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
@@ -742,16 +747,13 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
     const int per_sm = min(R == 8 ? 4 : 3, fit) * kWarps;
     a.warps = num_sms * per_sm;
-    // A CTA of the tiled prefix takes a whole SM. The units go to the SMs that
-    // those leave, so that they need not wait for the prefix: all units where
-    // these are most SMs, else only few units (16 a warp, some 6 us).
+    // A CTA of the tiled prefix takes a whole SM. The units go to the warps of the
+    // SMs that those leave, which need not wait for the prefix, or to all warps,
+    // where the first to run are the free ones': what ends first, at some 1.5 us
+    // a unit of a warp, U / free against p.us + U / all.
     const int taken = p.splits * a.Hkv * p.row_pairs;
-    a.free_warps = max(num_sms - taken, 0) * per_sm;
-    a.free_units = static_cast<int64_t>(a.free_warps) * 16;
-    if (2 * taken <= num_sms) {
-        a.warps = a.free_warps;
-        a.free_units = 0;
-    }
+    a.free_warps = taken ? max(num_sms - taken, 0) * per_sm : a.warps;
+    a.free_units = taken ? static_cast<int64_t>(p.us / 1.5f * a.free_warps * a.warps / (a.warps - a.free_warps)) : 0;
     a.warps = min(a.warps, kKv8MaxWarps);
     a.free_warps = min(a.free_warps, kKv8MaxWarps);
     cudaError_t e;

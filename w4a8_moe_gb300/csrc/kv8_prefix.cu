@@ -686,29 +686,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     }
 }
 
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int own_pairs)
+// Splits that a plan may have, whatever the sequences' own keys: two waves.
+int kv8_prefix_most_splits(int Hkv, int rows, int prefix_len)
+{
+    const int64_t base = static_cast<int64_t>(Hkv) * ((rows + 2 * kTile - 1) / (2 * kTile));
+    const int64_t fill = 2 * ((kKv8PrefixCtas + base - 1) / base);
+    const int64_t tiles = (prefix_len + kTile - 1) / kTile;
+    return static_cast<int>(fill < tiles ? (fill < kKv8MaxSplits ? fill : kKv8MaxSplits)
+                                         : (tiles < kKv8MaxSplits ? tiles : kKv8MaxSplits));
+}
+
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, int64_t own_max)
 {
     Kv8Prefix p = {};
     p.tiles = (prefix_len + kTile - 1) / kTile;
     p.row_pairs = (rows + 2 * kTile - 1) / (2 * kTile);
-    // Time in key tiles: waves of CTAs, each its tiles plus about three tiles'
-    // worth of start and end, plus the join's reading of every split. With most
-    // SMs taken and more (sequence, kv head) pairs than the others hold, pairs
-    // wait for the prefix: about four tiles' worth. 48 query heads, 4096 tokens, us
-    // with 128 / 64 CTAs: 32 sequences 24.4 / 20.8, 16 sequences 16.4 / 17.4.
+    // The split that should end first, in us. A CTA takes some 1.7 us for a key
+    // tile (one row tile or two: a tile's chain of products and softmax bounds
+    // both) and 6 for its start and end. The sequences' own keys, taken to be
+    // half of what their page tables hold, take 4 and their bytes, either on the
+    // SMs that the prefix leaves or on all, the others joining after the prefix.
+    // Every split is written and read once more. 128 sequences of 48 heads with
+    // 16-1024 own keys over 32768 tokens: 119 us with 144 CTAs, 112 with 120.
     const int64_t base = static_cast<int64_t>(Hkv) * p.row_pairs;
-    int64_t best = INT64_MAX;
-    for (int s = 1; s <= p.tiles && s <= kKv8MaxSplits; ++s) {
+    const double bytes_us = own_max > 0 ? 0.5 * static_cast<double>(own_max) * Hkv * 2 * D / 5.5e6 : 0.0;
+    double best = 0.0;
+    const int most = kv8_prefix_most_splits(Hkv, rows, prefix_len);
+    for (int s = 1; s <= most; ++s) {
         const int per = (p.tiles + s - 1) / s;
         const int splits = (p.tiles + per - 1) / per;
-        const int64_t waves = (base * splits + kKv8PrefixCtas - 1) / kKv8PrefixCtas;
-        const int64_t taken = base * splits;
-        const int64_t late = 2 * taken > kKv8PrefixCtas && own_pairs > (kKv8PrefixCtas - taken) * 8 ? 4 : 0;
-        const int64_t cost = (waves * (per + 3) + late) * 8 + splits;
-        if (cost < best) {
-            best = cost;
+        const int64_t taken = base * splits, waves = (taken + kKv8PrefixCtas - 1) / kKv8PrefixCtas;
+        const double us = static_cast<double>(waves) * (per * 1.7 + 6.0);
+        const double free = waves > 1 ? 0.0 : static_cast<double>(kKv8PrefixCtas - taken) / kKv8PrefixCtas;
+        double own = 0.0;
+        if (own_max > 0) {
+            const double early = free * (us > 4.0 ? us - 4.0 : 0.0);
+            own = us + 4.0 + (bytes_us > early ? bytes_us - early : 0.0);
+            if (free > 0.0 && 4.0 + bytes_us / free < own)
+                own = 4.0 + bytes_us / free;
+        }
+        const double join = static_cast<double>(splits) * Hkv * rows * D * 8 / 8e6;
+        const double total = (own > us ? own : us) + join;
+        if (s == 1 || total < best) {
+            best = total;
             p.splits = splits;
             p.tiles_per_split = per;
+            p.us = static_cast<float>(us);
         }
     }
     return p;

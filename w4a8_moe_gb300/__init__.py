@@ -324,78 +324,92 @@ def fp8_block_linear(x_bf16, w_e4m3, w_scale_inv, out=None, xq_out=None, xs_out=
 
 
 # The kv8_* calls are made once per layer and decode step, where a call takes a few microseconds on the GPU, so their
-# checks are written to cost little: one test per rule, no helper objects.
-_BF16, _F32, _I32, _U8, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+# checks are written to cost little: every tensor attribute is read once (some 0.1 us each), and what went wrong is told
+# apart only after a check has failed.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks a cache's four tensors -> (shape [pages, kv heads, page size, D], scale mode)."""
-    shape, scales = k_cache.shape, k_scale.shape
-    if k_cache.dtype not in (_U8, _F8) or v_cache.dtype not in (_U8, _F8) or len(shape) != 4 or v_cache.shape != shape \
-            or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError("k_cache and v_cache must be contiguous uint8 or float8_e4m3fn [pages, kv heads, page size, D]")
-    if k_scale.dtype != _F32 or v_scale.dtype != _F32 or v_scale.shape != scales \
-            or (scales != shape[1:2] and scales != shape[:3]) or not (k_scale.is_contiguous() and v_scale.is_contiguous()):
-        raise ValueError("k_scale and v_scale must be contiguous float32, both [kv heads] or both [pages, kv heads, page size]")
-    return shape, 1 if len(scales) == 3 else 0
+def _cache_refused(k_cache, v_cache, k_scale, v_scale):
+    if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES or k_cache.dim() != 4 \
+            or k_cache.shape != v_cache.shape or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        return ValueError("k_cache and v_cache must be contiguous uint8 or float8_e4m3fn [pages, kv heads, page size, D]")
+    return ValueError("k_scale and v_scale must be contiguous float32, both [kv heads] or both [pages, kv heads, page size]")
 
 
-def _row_stride(t, shape, what):
+def _devices_refused(*tensors):
+    if any(not t.is_cuda for t in tensors):
+        return ValueError("tensors must be on the GPU")
+    return ValueError("tensors must be on one GPU")
+
+
+def _row_stride(t, rows, heads, d, what):
     """The row stride of a bf16 [rows, heads, D] tensor whose rows may lie apart."""
-    if t.dtype != _BF16 or t.shape != shape:
-        raise ValueError(f"{what} must be bf16 of shape {list(shape)}")
+    if t.dtype is not _BF16 or t.shape != (rows, heads, d):
+        raise ValueError(f"{what} must be bf16 of shape {[rows, heads, d]}")
     row, head, one = t.stride()
-    if one != 1 or (head != shape[2] and shape[1] != 1):
+    if one != 1 or (head != d and heads != 1):
         raise ValueError(f"{what}: each token's heads must be contiguous")
-    return row if shape[0] > 1 else shape[1] * shape[2]   # one row may report any row stride
+    return row if rows > 1 else heads * d   # one row may report any row stride
 
 
-def _on_gpu(ref, *tensors):
-    where = ref.get_device()
-    for t in tensors:
-        if t.get_device() != where:
-            raise ValueError("tensors must be on one GPU")
-    if where < 0:
-        raise ValueError("tensors must be on the GPU")
-    return where
-
-
-def _raw_stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _vector_refused(what):
+    return ValueError(f"{what} must be a contiguous int32 vector")
 
 
 def kv8_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, min_scale: float = 0.0, stream=None) -> None:
     """Quantize bf16 keys and values [T, kv heads, D] (rows may lie apart, as in a fused projection's output) into
     slots [T] (int32; out of range: skipped) of the cache. k_scale / v_scale of shape [kv heads] are read; of shape
     [pages, kv heads, page size] they are computed and written."""
-    (n, h, page, d), mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    shape, scales = k_cache.shape, k_scale.shape
+    if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES or len(shape) != 4 or v_cache.shape != shape \
+            or k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or v_scale.shape != scales \
+            or (scales != shape[1:2] and scales != shape[:3]) or not k_cache.is_contiguous() \
+            or not v_cache.is_contiguous() or not k_scale.is_contiguous() or not v_scale.is_contiguous():
+        raise _cache_refused(k_cache, v_cache, k_scale, v_scale)
+    n, h, page, d = shape
+    if slots.dtype is not _I32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise _vector_refused("slots")
     T = slots.numel()
-    if slots.dtype != _I32 or slots.dim() != 1 or not slots.is_contiguous():
-        raise ValueError("slots must be contiguous int32 [T]")
-    k_stride, v_stride = _row_stride(k, (T, h, d), "k"), _row_stride(v, (T, h, d), "v")
-    device = _on_gpu(k_cache, v_cache, k_scale, v_scale, k, v, slots)
-    status = _load().kv8_write(k.data_ptr(), v.data_ptr(), T, k_stride, v_stride, slots.data_ptr(), h, d, n, page, mode,
-                               min_scale, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                               v_scale.data_ptr(), _raw_stream(stream, device))
+    k_stride, v_stride = _row_stride(k, T, h, d, "k"), _row_stride(v, T, h, d, "v")
+    device = k_cache.get_device()
+    if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                          == k.get_device() == v.get_device() == slots.get_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, k, v, slots)
+    status = (_lib or _load()).kv8_write(
+        k.data_ptr(), v.data_ptr(), T, k_stride, v_stride, slots.data_ptr(), h, d, n, page, len(scales) == 3, min_scale,
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _check(status)
 
 
 def kv8_read(k_cache, v_cache, k_scale, v_scale, slots, k_out=None, v_out=None, stream=None):
     """The cache's slots [T] (int32; out of range: zeros) as bf16 keys and values, each [T, kv heads, D]."""
-    (n, h, page, d), mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    shape, scales = k_cache.shape, k_scale.shape
+    if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES or len(shape) != 4 or v_cache.shape != shape \
+            or k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or v_scale.shape != scales \
+            or (scales != shape[1:2] and scales != shape[:3]) or not k_cache.is_contiguous() \
+            or not v_cache.is_contiguous() or not k_scale.is_contiguous() or not v_scale.is_contiguous():
+        raise _cache_refused(k_cache, v_cache, k_scale, v_scale)
+    n, h, page, d = shape
+    if slots.dtype is not _I32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise _vector_refused("slots")
     T = slots.numel()
-    if slots.dtype != _I32 or slots.dim() != 1 or not slots.is_contiguous():
-        raise ValueError("slots must be contiguous int32 [T]")
     if k_out is None or v_out is None:
         with _on(stream):
             k_out = k_out if k_out is not None else torch.empty(T, h, d, dtype=_BF16, device=k_cache.device)
             v_out = v_out if v_out is not None else torch.empty(T, h, d, dtype=_BF16, device=k_cache.device)
-    k_stride, v_stride = _row_stride(k_out, (T, h, d), "k_out"), _row_stride(v_out, (T, h, d), "v_out")
-    device = _on_gpu(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
-    status = _load().kv8_read(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                              slots.data_ptr(), T, h, d, n, page, mode, k_out.data_ptr(), k_stride, v_out.data_ptr(),
-                              v_stride, _raw_stream(stream, device))
+    k_stride, v_stride = _row_stride(k_out, T, h, d, "k_out"), _row_stride(v_out, T, h, d, "v_out")
+    device = k_cache.get_device()
+    if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                          == slots.get_device() == k_out.get_device() == v_out.get_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
+    status = (_lib or _load()).kv8_read(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), T, h, d, n,
+        page, len(scales) == 3, k_out.data_ptr(), k_stride, v_out.data_ptr(), v_stride,
+        _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _check(status)
     return k_out, v_out
@@ -407,45 +421,61 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
     None with 0) and each sequence's own tokens (page_table [B, max pages], suffix_lens [B]); returns (bf16 out [B,
     query heads, D], fp32 lse [B, query heads] or None). Pass `lse` (a tensor, or True to allocate one) to receive it.
     sm_scale defaults to D ** -0.5; logit_cap 0 is no cap."""
-    (n, h, page, d), mode = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3 or q.shape[2] != d:
+    shape, scales = k_cache.shape, k_scale.shape
+    if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES or len(shape) != 4 or v_cache.shape != shape \
+            or k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or v_scale.shape != scales \
+            or (scales != shape[1:2] and scales != shape[:3]) or not k_cache.is_contiguous() \
+            or not v_cache.is_contiguous() or not k_scale.is_contiguous() or not v_scale.is_contiguous():
+        raise _cache_refused(k_cache, v_cache, k_scale, v_scale)
+    n, h, page, d = shape
+    q_shape = q.shape
+    if len(q_shape) != 3:
         raise ValueError("q must be bf16 [B, query heads, D of the cache]")
-    B, hq, _ = shape = q.shape
-    q_stride = _row_stride(q, shape, "q")
-    device = _on_gpu(q, k_cache, v_cache, k_scale, v_scale, page_table, suffix_lens)
+    B, hq, _ = q_shape
+    q_stride = _row_stride(q, B, hq, d, "q")
+    if page_table.dtype is not _I32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max pages]")
+    rows, most = page_table.shape
+    row, one = page_table.stride()
+    if rows != B or (one != 1 and most > 1):
+        raise ValueError("page_table must be int32 [B, max pages], each sequence's pages contiguous")
+    if suffix_lens.dtype is not _I32 or suffix_lens.shape != (B,) or not suffix_lens.is_contiguous():
+        raise _vector_refused("suffix_lens")
+    device = k_cache.get_device()
+    if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                          == q.get_device() == page_table.get_device() == suffix_lens.get_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, page_table, suffix_lens)
     pages = None
     if prefix_len > 0:
-        if prefix_pages.dtype != _I32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous() \
-                or prefix_pages.numel() * page < prefix_len:
-            raise ValueError("prefix_pages must be contiguous int32 and cover prefix_len tokens")
-        _on_gpu(q, prefix_pages)
+        if prefix_pages.dtype is not _I32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
+            raise _vector_refused("prefix_pages")
+        if prefix_pages.numel() * page < prefix_len:
+            raise ValueError("prefix_pages must cover prefix_len tokens")
+        if prefix_pages.get_device() != device:
+            raise _devices_refused(k_cache, prefix_pages)
         pages = prefix_pages.data_ptr()
-    if page_table.dtype != _I32 or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be int32 [B, max pages]")
-    most = page_table.shape[1]
-    row, one = page_table.stride()
-    if one != 1 and most > 1:
-        raise ValueError("page_table: each sequence's pages must be contiguous")
-    if suffix_lens.dtype != _I32 or suffix_lens.shape != shape[:1] or not suffix_lens.is_contiguous():
-        raise ValueError("suffix_lens must be contiguous int32 [B]")
     if out is None or lse is True or ws is None:
         with _on(stream):
             out = out if out is not None else torch.empty(B, hq, d, dtype=_BF16, device=q.device)
             lse = torch.empty(B, hq, dtype=_F32, device=q.device) if lse is True else lse
             ws = ws if ws is not None else _ws(
                 kv8_prefix_attention_workspace_size(B, hq, h, d, prefix_len, most, page), q.device)
-    if out.dtype != _BF16 or out.shape != shape or not out.is_contiguous():
+    if out.dtype is not _BF16 or out.shape != q_shape or not out.is_contiguous():
         raise ValueError("out must be contiguous bf16 [B, query heads, D]")
+    if out.get_device() != device or ws.get_device() != device:
+        raise _devices_refused(k_cache, out, ws)
+    to = None
     if lse is not None:
-        if lse.dtype != _F32 or lse.shape != shape[:2] or not lse.is_contiguous():
+        if lse.dtype is not _F32 or lse.shape != (B, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [B, query heads]")
-        _on_gpu(q, lse)
-    _on_gpu(q, out, ws)
-    status = _load().kv8_prefix_attention(
+        if lse.get_device() != device:
+            raise _devices_refused(k_cache, lse)
+        to = lse.data_ptr()
+    status = (_lib or _load()).kv8_prefix_attention(
         q.data_ptr(), q_stride, B, hq, h, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), n, page, mode, pages, prefix_len, page_table.data_ptr(), row if B > 1 else most, most,
-        suffix_lens.data_ptr(), d ** -0.5 if sm_scale is None else sm_scale, logit_cap, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream, device))
+        v_scale.data_ptr(), n, page, len(scales) == 3, pages, prefix_len, page_table.data_ptr(), row if B > 1 else most,
+        most, suffix_lens.data_ptr(), d ** -0.5 if sm_scale is None else sm_scale, logit_cap, out.data_ptr(), to,
+        ws.data_ptr(), ws.nbytes, _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _check(status)
     return out, lse

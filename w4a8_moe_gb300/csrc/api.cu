@@ -759,15 +759,14 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
         !aligned4(suffix_lens) || !aligned4(lse) ||
         (scale_mode == 1 && (!aligned16(k_scale) || !aligned16(v_scale))))
         return W4A8_ERR_ALIGN;
-    if (!ws || ws_bytes < kv8_prefix_attention_workspace_size(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
+    Kv8Ws w;
+    if (!ws || ws_bytes < kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, &w, ws))
         return W4A8_ERR_WORKSPACE;
     if (!aligned16(ws))
         return W4A8_ERR_ALIGN;
     int sms;
     if (int st = current_device(&sms))
         return st;
-    Kv8Ws w;
-    kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, &w, ws);
     Kv8Attn a = {};
     a.q = q_bf16, a.q_stride = q_stride;
     a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;

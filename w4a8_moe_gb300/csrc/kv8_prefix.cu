@@ -715,6 +715,8 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, int64_t own_
     for (int s = 1; s <= most; ++s) {
         const int per = (p.tiles + s - 1) / s;
         const int splits = (p.tiles + per - 1) / per;
+        if (s > 1 && splits < s)
+            continue;   // the same as one before
         const int64_t taken = base * splits, waves = (taken + kKv8PrefixCtas - 1) / kKv8PrefixCtas;
         const double us = static_cast<double>(waves) * (per * 1.7 + 6.0);
         const double free = waves > 1 ? 0.0 : static_cast<double>(kKv8PrefixCtas - taken) / kKv8PrefixCtas;

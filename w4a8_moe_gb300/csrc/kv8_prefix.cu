@@ -59,8 +59,7 @@ enum Bar {
     kPHalf = kPFull + 2,             // [2]
     kOFull = kPHalf + 2,             // [2]
     kScFull = kOFull + 2,            // [kScaleRing]
-    kQRaw = kScFull + kScaleRing,    // [2]
-    kQFull = kQRaw + 2,              // [2]
+    kQFull = kScFull + kScaleRing,   // [2]
     kBars = kQFull + 2
 };
 static_assert(kBars * 8 + 8 <= 320, "barrier area");
@@ -158,6 +157,11 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void regs_inc()
 {
@@ -207,22 +211,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     const int nt = rows_all - row0 > kTile ? 2 : 1;
 
     grid_dep_launch();   // the kernel after this one needs nothing of it before its own end
-    if (tid == 0) {
-        abort_flag = 0;
-        for (int i = 0; i < kBars; ++i) {
-            uint32_t count = 1;
-            if (i >= kRawEmpty && i < kFull)
-                count = 2;          // a pair of converter warps
-            else if (i >= kFull && i < kEmpty)
-                count = 4;          // two pairs, a half each
-            else if (i >= kPFull && i < kOFull)
-                count = 4;          // a tile's softmax warps
-            else if (i >= kQRaw && i < kBars)
-                count = 4;          // the same
-            mbar_init(bar(i), count);
-        }
+    if (tid < kBars) {
+        uint32_t count = 1;
+        if (tid >= kRawEmpty && tid < kFull)
+            count = 2;          // a pair of converter warps
+        else if (tid >= kFull && tid < kEmpty)
+            count = 4;          // two pairs, a half each
+        else if ((tid >= kPFull && tid < kOFull) || tid >= kQFull)
+            count = 4;          // a tile's softmax warps
+        mbar_init(bar(tid), count);
         fence_mbar_init();
     }
+    if (tid == 0)
+        abort_flag = 0;
     if (warp == 13)
         tmem_alloc(smem_u32(&tmem_base), 512);
     __syncthreads();
@@ -249,51 +250,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     if (warp < 8) {
         const int t = warp >> 2;       // row tile
         const int my_row = row0 + t * kTile + (tid & 127);
+        const uint32_t staged = base + L::stage + L::kOperand + (tid & 255) * D * 2;
+        float ks_head = 1.0f, vs_head = 1.0f;
         if (t < nt) {
             // -------------------------------------------------------- queries
-            // A thread owns a row: it copies it to shared memory (where V_0 and
-            // K_1 will stand), finds its exponent, and writes it as an operand.
+            // A warp copies its 32 rows, whole rows at a time, to where V_0 and K_1
+            // will stand.
+            {
+                constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+                const int sub = lane / kLanes, chunk = lane % kLanes;
+                int row = my_row - lane + sub;
+                int b = row / a.group, g = row - b * a.group;
+#pragma unroll 4
+                for (int i = 0; i < 32; i += kPer) {
+                    const uint16_t* src = a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + g) * D + chunk * 8;
+                    const bool there = row < rows_all;   // else zeros
+                    copy16(staged + (i + sub - lane) * D * 2 + chunk * 16, there ? src : a.q, there ? 16 : 0);
+                    row += kPer;
+                    for (g += kPer; g >= a.group; g -= a.group)
+                        ++b;
+                }
+                if (!TOK) {
+                    ks_head = __ldg(a.k_scale + h);
+                    vs_head = __ldg(a.v_scale + h);
+                }
+            }
+            // A thread finds its row's exponent and writes the row as an operand.
             // Row r takes its 16-byte chunks in the order i ^ x r, with x r a
             // product in GF(8): both x r and x r + r then pass through all of
             // 0..7, so neither the reads (rows a whole number of banks apart)
             // nor the writes (at chunk ^ r) of eight rows collide.
+            copies_done();
+            __syncwarp();
             const int r = tid & 127;
             const int turn = ((r << 1) & 4) | (((r ^ (r >> 2)) & 1) << 1) | ((r >> 2) & 1);
-            const uint32_t staged = base + L::stage + L::kOperand + (t * kTile + r) * D * 2;
-            const bool there = my_row < rows_all;
-            const int there_n = __popc(__ballot_sync(0xFFFFFFFFu, there));
-            if (lane == 0)
-                mbar_arrive_expect_tx(bar(kQRaw + t), there_n * D * 2);
-            __syncwarp();
-            if (there) {
-                const int b = my_row / a.group;
-                bulk_load(staged, a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + my_row - b * a.group) * D, D * 2,
-                          bar(kQRaw + t));
-            }
-            const float ks_head = TOK ? 1.0f : __ldg(a.k_scale + h);
-            bool ok = wait_warp(kQRaw + t, 0);
+            bool ok = true;
+            uint4 w[D / 8];
             uint32_t top = 0;
-            if (there && ok) {
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 w = lds128(staged + (i ^ turn) * 16);
-                    // the larger magnitude of each half, side by side
-                    const uint32_t x = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
-                    top = __vmaxu2(top, __vmaxu2(x, __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-                }
-                top = max(top >> 16, top & 0xFFFFu);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                w[i] = lds128(staged + (i ^ turn) * 16);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {   // the larger magnitude of each half, side by side
+                constexpr uint32_t mags = 0x7FFF7FFFu;
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & mags, w[i].y & mags), __vmaxu2(w[i].z & mags, w[i].w & mags)));
             }
+            top = max(top >> 16, top & 0xFFFFu);
             const int ex = static_cast<int>(top >> 7);
             const int e = top == 0 || ex == 255 ? 0 : min(max(ex, 1), 253) - 127;
             // a negative factor goes into q, so that the largest product is the largest score
             const float down = ((a.sm_scale < 0.0f) != (ks_head < 0.0f) ? -1.0f : 1.0f) * __int_as_float((127 - e) << 23);
-#pragma unroll 4
+#pragma unroll
             for (int i = 0; i < D / 8; ++i) {
-                uint4 w = make_uint4(0, 0, 0, 0);
                 const int chunk = i ^ turn;
-                if (there && ok)
-                    w = lds128(staged + chunk * 16);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
                 uint32_t f[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -316,59 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             float m = -INFINITY;
             F2 l0(0.0f, 0.0f), l1(0.0f, 0.0f);
             const float* scales = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + L::scales);
-            // One key tile. kTail: keys past the prefix are masked.
-            auto tile = [&](int i, auto tail) {
-                constexpr bool kTail = decltype(tail)::value;
-                const float* ks = scales + (i % kScaleRing) * 2 * kTile;
-                const float* vs = ks + kTile;
-                const int live = a.prefix_len - (tile0 + i) * kTile;
-                float lift = 0.0f;   // log2 of the tile's largest value scale
-                if (TOK) {
-                    float v = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v = fmaxf(v, kTail && lane + 32 * j >= live ? 0.0f : fabsf(vs[lane + 32 * j]));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1)
-                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-                    lift = fmaxf(log2f(v), -100.0f);
-                }
-                if (!wait_warp(kSFull + t, i & 1))
-                    return false;
-                tc_fence_after();
-                uint32_t r[4][32];
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    tmem_ld32(ts + ch * 32, r[ch]);
-                float top[4];
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    ld_wait32(r[ch]);
-                    if (TOK) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 k4 = *reinterpret_cast<const float4*>(ks + ch * 32 + j);
-                            const F2 x = mul2(F2(__uint_as_float(r[ch][j]), __uint_as_float(r[ch][j + 1])), F2(k4.x, k4.y));
-                            const F2 y = mul2(F2(__uint_as_float(r[ch][j + 2]), __uint_as_float(r[ch][j + 3])), F2(k4.z, k4.w));
-                            r[ch][j] = __float_as_uint(x.lo()), r[ch][j + 1] = __float_as_uint(x.hi());
-                            r[ch][j + 2] = __float_as_uint(y.lo()), r[ch][j + 3] = __float_as_uint(y.hi());
-                        }
-                    }
-                    if (kTail) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            r[ch][j] = ch * 32 + j < live ? r[ch][j] : 0xFF800000u;
-                    }
-                    top[ch] = fmaxf(__uint_as_float(r[ch][0]), __uint_as_float(r[ch][1]));
-#pragma unroll
-                    for (int j = 2; j < 32; j += 2)
-                        top[ch] = max3(top[ch], __uint_as_float(r[ch][j]), __uint_as_float(r[ch][j + 1]));
-                }
-                // cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y})), c holding 2 log2(e) / cap
-                float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-                if (CAP)
-                    best = fmaf(-2.0f * capl, rcp(1.0f + ex2(best)), capl);
-                best += lift;
+            // What a tile does to the row, scores in units of c:
+            // the reference raised where the largest weight asks for it,
+            auto raise = [&](int i, float best) {
                 if (__any_sync(0xFFFFFFFFu, best > m + kSlack)) {
                     const float next = fmaxf(m, best);
                     const float f = next == -INFINITY ? 1.0f : ex2(m - next);
@@ -388,58 +348,144 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                         }
                     }
                 }
+            };
+            // the largest score in log2 units: cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y})),
+            // c holding 2 log2(e) / cap
+            auto in_log2 = [&](float top) {
+                const float x = top * c;
+                return CAP ? fmaf(-2.0f * capl, rcp(1.0f + ex2(x)), capl) : x;
+            };
+            // 32 keys' scores times their key scales,
+            auto times_scales = [&](uint32_t (&r)[32], const float* f) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 k4 = *reinterpret_cast<const float4*>(f + j);
+                    const F2 x = mul2(F2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), F2(k4.x, k4.y));
+                    const F2 y = mul2(F2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), F2(k4.z, k4.w));
+                    r[j] = __float_as_uint(x.lo()), r[j + 1] = __float_as_uint(x.hi());
+                    r[j + 2] = __float_as_uint(y.lo()), r[j + 3] = __float_as_uint(y.hi());
+                }
+            };
+            // their maximum,
+            auto largest = [&](const uint32_t (&r)[32]) {
+                float top = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+#pragma unroll
+                for (int j = 2; j < 32; j += 2)
+                    top = max3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                return top;
+            };
+            // and their weights as f16, added up on the way. Of the first `live` keys.
+            auto weigh = [&](const uint32_t (&r)[32], const float* vs, int ch, int live, auto masked) {
+                constexpr bool kMasked = decltype(masked)::value;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const F2 c2(c, c), add(CAP ? capl - ref : -ref, CAP ? capl - ref : -ref);
                 const F2 one(1.0f, 1.0f), two(-2.0f * capl, -2.0f * capl), zero(-0.0f, -0.0f);
+                uint32_t p[16];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t p[16];
+                for (int j = 0; j < 32; j += 4) {
+                    float4 v4;
+                    if (TOK)
+                        v4 = *reinterpret_cast<const float4*>(vs + j);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        float4 v4;
-                        if (TOK)
-                            v4 = *reinterpret_cast<const float4*>(vs + ch * 32 + j);
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const F2 s(__uint_as_float(r[ch][j + e]), __uint_as_float(r[ch][j + e + 1]));
-                            F2 x = fma2(s, c2, CAP ? zero : add);
-                            if (CAP) {
-                                x = add2(F2(ex2(x.lo()), ex2(x.hi())), one);
-                                x = fma2(F2(rcp(x.lo()), rcp(x.hi())), two, add);
-                            }
-                            float w0 = ex2(x.lo()), w1 = ex2(x.hi());
-                            if (kTail) {
-                                w0 = ch * 32 + j + e < live ? w0 : 0.0f;
-                                w1 = ch * 32 + j + e + 1 < live ? w1 : 0.0f;
-                            }
-                            F2 w(w0, w1);
-                            if (e == 0)
-                                l0 = add2(l0, w);
-                            else
-                                l1 = add2(l1, w);
-                            if (TOK) {
-                                F2 v = e == 0 ? F2(v4.x, v4.y) : F2(v4.z, v4.w);
-                                if (kTail)
-                                    v = F2(ch * 32 + j + e < live ? v.lo() : 0.0f, ch * 32 + j + e + 1 < live ? v.hi() : 0.0f);
-                                w = mul2(w, v);
-                            }
-                            p[(j + e) >> 1] = pack_f16(w.lo(), w.hi());
+                    for (int e = 0; e < 4; e += 2) {
+                        const F2 s(__uint_as_float(r[j + e]), __uint_as_float(r[j + e + 1]));
+                        F2 x = fma2(s, c2, CAP ? zero : add);
+                        if (CAP) {
+                            x = add2(F2(ex2(x.lo()), ex2(x.hi())), one);
+                            x = fma2(F2(rcp(x.lo()), rcp(x.hi())), two, add);
                         }
-                    }
-                    tmem_st16(ts + ch * 16, p);
-                    if (ch == 1) {   // O can take the first half of the keys
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(bar(kPHalf + t));
+                        float w0 = ex2(x.lo()), w1 = ex2(x.hi());
+                        if (kMasked) {
+                            w0 = j + e < live ? w0 : 0.0f;
+                            w1 = j + e + 1 < live ? w1 : 0.0f;
+                        }
+                        F2 w(w0, w1);
+                        if (e == 0)
+                            l0 = add2(l0, w);
+                        else
+                            l1 = add2(l1, w);
+                        if (TOK) {
+                            F2 v = e == 0 ? F2(v4.x, v4.y) : F2(v4.z, v4.w);
+                            if (kMasked)
+                                v = F2(j + e < live ? v.lo() : 0.0f, j + e + 1 < live ? v.hi() : 0.0f);
+                            w = mul2(w, v);
+                        }
+                        p[(j + e) >> 1] = pack_f16(w.lo(), w.hi());
                     }
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(kPFull + t));
+                tmem_st16(ts + ch * 16, p);
+                if (ch & 1) {   // O can take half of the keys
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar((ch == 1 ? kPHalf : kPFull) + t));
+                }
+            };
+            // A key tile: the whole row of scores in registers. The prefix's last
+            // tile, where keys past its end are masked, goes the other way, which
+            // reads S twice but is a quarter of the code: it runs once.
+            auto tile = [&](int i, auto brief) {
+                constexpr bool kBrief = decltype(brief)::value;
+                const float* ks = scales + (i % kScaleRing) * 2 * kTile;
+                const float* vs = ks + kTile;
+                const int live = a.prefix_len - (tile0 + i) * kTile;
+                float lift = 0.0f;   // log2 of the tile's largest value scale
+                if (TOK) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v = fmaxf(v, kBrief && lane + 32 * j >= live ? 0.0f : fabsf(vs[lane + 32 * j]));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+                    lift = fmaxf(log2f(v), -100.0f);
+                }
+                if (!wait_warp(kSFull + t, i & 1))
+                    return false;
+                tc_fence_after();
+                if constexpr (kBrief) {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t r[32];
+                        tmem_ld32(ts + ch * 32, r);
+                        ld_wait32(r);
+                        if (TOK)
+                            times_scales(r, ks + ch * 32);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            r[j] = ch * 32 + j < live ? r[j] : 0xFF800000u;
+                        top = fmaxf(top, largest(r));
+                    }
+                    raise(i, in_log2(top) + lift);
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t r[32];
+                        tmem_ld32(ts + ch * 32, r);
+                        ld_wait32(r);
+                        if (TOK)
+                            times_scales(r, ks + ch * 32);
+                        weigh(r, vs + ch * 32, ch, live - ch * 32, Const<true>());
+                    }
+                } else {
+                    uint32_t r[4][32];
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch)
+                        tmem_ld32(ts + ch * 32, r[ch]);
+                    float top[4];
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        ld_wait32(r[ch]);
+                        if (TOK)
+                            times_scales(r[ch], ks + ch * 32);
+                        top[ch] = largest(r[ch]);
+                    }
+                    raise(i, in_log2(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))) + lift);
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch)
+                        weigh(r[ch], vs + ch * 32, ch, kTile, Const<false>());
+                }
                 return true;
             };
             for (int i = 0; i < n && ok; ++i) {
@@ -455,7 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 ok = wait_warp(kOFull + x, 0);
             if (ok) {
                 tc_fence_after();
-                const float vscale = TOK ? 1.0f : __ldg(a.v_scale + h);
                 const int64_t at = (static_cast<int64_t>(split) * a.Hkv + h) * rows_all + my_row;
                 const uint32_t mine = base + L::stage + (tid & 255) * (D * 4 + 16);
 #pragma unroll 1
@@ -465,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     ld_wait32(r);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        r[j] = __float_as_uint(__uint_as_float(r[j]) * vscale);
+                        r[j] = __float_as_uint(__uint_as_float(r[j]) * vs_head);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         sts128(mine + ch * 128 + j * 4, r[j], r[j + 1], r[j + 2], r[j + 3]);

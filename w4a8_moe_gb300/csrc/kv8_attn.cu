@@ -624,6 +624,9 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
         n2 += warp_of(line, first + units - 1) - w + 1;
         at_own = static_cast<int64_t>(line.pairs_p + b * line.hr + j + w - n1) * R + gi % R;
     }
+    // Lane i of a warp finds piece first_piece + W i of the row and its weight;
+    // then every lane reads its values of all of them. Nothing that is read
+    // waits for anything but the kernel before.
     if (sum_here)
         grid_dep_wait();
     if (W == 1 && head >= a.B * a.Hq)
@@ -632,29 +635,66 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
 #pragma unroll
     for (int i = 0; i < V; ++i)
         acc[i] = 0.0f;
-#pragma unroll 4
-    for (int k = first_piece; k < n2; k += W) {
-        const bool tiled = k < n0;
-        const int64_t at = tiled ? (static_cast<int64_t>(k) * a.Hkv + h) * a.B * a.group + row
-                                 : (k < n1 ? at_pre : at_own) + static_cast<int64_t>(k) * R;
-        const float* o = (tiled ? p.part_o : a.part_o) + at * D;
-        const float2 ml = (tiled ? p.part_ml : a.part_ml)[at];
-        float v[V];
-        if (V == 4) {
-            const float4 w = *(reinterpret_cast<const float4*>(o) + lane);
-            v[0] = w.x, v[1] = w.y, v[V - 2] = w.z, v[V - 1] = w.w;
-        } else {
-            const float2 w = *(reinterpret_cast<const float2*>(o) + lane);
-            v[0] = w.x, v[1] = w.y;
+    for (int k0 = first_piece; k0 < n2; k0 += 32 * W) {
+        const int k = k0 + W * lane;
+        const float* src = a.part_o;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (k < n2) {
+            const bool tiled = k < n0;
+            const int64_t at = tiled ? (static_cast<int64_t>(k) * a.Hkv + h) * a.B * a.group + row
+                                     : (k < n1 ? at_pre : at_own) + static_cast<int64_t>(k) * R;
+            src = (tiled ? p.part_o : a.part_o) + at * D;
+            ml = (tiled ? p.part_ml : a.part_ml)[at];
         }
-        const float to = fmaxf(top, ml.x);
+        const int n = min(32, (n2 - k0 + W - 1) / W);
+        constexpr int kAhead = 8;   // pieces whose values are on their way together
+        float v[kAhead][V];
+        auto fetch = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const float* from = reinterpret_cast<const float*>(
+                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), j0 + j & 31));
+                if (j0 + j < n) {
+                    if (V == 4) {
+                        const float4 w = *(reinterpret_cast<const float4*>(from) + lane);
+                        v[j][0] = w.x, v[j][1] = w.y, v[j][V - 2] = w.z, v[j][V - 1] = w.w;
+                    } else {
+                        const float2 w = *(reinterpret_cast<const float2*>(from) + lane);
+                        v[j][0] = w.x, v[j][1] = w.y;
+                    }
+                }
+            }
+        };
+        fetch(0);
+        float best = ml.x;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, x));
+        const float to = fmaxf(top, best);
         const float ref = to == -INFINITY ? 0.0f : to;
         const float f0 = ex2(top - ref), f1 = ex2(ml.x - ref);
+        float l = ml.y * f1;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+        sum = sum * f0 + l;
+        top = to;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            acc[i] = acc[i] * f0 + v[i] * f1;
-        sum = sum * f0 + ml.y * f1;
-        top = to;
+            acc[i] *= f0;
+        for (int j0 = 0; j0 < n; j0 += kAhead) {
+            if (j0 > 0)
+                fetch(j0);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const float f = __shfl_sync(0xFFFFFFFFu, f1, j0 + j & 31);
+                if (j0 + j < n) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        acc[i] += v[j][i] * f;
+                }
+            }
+        }
     }
     if (W > 1) {
         __shared__ float so[W][D];
@@ -719,10 +759,12 @@ static cudaError_t launch_pieces(const Kv8Attn& a, bool after_prefix, cudaStream
 template <int D>
 static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
 {
+    // Warps a row: 17 sequences of 16 heads, 40 splits (272 rows), us in all with 8 / 4
+    // 12.7 / 14.6; 64 of 32 heads, 11 splits (2048 rows) with 4 / 1 30.4 / 27.5.
     const int heads = a.B * a.Hq;
-    if (heads <= num_sms * 4)
+    if (heads <= num_sms || (p.splits > 16 && heads <= 4 * num_sms))
         return launch_dependent(kv8_join_kernel<D, 8>, dim3(heads), dim3(8 * 32), 0, s, a, p, R);
-    if (heads <= num_sms * (p.splits >= 8 ? 32 : 8))
+    if (heads <= 2 * num_sms || (p.splits > 8 && heads <= 4 * num_sms))
         return launch_dependent(kv8_join_kernel<D, 4>, dim3(heads), dim3(4 * 32), 0, s, a, p, R);
     return launch_dependent(kv8_join_kernel<D, 1>, dim3((heads + kJoinCta - 1) / kJoinCta), dim3(kJoinCta * 32), 0, s, a,
                             p, R);

@@ -249,8 +249,8 @@ struct Kv8Ws {
     int tiles, ptiles;
     Kv8Prefix prefix;   // splits 0: the prefix is not tiled
 };
-static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size, Kv8Ws* w,
-                     void* ws)
+static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size, float tile_us,
+                     Kv8Ws* w, void* ws)
 {
     Carver c(ws);
     const int group = Hq / Hkv, R = kv8_attn_row_tile(group);
@@ -258,7 +258,7 @@ static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_page
     w->prefix = {};
     const bool tiled = prefix_len && kv8_prefix_tiled(Hkv, B * group, prefix_len);
     if (tiled)
-        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len, D,
+        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len, D, tile_us,
                                     static_cast<int64_t>(B) * max_pages * page_size);
     w->ptiles = prefix_len && !tiled ? (B * group + R - 1) / R : 0;
     const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxWarps;
@@ -736,7 +736,7 @@ size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int pr
     if (!kv8_attn_ok(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
         return 0;
     Kv8Ws w;
-    return kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, &w, nullptr);
+    return kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, 1.5f, &w, nullptr);
 }
 
 int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq, int Hkv, int D,
@@ -759,8 +759,11 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
         !aligned4(suffix_lens) || !aligned4(lse) ||
         (scale_mode == 1 && (!aligned16(k_scale) || !aligned16(v_scale))))
         return W4A8_ERR_ALIGN;
+    // a key tile of the tiled prefix: three exponential-class operations a score
+    // instead of one, or a scale for each key and value
+    const float tile_us = logit_cap > 0.0f ? 2.6f : scale_mode ? 1.8f : 1.5f;
     Kv8Ws w;
-    if (!ws || ws_bytes < kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, &w, ws))
+    if (!ws || ws_bytes < kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, tile_us, &w, ws))
         return W4A8_ERR_WORKSPACE;
     if (!aligned16(ws))
         return W4A8_ERR_ALIGN;

@@ -52,9 +52,9 @@ struct Kv8Attn {
     uint32_t* err;
     uint16_t* out;
     float* lse;
-    int warps;          // that the units go to, and how many units at most to how many of them
-    int free_warps;     // instead, while the tiled prefix holds the other SMs
-    int64_t free_units;
+    int warps;          // that the units go to
+    int free_warps;     // of them those that need not wait for the tiled prefix
+    float free_us;     // that the others wait, about
     int* cum;           // [B + 1] prefix sums of the sequences' units, left for the join
 };
 // The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key
@@ -70,7 +70,7 @@ struct Kv8Prefix {
     float2* part_ml;
 };
 int kv8_prefix_most_splits(int Hkv, int rows, int prefix_len);
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, int64_t own_max);
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max);
 cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s);
 bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);
 int kv8_attn_row_tile(int group);

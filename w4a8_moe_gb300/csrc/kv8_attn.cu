@@ -65,15 +65,18 @@ __device__ __forceinline__ uint2 lds64(uint32_t at)
 // ---------------------------------------------------------------------------
 // The split. A pair is (rows, keys): first the prefix's pairs (kv head, row
 // tile of the whole batch), then the sequences' (sequence, kv head, row tile of
-// the group). The keys of a pair are cut into units of 16, all units stand in
-// one line in pair order, and warp w of n takes units [U w / n, U (w + 1) / n):
-// equal work however ragged the lengths are. The piece of pair p done by warp w
-// is stored in slot p + w: along the line p + w rises with every piece, so no
-// two share a slot, and a reader finds a pair's slots from U and n alone.
+// the group). The keys of a pair are cut into units of 16 and all units stand in
+// one line in pair order. Warp w of n takes units [U w / n, U (w + 1) / n): equal
+// work however ragged the lengths are. Beside a tiled prefix, which holds SMs,
+// the warps that run at once get a longer share than those that start after it
+// (make_line). The piece of pair p done by warp w is stored in slot p + w: along
+// the line p + w rises with every piece, so no two share a slot, and a reader
+// finds a pair's slots from the shares' bounds alone.
 // ---------------------------------------------------------------------------
 struct Line {
     int64_t U;      // units
-    int n;          // warps with units
+    int64_t U1;     // of them for the first n1 warps
+    int n1, n;      // warps with units
     int up;         // units of a prefix pair
     int pairs_p;    // prefix pairs
     int64_t own;    // first unit of the sequences' pairs
@@ -95,17 +98,43 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
     l.up = (a.prefix_len + kKv8Unit - 1) / kKv8Unit;
     l.own = static_cast<int64_t>(l.pairs_p) * l.up;
     l.U = l.own + seq_total * l.hr;
-    const int64_t n = (l.U + kKv8MinUnits - 1) / kKv8MinUnits;
-    const int most = l.U <= a.free_units ? a.free_warps : a.warps;   // (no prefix CTAs: the same)
-    l.n = static_cast<int>(n < most ? n : most);
+    l.U1 = l.U;
+    const int late = a.warps - a.free_warps;
+    if (late > 0) {
+        const float unit_us = 1.6f, start_us = 3.0f;   // of a warp
+        const float work = unit_us * static_cast<float>(l.U), free = static_cast<float>(a.free_warps);
+        if (work > free * (a.free_us + start_us)) {
+            // the free warps work for free_us + y, the late ones for y less their start
+            const float y = (work - free * a.free_us + start_us * late) / a.warps;
+            const int64_t u1 = static_cast<int64_t>(free * (a.free_us + y) / unit_us);
+            l.U1 = u1 < l.U ? u1 : l.U;
+        }
+    }
+    const int64_t n1 = (l.U1 + kKv8MinUnits - 1) / kKv8MinUnits;
+    const int64_t n2 = (l.U - l.U1 + kKv8MinUnits - 1) / kKv8MinUnits;
+    l.n1 = static_cast<int>(n1 < a.free_warps ? n1 : a.free_warps);
+    l.n = l.n1 + static_cast<int>(n2 < late ? n2 : late);
     return l;
 }
-__device__ __forceinline__ int64_t warp_begin(const Line& l, int w) { return l.U * w / l.n; }
+// (32-bit division where the numbers allow it: warps are fewer than 2^12.)
+__device__ __forceinline__ int64_t share(int64_t units, int i, int n)
+{
+    return units < 1 << 20 ? static_cast<uint32_t>(units) * static_cast<uint32_t>(i) / static_cast<uint32_t>(n)
+                           : units * i / n;
+}
+__device__ __forceinline__ int share_of(int64_t units, int64_t u, int n)
+{
+    return units < 1 << 20 ? static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(n) - 1) /
+                                              static_cast<uint32_t>(units))
+                           : static_cast<int>(((u + 1) * n - 1) / units);
+}
+__device__ __forceinline__ int64_t warp_begin(const Line& l, int w)
+{
+    return w <= l.n1 ? share(l.U1, w, l.n1) : l.U1 + share(l.U - l.U1, w - l.n1, l.n - l.n1);
+}
 __device__ __forceinline__ int warp_of(const Line& l, int64_t u)
 {
-    if (l.U < 1 << 20)   // n < 2^12: no 64-bit division
-        return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(l.n) - 1) / static_cast<uint32_t>(l.U));
-    return static_cast<int>(((u + 1) * l.n - 1) / l.U);
+    return u < l.U1 ? share_of(l.U1, u, l.n1) : l.n1 + share_of(l.U - l.U1, u - l.U1, l.n - l.n1);
 }
 
 // A unit as its warp meets it, found by one lane for each of 32 units ahead.
@@ -245,13 +274,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
     __syncthreads();
 
     const Line line = make_line(a, carry);
-    // Few units: one warp on each SM before a second. Units for the SMs that the
-    // tiled prefix leaves go to the first CTAs, which those take at once; with
-    // more, warp order is CTA order.
+    // few units: one warp on each SM before a second; the first CTAs run first
     const int first = a.free_warps / kWarps;
-    const bool spread = line.U <= a.free_units || a.free_warps == a.warps;
-    int me = spread ? warp * first + static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kWarps + warp;
-    if (spread && blockIdx.x >= first)
+    int me = static_cast<int>(blockIdx.x) < first ? warp * first + static_cast<int>(blockIdx.x)
+                                                  : static_cast<int>(blockIdx.x) * kWarps + warp;
+    if (static_cast<int>(blockIdx.x) < first && me >= line.n1)
         me = line.n;
     const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
     const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
@@ -789,13 +816,10 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
     const int per_sm = min(R == 8 ? 4 : 3, fit) * kWarps;
     a.warps = num_sms * per_sm;
-    // A CTA of the tiled prefix takes a whole SM. The units go to the warps of the
-    // SMs that those leave, which need not wait for the prefix, or to all warps,
-    // where the first to run are the free ones': what ends first, at some 1.5 us
-    // a unit of a warp, U / free against p.us + U / all.
+    // a CTA of the tiled prefix takes a whole SM; the others' warps can start at once
     const int taken = p.splits * a.Hkv * p.row_pairs;
     a.free_warps = taken ? max(num_sms - taken, 0) * per_sm : a.warps;
-    a.free_units = taken ? static_cast<int64_t>(p.us / 1.5f * a.free_warps * a.warps / (a.warps - a.free_warps)) : 0;
+    a.free_us = p.us;
     a.warps = min(a.warps, kKv8MaxWarps);
     a.free_warps = min(a.free_warps, kKv8MaxWarps);
     cudaError_t e;

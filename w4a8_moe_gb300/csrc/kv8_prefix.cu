@@ -744,14 +744,14 @@ int kv8_prefix_most_splits(int Hkv, int rows, int prefix_len)
                                          : (tiles < kKv8MaxSplits ? tiles : kKv8MaxSplits));
 }
 
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, int64_t own_max)
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max)
 {
     Kv8Prefix p = {};
     p.tiles = (prefix_len + kTile - 1) / kTile;
     p.row_pairs = (rows + 2 * kTile - 1) / (2 * kTile);
-    // The split that should end first, in us. A CTA takes some 1.7 us for a key
-    // tile (one row tile or two: a tile's chain of products and softmax bounds
-    // both) and 6 for its start and end. The sequences' own keys, taken to be
+    // The split that should end first, in us. A CTA takes tile_us for a key tile
+    // (one row tile or two: a tile's chain of products and softmax bounds both) and
+    // some 5 for its start and end. The sequences' own keys, taken to be
     // half of what their page tables hold, take 4 and their bytes, either on the
     // SMs that the prefix leaves or on all, the others joining after the prefix.
     // Every split is written and read once more. 128 sequences of 48 heads with
@@ -766,7 +766,7 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, int64_t own_
         if (s > 1 && splits < s)
             continue;   // the same as one before
         const int64_t taken = base * splits, waves = (taken + kKv8PrefixCtas - 1) / kKv8PrefixCtas;
-        const double us = static_cast<double>(waves) * (per * 1.7 + 6.0);
+        const double us = static_cast<double>(waves) * (per * tile_us + 5.0);
         const double free = waves > 1 ? 0.0 : static_cast<double>(kKv8PrefixCtas - taken) / kKv8PrefixCtas;
         double own = 0.0;
         if (own_max > 0) {

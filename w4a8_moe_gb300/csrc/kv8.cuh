@@ -26,7 +26,7 @@ cudaError_t launch_kv8_read(const Kv8Rows& a, const uint8_t* k_cache, const uint
 // ---- attention
 constexpr int kKv8MaxBatch = 4096;  // the split's prefix sums live in shared memory
 constexpr int kKv8Unit = 16;        // keys per unit of the split (a unit never crosses a page)
-constexpr int kKv8MinUnits = 4;     // units a warp gets at least
+constexpr int kKv8MinUnits = 2;     // units a warp gets at least
 constexpr int kKv8MaxWarps = 152 * 16;   // warps the units are divided over, at most
 
 struct Kv8Attn {

@@ -23,7 +23,7 @@ namespace w4a8 {
 namespace {
 
 constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
-constexpr int kStages = 3;   // units in flight per warp
+constexpr int kStages = 2;   // units in flight per warp
 constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
 // A row's reference exponent is raised only when a weight passes 2^8 under it:
 // weights then stay far inside f16 and the row's accumulators are hardly ever
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
             ml = (tiled ? p.part_ml : a.part_ml)[at];
         }
         const int n = min(32, (n2 - k0 + W - 1) / W);
-        constexpr int kAhead = 8;   // pieces whose values are on their way together
+        constexpr int kAhead = 12;   // pieces whose values are on their way together
         float v[kAhead][V];
         auto fetch = [&](int j0) {
 #pragma unroll

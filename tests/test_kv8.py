@@ -346,6 +346,19 @@ def test_attention_prefix_lengths(lib, prefix):
         b.check(*b.run(lib))
 
 
+@pytest.mark.parametrize("batch,hq,hkv,d,prefix,own,mode", [
+    (24, 32, 8, 64, 20000, 1500, 0),    # own keys for longer than the prefix takes
+    (24, 32, 8, 128, 3000, 3000, 1),
+    (64, 32, 8, 64, 9000, 40, 1),       # every SM taken by the prefix, or nearly
+    (900, 48, 8, 64, 300, 5, 0),        # more tiles of rows than SMs
+    (300, 4, 1, 64, 1000, 3, 1),        # the lengths' sums left to the join
+])
+def test_attention_prefix_and_own_keys_side_by_side(lib, batch, hq, hkv, d, prefix, own, mode):
+    """Every way of sharing the SMs between the prefix and the sequences' own keys."""
+    b = Batch([(own + i) % (own + 1) if i % 5 == 4 else own for i in range(batch)], prefix, hq, hkv, d, 64, mode, seed=own)
+    b.check(*b.run(lib))
+
+
 @pytest.mark.parametrize("mode", [0, 1])
 @pytest.mark.parametrize("batch", [2, 40])
 def test_attention_logit_cap(lib, mode, batch):
@@ -411,6 +424,21 @@ def test_attention_same_bits_each_call_and_any_workspace_contents(lib):
             got = b.run(lib, ws=ws)
             assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
             assert lib.w4a8_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("batch,hq,hkv,d,prefix,own,mode", [
+    (24, 32, 8, 128, 3000, 3000, 1), (200, 48, 8, 128, 2048, 300, 0), (64, 32, 8, 64, 8192, 40, 1),
+])
+def test_attention_same_bits_over_many_calls(lib, batch, hq, hkv, d, prefix, own, mode):
+    """Copies land in another order each time; the result stays the same."""
+    b = Batch([own] * batch, prefix, hq, hkv, d, 64, mode, seed=own)
+    first = b.run(lib)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        got = b.run(lib)
+        differ += (got[0] != first[0]).sum() + (got[1] != first[1]).sum()
+    assert int(differ) == 0
+    b.check(*first)
 
 
 def test_attention_without_lse_and_without_own_tokens(lib):

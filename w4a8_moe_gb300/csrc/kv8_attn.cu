@@ -101,12 +101,16 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
     l.U1 = l.U;
     const int late = a.warps - a.free_warps;
     if (late > 0) {
+        // Rounded step by step: the writer and the reader of the pieces have to
+        // come to the same bounds, so nothing may be contracted in one of them.
         const float unit_us = 1.6f, start_us = 3.0f;   // of a warp
-        const float work = unit_us * static_cast<float>(l.U), free = static_cast<float>(a.free_warps);
-        if (work > free * (a.free_us + start_us)) {
+        const float work = __fmul_rn(unit_us, static_cast<float>(l.U)), free = static_cast<float>(a.free_warps);
+        if (work > __fmul_rn(free, __fadd_rn(a.free_us, start_us))) {
             // the free warps work for free_us + y, the late ones for y less their start
-            const float y = (work - free * a.free_us + start_us * late) / a.warps;
-            const int64_t u1 = static_cast<int64_t>(free * (a.free_us + y) / unit_us);
+            const float rest = __fadd_rn(work, -__fmul_rn(free, a.free_us));
+            const float y = __fdiv_rn(__fadd_rn(rest, __fmul_rn(start_us, static_cast<float>(late))),
+                                      static_cast<float>(a.warps));
+            const int64_t u1 = static_cast<int64_t>(__fdiv_rn(__fmul_rn(free, __fadd_rn(a.free_us, y)), unit_us));
             l.U1 = u1 < l.U ? u1 : l.U;
         }
     }
@@ -130,7 +134,7 @@ __device__ __forceinline__ int share_of(int64_t units, int64_t u, int n)
 }
 __device__ __forceinline__ int64_t warp_begin(const Line& l, int w)
 {
-    return w <= l.n1 ? share(l.U1, w, l.n1) : l.U1 + share(l.U - l.U1, w - l.n1, l.n - l.n1);
+    return w < l.n1 ? share(l.U1, w, l.n1) : l.U1 + (l.n > l.n1 ? share(l.U - l.U1, w - l.n1, l.n - l.n1) : 0);
 }
 __device__ __forceinline__ int warp_of(const Line& l, int64_t u)
 {

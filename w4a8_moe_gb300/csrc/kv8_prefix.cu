@@ -32,8 +32,14 @@ constexpr int kThreads = 512;
 constexpr int kTile = 128;        // keys per tile, rows per row tile
 constexpr int kHalf = 64;         // keys per raw slot
 constexpr int kStages = 3;        // f16 operand tiles, K and V in turn
-constexpr int kRaw = 7;           // raw slots
 constexpr int kPairs = 3;         // pairs of converter warps
+constexpr int kRaw = 6;           // raw slots
+// A parity wait cannot tell a phase from the one two before it, and copies land
+// out of order: whoever waits on a slot has to have seen each of its rounds, so
+// a slot belongs to one pair. (Seven slots, visited by the pairs in turn, let a
+// pair that was ahead take a slot's last round for its next: wrong values in one
+// call of some hundred.)
+static_assert(kRaw % kPairs == 0, "a raw slot has one pair of readers");
 constexpr int kScaleRing = 4;     // tiles whose per-token scales are held
 constexpr float kSlack = 8.0f;    // see kv8_attn.cu
 
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         *const_cast<volatile int*>(&abort_flag) = 1;
     };
     auto wait = [&](int i, uint32_t parity) {
-        if (mbar_wait_or_abort<1000>(bar(i), parity, abort))
+        if ((warp < 8 || warp == 13) ? mbar_wait_or_abort<0>(bar(i), parity, abort) : mbar_wait_or_abort<1000>(bar(i), parity, abort))
             return true;
         fail();
         return false;

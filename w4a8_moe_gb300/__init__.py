@@ -378,7 +378,7 @@ def kv8_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, min_scale: float 
                           == k.get_device() == v.get_device() == slots.get_device()):
         raise _devices_refused(k_cache, v_cache, k_scale, v_scale, k, v, slots)
     status = (_lib or _load()).kv8_write(
-        k.data_ptr(), v.data_ptr(), T, k_stride, v_stride, slots.data_ptr(), h, d, n, page, len(scales) == 3, min_scale,
+        k.data_ptr(), v.data_ptr(), T, k_stride, v_stride, slots.data_ptr(), h, d, n, page, len(scales) == 3, float(min_scale),
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
@@ -445,7 +445,7 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
                           == q.get_device() == page_table.get_device() == suffix_lens.get_device()):
         raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, page_table, suffix_lens)
-    pages = None
+    pages, prefix_len = None, int(prefix_len)
     if prefix_len > 0:
         if prefix_pages.dtype is not _I32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
             raise _vector_refused("prefix_pages")
@@ -474,7 +474,7 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
     status = (_lib or _load()).kv8_prefix_attention(
         q.data_ptr(), q_stride, B, hq, h, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), n, page, len(scales) == 3, pages, prefix_len, page_table.data_ptr(), row if B > 1 else most,
-        most, suffix_lens.data_ptr(), d ** -0.5 if sm_scale is None else sm_scale, logit_cap, out.data_ptr(), to,
+        most, suffix_lens.data_ptr(), d ** -0.5 if sm_scale is None else float(sm_scale), float(logit_cap), out.data_ptr(), to,
         ws.data_ptr(), ws.nbytes, _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _check(status)

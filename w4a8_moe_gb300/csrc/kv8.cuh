@@ -55,6 +55,7 @@ struct Kv8Attn {
     int warps;          // that the units go to
     int free_warps;     // of them those that need not wait for the tiled prefix
     float free_us;     // that the others wait, about
+    int beside;         // a tiled prefix runs beside
     int* cum;           // [B + 1] prefix sums of the sequences' units, left for the join
 };
 // The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key

@@ -113,10 +113,9 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
 // Every kernel of this library calls grid_dep_launch only after its own
 // grid_dep_wait has returned, except the block-FP8 activation quantizer, whose
 // only dependent (the block-FP8 GEMM) reads nothing but the weights before its
-// own wait, and the KV8 attention's kernels: the tiled prefix (launched after
-// everything before it) lets the kernel of the own keys run beside it, which
-// needs nothing of it and waits for it before it ends; the join, started early
-// by that one, reads the caller's lengths only until its own wait.
+// own wait, and the KV8 attention's kernel of the own keys beside a tiled prefix:
+// it needs nothing of the prefix and waits for it before it ends, and its
+// dependent, the join, reads only the caller's lengths before its own wait.
 __device__ __forceinline__ void grid_dep_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

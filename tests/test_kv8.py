@@ -134,7 +134,7 @@ class Batch:
             out.append(torch.cat(parts, 1))
         return out
 
-    def check(self, got, lse):
+    def check(self, got, lse, every=1):
         """Elementwise bounds from the arithmetic, none fitted to the outcome.
         The value that the kernel rounds to bf16 lies within `tol` of the exact
         one; rounding is monotone, so the output lies between the roundings of
@@ -145,7 +145,7 @@ class Batch:
         tail of f16's range (2^-25 of the largest weight, for each key)."""
         assert bool(torch.isfinite(got.float()).all())
         group = self.hq // self.hkv
-        for b in range(len(self.lens_list)):
+        for b in range(0, len(self.lens_list), every):
             n = self.prefix + self.lens_list[b]
             o, z = got[b].double(), lse[b].double()
             if n == 0:
@@ -336,6 +336,15 @@ def test_attention_batch_over_a_prefix(lib, batch, d):
     for prefix, mode in ((129, 0), (1000, 1), (2051, 0)):
         b = Batch(lens, prefix, 12, 2, d, 32, mode, seed=batch)
         b.check(*b.run(lib))
+
+
+@pytest.mark.parametrize("hq,hkv,d,mode", [(2, 1, 64, 0), (3, 1, 128, 1)])
+def test_attention_largest_batch(lib, hq, hkv, d, mode):
+    """4096 sequences, the most a call takes (every 37th checked)."""
+    lens = [(i * 7) % 40 for i in range(4096)]
+    for prefix in (0, 33, 500):
+        b = Batch(lens, prefix, hq, hkv, d, 16, mode, seed=20)
+        b.check(*b.run(lib), every=37)
 
 
 @pytest.mark.parametrize("prefix", [127, 128, 255, 256, 257, 383, 640, 4097])

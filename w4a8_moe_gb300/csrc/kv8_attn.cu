@@ -600,43 +600,45 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(
     grid_dep_wait();   // the join after this kernel also reads what the one before it wrote
 }
 
-// Adds up the pieces of a (sequence, query head): W warps take them in turn, a
-// lane D / 32 values. The fewer rows, the more warps take one: with few rows
-// each has many pieces, and only their number hides the loads' latency. Bound by
-// that latency: 1.5 us for one sequence, 4 us for 2048 rows of 13 pieces, 13 us for
-// 12288 rows of 5 (31 MB out of L2).
-constexpr int kJoinCta = 4;      // warps of a CTA where W < 4
+// Adds up the pieces of a (sequence, query head): W warps take them in turn, or,
+// where there are very many rows, half a warp (W = 0). The fewer rows, the more
+// warps take one: with few rows each has many pieces, and only their number hides
+// the loads' latency, which is what bounds this: 1.5 us for one sequence, 4 us for
+// 2048 rows of 13 pieces, 11 us for 12288 rows of 5 (31 MB out of L2).
+constexpr int kJoinCta = 4;      // warps of a CTA where a row has one or less
 constexpr int kJoinSums = 128;   // sequences up to which a warp sums their units itself
 template <int D, int W>
-__global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
-                                                                   const __grid_constant__ Kv8Prefix p, int R)
+__global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
+                                                                         const __grid_constant__ Kv8Prefix p, int R)
 {
-    constexpr int V = D / 32;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int head = W >= kJoinCta ? blockIdx.x : blockIdx.x * (kJoinCta / W) + warp / W;   // b * Hq + query head
-    const int first_piece = warp % W;
-    const int b = head / a.Hq, qh = head % a.Hq, h = qh / a.group, gi = qh % a.group;
+    constexpr int L = W ? 32 : 16;                  // lanes of a row
+    constexpr int V = D / L, F = V >= 4 ? 4 : 2;    // values of a lane, in groups of F that stand L F apart
+    constexpr int S = W ? W : 1;                    // strides over the pieces
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid % L;
+    const int head = W > 1 ? blockIdx.x : blockIdx.x * (kJoinCta * 32 / L) + tid / L;   // b * Hq + query head
+    const int first_piece = W > 1 ? warp : 0;
+    const bool there = head < a.B * a.Hq;
+    const int b = there ? head / a.Hq : 0, qh = there ? head - b * a.Hq : 0, h = qh / a.group, gi = qh - h * a.group;
     // units before the sequence's and all of them: a short sum over the lengths
     // while the kernel before is still at work, else what it left
     const bool sum_here = a.B <= kJoinSums;
     int before = 0, units = 0, all = 0;
     if (sum_here) {
-        for (int i = lane; i < a.B; i += 32) {
+        for (int i = lane; i < a.B; i += L) {
             const int n = seq_units(a, i);
             all += n;
             before += i < b ? n : 0;
             units += i == b ? n : 0;
         }
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) {
+        for (int x = L / 2; x > 0; x >>= 1) {
             all += __shfl_xor_sync(0xFFFFFFFFu, all, x);
             before += __shfl_xor_sync(0xFFFFFFFFu, before, x);
             units += __shfl_xor_sync(0xFFFFFFFFu, units, x);
         }
-    }
-    if (!sum_here) {
+    } else {
         grid_dep_wait();
-        if (a.max_pages && head < a.B * a.Hq) {
+        if (a.max_pages) {
             before = a.cum[b];
             units = a.cum[b + 1] - before;
             all = a.cum[a.B];
@@ -664,19 +666,19 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
         n2 += warp_of(line, first + units - 1) - w + 1;
         at_own = static_cast<int64_t>(line.pairs_p + b * line.hr + j + w - n1) * R + gi % R;
     }
-    // Lane i of a warp finds piece first_piece + W i of the row and its weight;
-    // then every lane reads its values of all of them. Nothing that is read
-    // waits for anything but the kernel before.
+    n2 = there ? n2 : 0;
     if (sum_here)
         grid_dep_wait();
-    if (W == 1 && head >= a.B * a.Hq)
-        return;
+    // Lane i of a row finds piece first_piece + S i and its weight; then every
+    // lane reads its values of all of them. Nothing that is read waits for
+    // anything but the kernel before. (Both halves of a warp go round together.)
+    const int most = W ? n2 : max(n2, __shfl_xor_sync(0xFFFFFFFFu, n2, 16));
     float top = -INFINITY, sum = 0.0f, acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
         acc[i] = 0.0f;
-    for (int k0 = first_piece; k0 < n2; k0 += 32 * W) {
-        const int k = k0 + W * lane;
+    for (int k0 = first_piece; k0 < most; k0 += L * S) {
+        const int k = k0 + S * lane;
         const float* src = a.part_o;
         float2 ml = make_float2(-INFINITY, 0.0f);
         if (k < n2) {
@@ -686,21 +688,25 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
             src = (tiled ? p.part_o : a.part_o) + at * D;
             ml = (tiled ? p.part_ml : a.part_ml)[at];
         }
-        const int n = min(32, (n2 - k0 + W - 1) / W);
-        constexpr int kAhead = 12;   // pieces whose values are on their way together
+        const int n = min(L, (n2 - k0 + S - 1) / S), rounds = min(L, (most - k0 + S - 1) / S);
+        constexpr int kAhead = W ? 12 : 6;   // pieces whose values are on their way together
         float v[kAhead][V];
         auto fetch = [&](int j0) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const float* from = reinterpret_cast<const float*>(
-                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), j0 + j & 31));
+                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), (j0 + j) % L, L));
                 if (j0 + j < n) {
-                    if (V == 4) {
-                        const float4 w = *(reinterpret_cast<const float4*>(from) + lane);
-                        v[j][0] = w.x, v[j][1] = w.y, v[j][V - 2] = w.z, v[j][V - 1] = w.w;
-                    } else {
-                        const float2 w = *(reinterpret_cast<const float2*>(from) + lane);
-                        v[j][0] = w.x, v[j][1] = w.y;
+#pragma unroll
+                    for (int i = 0; i < V; i += F) {
+                        const float* x = from + (i / F * L + lane) * F;
+                        if (F == 4) {
+                            const float4 w = *reinterpret_cast<const float4*>(x);
+                            v[j][i] = w.x, v[j][i + 1] = w.y, v[j][i + F - 2] = w.z, v[j][i + F - 1] = w.w;
+                        } else {
+                            const float2 w = *reinterpret_cast<const float2*>(x);
+                            v[j][i] = w.x, v[j][i + 1] = w.y;
+                        }
                     }
                 }
             }
@@ -708,26 +714,26 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
         fetch(0);
         float best = ml.x;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
+        for (int x = L / 2; x > 0; x >>= 1)
             best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, x));
         const float to = fmaxf(top, best);
         const float ref = to == -INFINITY ? 0.0f : to;
         const float f0 = ex2(top - ref), f1 = ex2(ml.x - ref);
         float l = ml.y * f1;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
+        for (int x = L / 2; x > 0; x >>= 1)
             l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
         sum = sum * f0 + l;
         top = to;
 #pragma unroll
         for (int i = 0; i < V; ++i)
             acc[i] *= f0;
-        for (int j0 = 0; j0 < n; j0 += kAhead) {
+        for (int j0 = 0; j0 < rounds; j0 += kAhead) {
             if (j0 > 0)
                 fetch(j0);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const float f = __shfl_sync(0xFFFFFFFFu, f1, j0 + j & 31);
+                const float f = __shfl_sync(0xFFFFFFFFu, f1, (j0 + j) % L, L);
                 if (j0 + j < n) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
@@ -737,18 +743,18 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
         }
     }
     if (W > 1) {
-        __shared__ float so[W][D];
-        __shared__ float2 sml[W];
+        __shared__ float so[S][D];
+        __shared__ float2 sml[S];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            so[warp][lane * V + i] = acc[i];
+            so[warp][i * L + lane] = acc[i];
         if (lane == 0)
             sml[warp] = make_float2(top, sum);
         __syncthreads();
         if (warp > 0)
             return;
 #pragma unroll
-        for (int w = 1; w < W; ++w)
+        for (int w = 1; w < S; ++w)
             top = fmaxf(top, sml[w].x);
         const float ref = top == -INFINITY ? 0.0f : top;
         sum = 0.0f;
@@ -756,25 +762,31 @@ __global__ void __launch_bounds__((W > kJoinCta ? W : kJoinCta) * 32) kv8_join_k
         for (int i = 0; i < V; ++i)
             acc[i] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
+        for (int w = 0; w < S; ++w) {
             const float f = ex2(sml[w].x - ref);
             sum += sml[w].y * f;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                acc[i] += so[w][lane * V + i] * f;
+                acc[i] += so[w][i * L + lane] * f;
         }
     }
+    if (!there)
+        return;
     const bool empty = sum == 0.0f;
-    uint32_t r[V / 2];
+    uint16_t* dst = a.out + static_cast<int64_t>(head) * D;
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-        r[i] = static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[2 * i] / sum)) |
-               (static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[2 * i + 1] / sum)) << 16);
-    uint16_t* dst = a.out + static_cast<int64_t>(head) * D + lane * V;
-    if (V == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[V / 2 - 1]);
-    else
-        *reinterpret_cast<uint32_t*>(dst) = r[0];
+    for (int i = 0; i < V; i += F) {
+        uint32_t r[F / 2];
+#pragma unroll
+        for (int j = 0; j < F; j += 2)
+            r[j / 2] = static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[i + j] / sum)) |
+                       (static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[i + j + 1] / sum)) << 16);
+        uint16_t* x = dst + (i / F * L + lane) * F;
+        if (F == 4)
+            *reinterpret_cast<uint2*>(x) = make_uint2(r[0], r[F / 2 - 1]);
+        else
+            *reinterpret_cast<uint32_t*>(x) = r[0];
+    }
     if (a.lse && lane == 0)
         a.lse[head] = empty ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
@@ -797,15 +809,19 @@ static cudaError_t launch_pieces(const Kv8Attn& a, cudaStream_t s)
 template <int D>
 static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
 {
-    // Warps a row: 17 sequences of 16 heads, 40 splits (272 rows), us in all with 8 / 4
-    // 12.7 / 14.6; 64 of 32 heads, 11 splits (2048 rows) with 4 / 1 30.4 / 27.5.
+    // Warps a row, us in all: 17 sequences of 16 heads, 40 splits (272 rows), 8 / 4 12.7 /
+    // 14.6; 64 of 32 heads, 11 splits (2048 rows), 4 / 1 30.4 / 27.5; 128 of 48 heads, 5
+    // splits and own keys (6144 rows), 1 / half 101.9 / 104.5; 256 of 48 heads and 16 own
+    // keys (12288 rows) 20.3 / 16.4.
     const int heads = a.B * a.Hq;
     if (heads <= num_sms || (p.splits > 16 && heads <= 4 * num_sms))
         return launch_dependent(kv8_join_kernel<D, 8>, dim3(heads), dim3(8 * 32), 0, s, a, p, R);
     if (heads <= 2 * num_sms || (p.splits > 8 && heads <= 4 * num_sms))
         return launch_dependent(kv8_join_kernel<D, 4>, dim3(heads), dim3(4 * 32), 0, s, a, p, R);
-    return launch_dependent(kv8_join_kernel<D, 1>, dim3((heads + kJoinCta - 1) / kJoinCta), dim3(kJoinCta * 32), 0, s, a,
-                            p, R);
+    const bool half = heads > 48 * num_sms;
+    const int rows = kJoinCta * (half ? 2 : 1);   // of a CTA
+    return launch_dependent(half ? kv8_join_kernel<D, 0> : kv8_join_kernel<D, 1>, dim3((heads + rows - 1) / rows),
+                            dim3(kJoinCta * 32), 0, s, a, p, R);
 }
 
 // Whether the tensor-core kernel takes the prefix. It costs a third launch and

@@ -368,6 +368,22 @@ def test_attention_prefix_and_own_keys_side_by_side(lib, batch, hq, hkv, d, pref
     b.check(*b.run(lib))
 
 
+@pytest.mark.parametrize("batch,hq,hkv,d,own,extra,mode", [
+    (1, 16, 1, 128, 9000, 1, 1),     # many pieces a row, joined by eight warps
+    (3, 8, 8, 64, 5000, 1, 0),
+    (70, 8, 1, 64, 1500, 1, 1),      # joined by four
+    (70, 12, 1, 64, 2000, 200, 0),
+    (70, 16, 1, 128, 900, 200, 1),   # tables wide enough for the form of 16 rows with more blocks an SM
+    (70, 16, 1, 128, 900, 1, 0),     # and not
+    (260, 6, 2, 128, 70, 1, 0),      # four units a warp
+])
+def test_attention_own_keys_alone(lib, batch, hq, hkv, d, own, extra, mode):
+    """Every way of cutting the sequences' own keys into pieces and of joining them."""
+    lens = [own - 37 * i % own if i % 6 != 5 else i % 3 for i in range(batch)]
+    b = Batch(lens, 0, hq, hkv, d, 64, mode, seed=own, extra=extra)
+    b.check(*b.run(lib))
+
+
 @pytest.mark.parametrize("mode", [0, 1])
 @pytest.mark.parametrize("batch", [2, 40])
 def test_attention_logit_cap(lib, mode, batch):

@@ -26,7 +26,6 @@ cudaError_t launch_kv8_read(const Kv8Rows& a, const uint8_t* k_cache, const uint
 // ---- attention
 constexpr int kKv8MaxBatch = 4096;  // the split's prefix sums live in shared memory
 constexpr int kKv8Unit = 16;        // keys per unit of the split (a unit never crosses a page)
-constexpr int kKv8MinUnits = 2;     // units a warp gets at least
 constexpr int kKv8MaxWarps = 152 * 16;   // warps the units are divided over, at most
 
 struct Kv8Attn {
@@ -54,7 +53,8 @@ struct Kv8Attn {
     float* lse;
     int warps;          // that the units go to
     int free_warps;     // of them those that need not wait for the tiled prefix
-    float free_us;     // that the others wait, about
+    int spread;         // warps up to which the units are spread by twos
+    float free_us;      // that the others wait, about
     int beside;         // a tiled prefix runs beside
     int* cum;           // [B + 1] prefix sums of the sequences' units, left for the join
 };

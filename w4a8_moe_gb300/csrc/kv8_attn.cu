@@ -90,6 +90,16 @@ __device__ __forceinline__ int seq_units(const Kv8Attn& a, int b)
 {
     return (seq_len(a, b) + kKv8Unit - 1) / kKv8Unit;
 }
+// Warps for so many units. Two units are in flight at once, so a second pair of
+// them costs a warp another latency (one sequence of 8 heads and 64 keys: 8.4 us
+// against 7.0); more pieces cost the join (256 of 48 heads and 60 keys: 22.6 us by
+// twos, 18.9 by fours). So few units are spread by twos, up to `spread` warps, and
+// more by fours, up to all warps.
+__host__ __device__ __forceinline__ int warps_for(int64_t units, int spread, int most)
+{
+    const int u = units < 1 << 16 ? static_cast<int>(units) : 1 << 16;
+    return min(max(min((u + 1) >> 1, spread), u >> 2), most);
+}
 __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
 {
     Line l;
@@ -114,10 +124,8 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
             l.U1 = u1 < l.U ? u1 : l.U;
         }
     }
-    const int64_t n1 = (l.U1 + kKv8MinUnits - 1) / kKv8MinUnits;
-    const int64_t n2 = (l.U - l.U1 + kKv8MinUnits - 1) / kKv8MinUnits;
-    l.n1 = static_cast<int>(n1 < a.free_warps ? n1 : a.free_warps);
-    l.n = l.n1 + static_cast<int>(n2 < late ? n2 : late);
+    l.n1 = warps_for(l.U1, a.spread, a.free_warps);
+    l.n = l.n1 + (late > 0 ? warps_for(l.U - l.U1, a.spread, late) : 0);
     return l;
 }
 // (32-bit division where the numbers allow it: warps are fewer than 2^12.)
@@ -229,8 +237,8 @@ int kv8_attn_row_tile(int group) { return group <= 8 ? 8 : 16; }
 // 2c, 2c+1, 2c+8, 2c+9, chunk g. P^T passes from the first product's layout to
 // the second's by an 8 x 8 transpose. A thread's rows are 2c and 2c + 1 in both,
 // so the running statistics need no exchange.
-template <int D, int NT, bool TOK>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv8_attn_kernel(const __grid_constant__ Kv8Attn a)
+template <int D, int NT, bool TOK, int PER_SM>
+__global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __grid_constant__ Kv8Attn a)
 {
     using S = Ring<D>;
     constexpr int R = 8 * NT;      // rows of a tile
@@ -793,11 +801,11 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
 
 static int ring_smem(int D, int B) { return kWarps * (D == 128 ? Ring<128>::total : Ring<64>::total) + (B + 1) * 4; }
 
-template <int D, int NT, bool TOK>
+template <int D, int NT, bool TOK, int PER_SM>
 static cudaError_t launch_pieces(const Kv8Attn& a, cudaStream_t s)
 {
     const int smem = ring_smem(D, a.B);
-    auto kern = kv8_attn_kernel<D, NT, TOK>;
+    auto kern = kv8_attn_kernel<D, NT, TOK, PER_SM>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
@@ -806,17 +814,35 @@ static cudaError_t launch_pieces(const Kv8Attn& a, cudaStream_t s)
     return launch_dependent(kern, dim3(a.warps / kWarps), dim3(kWarps * 32), smem, s, a);
 }
 
+template <int D, int NT, int PER_SM>
+static cudaError_t launch_pieces(const Kv8Attn& a, int per_token, cudaStream_t s)
+{
+    return per_token ? launch_pieces<D, NT, true, PER_SM>(a, s) : launch_pieces<D, NT, false, PER_SM>(a, s);
+}
+
+// Units of the sequences' own keys if they fill their page tables: what the host can know of them.
+static int64_t most_units(const Kv8Attn& a)
+{
+    return static_cast<int64_t>(a.B) * a.Hkv * a.tiles * ((a.max_pages << a.page_shift) / kKv8Unit);
+}
+
 template <int D>
 static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
 {
-    // Warps a row, us in all: 17 sequences of 16 heads, 40 splits (272 rows), 8 / 4 12.7 /
-    // 14.6; 64 of 32 heads, 11 splits (2048 rows), 4 / 1 30.4 / 27.5; 128 of 48 heads, 5
-    // splits and own keys (6144 rows), 1 / half 101.9 / 104.5; 256 of 48 heads and 16 own
+    // Warps a row, us in all. Few rows: 17 sequences of 16 heads over a prefix in 40
+    // splits (272 rows), 8 / 4 12.7 / 14.6; 32 sequences of 8 heads, 8192 own keys (76
+    // pieces), 19.4 / 20.6. More: 64 sequences of 8 heads, 1000-4000 own keys (512 rows of
+    // up to 38 pieces), 4 / 1 18.6 / 24.2; 64 of 16 heads, D 64 (1024 rows of 28), 20.0 /
+    // 23.6; but 17 of 48 heads, 4000 own keys (816 rows of 17), 34.6 / 32.6, and 64 of 32
+    // heads over a prefix in 11 splits (2048 rows) 30.4 / 27.5. Very many: 128 of 48 heads,
+    // 5 splits and own keys (6144 rows), 1 / half 101.9 / 104.5; 256 of 48 heads and 16 own
     // keys (12288 rows) 20.3 / 16.4.
-    const int heads = a.B * a.Hq;
-    if (heads <= num_sms || (p.splits > 16 && heads <= 4 * num_sms))
+    const int heads = a.B * a.Hq, pairs = a.B * a.Hkv * a.tiles;
+    const int pieces = p.splits + warps_for(most_units(a), a.spread, a.warps) / pairs;
+    if (heads <= num_sms || (pieces > 16 && heads <= 2 * num_sms) || (p.splits > 16 && heads <= 4 * num_sms))
         return launch_dependent(kv8_join_kernel<D, 8>, dim3(heads), dim3(8 * 32), 0, s, a, p, R);
-    if (heads <= 2 * num_sms || (p.splits > 8 && heads <= 4 * num_sms))
+    if (heads <= 2 * num_sms || (p.splits > 8 && heads <= 4 * num_sms) ||
+        (pieces > 16 && heads <= 4 * num_sms) || (pieces > 24 && heads <= 8 * num_sms))
         return launch_dependent(kv8_join_kernel<D, 4>, dim3(heads), dim3(4 * 32), 0, s, a, p, R);
     const bool half = heads > 48 * num_sms;
     const int rows = kJoinCta * (half ? 2 : 1);   // of a CTA
@@ -840,8 +866,12 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
 {
     Kv8Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
+    // CTAs an SM: as many as registers allow, but for 16 rows of D 128, which spill at
+    // three. 16 query and 1 kv heads, us at two / three: 64 sequences of 4000 own keys
+    // 25.3 / 28.1, 64 of 8000 39.3 / 42.1, 100 of 8000 55.7 / 51.9, 256 of 8000 124 / 114.
+    const bool two = R == 16 && D == 128 && most_units(a) < 40000;
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
-    const int per_sm = min(R == 8 ? 4 : 3, fit) * kWarps;
+    const int per_sm = min(R == 8 ? 4 : two ? 2 : 3, fit) * kWarps;
     a.warps = num_sms * per_sm;
     // a CTA of the tiled prefix takes a whole SM; the others' warps can start at once
     const int taken = p.splits * a.Hkv * p.row_pairs;
@@ -849,6 +879,11 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
     a.free_us = p.us;
     a.warps = min(a.warps, kKv8MaxWarps);
     a.free_warps = min(a.free_warps, kKv8MaxWarps);
+    // by twos up to 128 pieces a pair (one sequence of 16 heads and 30000 keys, 937 / 468
+    // pieces: 27.2 / 16.6 us) and 1536 warps (64 of 8 heads and 1000 keys, 1024 / 1536 /
+    // 2048: 12.6 / 12.2 / 13.3), or 2048 where a pair then has 8 pieces at most
+    const int64_t pairs = static_cast<int64_t>(a.Hkv) * (a.ptiles + static_cast<int64_t>(a.B) * a.tiles);
+    a.spread = static_cast<int>(min(max(min(8 * pairs, int64_t{2048}), int64_t{1536}), 128 * pairs));
     cudaError_t e;
     if (p.splits) {
         e = launch_kv8_prefix(a, p, D, per_token, s);
@@ -858,11 +893,11 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
     if (a.max_pages || a.ptiles) {
         a.beside = p.splits > 0;
         if (D == 128)
-            e = R == 8 ? (per_token ? launch_pieces<128, 1, true>(a, s) : launch_pieces<128, 1, false>(a, s))
-                       : (per_token ? launch_pieces<128, 2, true>(a, s) : launch_pieces<128, 2, false>(a, s));
+            e = R == 8 ? launch_pieces<128, 1, 4>(a, per_token, s)
+                : two  ? launch_pieces<128, 2, 2>(a, per_token, s)
+                       : launch_pieces<128, 2, 3>(a, per_token, s);
         else
-            e = R == 8 ? (per_token ? launch_pieces<64, 1, true>(a, s) : launch_pieces<64, 1, false>(a, s))
-                       : (per_token ? launch_pieces<64, 2, true>(a, s) : launch_pieces<64, 2, false>(a, s));
+            e = R == 8 ? launch_pieces<64, 1, 4>(a, per_token, s) : launch_pieces<64, 2, 3>(a, per_token, s);
         if (e != cudaSuccess)
             return e;
     }

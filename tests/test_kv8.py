@@ -373,6 +373,7 @@ def test_attention_prefix_and_own_keys_side_by_side(lib, batch, hq, hkv, d, pref
     (3, 8, 8, 64, 5000, 1, 0),
     (70, 8, 1, 64, 1500, 1, 1),      # joined by four
     (70, 12, 1, 64, 2000, 200, 0),
+    (30, 28, 4, 128, 1000, 1, 1),    # by two
     (70, 16, 1, 128, 900, 200, 1),   # tables wide enough for the form of 16 rows with more blocks an SM
     (70, 16, 1, 128, 900, 1, 0),     # and not
     (260, 6, 2, 128, 70, 1, 0),      # four units a warp

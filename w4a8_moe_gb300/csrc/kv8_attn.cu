@@ -831,12 +831,13 @@ static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int 
 {
     // Warps a row, us in all. Few rows: 17 sequences of 16 heads over a prefix in 40
     // splits (272 rows), 8 / 4 12.7 / 14.6; 32 sequences of 8 heads, 8192 own keys (76
-    // pieces), 19.4 / 20.6. More: 64 sequences of 8 heads, 1000-4000 own keys (512 rows of
-    // up to 38 pieces), 4 / 1 18.6 / 24.2; 64 of 16 heads, D 64 (1024 rows of 28), 20.0 /
-    // 23.6; but 17 of 48 heads, 4000 own keys (816 rows of 17), 34.6 / 32.6, and 64 of 32
-    // heads over a prefix in 11 splits (2048 rows) 30.4 / 27.5. Very many: 128 of 48 heads,
-    // 5 splits and own keys (6144 rows), 1 / half 101.9 / 104.5; 256 of 48 heads and 16 own
-    // keys (12288 rows) 20.3 / 16.4.
+    // pieces), 8 / 4 19.4 / 20.6. More: 64 of 8 heads, 1000-4000 own keys (512 rows of up
+    // to 38 pieces), 4 / 1 18.6 / 24.2; 64 of 16 heads of D 64, 2000-8000 (1024 rows of
+    // 28), 4 / 1 19.9 / 23.6. Between: 17 of 48 heads, 1000-4000 (816 rows of 17), 2 / 1
+    // 21.9 / 23.4; but 64 of 32 heads over a prefix in 11 splits (2048 rows, blocks of two
+    // warps no longer fit at once), 2 / 1 31.0 / 28.8. Very many: 128 of 48 heads, 5 splits
+    // and own keys (6144 rows), 1 / half 101.9 / 104.5; 256 of 48 heads and 16 own keys
+    // (12288 rows) 20.3 / 16.4.
     const int heads = a.B * a.Hq, pairs = a.B * a.Hkv * a.tiles;
     const int pieces = p.splits + warps_for(most_units(a), a.spread, a.warps) / pairs;
     if (heads <= num_sms || (pieces > 16 && heads <= 2 * num_sms) || (p.splits > 16 && heads <= 4 * num_sms))
@@ -844,6 +845,8 @@ static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int 
     if (heads <= 2 * num_sms || (p.splits > 8 && heads <= 4 * num_sms) ||
         (pieces > 16 && heads <= 4 * num_sms) || (pieces > 24 && heads <= 8 * num_sms))
         return launch_dependent(kv8_join_kernel<D, 4>, dim3(heads), dim3(4 * 32), 0, s, a, p, R);
+    if (pieces > 12 && heads <= 8 * num_sms)
+        return launch_dependent(kv8_join_kernel<D, 2>, dim3(heads), dim3(2 * 32), 0, s, a, p, R);
     const bool half = heads > 48 * num_sms;
     const int rows = kJoinCta * (half ? 2 : 1);   // of a CTA
     return launch_dependent(half ? kv8_join_kernel<D, 0> : kv8_join_kernel<D, 1>, dim3((heads + rows - 1) / rows),

@@ -12,7 +12,7 @@ namespace w4a8 {
 
 namespace {
 
-constexpr int kRowThreads = 128;   // (writing 32768 tokens, us: 64 33.7, 128 31.8, 256 32.4)
+constexpr int kRowThreads = 128;   // (writing 32768 tokens, us: 64 34.0, 128 32.0, 256 32.6)
 constexpr float kInv448Hi = static_cast<float>(1.0 / 448.0);
 constexpr float kInv448Lo = static_cast<float>(1.0 / 448.0 - static_cast<double>(kInv448Hi));
 
@@ -112,8 +112,9 @@ __device__ __forceinline__ uint32_t row_top(uint32_t top)
 }  // namespace
 
 // Bound by memory: 32768 tokens of 8 heads of 128 with per-token scales (203.6
-// MB) take 30.9 us, 6.6 TB/s or 97 % of a copy's rate (with the loads behind the
-// slot's 35.0); 32 tokens take 2.1 us, a launch and two dependent loads.
+// MB) take 32.0 us, 6.4 TB/s or 94 % of a copy's rate, three sets of tensors in
+// turn (with the loads behind the slot's 35.0; with streaming loads, `.cs`, 33.0);
+// 32 tokens take 2.1 us, a launch and two dependent loads.
 //
 // code = E4M3(x / s): fp32 division, round to nearest even, saturating; a NaN
 // keeps the NaN code. Per-token scales come from the row itself:
@@ -132,13 +133,13 @@ __global__ void __launch_bounds__(kRowThreads) kv8_write_kernel(const __grid_con
     grid_dep_wait();
     const RowAt r = row_at<D>(a, slots);
     const int lane = threadIdx.x % L;
-    uint4 raw[2][2];   // read once, and whatever the slot is: the loads need not wait for it
+    uint4 raw[2][2];   // read whatever the slot is: the loads need not wait for it
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const uint16_t* src = (y ? v + r.t * a.v_stride : k + r.t * a.k_stride) + static_cast<int64_t>(r.h) * D;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            raw[y][i] = r.live ? __ldcs(reinterpret_cast<const uint4*>(src) + i * L + lane) : make_uint4(0, 0, 0, 0);
+            raw[y][i] = r.live ? __ldg(reinterpret_cast<const uint4*>(src) + i * L + lane) : make_uint4(0, 0, 0, 0);
     }
     const bool ok = r.live && r.slot >= 0 && r.slot < a.num_slots;
     const int64_t at = ok ? cache_row(a, r.slot, r.h) : 0;

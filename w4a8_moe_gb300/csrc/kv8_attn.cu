@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
 // Adds up the pieces of a (sequence, query head): W warps take them in turn, or,
 // where there are very many rows, half a warp (W = 0). The fewer rows, the more
 // warps take one: with few rows each has many pieces, and only their number hides
-// the loads' latency, which is what bounds this: 1.5 us for one sequence, 4 us for
-// 2048 rows of 13 pieces, 11 us for 12288 rows of 5 (31 MB out of L2).
+// the loads' latency, which is what bounds this; with very many rows the warps of
+// others do, and each takes few registers.
 constexpr int kJoinCta = 4;      // warps of a CTA where a row has one or less
 constexpr int kJoinSums = 128;   // sequences up to which a warp sums their units itself
 template <int D, int W>
@@ -697,7 +697,10 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
             ml = (tiled ? p.part_ml : a.part_ml)[at];
         }
         const int n = min(L, (n2 - k0 + S - 1) / S), rounds = min(L, (most - k0 + S - 1) / S);
-        constexpr int kAhead = W ? 12 : 6;   // pieces whose values are on their way together
+        // Pieces whose values are on their way together: many where the rows are few (64
+        // sequences over 8192, 8 / 12 / 16 / 20: 29.7 / 28.6 / 27.9 / 28.1 us), else few, so
+        // that more rows fit an SM (100 of 48 heads and 60 own keys, 4 / 3 / 2 10.8 / 10.6 / 10.3).
+        constexpr int kAhead = W ? 16 : D == 128 ? 2 : 6;
         float v[kAhead][V];
         auto fetch = [&](int j0) {
 #pragma unroll
@@ -835,9 +838,10 @@ static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int 
     // to 38 pieces), 4 / 1 18.6 / 24.2; 64 of 16 heads of D 64, 2000-8000 (1024 rows of
     // 28), 4 / 1 19.9 / 23.6. Between: 17 of 48 heads, 1000-4000 (816 rows of 17), 2 / 1
     // 21.9 / 23.4; but 64 of 32 heads over a prefix in 11 splits (2048 rows, blocks of two
-    // warps no longer fit at once), 2 / 1 31.0 / 28.8. Very many: 128 of 48 heads, 5 splits
-    // and own keys (6144 rows), 1 / half 101.9 / 104.5; 256 of 48 heads and 16 own keys
-    // (12288 rows) 20.3 / 16.4.
+    // warps no longer fit at once), 2 / 1 31.0 / 28.8. Many, 1 / half: 64 of 48 heads and 60
+    // own keys (3072 rows) 12.3 / 9.7, over 20000 tokens 42.0 / 41.1; 128 over 32768 and own
+    // keys (6144 rows, the most pieces) 102.9 / 103.4, 128 of 900 own keys 39.8 / 34.6; but
+    // 40 of 48 heads and 1000 (1920 rows) 17.1 / 19.5.
     const int heads = a.B * a.Hq, pairs = a.B * a.Hkv * a.tiles;
     const int pieces = p.splits + warps_for(most_units(a), a.spread, a.warps) / pairs;
     if (heads <= num_sms || (pieces > 16 && heads <= 2 * num_sms) || (p.splits > 16 && heads <= 4 * num_sms))
@@ -847,7 +851,7 @@ static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int 
         return launch_dependent(kv8_join_kernel<D, 4>, dim3(heads), dim3(4 * 32), 0, s, a, p, R);
     if (pieces > 12 && heads <= 8 * num_sms)
         return launch_dependent(kv8_join_kernel<D, 2>, dim3(heads), dim3(2 * 32), 0, s, a, p, R);
-    const bool half = heads > 48 * num_sms;
+    const bool half = heads > 18 * num_sms;
     const int rows = kJoinCta * (half ? 2 : 1);   // of a CTA
     return launch_dependent(half ? kv8_join_kernel<D, 0> : kv8_join_kernel<D, 1>, dim3((heads + rows - 1) / rows),
                             dim3(kJoinCta * 32), 0, s, a, p, R);

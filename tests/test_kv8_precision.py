@@ -1,0 +1,93 @@
+"""What the attention over the FP8 cache keeps of keys that stand beside much
+heavier ones, against 64 bits."""
+import math
+
+import pytest
+import torch
+
+from test_kv8 import Batch, lib  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def many(b, rows, seed=0):
+    """`rows` sequences over the very same keys, each with a query of its own: positive, so that the scores follow the
+    keys' sums."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    b.q = (1.0 + 0.05 * torch.randn(rows, b.hq, b.d, generator=gen, device="cuda")).to(torch.bfloat16)
+    b.table = b.table[:1].repeat(rows, 1)
+    b.lens = b.lens[:1].repeat(rows)
+    b.lens_list = b.lens_list[:1] * rows
+    return b
+
+
+def key_at(b, i):
+    """Page and offset of key i of the prefix, or of the own keys where there is no prefix."""
+    pages = b.prefix_pages if b.prefix else b.table[0]
+    return int(pages[i // b.page]), i % b.page
+
+
+def scores_and_values(b, row):
+    k, v = b.keys(row)
+    q = b.q[row].double().reshape(b.hkv, -1, b.d)
+    s = q @ k.transpose(1, 2) * b.scale
+    # as in Batch.check: the fp32 sum of D products, q in f16, the scaling and exponent
+    size = (q.abs() @ k.abs().transpose(1, 2)) * abs(b.scale)
+    tiny = q.abs().amax(-1, keepdim=True) * k.abs().sum(-1)[:, None] * abs(b.scale)
+    ds = size * (b.d + 8) * 2.0 ** -23 + tiny * 2.0 ** -25 + 2.0 ** -21 * s.abs()
+    if b.cap:
+        s = b.cap * torch.tanh(s / b.cap)
+        ds = ds + 2.0 ** -20 * b.cap
+    return s, ds.amax(-1, keepdim=True) + 2.0 ** -21, v
+
+
+def check(b, out, lse, row, floor):
+    """Values are of one sign, so the output is as large as the sum of its parts and its error is counted against
+    itself: 2^-11 for the weights' rounding, twice a score's error, and `floor` for what f16's smallest numbers lose,
+    which has to be small against the output for the bound to say anything."""
+    s, ds, v = scores_and_values(b, row)
+    w = torch.softmax(s, -1)
+    want = w @ v
+    lost = floor(w, v, row)
+    assert bool((lost <= 2.0 ** -8 * want).all())
+    tol = (2.0 ** -11 + 2 * ds) * want * 1.01 + lost + 1e-30
+    o = out[row].double().reshape(want.shape)
+    low, high = (x.float().to(torch.bfloat16).double() for x in (want - tol, want + tol))
+    assert bool(((o >= low) & (o <= high)).all()), (row, float(((o - want) / want).abs().max()))
+    z = torch.logsumexp(s, -1)
+    assert bool(((lse[row].double().reshape(z.shape) - z).abs() <= ds[..., 0] + 2.0 ** -21 * (1 + z.abs())).all())
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("rows,hq,hkv,d,prefix,own,share", [
+    (60, 12, 2, 128, 65536, 0, 0.996),     # the prefix on the tensor cores, many ranges of it and one
+    (811, 48, 8, 64, 32768, 0, 0.998),
+    (300, 8, 8, 128, 0, 6000, 0.9996),     # own keys, long pieces of them
+    (300, 16, 1, 64, 0, 6000, 0.9996),
+    (2, 8, 2, 128, 900, 0, 0.9999),        # a short prefix among the own keys' pieces
+])
+def test_light_keys_beside_a_dominant_one_without_value(lib, mode, rows, hq, hkv, d, prefix, own, share):
+    """One key has nearly all of the weight and a value of zero: the output is the others' alone. A weight is rounded
+    where f16 has its smallest steps to 2^-25 of the unit, and the heaviest key of its piece stands 2^8 above the
+    unit at least: 2^-33 of the largest weight for each key."""
+    b = many(Batch([own], prefix, hq, hkv, d, 64, mode, seed=21, q_scale=1.0), rows)
+    b.v &= 0x7F
+    n = prefix + own
+    page, off = key_at(b, n // 3)
+    if mode:   # its value's scale is like the others'
+        b.vs[page, :, off] = b.vs[page, :, off - 1]
+    b.v[page, :, off] = 0
+    want = math.log(share / (1 - share) * n)
+    for h in range(hkv):   # all of its elements alike: its score is their value times the query's sum
+        scale = float(b.ks[page, h, off] if mode else b.ks[h])
+        x = torch.tensor([want / math.sqrt(d) / scale])
+        if mode and float(x) > 448:
+            b.ks[page, h, off] *= float(x) / 448
+        b.k[page, h, off] = x.clamp(max=448).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    out, lse = b.run(lib)
+
+    def floor(w, v, row):
+        return w.amax(-1, keepdim=True) * v.sum(1)[:, None] * 2.0 ** -33
+
+    for row in range(0, rows, max(1, rows // 4)):
+        check(b, out, lse, row, floor)

@@ -94,6 +94,24 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
         : "r"(w));
 }
 
+// A softmax weight goes into the second product in f16, relative to its row's
+// running reference. The reference is raised only when a weight would pass
+// 2^kWeightMost over it, and then to 2^kWeightTop under the largest one. So the
+// heaviest key of a piece stands 2^kWeightTop over f16's 1 at least, a weight loses
+// bits only below 2^-22 of that one, and none of them loses more than 2^-33 of it:
+// many light keys beside one that has nearly all of the weight, but no value, still
+// add up right. What is left above is for the maximum to grow without the
+// accumulators being rescaled (kWeightTop 7 / 8 / 10, us: 128 sequences over 32768
+// tokens 101.7 / 102.2 / 103.8, 256 over 65536 260.6 / 261.4 / 264.2).
+constexpr float kWeightTop = 8.0f;
+constexpr float kWeightMost = 15.0f;
+// Per-token scales: what is compared, and what goes into f16, is the weight times
+// its value's scale, and the reference carries the values' size too. Smaller scales
+// count as kLeastScale there, which keeps the weights themselves, and their sum
+// over up to 2^30 keys, inside fp32.
+constexpr float kLeastScale = 0x1p-64f;
+constexpr float kLeastScaleLog2 = -64.0f;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x)

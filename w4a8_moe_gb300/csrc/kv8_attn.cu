@@ -25,12 +25,7 @@ namespace {
 constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
 constexpr int kStages = 2;   // units in flight per warp
 constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
-// A row's reference exponent is raised only when a weight passes 2^8 under it:
-// weights then stay far inside f16 and the row's accumulators are hardly ever
-// rescaled. With per-token scales what is compared, and what goes into f16, is
-// the weight times its value's scale: the reference then carries the values'
-// size too, and drops out of o / l.
-constexpr float kMostWeight = 256.0f;
+constexpr float kMostWeight = 0x1p15f;   // 2^kWeightMost
 constexpr float kLowest = -1e30f;   // the reference of a row without keys
 
 // D[16x8] += A[16x16] B[16x8], f16 operands, fp32 accumulators.
@@ -520,7 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
                 for (int k = 0; k < 4; ++k) {
                     p[t][k] = ex2(s[t][k] - m[t][k & 1]);
                     // (the second bound holds a weight in range where its value's scale is 0)
-                    top = fmaxf(top, TOK ? p[t][k] * fmaxf(fabsf(vs[k >> 1]), 0x1p-92f) : p[t][k]);
+                    top = fmaxf(top, TOK ? p[t][k] * fmaxf(fabsf(vs[k >> 1]), kLeastScale) : p[t][k]);
                 }
             return top;
         };
@@ -531,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1)
                     lift = fmaxf(lift, __shfl_xor_sync(0xFFFFFFFFu, lift, x));
-                lift = fmaxf(log2f(lift), -100.0f);
+                lift = fmaxf(log2f(lift), kLeastScaleLog2);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -541,7 +536,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    const float to = fmaxf(m[t][y], top + lift);
+                    const float to = fmaxf(m[t][y], top + lift - kWeightTop);
                     const float f = ex2(m[t][y] - to);
                     m[t][y] = to;
                     l[t][y] *= f;

@@ -45,7 +45,6 @@ constexpr int kRaw = 6;           // raw slots
 // call of some hundred.)
 static_assert(kRaw % kPairs == 0, "a raw slot has one pair of readers");
 constexpr int kScaleRing = 4;     // tiles whose per-token scales are held
-constexpr float kSlack = 8.0f;    // see kv8_attn.cu
 
 template <int D>
 struct Smem {
@@ -333,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             F2 l0(0.0f, 0.0f), l1(0.0f, 0.0f);
             const float* scales = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + L::scales);
             // What a tile does to the row, scores in units of c:
-            // the reference raised where the largest weight asks for it,
+            // the reference raised where the largest weight asks for it (kWeightMost),
             auto raise = [&](int i, float best) {
-                if (__any_sync(0xFFFFFFFFu, best > m + kSlack)) {
-                    const float next = fmaxf(m, best);
+                if (__any_sync(0xFFFFFFFFu, best > m + kWeightMost)) {
+                    const float next = fmaxf(m, best - kWeightTop);
                     const float f = next == -INFINITY ? 1.0f : ex2(m - next);
                     m = next;
                     l0 = mul2(l0, F2(f, f));
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1)
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-                    lift = fmaxf(log2f(v), -100.0f);
+                    lift = fmaxf(log2f(v), kLeastScaleLog2);
                 }
                 if (!wait_warp(kSFull + t, i & 1))
                     return false;

@@ -412,8 +412,12 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
  *   For sequence b, head i and its keys j (the prefix's, then its own):
  *     s_j = sm_scale * sum_d q_d * k_j,d ;  logit_cap > 0: s_j = logit_cap * tanh(s_j / logit_cap)
  *     out [B, Hq, D] bf16 = bf16(sum_j softmax(s)_j * v_j), lse [B, Hq] fp32 = log sum_j exp(s_j)
- *   with fp32 scores, statistics and sums; the softmax weights enter the second
- *   product in f16, relative to a running reference. A sequence without any key
+ *   with fp32 scores, statistics and sums (a capped score is off by 2^-20 of the
+ *   cap at most). The softmax weights enter the second product in f16, relative
+ *   to a running reference: each is off by 2^-11 of itself and 2^-33 of the
+ *   largest one. With scale_mode 1 that is the weight times its value's scale, off
+ *   by 2^-11 of itself and 2^-27 of the largest such product among the keys whose
+ *   values are not all zero, whatever their scales. A sequence without any key
  *   has out = 0 and lse = -infinity. lse may be NULL. Cache bytes behind the
  *   last token of a page have no influence. The same call gives the same bits.
  *   Several query tokens of one sequence are several rows that share its pages,

@@ -44,12 +44,12 @@ def scores_and_values(b, row):
 def check(b, out, lse, row, floor):
     """Values are of one sign, so the output is as large as the sum of its parts and its error is counted against
     itself: 2^-11 for the weights' rounding, twice a score's error, and `floor` for what f16's smallest numbers lose,
-    which has to be small against the output for the bound to say anything."""
+    which has to be small against the output's row for the bound to say anything."""
     s, ds, v = scores_and_values(b, row)
     w = torch.softmax(s, -1)
     want = w @ v
     lost = floor(w, v, row)
-    assert bool((lost <= 2.0 ** -8 * want).all())
+    assert bool((lost <= 2.0 ** -8 * want.amax(-1, keepdim=True)).all())
     tol = (2.0 ** -11 + 2 * ds) * want * 1.01 + lost + 1e-30
     o = out[row].double().reshape(want.shape)
     low, high = (x.float().to(torch.bfloat16).double() for x in (want - tol, want + tol))
@@ -90,4 +90,56 @@ def test_light_keys_beside_a_dominant_one_without_value(lib, mode, rows, hq, hkv
         return w.amax(-1, keepdim=True) * v.sum(1)[:, None] * 2.0 ** -33
 
     for row in range(0, rows, max(1, rows // 4)):
+        check(b, out, lse, row, floor)
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d,prefix,own,cap", [
+    (60, 12, 2, 128, 4000, 0, 0.0),      # the prefix on the tensor cores, its last tile cut off
+    (50, 16, 2, 64, 3840, 0, 30.0),
+    (300, 8, 8, 128, 0, 1500, 0.0),      # own keys
+    (40, 16, 1, 64, 0, 1500, 30.0),
+    (2, 8, 2, 128, 900, 300, 0.0),       # a short prefix and own keys
+    (60, 12, 2, 128, 2000, 500, 0.0),    # a tiled one and own keys
+])
+@pytest.mark.parametrize("apart", [-10, -15, -20, -40])
+@pytest.mark.parametrize("what", ["zero rows", "large rows", "a light row of large scale", "a heavy row of small scale"])
+def test_value_scales_far_apart(lib, what, apart, rows, hq, hkv, d, prefix, own, cap):
+    """Per-token value scales 2^apart beside ordinary ones: what counts is the largest weight times scale among the keys
+    that have a value. f16 loses 2^-25 of the unit of each such product, and the largest of a piece stands 2^8 above the
+    unit, less the factor 2^6 up to which a tile is not looked at key by key."""
+    b = many(Batch([own], prefix, hq, hkv, d, 64, 1, cap=cap, seed=22, q_scale=1.0), rows)
+    b.v &= 0x7F
+    n = prefix + own
+    if what == "zero rows":      # kv8_write gives these the scale 1
+        b.vs *= 2.0 ** apart
+        some = [0, 1, 127, 128, 200] + list(range(333, n, 97)) + [n - 1]
+    elif what == "large rows":   # ordinary keys among keys of next to no value
+        b.vs *= 2.0 ** apart
+        some = list(range(5, n, 70))
+    else:
+        some = [n // 3]
+    for i in some:
+        pages = b.prefix_pages if i < prefix else b.table[0]
+        at = i if i < prefix else i - prefix
+        page, off = int(pages[at // b.page]), at % b.page
+        if what == "zero rows":
+            b.v[page, :, off], b.vs[page, :, off] = 0x80 if i % 2 else 0, 1.0
+        elif what == "large rows":
+            b.vs[page, :, off] *= 2.0 ** -apart
+        else:   # all of the key's elements alike: its score is their value times the query's sum
+            sign = 1 if what == "a heavy row of small scale" else -1
+            b.vs[page, :, off] *= 2.0 ** (apart * sign)
+            x = 8.0 * sign / math.sqrt(d) / b.ks[page, :, off]
+            b.k[page, :, off] = x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)[:, None]
+    out, lse = b.run(lib)
+
+    def floor(w, v, row):
+        top = v.amax(-1)   # a row of kv8_write's own making has its scale times 448 for largest; here less, at most
+        scale = torch.cat([b.vs[b.prefix_pages.long()].permute(1, 0, 2).reshape(hkv, -1)[:, :prefix],
+                           b.vs[b.table[0][:-(-own // b.page)].long()].permute(1, 0, 2).reshape(hkv, -1)[:, :own]], 1).double()
+        products = w * torch.where(top > 0, scale, 0.0)[:, None]
+        dec = v / scale[..., None]
+        return products.amax(-1, keepdim=True) * dec.sum(1)[:, None] * 2.0 ** -27
+
+    for row in (0, rows - 1):
         check(b, out, lse, row, floor)

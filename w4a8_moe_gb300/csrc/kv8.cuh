@@ -106,9 +106,10 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
 constexpr float kWeightTop = 8.0f;
 constexpr float kWeightMost = 15.0f;
 // Per-token scales: what is compared, and what goes into f16, is the weight times
-// its value's scale, and the reference carries the values' size too. Smaller scales
-// count as kLeastScale there, which keeps the weights themselves, and their sum
-// over up to 2^30 keys, inside fp32.
+// its value's scale (the reference then carries the values' size too, and drops out
+// of o / l), the largest of these products of single keys; a key whose values are
+// all zero has none. Smaller scales count as kLeastScale there, which keeps the
+// weights themselves, and their sum over up to 2^30 keys, inside fp32.
 constexpr float kLeastScale = 0x1p-64f;
 constexpr float kLeastScaleLog2 = -64.0f;
 

@@ -520,23 +520,33 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
             return top;
         };
         if (__any_sync(0xFFFFFFFFu, weigh() > kMostWeight)) {
-            float lift = 0.0f;   // log2 of the unit's largest value scale
+            float lift[2] = {0.0f, 0.0f};   // log2 of the value scales of keys g, g + 8
             if (TOK) {
-                lift = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+                // values of a key that are all zero add nothing, whatever their scale
+                // (kv8_write gives them 1): 0 then, so that they lead no reference
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1)
-                    lift = fmaxf(lift, __shfl_xor_sync(0xFFFFFFFFu, lift, x));
-                lift = fmaxf(log2f(lift), kLeastScaleLog2);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w)
+                        any |= xv[k][w];
+                    const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, (any & 0x7F7F7F7Fu) != 0);
+                    if ((g & 1) == (k & 1) && !(lanes & (0x11111111u << (g >> 1))))
+                        vs[k >> 1] = 0.0f;
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    lift[x] = fmaxf(log2f(fabsf(vs[x])), kLeastScaleLog2);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    float top = fmaxf(s[t][y], s[t][2 + y]);
+                    float top = TOK ? fmaxf(s[t][y] + lift[0], s[t][2 + y] + lift[1]) : fmaxf(s[t][y], s[t][2 + y]);
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    const float to = fmaxf(m[t][y], top + lift - kWeightTop);
+                    const float to = fmaxf(m[t][y], top - kWeightTop);
                     const float f = ex2(m[t][y] - to);
                     m[t][y] = to;
                     l[t][y] *= f;

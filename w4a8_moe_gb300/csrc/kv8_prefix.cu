@@ -45,6 +45,10 @@ constexpr int kRaw = 6;           // raw slots
 // call of some hundred.)
 static_assert(kRaw % kPairs == 0, "a raw slot has one pair of readers");
 constexpr int kScaleRing = 4;     // tiles whose per-token scales are held
+// A tile whose value scales lie within this factor takes its largest score and its
+// largest scale for its largest product: at most this factor too much. Others look
+// at every key (tile()).
+constexpr float kNear = 64.0f;
 
 template <int D>
 struct Smem {
@@ -379,8 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     top = max3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
                 return top;
             };
-            // and their weights as f16, added up on the way. Of the first `live` keys.
-            auto weigh = [&](const uint32_t (&r)[32], const float* vs, int ch, int live, auto masked) {
+            // and their weights as f16, added up on the way. Of the first `live` keys;
+            // value_scales(j): of keys j to j + 3.
+            auto weigh = [&](const uint32_t (&r)[32], auto value_scales, int ch, int live, auto masked) {
                 constexpr bool kMasked = decltype(masked)::value;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const F2 c2(c, c), add(CAP ? capl - ref : -ref, CAP ? capl - ref : -ref);
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 for (int j = 0; j < 32; j += 4) {
                     float4 v4;
                     if (TOK)
-                        v4 = *reinterpret_cast<const float4*>(vs + j);
+                        v4 = value_scales(j);
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         const F2 s(__uint_as_float(r[j + e]), __uint_as_float(r[j + e + 1]));
@@ -409,12 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                             l0 = add2(l0, w);
                         else
                             l1 = add2(l1, w);
-                        if (TOK) {
-                            F2 v = e == 0 ? F2(v4.x, v4.y) : F2(v4.z, v4.w);
-                            if (kMasked)
-                                v = F2(j + e < live ? v.lo() : 0.0f, j + e + 1 < live ? v.hi() : 0.0f);
-                            w = mul2(w, v);
-                        }
+                        if (TOK)
+                            w = mul2(w, e == 0 ? F2(v4.x, v4.y) : F2(v4.z, v4.w));
                         p[(j + e) >> 1] = pack_f16(w.lo(), w.hi());
                     }
                 }
@@ -427,43 +428,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                         mbar_arrive(bar((ch == 1 ? kPHalf : kPFull) + t));
                 }
             };
-            // A key tile: the whole row of scores in registers. The prefix's last
-            // tile, where keys past its end are masked, goes the other way, which
-            // reads S twice but is a quarter of the code: it runs once.
-            auto tile = [&](int i, auto brief) {
+            // A key tile: the whole row of scores in registers, `lift` the log2 of
+            // the largest value scale. The prefix's last tile, where keys past its
+            // end are masked, and tiles whose value scales lie far apart go the other
+            // way, which reads S twice but is a quarter of the code; there a lane
+            // holds the value scales v[j] of the keys lane + 32 j (0 past the end).
+            auto tile = [&](int i, float lift, float (&v)[4], auto brief) {
                 constexpr bool kBrief = decltype(brief)::value;
                 const float* ks = scales + (i % kScaleRing) * 2 * kTile;
                 const float* vs = ks + kTile;
-                const int live = a.prefix_len - (tile0 + i) * kTile;
-                float lift = 0.0f;   // log2 of the tile's largest value scale
-                if (TOK) {
-                    float v = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v = fmaxf(v, kBrief && lane + 32 * j >= live ? 0.0f : fabsf(vs[lane + 32 * j]));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1)
-                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-                    lift = fmaxf(log2f(v), kLeastScaleLog2);
-                }
                 if (!wait_warp(kSFull + t, i & 1))
                     return false;
                 tc_fence_after();
                 if constexpr (kBrief) {
+                    const int live = a.prefix_len - (tile0 + i) * kTile;
+                    if (TOK) {
+                        // Values of a key that are all zero add nothing, whatever their
+                        // scale (kv8_write gives them 1): 0 then, so that they lead no
+                        // reference. V stands in its stage until this tile's weights are
+                        // given; its barrier's phase before this one was K's of the tile
+                        // before, which S is behind.
+                        const int jv = 2 * i + 1;
+                        if (!wait_warp(kFull + jv % kStages, (jv / kStages) & 1))
+                            return false;
+                        const uint32_t at = base + L::stage + (jv % kStages) * L::kOperand + lane * 128;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t any = 0;
+#pragma unroll 4
+                            for (int x = 0; x < D / 8; ++x) {   // 16 bytes each, another bank group a lane
+                                const uint4 w = lds128(at + j * 32 * 128 + (x >> 3) * L::kPanel + (((x + lane) & 7) << 4));
+                                any |= w.x | w.y | w.z | w.w;
+                            }
+                            v[j] = (any & 0x7FFF7FFFu) ? v[j] : 0.0f;
+                        }
+                    }
+                    auto of_chunk = [&](const float (&x)[4], int ch) { return ch < 2 ? (ch ? x[1] : x[0]) : (ch == 2 ? x[2] : x[3]); };
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int ch = 0; ch < 4; ++ch) {
                         uint32_t r[32];
                         tmem_ld32(ts + ch * 32, r);
                         ld_wait32(r);
-                        if (TOK)
+                        if (TOK) {
                             times_scales(r, ks + ch * 32);
+                            const float mine = fmaxf(log2f(fabsf(of_chunk(v, ch))), kLeastScaleLog2);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            r[j] = ch * 32 + j < live ? r[j] : 0xFF800000u;
-                        top = fmaxf(top, largest(r));
+                            for (int j = 0; j < 32; ++j) {
+                                const float y = in_log2(__uint_as_float(r[j])) + __shfl_sync(0xFFFFFFFFu, mine, j);
+                                top = fmaxf(top, ch * 32 + j < live ? y : -INFINITY);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                r[j] = ch * 32 + j < live ? r[j] : 0xFF800000u;
+                            top = fmaxf(top, largest(r));
+                        }
                     }
-                    raise(i, in_log2(top) + lift);
+                    raise(i, TOK ? top : in_log2(top));
 #pragma unroll 1
                     for (int ch = 0; ch < 4; ++ch) {
                         uint32_t r[32];
@@ -471,7 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                         ld_wait32(r);
                         if (TOK)
                             times_scales(r, ks + ch * 32);
-                        weigh(r, vs + ch * 32, ch, live - ch * 32, Const<true>());
+                        const float mine = of_chunk(v, ch);
+                        auto value_scales = [&](int j) {
+                            return make_float4(__shfl_sync(0xFFFFFFFFu, mine, j), __shfl_sync(0xFFFFFFFFu, mine, j + 1),
+                                               __shfl_sync(0xFFFFFFFFu, mine, j + 2), __shfl_sync(0xFFFFFFFFu, mine, j + 3));
+                        };
+                        weigh(r, value_scales, ch, live - ch * 32, Const<true>());
                     }
                 } else {
                     uint32_t r[4][32];
@@ -488,16 +515,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     }
                     raise(i, in_log2(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))) + lift);
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch)
-                        weigh(r[ch], vs + ch * 32, ch, kTile, Const<false>());
+                    for (int ch = 0; ch < 4; ++ch) {
+                        auto value_scales = [&](int j) { return *reinterpret_cast<const float4*>(vs + ch * 32 + j); };
+                        weigh(r[ch], value_scales, ch, kTile, Const<false>());
+                    }
                 }
                 return true;
             };
             for (int i = 0; i < n && ok; ++i) {
-                if (TOK)
+                bool whole = (tile0 + i + 1) * kTile <= a.prefix_len;
+                float lift = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (TOK) {
+                    const int live = a.prefix_len - (tile0 + i) * kTile;
                     ok = wait_warp(kScFull + i % kScaleRing, (i / kScaleRing) & 1);
-                if (ok)
-                    ok = (tile0 + i + 1) * kTile <= a.prefix_len ? tile(i, Const<false>()) : tile(i, Const<true>());
+                    if (!ok)
+                        break;
+                    // magnitudes compare like their bits; a NaN counts as the largest
+                    const float* vs = scales + ((i % kScaleRing) * 2 + 1) * kTile;
+                    uint32_t most = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = lane + 32 * j < live ? vs[lane + 32 * j] : 0.0f;
+                        most = max(most, __float_as_uint(fabsf(v[j])));
+                        least = min(least, __float_as_uint(fabsf(v[j])));
+                    }
+                    const float hi = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, most));
+                    whole = whole && __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, least)) * kNear >= hi;
+                    lift = fmaxf(log2f(hi), kLeastScaleLog2);
+                }
+                ok = whole ? tile(i, lift, v, Const<false>()) : tile(i, lift, v, Const<true>());
             }
             // -------------------------------------------------------- results
             // Each thread lays its row of O in shared memory (the operands are

@@ -329,6 +329,7 @@ def fp8_block_linear(x_bf16, w_e4m3, w_scale_inv, out=None, xq_out=None, xs_out=
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _cache_refused(k_cache, v_cache, k_scale, v_scale):
@@ -341,7 +342,17 @@ def _cache_refused(k_cache, v_cache, k_scale, v_scale):
 def _devices_refused(*tensors):
     if any(not t.is_cuda for t in tensors):
         return ValueError("tensors must be on the GPU")
-    return ValueError("tensors must be on one GPU")
+    if len({t.get_device() for t in tensors}) > 1:
+        return ValueError("tensors must be on one GPU")
+    return ValueError(f"tensors are on cuda:{tensors[0].get_device()}, but the current device, on which the library "
+                      f"launches, is cuda:{_current_device()}")
+
+
+def _handle(stream, device):
+    """The handle of the caller's stream, which has to belong to the tensors' GPU."""
+    if stream.device_index != device:
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the tensors are on cuda:{device}")
+    return stream.cuda_stream
 
 
 def _row_stride(t, rows, heads, d, what):
@@ -375,12 +386,13 @@ def kv8_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, min_scale: float 
     k_stride, v_stride = _row_stride(k, T, h, d, "k"), _row_stride(v, T, h, d, "v")
     device = k_cache.get_device()
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
-                          == k.get_device() == v.get_device() == slots.get_device()):
+                          == k.get_device() == v.get_device() == slots.get_device() == _current_device()):
         raise _devices_refused(k_cache, v_cache, k_scale, v_scale, k, v, slots)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     status = (_lib or _load()).kv8_write(
         k.data_ptr(), v.data_ptr(), T, k_stride, v_stride, slots.data_ptr(), h, d, n, page, len(scales) == 3, float(min_scale),
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        _raw_stream(device) if stream is None else stream.cuda_stream)
+        to_stream)
     if status:
         _check(status)
 
@@ -404,12 +416,13 @@ def kv8_read(k_cache, v_cache, k_scale, v_scale, slots, k_out=None, v_out=None, 
     k_stride, v_stride = _row_stride(k_out, T, h, d, "k_out"), _row_stride(v_out, T, h, d, "v_out")
     device = k_cache.get_device()
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
-                          == slots.get_device() == k_out.get_device() == v_out.get_device()):
+                          == slots.get_device() == k_out.get_device() == v_out.get_device() == _current_device()):
         raise _devices_refused(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     status = (_lib or _load()).kv8_read(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), T, h, d, n,
         page, len(scales) == 3, k_out.data_ptr(), k_stride, v_out.data_ptr(), v_stride,
-        _raw_stream(device) if stream is None else stream.cuda_stream)
+        to_stream)
     if status:
         _check(status)
     return k_out, v_out
@@ -443,8 +456,9 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
         raise _vector_refused("suffix_lens")
     device = k_cache.get_device()
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
-                          == q.get_device() == page_table.get_device() == suffix_lens.get_device()):
+                          == q.get_device() == page_table.get_device() == suffix_lens.get_device() == _current_device()):
         raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, page_table, suffix_lens)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     pages, prefix_len = None, int(prefix_len)
     if prefix_len > 0:
         if prefix_pages.dtype is not _I32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
@@ -475,7 +489,7 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
         q.data_ptr(), q_stride, B, hq, h, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), n, page, len(scales) == 3, pages, prefix_len, page_table.data_ptr(), row if B > 1 else most,
         most, suffix_lens.data_ptr(), d ** -0.5 if sm_scale is None else float(sm_scale), float(logit_cap), out.data_ptr(), to,
-        ws.data_ptr(), ws.nbytes, _raw_stream(device) if stream is None else stream.cuda_stream)
+        ws.data_ptr(), ws.nbytes, to_stream)
     if status:
         _check(status)
     return out, lse

@@ -94,3 +94,24 @@ def test_tensors_of_two_gpus_are_refused(calls, name):
             with pytest.raises(ValueError):
                 fn(*args[:i], other, *args[i + 1:], **kw)
     assert not calls
+
+
+def test_attention_without_own_tokens(calls):
+    """No page table and no lengths, as in the C call: the prefix alone. `lse=False` asks for none."""
+    fn, args, kw = arguments()["kv8_prefix_attention"]
+    out, lse = fn(*args[:7], None, None, lse=False, **kw)
+    got = calls[0][1]
+    assert out is kw["out"] and lse is None
+    table, stride, most, lens = got[15:19]
+    assert table is None and stride == most == 0 and lens is None
+    assert got[22] is None   # lse
+
+
+def test_attention_refuses_what_is_missing(calls):
+    fn, args, kw = arguments()["kv8_prefix_attention"]
+    for i, what in ((5, "prefix_pages"), (7, "page_table"), (8, "suffix_lens")):
+        with pytest.raises(ValueError, match=what):
+            fn(*args[:i], None, *args[i + 1:], **kw)
+    assert not calls
+    fn(*args[:5], None, 0, *args[7:], **kw)   # no prefix: no pages of it
+    assert calls[0][1][13] is None and calls[0][1][14] == 0

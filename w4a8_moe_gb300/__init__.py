@@ -431,8 +431,8 @@ def kv8_read(k_cache, v_cache, k_scale, v_scale, slots, k_out=None, v_out=None, 
 def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, prefix_len: int, page_table, suffix_lens,
                          sm_scale=None, logit_cap: float = 0.0, out=None, lse=None, ws=None, stream=None):
     """Decode attention of bf16 q [B, query heads, D] over a shared prefix (prefix_pages, the first prefix_len tokens;
-    None with 0) and each sequence's own tokens (page_table [B, max pages], suffix_lens [B]); returns (bf16 out [B,
-    query heads, D], fp32 lse [B, query heads] or None). Pass `lse` (a tensor, or True to allocate one) to receive it.
+    None with 0) and each sequence's own tokens (page_table [B, max pages], suffix_lens [B]; both None: no own tokens);
+    returns (bf16 out [B, query heads, D], fp32 lse [B, query heads] or None). Pass `lse` (a tensor, or True to allocate one) to receive it.
     sm_scale defaults to D ** -0.5; logit_cap 0 is no cap."""
     shape, scales = k_cache.shape, k_scale.shape
     if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES or len(shape) != 4 or v_cache.shape != shape \
@@ -446,28 +446,37 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
         raise ValueError("q must be bf16 [B, query heads, D of the cache]")
     B, hq, _ = q_shape
     q_stride = _row_stride(q, B, hq, d, "q")
-    if page_table.dtype is not _I32 or page_table.dim() != 2:
-        raise ValueError("page_table must be int32 [B, max pages]")
-    rows, most = page_table.shape
-    row, one = page_table.stride()
-    if rows != B or (one != 1 and most > 1):
-        raise ValueError("page_table must be int32 [B, max pages], each sequence's pages contiguous")
-    if suffix_lens.dtype is not _I32 or suffix_lens.shape != (B,) or not suffix_lens.is_contiguous():
-        raise _vector_refused("suffix_lens")
+    if page_table is None and suffix_lens is None:
+        row = most = 0
+        table = lens = None
+        own = q, q   # (for the check of the devices)
+    else:
+        if page_table is None or page_table.dtype is not _I32 or page_table.dim() != 2:
+            raise ValueError("page_table must be int32 [B, max pages]; None only with suffix_lens None")
+        rows, most = page_table.shape
+        row, one = page_table.stride()
+        if rows != B or (one != 1 and most > 1):
+            raise ValueError("page_table must be int32 [B, max pages], each sequence's pages contiguous")
+        if suffix_lens is None or suffix_lens.dtype is not _I32 or suffix_lens.shape != (B,) \
+                or not suffix_lens.is_contiguous():
+            raise _vector_refused("suffix_lens")
+        table, lens, own = page_table.data_ptr(), suffix_lens.data_ptr(), (page_table, suffix_lens)
     device = k_cache.get_device()
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
-                          == q.get_device() == page_table.get_device() == suffix_lens.get_device() == _current_device()):
-        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, page_table, suffix_lens)
+                          == q.get_device() == own[0].get_device() == own[1].get_device() == _current_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, *own)
     to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     pages, prefix_len = None, int(prefix_len)
     if prefix_len > 0:
-        if prefix_pages.dtype is not _I32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
+        if prefix_pages is None or prefix_pages.dtype is not _I32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
             raise _vector_refused("prefix_pages")
         if prefix_pages.numel() * page < prefix_len:
             raise ValueError("prefix_pages must cover prefix_len tokens")
         if prefix_pages.get_device() != device:
             raise _devices_refused(k_cache, prefix_pages)
         pages = prefix_pages.data_ptr()
+    if lse is False:
+        lse = None
     if out is None or lse is True or ws is None:
         with _on(stream):
             out = out if out is not None else torch.empty(B, hq, d, dtype=_BF16, device=q.device)
@@ -487,8 +496,8 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
         to = lse.data_ptr()
     status = (_lib or _load()).kv8_prefix_attention(
         q.data_ptr(), q_stride, B, hq, h, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), n, page, len(scales) == 3, pages, prefix_len, page_table.data_ptr(), row if B > 1 else most,
-        most, suffix_lens.data_ptr(), d ** -0.5 if sm_scale is None else float(sm_scale), float(logit_cap), out.data_ptr(), to,
+        v_scale.data_ptr(), n, page, len(scales) == 3, pages, prefix_len, table, row if B > 1 else most,
+        most, lens, d ** -0.5 if sm_scale is None else float(sm_scale), float(logit_cap), out.data_ptr(), to,
         ws.data_ptr(), ws.nbytes, to_stream)
     if status:
         _check(status)

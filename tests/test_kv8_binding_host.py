@@ -115,3 +115,12 @@ def test_attention_refuses_what_is_missing(calls):
     assert not calls
     fn(*args[:5], None, 0, *args[7:], **kw)   # no prefix: no pages of it
     assert calls[0][1][13] is None and calls[0][1][14] == 0
+
+
+def test_workspace_has_to_be_as_large_as_it_says(calls):
+    """A view that repeats its memory counts bytes that are not there."""
+    fn, args, kw = arguments()["kv8_prefix_attention"]
+    for ws in (gpu(1, dtype=torch.uint8).expand(4096), gpu(8192, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            fn(*args, **dict(kw, ws=ws.as_subclass(OnGpu)))
+    assert not calls

@@ -485,6 +485,8 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
                 kv8_prefix_attention_workspace_size(B, hq, h, d, prefix_len, most, page), q.device)
     if out.dtype is not _BF16 or out.shape != q_shape or not out.is_contiguous():
         raise ValueError("out must be contiguous bf16 [B, query heads, D]")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     if out.get_device() != device or ws.get_device() != device:
         raise _devices_refused(k_cache, out, ws)
     to = None

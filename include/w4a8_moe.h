@@ -428,7 +428,9 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
  *   A page index outside [0, num_pages) or a suffix length outside
  *   [0, max_pages * page_size] touches no memory out of range; the call's
  *   outputs are then unspecified and w4a8_device_error reports W4A8_ERR_INDEX.
- *   ws: kv8_prefix_attention_workspace_size(...) bytes, header zeroed once.
+ *   ws: kv8_prefix_attention_workspace_size(...) bytes, header zeroed once. The
+ *        size does not fall as B, prefix_len or max_pages grows: a workspace for
+ *        the largest of them serves every smaller call.
  */
 int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq, int Hkv, int D,
                          const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,

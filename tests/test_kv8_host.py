@@ -104,3 +104,21 @@ def test_attention_workspace_size(lib):
     assert 256 < size(1, 48, 8, 128, 0, 1, 64) <= size(1, 48, 8, 128, 1024, 1, 64) <= size(64, 48, 8, 128, 1024, 1, 64)
     assert size(4096, 48, 8, 128, 1 << 20, 1 << 10, 64) < 8 << 30
     assert size(32, 48, 8, 128, 1024, 8, 64) == size(32, 48, 8, 128, 1024, 800, 64)    # lengths are read on the device
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(48, 8, 128), (32, 8, 128), (16, 1, 64), (28, 4, 64), (8, 8, 128), (9, 1, 128)])
+def test_attention_workspace_of_the_largest_serves_the_smaller(lib, hq, hkv, d):
+    """The size does not fall as the batch, the prefix or the tables grow, so one workspace serves a program whose batch
+    shrinks and grows."""
+    size = lib.kv8_prefix_attention_workspace_size
+    for prefix in (0, 1, 500, 1024, 8192, 65536):
+        sizes = [size(b, hq, hkv, d, prefix, 8, 64) for b in list(range(1, 700)) + [1000, 2000, 4095, 4096]]
+        assert sizes == sorted(sizes), prefix
+    for b in (1, 2, 17, 42, 43, 85, 86, 300, 4096):
+        sizes = [size(b, hq, hkv, d, prefix, 8, 64) for prefix in list(range(0, 3000, 7)) + [8192, 20000, 65536, 1 << 20]]
+        assert sizes == sorted(sizes), b
+        sizes = [size(b, hq, hkv, d, 8192, most, 64) for most in (0, 1, 2, 100, 4096)]
+        assert sizes == sorted(sizes), b
+    for b in (42, 85):   # just before another pair of row tiles
+        args = dict(B=b, Hq=48, Hkv=8, prefix=8192, nbytes=size(b + 1, 48, 8, 128, 8192, 8, 64))
+        assert call(lib.kv8_prefix_attention, ATTN, ATTN, **args) != 4

@@ -260,12 +260,15 @@ static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_page
     if (tiled)
         w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len, D, tile_us,
                                     static_cast<int64_t>(B) * max_pages * page_size);
-    w->ptiles = prefix_len && !tiled ? (B * group + R - 1) / R : 0;
-    const size_t slots = static_cast<size_t>(Hkv) * (w->ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxWarps;
+    // The sizes go by bounds that grow with every argument (not by the plan, and
+    // the untiled prefix's pairs are counted in any case): a smaller call fits.
+    const int most_ptiles = prefix_len ? (B * group + R - 1) / R : 0;
+    w->ptiles = tiled ? 0 : most_ptiles;
+    const size_t slots = static_cast<size_t>(Hkv) * (most_ptiles + static_cast<size_t>(B) * w->tiles) + kKv8MaxWarps;
     w->part_o = c.take<float>(slots * R * D * 4);
     w->part_ml = c.take<float2>(slots * R * 8);
     w->cum = c.take<int>((static_cast<size_t>(B) + 1) * 4);
-    const size_t rows = tiled ? static_cast<size_t>(kv8_prefix_most_splits(Hkv, B * group, prefix_len)) * B * Hq : 0;
+    const size_t rows = tiled ? static_cast<size_t>(kv8_prefix_most_rows(Hkv, B * group, prefix_len)) * Hkv : 0;
     w->prefix.part_o = c.take<float>(rows * D * 4);
     w->prefix.part_ml = c.take<float2>(rows * 8);
     return c.off;

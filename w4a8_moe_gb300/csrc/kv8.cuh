@@ -71,6 +71,7 @@ struct Kv8Prefix {
     float2* part_ml;
 };
 int kv8_prefix_most_splits(int Hkv, int rows, int prefix_len);
+int64_t kv8_prefix_most_rows(int Hkv, int rows, int prefix_len);
 Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max);
 cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s);
 bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);

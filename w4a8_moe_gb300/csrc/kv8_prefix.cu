@@ -800,6 +800,19 @@ int kv8_prefix_most_splits(int Hkv, int rows, int prefix_len)
                                          : (tiles < kKv8MaxSplits ? tiles : kKv8MaxSplits));
 }
 
+// Rows of partial results of a kv head (splits times `rows`) that a plan may have,
+// as a bound that grows with `rows` and `prefix_len`: the splits go down where
+// another pair of row tiles begins, but a workspace for the largest batch has to
+// serve the smaller ones. With c = ceil(kKv8PrefixCtas / Hkv), r pairs have at
+// most 2 ceil(c / r) splits of 2 kTile r rows, 4 kTile (c - 1 + r) in all.
+int64_t kv8_prefix_most_rows(int Hkv, int rows, int prefix_len)
+{
+    const int64_t c = (kKv8PrefixCtas + Hkv - 1) / Hkv, r = (rows + 2 * kTile - 1) / (2 * kTile);
+    const int64_t few = static_cast<int64_t>(kv8_prefix_most_splits(Hkv, 1, prefix_len)) * rows;
+    const int64_t many = 4 * kTile * (c - 1 + r);
+    return few < many ? few : many;
+}
+
 Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max)
 {
     Kv8Prefix p = {};

@@ -288,11 +288,11 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
     __syncthreads();
 
     const Line line = make_line(a, carry);
-    // few units: one warp on each SM before a second; the first CTAs run first
-    const int first = a.free_warps / kWarps;
-    int me = static_cast<int>(blockIdx.x) < first ? warp * first + static_cast<int>(blockIdx.x)
-                                                  : static_cast<int>(blockIdx.x) * kWarps + warp;
-    if (static_cast<int>(blockIdx.x) < first && me >= line.n1)
+    // few units: one warp on each SM before a second; the first CTAs run first, and
+    // the late ones go on from the last warp of theirs that has a share
+    const int first = a.free_warps / kWarps, block = static_cast<int>(blockIdx.x);
+    int me = block < first ? warp * first + block : line.n1 + (block - first) * kWarps + warp;
+    if (block < first && me >= line.n1)
         me = line.n;
     const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
     const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;

@@ -442,6 +442,21 @@ size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int pr
                                            int page_size);
 
 /*
+ * kv8_prefix_attention_plan -- how a kv8_prefix_attention call of this shape is
+ * cut up on a GPU with num_sms SMs. Host only: no device is touched. The plan
+ * does not change the result beyond the order in which partial sums are added.
+ *
+ *   plan [4] int32 (host), out:
+ *     [0] ranges of keys that the tiled prefix is cut into (0: a short prefix,
+ *         which is not tiled)
+ *     [1] 128-key tiles of a range
+ *     [2] thread blocks of the tiled prefix, each of which takes an SM
+ *     [3] kernel launches of the call
+ */
+int kv8_prefix_attention_plan(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size,
+                              int scale_mode, float logit_cap, int num_sms, int32_t* plan);
+
+/*
  * w4a8_set_profile_events -- measurement hook (not part of the method). Sets,
  * for the calling host thread, up to four cudaEvent_t handles that
  * moe_w4a8_forward records on its stream: [0] before the gate_up GEMM,

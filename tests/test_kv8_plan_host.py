@@ -1,0 +1,45 @@
+"""CPU checks of how the attention over the FP8 cache cuts up a shared prefix."""
+import ctypes
+
+import pytest
+
+from helpers import ensure_built
+
+
+@pytest.fixture(scope="module")
+def plan():
+    ensure_built()
+    import w4a8_moe_gb300 as pkg
+    return pkg.kv8_prefix_attention_plan
+
+
+def test_plan_refusals(plan):
+    import w4a8_moe_gb300 as pkg
+    lib = pkg._load()
+    out = (ctypes.c_int32 * 4)()
+    good = [32, 48, 8, 128, 1024, 8, 64, 0, 0.0, 152]
+    assert lib.kv8_prefix_attention_plan(*good, None) == 1
+    assert lib.kv8_prefix_attention_plan(*good, out) == 0
+    for i, bad in ((0, 0), (1, 47), (2, 0), (3, 96), (4, -1), (5, -1), (6, 48), (7, 2), (8, -1.0), (8, float("nan")), (9, 0)):
+        assert lib.kv8_prefix_attention_plan(*good[:i], bad, *good[i + 1:], out) == 2, (i, bad)
+
+
+def test_plan_launches(plan):
+    assert plan(32, 48, 8, 128, 8192, 8, 64, num_sms=152)["launches"] == 3
+    assert plan(32, 48, 8, 128, 8192, 0, 64, num_sms=152)["launches"] == 2    # no own tokens
+    assert plan(1, 48, 8, 128, 1024, 8, 64, num_sms=152) == dict(ranges=0, tiles_per_range=0, prefix_blocks=0, launches=2)
+    assert plan(1, 48, 8, 128, 0, 8, 64, num_sms=152)["launches"] == 2
+    assert plan(1, 48, 8, 128, 0, 0, 64, num_sms=152)["launches"] == 1
+
+
+@pytest.mark.parametrize("num_sms", [100, 132, 148, 152])
+def test_plan_fills_the_sms_that_there_are(plan, num_sms):
+    """A long prefix is cut so that the waves of blocks are full, on this GPU's number of SMs: no further range or two
+    would have had room in the same number of waves."""
+    for batch, hq, hkv in ((32, 48, 8), (17, 16, 1), (100, 32, 8), (64, 40, 8), (40, 28, 4)):
+        p = plan(batch, hq, hkv, 128, 200000, 0, 64, num_sms=num_sms)
+        pairs = hkv * -(-batch * (hq // hkv) // 256)
+        assert p["prefix_blocks"] == p["ranges"] * pairs
+        waves = -(-p["prefix_blocks"] // num_sms)
+        most = min(64, 2 * -(-152 // pairs))
+        assert p["prefix_blocks"] + 2 * pairs > waves * num_sms or p["ranges"] >= most - 1, (batch, hq, hkv, p)

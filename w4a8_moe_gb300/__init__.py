@@ -25,7 +25,7 @@ __all__ = [
     "moe_w4a8_forward_dynamic", "moe_w4a8_dynamic_workspace_size", "moe_w4a8_workspace_layout",
     "moe_w4a8_plan",
     "w4a8_quantize_act_workspace_size", "kv8_write", "kv8_read", "kv8_prefix_attention",
-    "kv8_prefix_attention_workspace_size", "RouteResult", "library_path", "W4A8Error",
+    "kv8_prefix_attention_workspace_size", "kv8_prefix_attention_plan", "RouteResult", "library_path", "W4A8Error",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -80,6 +80,7 @@ def _load():
         "kv8_prefix_attention": (i32, [P, i64, i32, i32, i32, i32, P, P, P, P, i32, i32, i32, P, i32, P, i64, i32, P,
                                        f32, f32, P, P, P, sz, P]),
         "kv8_prefix_attention_workspace_size": (sz, [i32] * 7),
+        "kv8_prefix_attention_plan": (i32, [i32] * 8 + [f32, i32, P]),
         "w4a8_device_error": (i32, [P, P, P]),
         "w4a8_selftest_wait_timeout": (i32, [P, P]),
         "w4a8_set_profile_events": (i32, [P, i32]),
@@ -177,6 +178,18 @@ def w4a8_quantize_act_workspace_size(numel) -> int:
 
 def kv8_prefix_attention_workspace_size(B, Hq, Hkv, D, prefix_len, max_pages, page_size) -> int:
     return int(_load().kv8_prefix_attention_workspace_size(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
+
+
+def kv8_prefix_attention_plan(B, Hq, Hkv, D, prefix_len, max_pages, page_size, scale_mode=0, logit_cap=0.0,
+                              num_sms=None) -> dict:
+    """How a kv8_prefix_attention call of this shape is cut up (host only; see kv8_prefix_attention_plan in
+    include/w4a8_moe.h). num_sms defaults to the current device's SM count."""
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    plan = (ctypes.c_int32 * 4)()
+    _check(_load().kv8_prefix_attention_plan(B, Hq, Hkv, D, prefix_len, max_pages, page_size, scale_mode, logit_cap,
+                                             num_sms, plan))
+    return dict(zip(("ranges", "tiles_per_range", "prefix_blocks", "launches"), list(plan)))
 
 
 # --------------------------------------------------------------------------- calls

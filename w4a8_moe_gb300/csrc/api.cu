@@ -245,21 +245,33 @@ static bool kv8_attn_ok(int B, int Hq, int Hkv, int D, int prefix_len, int max_p
 struct Kv8Ws {
     float* part_o;
     float2* part_ml;
+    float* prefix_o;
+    float2* prefix_ml;
     int* cum;
     int tiles, ptiles;
-    Kv8Prefix prefix;   // splits 0: the prefix is not tiled
 };
-static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size, float tile_us,
-                     Kv8Ws* w, void* ws)
+static bool kv8_tiled(int B, int Hq, int Hkv, int prefix_len)
+{
+    return prefix_len && kv8_prefix_tiled(Hkv, B * (Hq / Hkv), prefix_len);
+}
+// What the tiled prefix is cut into; splits 0: it is not tiled.
+static Kv8Prefix kv8_plan(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size, int scale_mode,
+                          float logit_cap, int num_sms)
+{
+    if (!kv8_tiled(B, Hq, Hkv, prefix_len))
+        return {};
+    // a key tile: three exponential-class operations a score instead of one, or a
+    // scale for each key and value
+    const float tile_us = logit_cap > 0.0f ? 2.6f : scale_mode ? 1.8f : 1.5f;
+    return kv8_prefix_plan(Hkv, B * (Hq / Hkv), prefix_len, D, tile_us, static_cast<int64_t>(B) * max_pages * page_size,
+                           num_sms);
+}
+static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, Kv8Ws* w, void* ws)
 {
     Carver c(ws);
     const int group = Hq / Hkv, R = kv8_attn_row_tile(group);
     w->tiles = (group + R - 1) / R;
-    w->prefix = {};
-    const bool tiled = prefix_len && kv8_prefix_tiled(Hkv, B * group, prefix_len);
-    if (tiled)
-        w->prefix = kv8_prefix_plan(Hkv, B * group, prefix_len, D, tile_us,
-                                    static_cast<int64_t>(B) * max_pages * page_size);
+    const bool tiled = kv8_tiled(B, Hq, Hkv, prefix_len);
     // The sizes go by bounds that grow with every argument (not by the plan, and
     // the untiled prefix's pairs are counted in any case): a smaller call fits.
     const int most_ptiles = prefix_len ? (B * group + R - 1) / R : 0;
@@ -269,8 +281,8 @@ static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, int max_page
     w->part_ml = c.take<float2>(slots * R * 8);
     w->cum = c.take<int>((static_cast<size_t>(B) + 1) * 4);
     const size_t rows = tiled ? static_cast<size_t>(kv8_prefix_most_rows(Hkv, B * group, prefix_len)) * Hkv : 0;
-    w->prefix.part_o = c.take<float>(rows * D * 4);
-    w->prefix.part_ml = c.take<float2>(rows * 8);
+    w->prefix_o = c.take<float>(rows * D * 4);
+    w->prefix_ml = c.take<float2>(rows * 8);
     return c.off;
 }
 
@@ -739,7 +751,23 @@ size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int pr
     if (!kv8_attn_ok(B, Hq, Hkv, D, prefix_len, max_pages, page_size))
         return 0;
     Kv8Ws w;
-    return kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, 1.5f, &w, nullptr);
+    return kv8_ws(B, Hq, Hkv, D, prefix_len, &w, nullptr);
+}
+
+int kv8_prefix_attention_plan(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size,
+                              int scale_mode, float logit_cap, int num_sms, int32_t* plan)
+{
+    if (!plan)
+        return W4A8_ERR_NULL;
+    if (!kv8_attn_ok(B, Hq, Hkv, D, prefix_len, max_pages, page_size) || (scale_mode != 0 && scale_mode != 1) ||
+        !std::isfinite(logit_cap) || logit_cap < 0.0f || num_sms < 1)
+        return W4A8_ERR_SHAPE;
+    const Kv8Prefix p = kv8_plan(B, Hq, Hkv, D, prefix_len, max_pages, page_size, scale_mode, logit_cap, num_sms);
+    plan[0] = p.splits;
+    plan[1] = p.tiles_per_split;
+    plan[2] = p.splits * Hkv * p.row_pairs;
+    plan[3] = (p.splits ? 1 : 0) + (max_pages || (prefix_len && !p.splits) ? 1 : 0) + 1;
+    return W4A8_OK;
 }
 
 int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq, int Hkv, int D,
@@ -762,11 +790,8 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
         !aligned4(suffix_lens) || !aligned4(lse) ||
         (scale_mode == 1 && (!aligned16(k_scale) || !aligned16(v_scale))))
         return W4A8_ERR_ALIGN;
-    // a key tile of the tiled prefix: three exponential-class operations a score
-    // instead of one, or a scale for each key and value
-    const float tile_us = logit_cap > 0.0f ? 2.6f : scale_mode ? 1.8f : 1.5f;
     Kv8Ws w;
-    if (!ws || ws_bytes < kv8_ws(B, Hq, Hkv, D, prefix_len, max_pages, page_size, tile_us, &w, ws))
+    if (!ws || ws_bytes < kv8_ws(B, Hq, Hkv, D, prefix_len, &w, ws))
         return W4A8_ERR_WORKSPACE;
     if (!aligned16(ws))
         return W4A8_ERR_ALIGN;
@@ -784,8 +809,10 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
     a.tiles = w.tiles, a.ptiles = w.ptiles, a.part_o = w.part_o, a.part_ml = w.part_ml, a.cum = w.cum;
     a.err = static_cast<uint32_t*>(ws);
     a.out = out_bf16, a.lse = lse;
-    return launch_kv8_attn(a, w.prefix, D, scale_mode, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK
-                                                                                                   : W4A8_ERR_LAUNCH;
+    Kv8Prefix prefix = kv8_plan(B, Hq, Hkv, D, prefix_len, max_pages, page_size, scale_mode, logit_cap, sms);
+    prefix.part_o = w.prefix_o, prefix.part_ml = w.prefix_ml;
+    return launch_kv8_attn(a, prefix, D, scale_mode, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK
+                                                                                                 : W4A8_ERR_LAUNCH;
 }
 
 int w4a8_device_error(void* ws, int* code_out, void* stream)

@@ -60,7 +60,7 @@ struct Kv8Attn {
 };
 // The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key
 // tiles); part_* [split][kv head][row] as above.
-constexpr int kKv8PrefixCtas = 152;  // SMs the plan fills
+constexpr int kKv8PrefixCtas = 152;  // SMs the workspace is sized for
 constexpr int kKv8MaxSplits = 64;
 struct Kv8Prefix {
     int tiles;            // 128-key tiles of the prefix
@@ -72,7 +72,7 @@ struct Kv8Prefix {
 };
 int kv8_prefix_most_splits(int Hkv, int rows, int prefix_len);
 int64_t kv8_prefix_most_rows(int Hkv, int rows, int prefix_len);
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max);
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max, int num_sms);
 cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s);
 bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);
 int kv8_attn_row_tile(int group);

@@ -813,7 +813,8 @@ int64_t kv8_prefix_most_rows(int Hkv, int rows, int prefix_len)
     return few < many ? few : many;
 }
 
-Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max)
+Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_us, int64_t own_max,
+                          int num_sms)
 {
     Kv8Prefix p = {};
     p.tiles = (prefix_len + kTile - 1) / kTile;
@@ -834,9 +835,9 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_u
         const int splits = (p.tiles + per - 1) / per;
         if (s > 1 && splits < s)
             continue;   // the same as one before
-        const int64_t taken = base * splits, waves = (taken + kKv8PrefixCtas - 1) / kKv8PrefixCtas;
+        const int64_t taken = base * splits, waves = (taken + num_sms - 1) / num_sms;
         const double us = static_cast<double>(waves) * (per * tile_us + 5.0);
-        const double free = waves > 1 ? 0.0 : static_cast<double>(kKv8PrefixCtas - taken) / kKv8PrefixCtas;
+        const double free = waves > 1 ? 0.0 : static_cast<double>(num_sms - taken) / num_sms;
         double own = 0.0;
         if (own_max > 0) {
             const double early = free * (us > 4.0 ? us - 4.0 : 0.0);

@@ -43,3 +43,21 @@ def test_plan_fills_the_sms_that_there_are(plan, num_sms):
         waves = -(-p["prefix_blocks"] // num_sms)
         most = min(64, 2 * -(-152 // pairs))
         assert p["prefix_blocks"] + 2 * pairs > waves * num_sms or p["ranges"] >= most - 1, (batch, hq, hkv, p)
+
+
+@pytest.mark.parametrize("batch,hq,hkv,d,prefix,page,own,scale_mode,cap", [
+    (64, 32, 8, 128, 8192, 64, 512, 1, 0.0),
+    (128, 48, 8, 128, 32768, 64, 1024, 0, 0.0),
+    (256, 48, 8, 128, 65536, 128, 256, 0, 0.0),
+    (32, 48, 8, 128, 1024, 64, 256, 0, 30.0),
+    (17, 16, 1, 64, 4999, 16, 784, 0, 0.0),
+    (24, 32, 8, 128, 3000, 64, 128, 0, 0.0),
+    (8, 32, 8, 128, 20000, 64, 128, 0, 0.0),
+])
+def test_plan_hardly_follows_the_tables_width(plan, batch, hq, hkv, d, prefix, page, own, scale_mode, cap):
+    """A page table is as wide as the longest context a program allows, which says little about the lengths: the prefix
+    keeps its SMs however wide the table is."""
+    tight = plan(batch, hq, hkv, d, prefix, -(-own // page), page, scale_mode, cap, num_sms=152)
+    for tokens in (4096, 32768, 131072, 1 << 20):
+        wide = plan(batch, hq, hkv, d, prefix, tokens // page, page, scale_mode, cap, num_sms=152)
+        assert wide["tiles_per_range"] <= 2 * tight["tiles_per_range"], (tokens, tight, wide)

@@ -819,41 +819,79 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_u
     Kv8Prefix p = {};
     p.tiles = (prefix_len + kTile - 1) / kTile;
     p.row_pairs = (rows + 2 * kTile - 1) / (2 * kTile);
-    // The split that should end first, in us. A CTA takes tile_us for a key tile
-    // (one row tile or two: a tile's chain of products and softmax bounds both) and
-    // some 5 for its start and end. The sequences' own keys, taken to be
-    // half of what their page tables hold, take 4 and their bytes, either on the
-    // SMs that the prefix leaves or on all, the others joining after the prefix.
-    // Every split is written and read once more. 128 sequences of 48 heads with
-    // 16-1024 own keys over 32768 tokens: 119 us with 144 CTAs, 112 with 120.
+    // The time of a split, in us. A CTA takes tile_us for a key tile (one row tile
+    // or two: a tile's chain of products and softmax bounds both) and some 5 for its
+    // start and end. The sequences' own keys take 4 and their bytes, either on the
+    // SMs that the prefix leaves or on all, the others joining after the prefix; a
+    // part f of the SMs reads at some f (2 - f) of the full rate (beside a prefix on
+    // 72 and 48 SMs: 0.80 and 0.87). Every split is written and read once more.
+    struct Split {
+        int splits, per;
+        double us, rate, join;
+        double with(double own_us) const
+        {
+            double own = 0.0;
+            if (own_us > 0.0) {
+                const double early = rate * (us > 4.0 ? us - 4.0 : 0.0);
+                own = us + 4.0 + (own_us > early ? own_us - early : 0.0);
+                if (rate > 0.0 && 4.0 + own_us / rate < own)
+                    own = 4.0 + own_us / rate;
+            }
+            return (own > us ? own : us) + join;
+        }
+    };
     const int64_t base = static_cast<int64_t>(Hkv) * p.row_pairs;
-    const double bytes_us = own_max > 0 ? 0.5 * static_cast<double>(own_max) * Hkv * 2 * D / 5.5e6 : 0.0;
-    double best = 0.0;
     const int most = kv8_prefix_most_splits(Hkv, rows, prefix_len);
+    Split all[kKv8MaxSplits];
+    int n = 0;
+    double alone = 0.0;
     for (int s = 1; s <= most; ++s) {
         const int per = (p.tiles + s - 1) / s;
         const int splits = (p.tiles + per - 1) / per;
         if (s > 1 && splits < s)
             continue;   // the same as one before
         const int64_t taken = base * splits, waves = (taken + num_sms - 1) / num_sms;
-        const double us = static_cast<double>(waves) * (per * tile_us + 5.0);
+        Split& x = all[n++];
+        x.splits = splits;
+        x.per = per;
+        x.us = static_cast<double>(waves) * (per * tile_us + 5.0);
         const double free = waves > 1 ? 0.0 : static_cast<double>(num_sms - taken) / num_sms;
-        double own = 0.0;
-        if (own_max > 0) {
-            const double early = free * (us > 4.0 ? us - 4.0 : 0.0);
-            own = us + 4.0 + (bytes_us > early ? bytes_us - early : 0.0);
-            if (free > 0.0 && 4.0 + bytes_us / free < own)
-                own = 4.0 + bytes_us / free;
-        }
-        const double join = static_cast<double>(splits) * Hkv * rows * D * 8 / 8e6;
-        const double total = (own > us ? own : us) + join;
-        if (s == 1 || total < best) {
-            best = total;
-            p.splits = splits;
-            p.tiles_per_split = per;
-            p.us = static_cast<float>(us);
-        }
+        x.rate = free * (2.0 - free);
+        x.join = static_cast<double>(splits) * Hkv * rows * D * 8 / 8e6;
+        const double us = x.us + x.join;
+        alone = n == 1 || us < alone ? us : alone;
     }
+    // The lengths stand on the device, and a page table's width only bounds them. So
+    // the split is taken that is the least behind the best one for any own keys
+    // between a quarter of the prefix's work and as much again (more of them, and
+    // the split hardly matters), as far as the tables hold so many. Of 38 batches of
+    // 8-256 sequences over 1024-65536 tokens with up to 40000 own tokens each, tables
+    // tight and 32768 wide, the time is 1.05 times the best split's in the mean and
+    // 1.20 times at most. By half of what the tables hold, with the wide ones, us: 64
+    // sequences over 8192 131 (now 29.6), 128 over 32768 365 (103), 256 over 65536 707
+    // (266), 32 over 1024, capped, 34.9 (14.8).
+    const double bytes_us = static_cast<double>(own_max) * Hkv * 2 * D / 5.5e6;
+    constexpr int kLoads = 3;
+    constexpr double kLoad[kLoads] = {0.25, 0.5, 1.0};
+    double worst[kKv8MaxSplits] = {};
+    for (int j = 0; j < kLoads; ++j) {
+        const double own_us = kLoad[j] * alone < bytes_us ? kLoad[j] * alone : bytes_us;
+        double us[kKv8MaxSplits], best = 0.0;
+        for (int i = 0; i < n; ++i) {
+            us[i] = all[i].with(own_us);
+            best = i == 0 || us[i] < best ? us[i] : best;
+        }
+        for (int i = 0; i < n; ++i)
+            worst[i] = us[i] > worst[i] * best ? us[i] / best : worst[i];
+        if (own_us >= bytes_us)
+            break;
+    }
+    int at = 0;
+    for (int i = 1; i < n; ++i)
+        at = worst[i] < worst[at] ? i : at;
+    p.splits = all[at].splits;
+    p.tiles_per_split = all[at].per;
+    p.us = static_cast<float>(all[at].us);
     return p;
 }
 

@@ -446,12 +446,15 @@ size_t kv8_prefix_attention_workspace_size(int B, int Hq, int Hkv, int D, int pr
  * cut up on a GPU with num_sms SMs. Host only: no device is touched. The plan
  * does not change the result beyond the order in which partial sums are added.
  *
- *   plan [4] int32 (host), out:
+ *   plan [6] int32 (host), out:
  *     [0] ranges of keys that the tiled prefix is cut into (0: a short prefix,
  *         which is not tiled)
  *     [1] 128-key tiles of a range
  *     [2] thread blocks of the tiled prefix, each of which takes an SM
  *     [3] kernel launches of the call
+ *     [4] thread blocks an SM of the kernel for the sequences' own keys
+ *     [5] warps that add up the partial results of a row (a query head of a
+ *         sequence), 0: half a warp
  */
 int kv8_prefix_attention_plan(int B, int Hq, int Hkv, int D, int prefix_len, int max_pages, int page_size,
                               int scale_mode, float logit_cap, int num_sms, int32_t* plan);

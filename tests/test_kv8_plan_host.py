@@ -16,7 +16,7 @@ def plan():
 def test_plan_refusals(plan):
     import w4a8_moe_gb300 as pkg
     lib = pkg._load()
-    out = (ctypes.c_int32 * 4)()
+    out = (ctypes.c_int32 * 6)()
     good = [32, 48, 8, 128, 1024, 8, 64, 0, 0.0, 152]
     assert lib.kv8_prefix_attention_plan(*good, None) == 1
     assert lib.kv8_prefix_attention_plan(*good, out) == 0
@@ -27,7 +27,8 @@ def test_plan_refusals(plan):
 def test_plan_launches(plan):
     assert plan(32, 48, 8, 128, 8192, 8, 64, num_sms=152)["launches"] == 3
     assert plan(32, 48, 8, 128, 8192, 0, 64, num_sms=152)["launches"] == 2    # no own tokens
-    assert plan(1, 48, 8, 128, 1024, 8, 64, num_sms=152) == dict(ranges=0, tiles_per_range=0, prefix_blocks=0, launches=2)
+    short = plan(1, 48, 8, 128, 1024, 8, 64, num_sms=152)
+    assert (short["ranges"], short["tiles_per_range"], short["prefix_blocks"], short["launches"]) == (0, 0, 0, 2)
     assert plan(1, 48, 8, 128, 0, 8, 64, num_sms=152)["launches"] == 2
     assert plan(1, 48, 8, 128, 0, 0, 64, num_sms=152)["launches"] == 1
 
@@ -61,3 +62,26 @@ def test_plan_hardly_follows_the_tables_width(plan, batch, hq, hkv, d, prefix, p
     for tokens in (4096, 32768, 131072, 1 << 20):
         wide = plan(batch, hq, hkv, d, prefix, tokens // page, page, scale_mode, cap, num_sms=152)
         assert wide["tiles_per_range"] <= 2 * tight["tiles_per_range"], (tokens, tight, wide)
+
+
+HEADS = [(48, 8, 128), (32, 8, 128), (28, 4, 128), (8, 1, 128), (16, 1, 128), (16, 1, 64), (64, 8, 64), (8, 8, 128)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+@pytest.mark.parametrize("prefix", [0, 5000, 20000])
+def test_plan_join_fits_the_sms(plan, hq, hkv, d, prefix):
+    """Several warps a row only while the blocks of all rows are on the SMs at once, whatever the tables would allow."""
+    for batch in list(range(1, 160)) + [200, 256, 600]:
+        for tokens in (64, 1024, 32768, 131072):
+            w = plan(batch, hq, hkv, d, prefix, tokens // 64, 64, num_sms=152)["join_warps"]
+            fits = {8: 2, 4: 4 if d == 128 else 7, 2: 8}
+            assert w in (0, 1) or batch * hq <= fits[w] * 152, (batch, tokens, w)
+
+
+def test_plan_blocks_of_few_sequences(plan):
+    """The form of 16 rows whose registers spill is for very many keys of many sequences, not for wide tables alone."""
+    for batch in (1, 17, 40, 64):
+        for tokens in (64, 8192, 131072):
+            assert plan(batch, 16, 1, 128, 0, tokens // 64, 64, num_sms=152)["own_blocks_per_sm"] == 2
+    assert plan(256, 16, 1, 128, 0, 128, 64, num_sms=152)["own_blocks_per_sm"] == 3
+    assert plan(256, 16, 1, 64, 0, 1, 64, num_sms=152)["own_blocks_per_sm"] == 3   # D 64 does not spill

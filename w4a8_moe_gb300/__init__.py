@@ -186,10 +186,11 @@ def kv8_prefix_attention_plan(B, Hq, Hkv, D, prefix_len, max_pages, page_size, s
     include/w4a8_moe.h). num_sms defaults to the current device's SM count."""
     if num_sms is None:
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
-    plan = (ctypes.c_int32 * 4)()
+    plan = (ctypes.c_int32 * 6)()
     _check(_load().kv8_prefix_attention_plan(B, Hq, Hkv, D, prefix_len, max_pages, page_size, scale_mode, logit_cap,
                                              num_sms, plan))
-    return dict(zip(("ranges", "tiles_per_range", "prefix_blocks", "launches"), list(plan)))
+    return dict(zip(("ranges", "tiles_per_range", "prefix_blocks", "launches", "own_blocks_per_sm", "join_warps"),
+                    list(plan)))
 
 
 # --------------------------------------------------------------------------- calls

@@ -767,6 +767,12 @@ int kv8_prefix_attention_plan(int B, int Hq, int Hkv, int D, int prefix_len, int
     plan[1] = p.tiles_per_split;
     plan[2] = p.splits * Hkv * p.row_pairs;
     plan[3] = (p.splits ? 1 : 0) + (max_pages || (prefix_len && !p.splits) ? 1 : 0) + 1;
+    Kv8Ws w;
+    kv8_ws(B, Hq, Hkv, D, prefix_len, &w, nullptr);
+    Kv8Attn a = {};
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv, a.page_shift = kv8_page_shift(page_size);
+    a.prefix_len = prefix_len, a.max_pages = max_pages, a.tiles = w.tiles, a.ptiles = w.ptiles;
+    kv8_attn_layout(a, p, D, num_sms, &plan[4], &plan[5]);
     return W4A8_OK;
 }
 

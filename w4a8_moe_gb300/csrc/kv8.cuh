@@ -76,6 +76,7 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_u
 cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, cudaStream_t s);
 bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);
 int kv8_attn_row_tile(int group);
+void kv8_attn_layout(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms, int* blocks_per_sm, int* warps_a_row);
 cudaError_t launch_kv8_attn(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s);
 
 // Two E4M3 codes (low byte first) to two f16 values: exact for every code.

@@ -834,31 +834,45 @@ static int64_t most_units(const Kv8Attn& a)
     return static_cast<int64_t>(a.B) * a.Hkv * a.tiles * ((a.max_pages << a.page_shift) / kKv8Unit);
 }
 
+// Warps that take a row of the join (0: half a warp). Several warps pay while a row
+// may have many pieces and all of the rows' blocks fit the SMs at once: 8 up to 2
+// rows an SM, 4 up to 4 (7 with D 64), 2 up to 8. `pieces` is what the page tables
+// allow, an upper bound: inside those limits a row of few pieces loses little by
+// too many warps, but beyond them much. us in all, own keys alone but for the last:
+//   576 rows (12 sequences of 48 heads), 4 / 2 / 1: 60 own keys 8.7 / 8.6 / 8.3,
+//     1-4000 20.7 / 21.8 / 23.9; 840 (30 of 28) 11.2 / 8.9 / 8.5, 24.8 / 23.0 / 24.3
+//   1024 of D 64 (64 of 16), 4 / 2 / 1: 9.9 / 10.1 / 9.9, 14.1 / 15.7 / 18.8; 1120
+//     (70 of 16) 12.1 / 10.1 / 9.9, 16.9 / 15.8 / 18.5
+//   1280 (10 of 128), 2 / 1: 12.6 / 10.4, 31.0 / 29.5
+//   over a prefix, 8 / 4: 272 of D 64 over 4999 tokens and 1-2000 own keys 12.0 /
+//     13.9; 320 over 9000 and 60 17.3 / 15.0, 576 over 20000 25.5 / 22.4
+// Half a warp a row where rows are very many, 1 / half: 4800 of 60 own keys 13.8 /
+// 10.5, of 1-1000 36.7 / 34.6; 2400 11.6 / 11.5, 19.5 / 23.3.
+static int join_warps(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms)
+{
+    const int heads = a.B * a.Hq, pairs = a.B * a.Hkv * a.tiles;
+    const int pieces = p.splits + warps_for(most_units(a), a.spread, a.warps) / pairs;
+    if (heads <= num_sms || (pieces > 16 && heads <= 2 * num_sms))
+        return 8;
+    if (heads <= 2 * num_sms || ((pieces > 16 || p.splits > 8) && heads <= 4 * num_sms) ||
+        (pieces > 24 && D == 64 && heads <= 7 * num_sms))
+        return 4;
+    if (pieces > 12 && heads <= 8 * num_sms)
+        return 2;
+    return heads > 18 * num_sms ? 0 : 1;
+}
+
 template <int D>
 static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
 {
-    // Warps a row, us in all. Few rows: 17 sequences of 16 heads over a prefix in 40
-    // splits (272 rows), 8 / 4 12.7 / 14.6; 32 sequences of 8 heads, 8192 own keys (76
-    // pieces), 8 / 4 19.4 / 20.6. More: 64 of 8 heads, 1000-4000 own keys (512 rows of up
-    // to 38 pieces), 4 / 1 18.6 / 24.2; 64 of 16 heads of D 64, 2000-8000 (1024 rows of
-    // 28), 4 / 1 19.9 / 23.6. Between: 17 of 48 heads, 1000-4000 (816 rows of 17), 2 / 1
-    // 21.9 / 23.4; but 64 of 32 heads over a prefix in 11 splits (2048 rows, blocks of two
-    // warps no longer fit at once), 2 / 1 31.0 / 28.8. Many, 1 / half: 64 of 48 heads and 60
-    // own keys (3072 rows) 12.3 / 9.7, over 20000 tokens 42.0 / 41.1; 128 over 32768 and own
-    // keys (6144 rows, the most pieces) 102.9 / 103.4, 128 of 900 own keys 39.8 / 34.6; but
-    // 40 of 48 heads and 1000 (1920 rows) 17.1 / 19.5.
-    const int heads = a.B * a.Hq, pairs = a.B * a.Hkv * a.tiles;
-    const int pieces = p.splits + warps_for(most_units(a), a.spread, a.warps) / pairs;
-    if (heads <= num_sms || (pieces > 16 && heads <= 2 * num_sms) || (p.splits > 16 && heads <= 4 * num_sms))
-        return launch_dependent(kv8_join_kernel<D, 8>, dim3(heads), dim3(8 * 32), 0, s, a, p, R);
-    if (heads <= 2 * num_sms || (p.splits > 8 && heads <= 4 * num_sms) ||
-        (pieces > 16 && heads <= 4 * num_sms) || (pieces > 24 && heads <= 8 * num_sms))
-        return launch_dependent(kv8_join_kernel<D, 4>, dim3(heads), dim3(4 * 32), 0, s, a, p, R);
-    if (pieces > 12 && heads <= 8 * num_sms)
-        return launch_dependent(kv8_join_kernel<D, 2>, dim3(heads), dim3(2 * 32), 0, s, a, p, R);
-    const bool half = heads > 18 * num_sms;
-    const int rows = kJoinCta * (half ? 2 : 1);   // of a CTA
-    return launch_dependent(half ? kv8_join_kernel<D, 0> : kv8_join_kernel<D, 1>, dim3((heads + rows - 1) / rows),
+    const int heads = a.B * a.Hq, warps = join_warps(a, p, D, num_sms);
+    if (warps > 1)
+        return launch_dependent(warps == 8   ? kv8_join_kernel<D, 8>
+                                : warps == 4 ? kv8_join_kernel<D, 4>
+                                             : kv8_join_kernel<D, 2>,
+                                dim3(heads), dim3(warps * 32), 0, s, a, p, R);
+    const int rows = kJoinCta * (warps ? 1 : 2);   // of a CTA
+    return launch_dependent(warps ? kv8_join_kernel<D, 1> : kv8_join_kernel<D, 0>, dim3((heads + rows - 1) / rows),
                             dim3(kJoinCta * 32), 0, s, a, p, R);
 }
 
@@ -874,16 +888,19 @@ bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len)
     return units > 3072;
 }
 
-cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s)
+// How the units are shared out (a.warps to a.spread); blocks an SM of their kernel.
+static int lay_out(Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms)
 {
-    Kv8Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
-    // CTAs an SM: as many as registers allow, but for 16 rows of D 128, which spill at
-    // three. 16 query and 1 kv heads, us at two / three: 64 sequences of 4000 own keys
-    // 25.3 / 28.1, 64 of 8000 39.3 / 42.1, 100 of 8000 55.7 / 51.9, 256 of 8000 124 / 114.
-    const bool two = R == 16 && D == 128 && most_units(a) < 40000;
+    const int64_t pairs = static_cast<int64_t>(a.Hkv) * (a.ptiles + static_cast<int64_t>(a.B) * a.tiles);
+    // As many as registers allow, but for 16 rows of D 128, which spill at three: three
+    // only where the tables allow very many units and the sequences are many too. 16
+    // query and 1 kv heads, us at two / three: 40 sequences of 1-4000 own keys 16.9 /
+    // 18.9, 64 of 8000 39.3 / 42.1, 100 of 1-4000 25.0 / 27.6, of 8000 55.7 / 51.9, 256
+    // of 8000 124 / 114.
+    const bool two = R == 16 && D == 128 && (most_units(a) < 40000 || pairs < 96);
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
-    const int per_sm = min(R == 8 ? 4 : two ? 2 : 3, fit) * kWarps;
+    const int blocks = min(R == 8 ? 4 : two ? 2 : 3, fit), per_sm = blocks * kWarps;
     a.warps = num_sms * per_sm;
     // a CTA of the tiled prefix takes a whole SM; the others' warps can start at once
     const int taken = p.splits * a.Hkv * p.row_pairs;
@@ -894,8 +911,22 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
     // by twos up to 128 pieces a pair (one sequence of 16 heads and 30000 keys, 937 / 468
     // pieces: 27.2 / 16.6 us) and 1536 warps (64 of 8 heads and 1000 keys, 1024 / 1536 /
     // 2048: 12.6 / 12.2 / 13.3), or 2048 where a pair then has 8 pieces at most
-    const int64_t pairs = static_cast<int64_t>(a.Hkv) * (a.ptiles + static_cast<int64_t>(a.B) * a.tiles);
     a.spread = static_cast<int>(min(max(min(8 * pairs, int64_t{2048}), int64_t{1536}), 128 * pairs));
+    return blocks;
+}
+
+void kv8_attn_layout(const Kv8Attn& in, const Kv8Prefix& p, int D, int num_sms, int* blocks_per_sm, int* warps_a_row)
+{
+    Kv8Attn a = in;
+    *blocks_per_sm = lay_out(a, p, D, num_sms);
+    *warps_a_row = join_warps(a, p, D, num_sms);
+}
+
+cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s)
+{
+    Kv8Attn a = in;
+    const int R = kv8_attn_row_tile(a.group);
+    const bool two = lay_out(a, p, D, num_sms) == 2;
     cudaError_t e;
     if (p.splits) {
         e = launch_kv8_prefix(a, p, D, per_token, s);

@@ -397,8 +397,11 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
 
 /*
  * kv8_prefix_attention -- decode attention (one query token per sequence) over
- * the cache for B sequences that share their first prefix_len tokens. The
- * prefix is read and multiplied once for the whole batch.
+ * the cache for B sequences that share their first prefix_len tokens. A prefix
+ * that is worth it (more than 3072 units of 16 keys by 8 rows, a kv head's rows
+ * being those of all sequences) goes through the tensor cores for the whole batch
+ * at once, 256 rows reading each of its keys once; a shorter one is read anew
+ * for every 8 or 16 rows.
  *
  *   q_bf16 [B, Hq, D] bf16 : rows of Hq*D values q_stride elements apart (>=
  *        Hq*D and a multiple of 8). Query head i uses kv head i / (Hq / Hkv).
@@ -421,9 +424,9 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
  *   has out = 0 and lse = -infinity. lse may be NULL. Cache bytes behind the
  *   last token of a page have no influence. The same call gives the same bits.
  *   Several query tokens of one sequence are several rows that share its pages,
- *   each with its own length.
+ *   each with its own length; each of them reads the sequence's own keys.
  *   Requires 1 <= B <= 4096, Hq a multiple of Hkv, Hq <= 65535,
- *   prefix_len >= 0, max_pages >= 0, max_pages * page_size < 2^31 and times B
+ *   prefix_len in 0..2^31 - 256, max_pages >= 0, max_pages * page_size < 2^31 and times B
  *   <= 2^34, sm_scale finite, logit_cap finite and >= 0.
  *   A page index outside [0, num_pages) or a suffix length outside
  *   [0, max_pages * page_size] touches no memory out of range; the call's

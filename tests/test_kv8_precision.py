@@ -1,5 +1,5 @@
-"""What the attention over the FP8 cache keeps of keys that stand beside much
-heavier ones, against 64 bits."""
+"""The attention over the FP8 cache against 64 bits: keys that stand beside much
+heavier ones, and sequences with several query tokens."""
 import math
 
 import pytest
@@ -143,3 +143,20 @@ def test_value_scales_far_apart(lib, what, apart, rows, hq, hkv, d, prefix, own,
 
     for row in (0, rows - 1):
         check(b, out, lse, row, floor)
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("lens,prefix,tokens,hq,hkv,d", [
+    ([40, 7, 129], 200, 4, 12, 2, 128),           # a short prefix
+    ([300, 64, 65, 2] * 5, 3000, 3, 16, 2, 64),   # a tiled one
+    ([90, 4], 0, 4, 8, 8, 128),
+])
+def test_several_query_tokens_of_a_sequence(lib, mode, lens, prefix, tokens, hq, hkv, d):
+    """A sequence's last tokens as rows that share its pages, each seeing one token more than the one before."""
+    b = Batch(lens, prefix, hq, hkv, d, 16, mode, seed=23)
+    b.table = b.table.repeat_interleave(tokens, 0)
+    b.lens_list = [max(n - tokens + 1 + i, 0) for n in lens for i in range(tokens)]
+    b.lens = torch.tensor(b.lens_list, dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    b.q = (1.5 * torch.randn(len(b.lens_list), hq, d, generator=gen, device="cuda")).to(torch.bfloat16)
+    b.check(*b.run(lib))

@@ -160,3 +160,34 @@ def test_several_query_tokens_of_a_sequence(lib, mode, lens, prefix, tokens, hq,
     gen = torch.Generator(device="cuda").manual_seed(24)
     b.q = (1.5 * torch.randn(len(b.lens_list), hq, d, generator=gen, device="cuda")).to(torch.bfloat16)
     b.check(*b.run(lib))
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("rows,prefix,own", [(1, 0, 40), (3, 30, 20), (60, 3840, 0), (60, 3840, 30)])
+def test_enormous_scores(lib, mode, rows, prefix, own, sign):
+    """Scores of 1e34 of either sign: the largest of them takes all of the weight, as anywhere else."""
+    d, hkv, hq = 64, 2, 16
+    b = Batch([own] * rows, prefix, hq, hkv, d, 16, mode, seed=25)
+    n = prefix + own
+    b.q = torch.full((rows, hq, d), sign * 2.0 ** 60, dtype=torch.bfloat16, device="cuda")
+    b.ks = torch.full_like(b.ks, 2.0 ** 45)
+    usual, special = (0x7E, 0x70) if sign < 0 else (0x70, 0x7E)   # 448 and 128: one key of each head stands out
+    b.k[:] = usual
+    for row in range(rows if own else 1):
+        for h in range(hkv):
+            i = (7 * row + 11 * h + prefix + 3) % own + prefix if own else 5 + h
+            pages = b.prefix_pages if i < prefix else b.table[row]
+            at = i if i < prefix else i - prefix
+            b.k[int(pages[at // 16]), h, at % 16] = special
+    out, lse = b.run(lib)
+    for row in range(0, rows, 7):
+        k, v = b.keys(row)
+        s = b.q[row].double().reshape(hkv, -1, d) @ k.transpose(1, 2) * b.scale
+        assert float(s.abs().min()) > 1e33
+        best = s.argmax(-1)
+        want = torch.stack([v[h, best[h, 0]] for h in range(hkv)]).repeat_interleave(hq // hkv, 0)
+        # one rounding of the weight times scale to f16, one of the sum to bf16
+        assert bool(((out[row].double() - want).abs() <= want.abs() * (2.0 ** -11 + 2.0 ** -8)).all())
+        z = s.amax(-1).reshape(-1)
+        assert bool(((lse[row].double() - z).abs() <= z.abs() * (d + 8) * 2.0 ** -23).all())

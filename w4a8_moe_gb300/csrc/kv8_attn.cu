@@ -26,7 +26,7 @@ constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
 constexpr int kStages = 2;   // units in flight per warp
 constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
 constexpr float kMostWeight = 0x1p15f;   // 2^kWeightMost
-constexpr float kLowest = -1e30f;   // the reference of a row without keys
+constexpr float kLowest = -3.4028235e38f;   // the reference of a row without keys
 
 // D[16x8] += A[16x16] B[16x8], f16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -486,9 +486,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                s[t][k] *= qs[t][k & 1];
-                if (TOK)
-                    s[t][k] *= ks[k >> 1];
+                // (rounded once: the reference and the weights see the same score)
+                s[t][k] = TOK ? __fmul_rn(s[t][k] * qs[t][k & 1], ks[k >> 1]) : __fmul_rn(s[t][k], qs[t][k & 1]);
             }
         if (a.cap > 0.0f) {
 #pragma unroll

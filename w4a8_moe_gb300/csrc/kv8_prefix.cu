@@ -47,8 +47,14 @@ static_assert(kRaw % kPairs == 0, "a raw slot has one pair of readers");
 constexpr int kScaleRing = 4;     // tiles whose per-token scales are held
 // A tile whose value scales lie within this factor takes its largest score and its
 // largest scale for its largest product: at most this factor too much. Others look
-// at every key (tile()).
+// at every key (careful_tile).
 constexpr float kNear = 64.0f;
+// References (log2) up to which a tile goes the short way: there a weight's exponent
+// is a fused product and difference, off from the rounded score that the reference
+// was taken from by 2^-4 at most, and stays far inside f16. (A product and a
+// difference of pairs, each with its own rounding, are fused by the compiler too:
+// the other way takes single ones.)
+constexpr float kFused = 0x1p20f;
 
 template <int D>
 struct Smem {
@@ -333,35 +339,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             const uint32_t ts = tmem + (static_cast<uint32_t>(warp & 3) << 21) + t * kTile;         // S, then P
             const uint32_t to = tmem + (static_cast<uint32_t>(warp & 3) << 21) + 2 * kTile + t * D;  // O
             float m = -INFINITY;
+            bool enormous = false;   // whether a row of the warp has such a reference
             F2 l0(0.0f, 0.0f), l1(0.0f, 0.0f);
             const float* scales = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + L::scales);
             // What a tile does to the row, scores in units of c:
-            // the reference raised where the largest weight asks for it (kWeightMost),
+            // the reference raised where the largest weight asks for it (kWeightMost;
+            // the whole warp goes through its accumulators together),
             auto raise = [&](int i, float best) {
-                if (__any_sync(0xFFFFFFFFu, best > m + kWeightMost)) {
-                    const float next = fmaxf(m, best - kWeightTop);
-                    const float f = next == -INFINITY ? 1.0f : ex2(m - next);
-                    m = next;
-                    l0 = mul2(l0, F2(f, f));
-                    l1 = mul2(l1, F2(f, f));
-                    if (i > 0) {
+                const float next = fmaxf(m, best - kWeightTop);
+                const float f = next == -INFINITY ? 1.0f : ex2(m - next);
+                m = next;
+                enormous = __any_sync(0xFFFFFFFFu, m > -INFINITY && fabsf(m) > kFused);
+                l0 = mul2(l0, F2(f, f));
+                l1 = mul2(l1, F2(f, f));
+                if (i > 0) {
 #pragma unroll 1
-                        for (int ch = 0; ch < D / 16; ++ch) {
-                            uint32_t x[16];
-                            tmem_ld16(to + ch * 16, x);
-                            ld_wait16(x);
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        uint32_t x[16];
+                        tmem_ld16(to + ch * 16, x);
+                        ld_wait16(x);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                            tmem_st16(to + ch * 16, x);
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                        tmem_st16(to + ch * 16, x);
                     }
                 }
             };
             // the largest score in log2 units: cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y})),
             // c holding 2 log2(e) / cap
             auto in_log2 = [&](float top) {
-                const float x = top * c;
+                const float x = __fmul_rn(top, c);   // what weigh() takes, where it does not fuse
                 return CAP ? fmaf(-2.0f * capl, rcp(1.0f + ex2(x)), capl) : x;
             };
             // 32 keys' scores times their key scales,
@@ -383,10 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     top = max3(top, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
                 return top;
             };
-            // and their weights as f16, added up on the way. Of the first `live` keys;
-            // value_scales(j): of keys j to j + 3.
-            auto weigh = [&](const uint32_t (&r)[32], auto value_scales, int ch, int live, auto masked) {
-                constexpr bool kMasked = decltype(masked)::value;
+            // and their weights as f16, added up on the way. kCareful: of the first
+            // `live` keys, the score rounded like the reference's before their
+            // difference is taken. value_scales(j): of keys j to j + 3.
+            auto weigh = [&](const uint32_t (&r)[32], auto value_scales, int ch, int live, auto careful) {
+                constexpr bool kCareful = decltype(careful)::value;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const F2 c2(c, c), add(CAP ? capl - ref : -ref, CAP ? capl - ref : -ref);
                 const F2 one(1.0f, 1.0f), two(-2.0f * capl, -2.0f * capl), zero(-0.0f, -0.0f);
@@ -400,12 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     for (int e = 0; e < 4; e += 2) {
                         const F2 s(__uint_as_float(r[j + e]), __uint_as_float(r[j + e + 1]));
                         F2 x = fma2(s, c2, CAP ? zero : add);
-                        if (CAP) {
+                        if (kCareful) {
+                            x = F2(__fadd_rn(in_log2(s.lo()), -ref), __fadd_rn(in_log2(s.hi()), -ref));
+                        } else if (CAP) {
                             x = add2(F2(ex2(x.lo()), ex2(x.hi())), one);
                             x = fma2(F2(rcp(x.lo()), rcp(x.hi())), two, add);
                         }
                         float w0 = ex2(x.lo()), w1 = ex2(x.hi());
-                        if (kMasked) {
+                        if (kCareful) {
                             w0 = j + e < live ? w0 : 0.0f;
                             w1 = j + e + 1 < live ? w1 : 0.0f;
                         }
@@ -429,96 +439,108 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                 }
             };
             // A key tile: the whole row of scores in registers, `lift` the log2 of
-            // the largest value scale. The prefix's last tile, where keys past its
-            // end are masked, and tiles whose value scales lie far apart go the other
-            // way, which reads S twice but is a quarter of the code; there a lane
-            // holds the value scales v[j] of the keys lane + 32 j (0 past the end).
-            auto tile = [&](int i, float lift, float (&v)[4], auto brief) {
-                constexpr bool kBrief = decltype(brief)::value;
+            // the largest value scale. Nothing but the raised reference where that is
+            // enormous.
+            auto tile = [&](int i, float lift) {
                 const float* ks = scales + (i % kScaleRing) * 2 * kTile;
                 const float* vs = ks + kTile;
                 if (!wait_warp(kSFull + t, i & 1))
                     return false;
                 tc_fence_after();
-                if constexpr (kBrief) {
-                    const int live = a.prefix_len - (tile0 + i) * kTile;
-                    if (TOK) {
-                        // Values of a key that are all zero add nothing, whatever their
-                        // scale (kv8_write gives them 1): 0 then, so that they lead no
-                        // reference. V stands in its stage until this tile's weights are
-                        // given; its barrier's phase before this one was K's of the tile
-                        // before, which S is behind.
-                        const int jv = 2 * i + 1;
-                        if (!wait_warp(kFull + jv % kStages, (jv / kStages) & 1))
-                            return false;
-                        const uint32_t at = base + L::stage + (jv % kStages) * L::kOperand + lane * 128;
+                uint32_t r[4][32];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t any = 0;
+                for (int ch = 0; ch < 4; ++ch)
+                    tmem_ld32(ts + ch * 32, r[ch]);
+                float top[4];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    ld_wait32(r[ch]);
+                    if (TOK)
+                        times_scales(r[ch], ks + ch * 32);
+                    top[ch] = largest(r[ch]);
+                }
+                const float best = in_log2(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))) + lift;
+                if (__any_sync(0xFFFFFFFFu, best > m + kWeightMost)) {
+                    raise(i, best);
+                    if (enormous)
+                        return true;
+                }
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    auto value_scales = [&](int j) { return *reinterpret_cast<const float4*>(vs + ch * 32 + j); };
+                    weigh(r[ch], value_scales, ch, kTile, Const<false>());
+                }
+                return true;
+            };
+            // The other way, for the prefix's last tile, where keys past its end are
+            // masked, for tiles whose value scales lie far apart and for those under an
+            // enormous reference: it reads S twice but is a quarter of the code. A
+            // lane holds the value scales v[j] of the keys lane + 32 j (0 past the end).
+            auto careful_tile = [&](int i, float (&v)[4]) {
+                const float* ks = scales + (i % kScaleRing) * 2 * kTile;
+                if (!wait_warp(kSFull + t, i & 1))
+                    return false;
+                tc_fence_after();
+                const int live = a.prefix_len - (tile0 + i) * kTile;
+                if (TOK) {
+                    // Values of a key that are all zero add nothing, whatever their
+                    // scale (kv8_write gives them 1): 0 then, so that they lead no
+                    // reference. V stands in its stage until this tile's weights are
+                    // given; its barrier's phase before this one was K's of the tile
+                    // before, which S is behind.
+                    const int jv = 2 * i + 1;
+                    if (!wait_warp(kFull + jv % kStages, (jv / kStages) & 1))
+                        return false;
+                    const uint32_t at = base + L::stage + (jv % kStages) * L::kOperand + lane * 128;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t any = 0;
 #pragma unroll 4
-                            for (int x = 0; x < D / 8; ++x) {   // 16 bytes each, another bank group a lane
-                                const uint4 w = lds128(at + j * 32 * 128 + (x >> 3) * L::kPanel + (((x + lane) & 7) << 4));
-                                any |= w.x | w.y | w.z | w.w;
-                            }
-                            v[j] = (any & 0x7FFF7FFFu) ? v[j] : 0.0f;
+                        for (int x = 0; x < D / 8; ++x) {   // 16 bytes each, another bank group a lane
+                            const uint4 w = lds128(at + j * 32 * 128 + (x >> 3) * L::kPanel + (((x + lane) & 7) << 4));
+                            any |= w.x | w.y | w.z | w.w;
                         }
+                        v[j] = (any & 0x7FFF7FFFu) ? v[j] : 0.0f;
                     }
-                    auto of_chunk = [&](const float (&x)[4], int ch) { return ch < 2 ? (ch ? x[1] : x[0]) : (ch == 2 ? x[2] : x[3]); };
-                    float top = -INFINITY;
+                }
+                auto of_chunk = [&](const float (&x)[4], int ch) { return ch < 2 ? (ch ? x[1] : x[0]) : (ch == 2 ? x[2] : x[3]); };
+                float top = -INFINITY;
 #pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t r[32];
-                        tmem_ld32(ts + ch * 32, r);
-                        ld_wait32(r);
-                        if (TOK) {
-                            times_scales(r, ks + ch * 32);
-                            const float mine = fmaxf(log2f(fabsf(of_chunk(v, ch))), kLeastScaleLog2);
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t r[32];
+                    tmem_ld32(ts + ch * 32, r);
+                    ld_wait32(r);
+                    if (TOK) {
+                        times_scales(r, ks + ch * 32);
+                        const float mine = fmaxf(log2f(fabsf(of_chunk(v, ch))), kLeastScaleLog2);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float y = in_log2(__uint_as_float(r[j])) + __shfl_sync(0xFFFFFFFFu, mine, j);
-                                top = fmaxf(top, ch * 32 + j < live ? y : -INFINITY);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                r[j] = ch * 32 + j < live ? r[j] : 0xFF800000u;
-                            top = fmaxf(top, largest(r));
+                        for (int j = 0; j < 32; ++j) {
+                            const float y = in_log2(__uint_as_float(r[j])) + __shfl_sync(0xFFFFFFFFu, mine, j);
+                            top = fmaxf(top, ch * 32 + j < live ? y : -INFINITY);
                         }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            r[j] = ch * 32 + j < live ? r[j] : 0xFF800000u;
+                        top = fmaxf(top, largest(r));
                     }
-                    raise(i, TOK ? top : in_log2(top));
+                }
+                top = TOK ? top : in_log2(top);
+                if (__any_sync(0xFFFFFFFFu, top > m + kWeightMost))
+                    raise(i, top);
 #pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t r[32];
-                        tmem_ld32(ts + ch * 32, r);
-                        ld_wait32(r);
-                        if (TOK)
-                            times_scales(r, ks + ch * 32);
-                        const float mine = of_chunk(v, ch);
-                        auto value_scales = [&](int j) {
-                            return make_float4(__shfl_sync(0xFFFFFFFFu, mine, j), __shfl_sync(0xFFFFFFFFu, mine, j + 1),
-                                               __shfl_sync(0xFFFFFFFFu, mine, j + 2), __shfl_sync(0xFFFFFFFFu, mine, j + 3));
-                        };
-                        weigh(r, value_scales, ch, live - ch * 32, Const<true>());
-                    }
-                } else {
-                    uint32_t r[4][32];
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch)
-                        tmem_ld32(ts + ch * 32, r[ch]);
-                    float top[4];
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        ld_wait32(r[ch]);
-                        if (TOK)
-                            times_scales(r[ch], ks + ch * 32);
-                        top[ch] = largest(r[ch]);
-                    }
-                    raise(i, in_log2(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))) + lift);
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        auto value_scales = [&](int j) { return *reinterpret_cast<const float4*>(vs + ch * 32 + j); };
-                        weigh(r[ch], value_scales, ch, kTile, Const<false>());
-                    }
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t r[32];
+                    tmem_ld32(ts + ch * 32, r);
+                    ld_wait32(r);
+                    if (TOK)
+                        times_scales(r, ks + ch * 32);
+                    const float mine = of_chunk(v, ch);
+                    auto value_scales = [&](int j) {
+                        return make_float4(__shfl_sync(0xFFFFFFFFu, mine, j), __shfl_sync(0xFFFFFFFFu, mine, j + 1),
+                                           __shfl_sync(0xFFFFFFFFu, mine, j + 2), __shfl_sync(0xFFFFFFFFu, mine, j + 3));
+                    };
+                    weigh(r, value_scales, ch, live - ch * 32, Const<true>());
                 }
                 return true;
             };
@@ -543,7 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
                     whole = whole && __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, least)) * kNear >= hi;
                     lift = fmaxf(log2f(hi), kLeastScaleLog2);
                 }
-                ok = whole ? tile(i, lift, v, Const<false>()) : tile(i, lift, v, Const<true>());
+                if (whole && !enormous)
+                    ok = tile(i, lift);
+                if (ok && (!whole || enormous))
+                    ok = careful_tile(i, v);
             }
             // -------------------------------------------------------- results
             // Each thread lays its row of O in shared memory (the operands are

@@ -420,7 +420,7 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
  *   to a running reference: each is off by 2^-11 of itself and 2^-33 of the
  *   largest one. With scale_mode 1 that is the weight times its value's scale, off
  *   by 2^-11 of itself and 2^-27 of the largest such product among the keys whose
- *   values are not all zero, whatever their scales. A sequence without any key
+ *   values are not all zero (scales below 2^-92 lose more). A sequence without any key
  *   has out = 0 and lse = -infinity. lse may be NULL. Cache bytes behind the
  *   last token of a page have no influence. The same call gives the same bits.
  *   Several query tokens of one sequence are several rows that share its pages,

@@ -191,3 +191,53 @@ def test_enormous_scores(lib, mode, rows, prefix, own, sign):
         assert bool(((out[row].double() - want).abs() <= want.abs() * (2.0 ** -11 + 2.0 ** -8)).all())
         z = s.amax(-1).reshape(-1)
         assert bool(((lse[row].double() - z).abs() <= z.abs() * (d + 8) * 2.0 ** -23).all())
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d,prefix,own", [(60, 12, 2, 128, 4000, 0), (300, 8, 8, 128, 0, 1500), (60, 12, 2, 64, 2000, 500)])
+def test_value_scales_tiny_throughout(lib, rows, hq, hkv, d, prefix, own):
+    """Values of 1e-24: scales down to 2^-92 keep everything."""
+    b = many(Batch([own], prefix, hq, hkv, d, 64, 1, seed=26, q_scale=1.0), rows)
+    b.v &= 0x7F
+    b.vs *= 2.0 ** -80
+    assert float(torch.where(torch.isfinite(b.vs), b.vs, 1.0).min()) >= 2.0 ** -92
+    out, lse = b.run(lib)
+    for row in (0, rows - 1):
+        check(b, out, lse, row, lambda w, v, row: w.amax(-1, keepdim=True) * v.sum(1)[:, None] * 2.0 ** -27)
+
+
+@pytest.mark.parametrize("every", [1, 3])
+def test_many_tiles_key_by_key(lib, every):
+    """A long run of tiles of one block, all or some of them with value scales far apart: the same bits in every call."""
+    rows, hq, hkv, d, prefix = 230, 48, 8, 128, 12800
+    b = many(Batch([0], prefix, hq, hkv, d, 64, 1, seed=27, q_scale=1.0), rows)
+    assert lib.kv8_prefix_attention_plan(rows, hq, hkv, d, prefix, b.table.shape[1], 64, 1)["tiles_per_range"] >= 20
+    b.v &= 0x7F
+    b.vs *= 2.0 ** -12
+    for i in range(0, prefix, 128 * every):
+        page, off = key_at(b, i + i // 128 % 128)
+        b.v[page, :, off], b.vs[page, :, off] = 0, 1.0
+    out, lse = b.run(lib)
+
+    def floor(w, v, row):   # 2^-27 of the largest weight times scale; a key's scale is its largest value / 448 or more
+        return (w * v.amax(-1)[:, None]).amax(-1, keepdim=True) * 2.0 ** -27 * prefix
+
+    for row in (0, 100, rows - 1):
+        check(b, out, lse, row, floor)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        got = b.run(lib)
+        differ += (got[0] != out).sum() + (got[1] != lse).sum()
+    assert int(differ) == 0
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("rows,prefix,own", [(50, 6000, 0), (3, 100, 700), (40, 3000, 333)])
+def test_empty_cache(lib, mode, rows, prefix, own):
+    """Codes and scales of zero throughout: all keys weigh the same and there is no value."""
+    b = Batch([own] * rows, prefix, 12, 2, 128, 16, mode, seed=28)
+    for x in (b.k, b.v, b.ks, b.vs):
+        x.zero_()
+    out, lse = b.run(lib)
+    assert bool((out == 0).all())
+    want = math.log(prefix + own)   # fp32 exponents about the reference (under 2^7) and a sum of n weights
+    assert bool(((lse.double() - want).abs() <= 2.0 ** -16).all())

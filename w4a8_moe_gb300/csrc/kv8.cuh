@@ -111,9 +111,10 @@ constexpr float kWeightMost = 15.0f;
 // its value's scale (the reference then carries the values' size too, and drops out
 // of o / l), the largest of these products of single keys; a key whose values are
 // all zero has none. Smaller scales count as kLeastScale there, which keeps the
-// weights themselves, and their sum over up to 2^30 keys, inside fp32.
-constexpr float kLeastScale = 0x1p-64f;
-constexpr float kLeastScaleLog2 = -64.0f;
+// weights themselves inside fp32: 2^100 where the reference was raised, 2^107 at
+// most, added up over the keys of a piece.
+constexpr float kLeastScale = 0x1p-92f;
+constexpr float kLeastScaleLog2 = -92.0f;
 
 constexpr float kLog2e = 1.4426950408889634f;
 

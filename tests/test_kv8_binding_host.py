@@ -36,6 +36,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(pkg, "_lib", lib)
     monkeypatch.setattr(pkg, "_raw_stream", lambda device: 1000 + device)
     monkeypatch.setattr(pkg, "_current_device", lambda: DEVICE, raising=False)
+    monkeypatch.setattr(pkg, "_gpus", 2, raising=False)
     return seen
 
 

@@ -344,6 +344,13 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_gpus = 0   # how many there are, once known: with one, tensors on a GPU are on the current one
+
+
+def _count_gpus():
+    global _gpus
+    _gpus = torch.cuda.device_count()
+    return _gpus
 
 
 def _cache_refused(k_cache, v_cache, k_scale, v_scale):
@@ -400,7 +407,8 @@ def kv8_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, min_scale: float 
     k_stride, v_stride = _row_stride(k, T, h, d, "k"), _row_stride(v, T, h, d, "v")
     device = k_cache.get_device()
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
-                          == k.get_device() == v.get_device() == slots.get_device() == _current_device()):
+                          == k.get_device() == v.get_device() == slots.get_device()) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
         raise _devices_refused(k_cache, v_cache, k_scale, v_scale, k, v, slots)
     to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     status = (_lib or _load()).kv8_write(
@@ -430,7 +438,8 @@ def kv8_read(k_cache, v_cache, k_scale, v_scale, slots, k_out=None, v_out=None, 
     k_stride, v_stride = _row_stride(k_out, T, h, d, "k_out"), _row_stride(v_out, T, h, d, "v_out")
     device = k_cache.get_device()
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
-                          == slots.get_device() == k_out.get_device() == v_out.get_device() == _current_device()):
+                          == slots.get_device() == k_out.get_device() == v_out.get_device()) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
         raise _devices_refused(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
     to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     status = (_lib or _load()).kv8_read(
@@ -460,10 +469,11 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
         raise ValueError("q must be bf16 [B, query heads, D of the cache]")
     B, hq, _ = q_shape
     q_stride = _row_stride(q, B, hq, d, "q")
+    device = k_cache.get_device()
     if page_table is None and suffix_lens is None:
         row = most = 0
         table = lens = None
-        own = q, q   # (for the check of the devices)
+        own_device = device
     else:
         if page_table is None or page_table.dtype is not _I32 or page_table.dim() != 2:
             raise ValueError("page_table must be int32 [B, max pages]; None only with suffix_lens None")
@@ -474,11 +484,13 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
         if suffix_lens is None or suffix_lens.dtype is not _I32 or suffix_lens.shape != (B,) \
                 or not suffix_lens.is_contiguous():
             raise _vector_refused("suffix_lens")
-        table, lens, own = page_table.data_ptr(), suffix_lens.data_ptr(), (page_table, suffix_lens)
-    device = k_cache.get_device()
+        table, lens, own_device = page_table.data_ptr(), suffix_lens.data_ptr(), page_table.get_device()
+        if suffix_lens.get_device() != own_device:
+            raise _devices_refused(k_cache, page_table, suffix_lens)
     if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
-                          == q.get_device() == own[0].get_device() == own[1].get_device() == _current_device()):
-        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, *own)
+                          == q.get_device() == own_device) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, *(() if table is None else (page_table,)))
     to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     pages, prefix_len = None, int(prefix_len)
     if prefix_len > 0:

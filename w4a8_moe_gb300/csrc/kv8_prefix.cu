@@ -852,38 +852,40 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_u
     // 72 and 48 SMs: 0.80 and 0.87). Every split is written and read once more.
     struct Split {
         int splits, per;
-        double us, rate, join;
-        double with(double own_us) const
+        float us, rate, slow, join;   // slow: 1 / rate
+        float with(float own_us) const
         {
-            double own = 0.0;
-            if (own_us > 0.0) {
-                const double early = rate * (us > 4.0 ? us - 4.0 : 0.0);
-                own = us + 4.0 + (own_us > early ? own_us - early : 0.0);
-                if (rate > 0.0 && 4.0 + own_us / rate < own)
-                    own = 4.0 + own_us / rate;
+            float own = 0.0f;
+            if (own_us > 0.0f) {
+                const float early = rate * (us > 4.0f ? us - 4.0f : 0.0f);
+                own = us + 4.0f + (own_us > early ? own_us - early : 0.0f);
+                if (rate > 0.0f && 4.0f + own_us * slow < own)
+                    own = 4.0f + own_us * slow;
             }
             return (own > us ? own : us) + join;
         }
     };
-    const int64_t base = static_cast<int64_t>(Hkv) * p.row_pairs;
+    const int base = Hkv * p.row_pairs;   // below 2^21, and 2^27 times the splits
+    const float join_us = static_cast<float>(Hkv) * rows * D * (8 / 8e6f);
     const int most = kv8_prefix_most_splits(Hkv, rows, prefix_len);
     Split all[kKv8MaxSplits];
     int n = 0;
-    double alone = 0.0;
+    float alone = 0.0f;
     for (int s = 1; s <= most; ++s) {
         const int per = (p.tiles + s - 1) / s;
         const int splits = (p.tiles + per - 1) / per;
         if (s > 1 && splits < s)
             continue;   // the same as one before
-        const int64_t taken = base * splits, waves = (taken + num_sms - 1) / num_sms;
+        const int taken = base * splits, waves = (taken + num_sms - 1) / num_sms;
         Split& x = all[n++];
         x.splits = splits;
         x.per = per;
-        x.us = static_cast<double>(waves) * (per * tile_us + 5.0);
-        const double free = waves > 1 ? 0.0 : static_cast<double>(num_sms - taken) / num_sms;
-        x.rate = free * (2.0 - free);
-        x.join = static_cast<double>(splits) * Hkv * rows * D * 8 / 8e6;
-        const double us = x.us + x.join;
+        x.us = waves * (per * tile_us + 5.0f);
+        const float free = waves > 1 ? 0.0f : static_cast<float>(num_sms - taken) / num_sms;
+        x.rate = free * (2.0f - free);
+        x.slow = 1.0f / x.rate;
+        x.join = splits * join_us;
+        const float us = x.us + x.join;
         alone = n == 1 || us < alone ? us : alone;
     }
     // The lengths stand on the device, and a page table's width only bounds them. So
@@ -895,19 +897,20 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_u
     // 1.20 times at most. By half of what the tables hold, with the wide ones, us: 64
     // sequences over 8192 131 (now 29.6), 128 over 32768 365 (103), 256 over 65536 707
     // (266), 32 over 1024, capped, 34.9 (14.8).
-    const double bytes_us = static_cast<double>(own_max) * Hkv * 2 * D / 5.5e6;
+    const float bytes_us = static_cast<float>(own_max) * Hkv * (2 * D / 5.5e6f);
     constexpr int kLoads = 3;
-    constexpr double kLoad[kLoads] = {0.25, 0.5, 1.0};
-    double worst[kKv8MaxSplits] = {};
+    constexpr float kLoad[kLoads] = {0.25f, 0.5f, 1.0f};
+    float worst[kKv8MaxSplits];
     for (int j = 0; j < kLoads; ++j) {
-        const double own_us = kLoad[j] * alone < bytes_us ? kLoad[j] * alone : bytes_us;
-        double us[kKv8MaxSplits], best = 0.0;
+        const float own_us = kLoad[j] * alone < bytes_us ? kLoad[j] * alone : bytes_us;
+        float us[kKv8MaxSplits], best = 0.0f;
         for (int i = 0; i < n; ++i) {
             us[i] = all[i].with(own_us);
             best = i == 0 || us[i] < best ? us[i] : best;
         }
+        const float scale = 1.0f / best;
         for (int i = 0; i < n; ++i)
-            worst[i] = us[i] > worst[i] * best ? us[i] / best : worst[i];
+            worst[i] = j == 0 || us[i] * scale > worst[i] ? us[i] * scale : worst[i];
         if (own_us >= bytes_us)
             break;
     }
@@ -916,7 +919,7 @@ Kv8Prefix kv8_prefix_plan(int Hkv, int rows, int prefix_len, int D, float tile_u
         at = worst[i] < worst[at] ? i : at;
     p.splits = all[at].splits;
     p.tiles_per_split = all[at].per;
-    p.us = static_cast<float>(all[at].us);
+    p.us = all[at].us;
     return p;
 }
 

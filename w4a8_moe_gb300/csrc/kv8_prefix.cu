@@ -20,8 +20,9 @@
 //
 // Numbers: q is normalized per row by a power of two and held in f16 (at most
 // 2^-25 of the row's largest element is lost, one fp32 rounding), codes are
-// exact in f16, S and O are fp32, P is rounded to f16 (2^-11 of each weight),
-// its sum is taken in fp32 before that rounding.
+// exact in f16, S and O are fp32, P is rounded to f16 (2^-11 of each weight and
+// 2^-33 of the largest, see kWeightTop), its sum is taken in fp32 before that
+// rounding.
 #include <math.h>
 
 #include "internal.h"

@@ -1,5 +1,5 @@
 """The attention over the FP8 cache against 64 bits: keys that stand beside much
-heavier ones, and sequences with several query tokens."""
+heavier ones, sequences with several query tokens, wide page tables."""
 import math
 
 import pytest
@@ -241,3 +241,17 @@ def test_empty_cache(lib, mode, rows, prefix, own):
     assert bool((out == 0).all())
     want = math.log(prefix + own)   # fp32 exponents about the reference (under 2^7) and a sum of n weights
     assert bool(((lse.double() - want).abs() <= 2.0 ** -16).all())
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("batch,hq,hkv,d,prefix,own,page,extra", [
+    (64, 32, 8, 128, 2048, 60, 64, 2048),    # tables of 131072 tokens
+    (17, 16, 1, 64, 4999, 300, 16, 8192),
+    (70, 16, 1, 64, 0, 60, 64, 512),
+    (40, 16, 1, 128, 0, 250, 64, 512),
+    (3, 48, 8, 128, 200, 17, 256, 100),
+])
+def test_tables_far_wider_than_the_lengths(lib, mode, batch, hq, hkv, d, prefix, own, page, extra):
+    """Page tables sized for the longest context, with next to nothing in them."""
+    b = Batch([own - 7 * i % own for i in range(batch)], prefix, hq, hkv, d, page, mode, seed=29, extra=extra)
+    b.check(*b.run(lib))

@@ -455,7 +455,7 @@ def _plain_pages(s):
     taken = torch.where(fits, need, 0).sum()
     s.count.sub_(taken)
     step = [starts.to(i32), torch.where(there, seq, -1).to(i32), torch.where(there, pos, 0).to(i32),
-            torch.where(there, pos + 1, 0).to(i32), torch.where(there & fits[seq], slot, -1).to(i32), grown]
+            torch.where(there & fits[seq], pos + 1, 0).to(i32), torch.where(there & fits[seq], slot, -1).to(i32), grown]
     # and back: the pages behind the kept tokens, the first sequence's first page on top of the stack
     give = torch.where(fits, need, 0)
     ahead = torch.cumsum(give, 0) - give

@@ -29,8 +29,8 @@
  *    *_workspace_size(). The first 256 bytes of every workspace are a header:
  *    the caller zero-fills them once when it allocates the workspace. Byte 0
  *    holds a device error word that kernels only OR bits into (a bounded wait
- *    that ran out sets bit 0, an index out of range bit 1); w4a8_device_error()
- *    reads and clears it. Calls
+ *    that ran out sets bit 0, an index out of range bit 1, a pool without pages
+ *    bit 2); w4a8_device_error() reads and clears it. Calls
  *    may keep other counters in the header; every call leaves them zero.
  *  - Stateless and thread-safe; concurrent calls must use distinct workspaces.
  */
@@ -53,8 +53,9 @@ typedef enum {
     W4A8_ERR_DEVICE = 5,    /* no sm_103 device, or the kernel image is absent */
     W4A8_ERR_LAUNCH = 6,    /* a CUDA launch or driver call failed             */
     W4A8_ERR_TIMEOUT = 7,   /* reported by w4a8_device_error: a bounded wait ran out */
-    W4A8_ERR_INDEX = 8      /* reported by w4a8_device_error: a page index or a length
+    W4A8_ERR_INDEX = 8,     /* reported by w4a8_device_error: a page index or a length
                                read on the device was out of range                  */
+    W4A8_ERR_PAGES = 9      /* reported by w4a8_device_error: the pool of pages ran out */
 } w4a8_status_t;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -463,6 +464,209 @@ int kv8_prefix_attention_plan(int B, int Hq, int Hkv, int D, int prefix_len, int
                               int scale_mode, float logit_cap, int num_sms, int32_t* plan);
 
 /*
+ * rope_table -- the frequencies of a rotary position embedding, laid out for
+ * qk_norm_rope and kv8_norm_rope_write. Host only: no device is touched; the
+ * caller copies `turns` to the device once, when the model is loaded.
+ *
+ *   rotary_dim R : values of a head that are rotated, a multiple of 16 in 16..256.
+ *   inv_freq [R/2] double (host) : the model's own frequencies, in radians per
+ *        position; with NULL they are f_i = base^(-2i/R), stretched by `scaling`:
+ *        0  f_i
+ *        1  linear: f_i / factor
+ *        2  raised base: base * factor^(R/(R-2)) in base's place
+ *        3  by pairs (YaRN): f_i of the pairs that turn more than `high` times over
+ *           original_len positions, f_i / factor of those that turn less than `low`
+ *           times, between them a linear ramp over i; magnitude 0.1 ln(factor) + 1
+ *        4  by wavelength: with r = original_len f_i / 2 pi, f_i where r > high,
+ *           f_i / factor where r < low, between them a linear blend in r
+ *   turns [R/2] u64 (host), out: |f_i| / 2 pi as a fraction of 2^64, rounded down
+ *        (negative frequencies as the complement).
+ *   magnitude [1] (host), out: what the rotated values are multiplied by (1, but
+ *        for scaling 3).
+ *   Requires base > 1, factor >= 1 for the scalings that use it, original_len >= 1
+ *   and 0 < low < high for 3 and 4, |inv_freq| <= 2 pi.
+ */
+int rope_table(int rotary_dim, const double* inv_freq, double base, int scaling, double factor, double original_len,
+               double low, double high, uint64_t* turns, float* magnitude);
+
+/*
+ * qk_norm_rope -- queries and keys of T tokens: a norm of each head (where
+ * weights are given) and the rotation by the token's position, in one pass.
+ *
+ *   q_bf16 [T, Hq, D], k_bf16 [T, Hkv, D] bf16 : rows of heads, *_stride elements
+ *        apart (columns of a fused projection's output are fine). k_bf16 may be
+ *        NULL with Hkv 0.
+ *   positions [T] i32 : any value (a token's angle for the pair i is position * f_i,
+ *        exact modulo a turn for every position).
+ *   turns [R/2] u64 (device), magnitude: from rope_table.
+ *   interleaved 0: pairs (i, i + R/2), 1: pairs (2i, 2i + 1), i < R/2; the other
+ *        D - R values of a head are not rotated.
+ *   q_weight, k_weight [D] bf16 : x -> x / sqrt(mean(x^2) + eps) * w over the D
+ *        values of a head, before the rotation; NULL: no norm.
+ *   q_out, k_out bf16 : out, the same shapes; each may be its own input (same
+ *        pointer and stride), else they must not overlap the inputs.
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin), all of it in fp32,
+ *   rounded once.
+ *   Requires T >= 1, Hq >= 1, Hkv >= 0, Hq + Hkv <= 65535, D a multiple of 16 in
+ *   16..256, R <= D a multiple of 16, strides multiples of 8 and at least Hq*D or
+ *   Hkv*D, eps >= 0 and magnitude finite.
+ *   No workspace; one kernel.
+ */
+int qk_norm_rope(const uint16_t* q_bf16, int64_t q_stride, int Hq, const uint16_t* k_bf16, int64_t k_stride, int Hkv,
+                 int T, int D, const int32_t* positions, const uint64_t* turns, int rotary_dim, float magnitude,
+                 int interleaved, const uint16_t* q_weight, const uint16_t* k_weight, float eps, uint16_t* q_out,
+                 int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * kv8_norm_rope_write -- qk_norm_rope and kv8_write in one pass: the queries are
+ * normed, rotated and written to q_out; the keys are normed, rotated and, with the
+ * values, quantized into their slots. The keys are quantized from fp32, without a
+ * rounding to bf16 between (which would move a row's scale by up to 2^-9).
+ *
+ *   Arguments as of qk_norm_rope (q_out may be q_bf16) and of kv8_write: a token
+ *   whose slot is out of range is left out of the cache, but its queries are still
+ *   written.
+ *   Requires what both require; Hkv >= 1, Hq + 2 Hkv <= 65535.
+ *   No workspace; one kernel.
+ */
+int kv8_norm_rope_write(const uint16_t* q_bf16, int64_t q_stride, int Hq, const uint16_t* k_bf16, int64_t k_stride,
+                        const uint16_t* v_bf16, int64_t v_stride, int Hkv, int T, int D, const int32_t* positions,
+                        const int32_t* slots, const uint64_t* turns, int rotary_dim, float magnitude, int interleaved,
+                        const uint16_t* q_weight, const uint16_t* k_weight, float eps, int num_pages, int page_size,
+                        int scale_mode, float min_scale, uint16_t* q_out, int64_t q_out_stride, uint8_t* k_cache,
+                        uint8_t* v_cache, float* k_scale, float* v_scale, void* stream);
+
+/*
+ * kv_pages_extend -- the pages and slots of a step's new tokens, from the lengths
+ * of the sequences and a stack of free pages, all of it on the GPU: nothing but the
+ * sizes below has to be known on the host, so a captured step stays valid while the
+ * sequences grow.
+ *
+ *   lens [B] i32 : tokens that each sequence has in the cache; new_lens [B] i32 :
+ *        tokens that come to it now (0 allowed).
+ *   page_table [B, max_pages] i32, rows table_stride elements apart (>= max_pages):
+ *        in, the pages of the tokens that are there; out, those of the new tokens
+ *        as well. Other entries are left as they are.
+ *   free_pages [num_pages] i32, free_count [1] i32 (device): the stack of pages that
+ *        nobody has, its top at free_pages[free_count - 1]. In the order of the
+ *        sequences, and of each one's tokens, pages are taken off the top;
+ *        free_count, out, is what is left.
+ *   capacity: tokens that the outputs have room for.
+ *   starts [B + 1] i32, out: the first token of each sequence; starts[B] their number
+ *        (at most capacity).
+ *   seqs, positions, seen, slots [capacity] i32, out, of each new token: its
+ *        sequence, its position there, the keys it sees (position + 1: what an
+ *        attention takes as its length), and its slot. Behind the last token: -1, 0, 0, -1.
+ *   lens_out [B] i32, out: lens + new_lens; may be lens.
+ *   A sequence that cannot have all that it needs gets nothing: its tokens have the
+ *   slot -1 and see no key, its table row stays, its lens_out is lens. Such are
+ *   those for whose pages the pool does not reach, with all later ones that need
+ *   pages (w4a8_device_error: W4A8_ERR_PAGES), and those with a negative length, with more
+ *   tokens than max_pages * page_size, or with tokens behind the capacity
+ *   (W4A8_ERR_INDEX; positions are then unspecified). A page number out of range in
+ *   the table or on the stack, or a free_count outside [0, num_pages], is an
+ *   W4A8_ERR_INDEX too and touches no memory out of range.
+ *   Requires 1 <= B <= 4096, 1 <= capacity < 2^30, page_size a power of two in
+ *   16..256, num_pages >= 1, max_pages >= 1, each times page_size < 2^31.
+ *   ws: kv_pages_workspace_size() bytes, header zeroed once; calls that share one must not overlap.
+ *   One kernel. int32 arrays need their natural alignment only.
+ */
+int kv_pages_extend(const int32_t* lens, const int32_t* new_lens, int B, int32_t* page_table, int64_t table_stride,
+                    int max_pages, int page_size, int32_t* free_pages, int32_t* free_count, int num_pages, int capacity,
+                    int32_t* starts, int32_t* seqs, int32_t* positions, int32_t* seen, int32_t* slots, int32_t* lens_out,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * kv_pages_truncate -- the way back: sequence b keeps its first keep_lens[b] tokens
+ * (0: it is finished), and the pages behind them go back on the stack, in the reverse
+ * of the order in which they stand, so that truncating what was just extended leaves
+ * the stack as it was. The table's entries stay; nothing reads them any more.
+ *
+ *   lens, keep_lens, lens_out [B] i32: lens_out = keep_lens; may be either input.
+ *   Other arguments as of kv_pages_extend.
+ *   A sequence with keep_lens outside [0, lens] or lens above max_pages * page_size
+ *   keeps all; if the pages do not fit the stack nothing goes back at all and every
+ *   lens_out is lens; a page number out of range goes back as it is: W4A8_ERR_INDEX each.
+ */
+int kv_pages_truncate(const int32_t* lens, const int32_t* keep_lens, int B, const int32_t* page_table,
+                      int64_t table_stride, int max_pages, int page_size, int32_t* free_pages, int32_t* free_count,
+                      int num_pages, int32_t* lens_out, void* ws, size_t ws_bytes, void* stream);
+size_t kv_pages_workspace_size(void);
+
+/*
+ * The key/value cache of 4 bits (W4A8KV4), shared by the three kv4_* calls:
+ *
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D/2] u8 : value 2i of a row in the low
+ *        half of its byte i, value 2i + 1 in the high half. Slots as in the FP8 cache.
+ *   k_scale, v_scale [num_pages, Hkv, page_size, 2] bf16 : step s and least value m
+ *        of each token and head; a code c in 0..15 stands for c * s + m.
+ *   D is 64 or 128; page_size a power of two in 16..256; num_pages >= 1 and
+ *   num_pages * page_size < 2^31; Hkv in 1..1024.
+ *   int32 and fp32 arrays need their natural alignment only; all other pointers 16 bytes.
+ */
+
+/*
+ * kv4_write -- quantize the keys and values of T tokens into their slots.
+ *
+ *   k_bf16, v_bf16, slots, T: as of kv8_write.
+ *   m = min x (exact: one of the row's bf16 values), s = bf16((max x - min x) / 15),
+ *   over the row's finite values; codes clamp(rint((x - m) / s), 0, 15) in fp32, ties
+ *   to even, 0 where s is 0. Infinities take the codes 0 and 15; a row with a NaN has
+ *   NaN for s and m, and reads as NaN.
+ *   No workspace; one kernel.
+ */
+int kv4_write(const uint16_t* k_bf16, const uint16_t* v_bf16, int T, int64_t k_stride, int64_t v_stride,
+              const int32_t* slots, int Hkv, int D, int num_pages, int page_size, uint8_t* k_cache, uint8_t* v_cache,
+              uint16_t* k_scale, uint16_t* v_scale, void* stream);
+
+/*
+ * kv4_read -- the keys and values of T slots as bf16: x = bf16(c * s + m). Arguments as
+ * of kv8_read: a slot out of range reads as zeros, slots may repeat.
+ * No workspace; one kernel.
+ */
+int kv4_read(const uint8_t* k_cache, const uint8_t* v_cache, const uint16_t* k_scale, const uint16_t* v_scale,
+             const int32_t* slots, int T, int Hkv, int D, int num_pages, int page_size, uint16_t* k_bf16,
+             int64_t k_stride, uint16_t* v_bf16, int64_t v_stride, void* stream);
+
+/*
+ * kv4_attention -- decode attention of T query tokens over the cache, each over the
+ * first lens[t] keys of its sequence: one token of each of T sequences, or several
+ * tokens of a sequence (drafted ones on trial) with a length each.
+ *
+ *   q_bf16 [T, Hq, D] bf16 : rows of Hq*D values q_stride elements apart (>= Hq*D and a
+ *        multiple of 8). Query head i uses kv head i / (Hq / Hkv).
+ *   page_table [S, max_pages] i32 : the pages of each of S = num_seqs sequences, in
+ *        order, rows table_stride elements apart (>= max_pages); entries past a
+ *        token's last key are not read for it.
+ *   seqs [T] i32 : each token's sequence; NULL: token t is of sequence t (S >= T).
+ *   lens [T] i32 : keys that each token sees (0 allowed; then seqs is not read).
+ *   With k_j and v_j as the cache holds them (c * s + m in exact arithmetic):
+ *     s_j = sm_scale * sum_d q_d * k_j,d ;  logit_cap > 0: s_j = logit_cap * tanh(s_j / logit_cap)
+ *     out [T, Hq, D] bf16 = bf16(sum_j softmax(s)_j * v_j), lse [T, Hq] fp32 = log sum_j exp(s_j)
+ *   with fp32 scores, statistics and sums (a capped score is off by 2^-20 of the cap at
+ *   most). Where a softmax weight meets codes it is multiplied by its value's step and
+ *   rounded to f16, relative to a running reference: off by 2^-11 of itself and 2^-32 of
+ *   the largest product of a weight with max(step, |least value|); where it meets least
+ *   values it stays in fp32.
+ *   A token without keys has out = 0 and lse = -infinity. lse may be NULL. What lies
+ *   behind the last key of a page has no influence. The same call gives the same bits.
+ *   Requires 1 <= T <= 4096, Hq a multiple of Hkv, Hq <= 65535, max_pages >= 0,
+ *   max_pages * page_size < 2^31 and times T <= 2^34, sm_scale finite, logit_cap finite
+ *   and >= 0. With max_pages 0 page_table, seqs and lens may be NULL.
+ *   A page number, a sequence or a length out of range touches no memory out of range;
+ *   the outputs are then unspecified and w4a8_device_error reports W4A8_ERR_INDEX.
+ *   ws: kv4_attention_workspace_size(...) bytes, header zeroed once. The size does not
+ *        fall as T grows and does not depend on max_pages: a workspace for the most
+ *        tokens serves every smaller call.
+ */
+int kv4_attention(const uint16_t* q_bf16, int64_t q_stride, int T, int Hq, int Hkv, int D, const uint8_t* k_cache,
+                  const uint8_t* v_cache, const uint16_t* k_scale, const uint16_t* v_scale, int num_pages, int page_size,
+                  const int32_t* page_table, int64_t table_stride, int num_seqs, int max_pages, const int32_t* seqs,
+                  const int32_t* lens, float sm_scale, float logit_cap, uint16_t* out_bf16, float* lse, void* ws,
+                  size_t ws_bytes, void* stream);
+size_t kv4_attention_workspace_size(int T, int Hq, int Hkv, int D, int max_pages, int page_size);
+
+/*
  * w4a8_set_profile_events -- measurement hook (not part of the method). Sets,
  * for the calling host thread, up to four cudaEvent_t handles that
  * moe_w4a8_forward records on its stream: [0] before the gate_up GEMM,
@@ -487,7 +691,8 @@ int w4a8_selftest_wait_timeout(void* ws, void* stream);
  * w4a8_device_error -- read and clear the device error word of a workspace.
  * Synchronizes `stream` (the only call that does). *code_out receives
  * W4A8_OK, or W4A8_ERR_TIMEOUT when a kernel gave up on a bounded wait since
- * the last read, else W4A8_ERR_INDEX when one met an index out of range. Returns W4A8_OK or W4A8_ERR_NULL / W4A8_ERR_LAUNCH.
+ * the last read, else W4A8_ERR_INDEX when one met an index out of range, else
+ * W4A8_ERR_PAGES when a pool of pages ran out. Returns W4A8_OK or W4A8_ERR_NULL / W4A8_ERR_LAUNCH.
  */
 int w4a8_device_error(void* ws, int* code_out, void* stream);
 

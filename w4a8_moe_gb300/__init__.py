@@ -1,5 +1,6 @@
-"""W4A8 mixture-of-experts FFN, FP8 projections and the FP8 key/value cache with
-its decode attention for GB300 (sm_103a).
+"""W4A8 mixture-of-experts FFN, FP8 projections, and key/value caches of 8 and of 4
+bits with their decode attention, page tables and query/key rotation for GB300
+(sm_103a).
 
 Thin Python binding over the C ABI in include/w4a8_moe.h: each function has
 the C entry point's name, takes torch CUDA tensors, allocates outputs and
@@ -26,6 +27,8 @@ __all__ = [
     "moe_w4a8_plan",
     "w4a8_quantize_act_workspace_size", "kv8_write", "kv8_read", "kv8_prefix_attention",
     "kv8_prefix_attention_workspace_size", "kv8_prefix_attention_plan", "RouteResult", "library_path", "W4A8Error",
+    "rope_table", "RopeTable", "qk_norm_rope", "kv8_norm_rope_write", "kv_pages_extend", "kv_pages_truncate", "PageStep",
+    "kv_pages_workspace_size", "kv4_write", "kv4_read", "kv4_attention", "kv4_attention_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,6 +36,8 @@ _LIB_PATH = os.path.join(_HERE, "libw4a8_moe.so")
 _lib = None
 
 RouteResult = namedtuple("RouteResult", "topk_ids topk_w counts offsets sorted_ids inv_perm")
+RopeTable = namedtuple("RopeTable", "turns magnitude")
+PageStep = namedtuple("PageStep", "starts seqs positions seen slots lens")
 
 
 class W4A8Error(RuntimeError):
@@ -52,7 +57,7 @@ def _load():
                         "`python -m w4a8_moe_gb300.build` (or __graft_entry__.build())")
     lib = ctypes.CDLL(_LIB_PATH)
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-    f32 = ctypes.c_float
+    f32, f64 = ctypes.c_float, ctypes.c_double
     sig = {
         "w4a8_status_string": (ctypes.c_char_p, [i32]),
         "w4a8_version": (i32, []),
@@ -81,6 +86,18 @@ def _load():
                                        f32, f32, P, P, P, sz, P]),
         "kv8_prefix_attention_workspace_size": (sz, [i32] * 7),
         "kv8_prefix_attention_plan": (i32, [i32] * 8 + [f32, i32, P]),
+        "rope_table": (i32, [i32, P, f64, i32, f64, f64, f64, f64, P, P]),
+        "qk_norm_rope": (i32, [P, i64, i32, P, i64, i32, i32, i32, P, P, i32, f32, i32, P, P, f32, P, i64, P, i64, P]),
+        "kv8_norm_rope_write": (i32, [P, i64, i32, P, i64, P, i64, i32, i32, i32, P, P, P, i32, f32, i32, P, P, f32,
+                                      i32, i32, i32, f32, P, i64, P, P, P, P, P]),
+        "kv_pages_extend": (i32, [P, P, i32, P, i64, i32, i32, P, P, i32, i32, P, P, P, P, P, P, P, sz, P]),
+        "kv_pages_truncate": (i32, [P, P, i32, P, i64, i32, i32, P, P, i32, P, P, sz, P]),
+        "kv_pages_workspace_size": (sz, []),
+        "kv4_write": (i32, [P, P, i32, i64, i64, P, i32, i32, i32, i32, P, P, P, P, P]),
+        "kv4_read": (i32, [P, P, P, P, P, i32, i32, i32, i32, i32, P, i64, P, i64, P]),
+        "kv4_attention": (i32, [P, i64, i32, i32, i32, i32, P, P, P, P, i32, i32, P, i64, i32, i32, P, P, f32, f32, P,
+                                P, P, sz, P]),
+        "kv4_attention_workspace_size": (sz, [i32] * 6),
         "w4a8_device_error": (i32, [P, P, P]),
         "w4a8_selftest_wait_timeout": (i32, [P, P]),
         "w4a8_set_profile_events": (i32, [P, i32]),
@@ -191,6 +208,14 @@ def kv8_prefix_attention_plan(B, Hq, Hkv, D, prefix_len, max_pages, page_size, s
                                              num_sms, plan))
     return dict(zip(("ranges", "tiles_per_range", "prefix_blocks", "launches", "own_blocks_per_sm", "join_warps"),
                     list(plan)))
+
+
+def kv4_attention_workspace_size(T, Hq, Hkv, D, max_pages, page_size) -> int:
+    return int(_load().kv4_attention_workspace_size(T, Hq, Hkv, D, max_pages, page_size))
+
+
+def kv_pages_workspace_size() -> int:
+    return int(_load().kv_pages_workspace_size())
 
 
 # --------------------------------------------------------------------------- calls
@@ -340,7 +365,7 @@ def fp8_block_linear(x_bf16, w_e4m3, w_scale_inv, out=None, xq_out=None, xs_out=
 # The kv8_* calls are made once per layer and decode step, where a call takes a few microseconds on the GPU, so their
 # checks are written to cost little: every tensor attribute is read once (some 0.1 us each), and what went wrong is told
 # apart only after a check has failed.
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -527,6 +552,348 @@ def kv8_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, pr
         v_scale.data_ptr(), n, page, len(scales) == 3, pages, prefix_len, table, row if B > 1 else most,
         most, lens, d ** -0.5 if sm_scale is None else float(sm_scale), float(logit_cap), out.data_ptr(), to,
         ws.data_ptr(), ws.nbytes, to_stream)
+    if status:
+        _check(status)
+    return out, lse
+
+
+# ---- rotation of queries and keys
+_ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "yarn": 3, "wave": 4}
+_ROPE_HIGH = {"yarn": 32.0, "wave": 4.0}
+
+
+def rope_table(rotary_dim: int, base: float = 10000.0, scaling=None, factor: float = 1.0, original_len: float = 0.0,
+               low: float = 1.0, high=None, inv_freq=None, device="cuda") -> RopeTable:
+    """The frequencies of a rotary embedding as qk_norm_rope and kv8_norm_rope_write take them: base^(-2i / rotary_dim),
+    stretched for long contexts by `scaling` (None, "linear", "base", "yarn" or "wave"; see rope_table in
+    include/w4a8_moe.h), or the model's own inv_freq (radians per position, rotary_dim / 2 numbers). high defaults to 32
+    for "yarn" and 4 for "wave"."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(_ROPE_SCALINGS)}")
+    own = None
+    if inv_freq is not None:
+        if scaling is not None:
+            raise ValueError("inv_freq are the frequencies as they are: scaling must be None")
+        own = [float(f) for f in inv_freq]
+        if 2 * len(own) != rotary_dim:
+            raise ValueError("inv_freq must hold rotary_dim / 2 numbers")
+        own = (ctypes.c_double * len(own))(*own)
+    n = max(int(rotary_dim) // 2, 1)
+    turns, magnitude = (ctypes.c_uint64 * n)(), ctypes.c_float(0.0)
+    _check(_load().rope_table(rotary_dim, own, base, _ROPE_SCALINGS[scaling], factor, original_len, low,
+                              _ROPE_HIGH.get(scaling, 2.0 * low) if high is None else high, turns,
+                              ctypes.byref(magnitude)))
+    bits = torch.frombuffer(bytearray(turns), dtype=torch.int64)   # the same 64 bits; torch computes with signed ones
+    return RopeTable(bits.to(device), magnitude.value)
+
+
+def _rope_refused():
+    return ValueError("rope must be a RopeTable: contiguous int64 turns, a number")
+
+
+def _weight(w, d, device, what):
+    """The address of a norm's weights (None: no norm)."""
+    if w is None:
+        return None
+    if w.dtype is not _BF16 or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{what} must be contiguous bf16 [D]")
+    if w.get_device() != device:
+        raise _devices_refused(w)
+    return w.data_ptr()
+
+
+def qk_norm_rope(q, k, positions, rope: RopeTable, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Norms (where weights are given) and rotates bf16 queries [T, query heads, D] and keys [T, kv heads, D] (None: no
+    keys) by positions [T] (int32); rows may lie apart, as in a fused projection's output, and q_out / k_out may be q / k
+    themselves. Returns (q_out, k_out)."""
+    q_shape = q.shape
+    if len(q_shape) != 3 or positions.dtype is not _I32 or positions.shape != q_shape[:1] or not positions.is_contiguous():
+        raise ValueError("q must be bf16 [T, query heads, D], positions a contiguous int32 vector [T]")
+    T, hq, d = q_shape
+    turns, magnitude = rope
+    if turns.dtype is not _I64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise _rope_refused()
+    hkv = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must be bf16 [T, kv heads, D]")
+        hkv = k.shape[1]
+    if q_out is None or (k is not None and k_out is None):
+        with _on(stream):
+            q_out = q_out if q_out is not None else torch.empty(T, hq, d, dtype=_BF16, device=q.device)
+            if k is not None and k_out is None:
+                k_out = torch.empty(T, hkv, d, dtype=_BF16, device=q.device)
+    q_stride, q_to = _row_stride(q, T, hq, d, "q"), _row_stride(q_out, T, hq, d, "q_out")
+    device = q.get_device()
+    same = device == positions.get_device() == turns.get_device() == q_out.get_device()
+    k_at = k_to_at = None
+    k_stride = k_to = 0
+    if k is not None:
+        k_stride, k_to = _row_stride(k, T, hkv, d, "k"), _row_stride(k_out, T, hkv, d, "k_out")
+        same = same and device == k.get_device() == k_out.get_device()
+        k_at, k_to_at = k.data_ptr(), k_out.data_ptr()
+    if device < 0 or not same or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(q, positions, turns, q_out, *(() if k is None else (k, k_out)))
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    status = (_lib or _load()).qk_norm_rope(
+        q.data_ptr(), q_stride, hq, k_at, k_stride, hkv, T, d, positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(),
+        magnitude, 1 if interleaved else 0, _weight(q_weight, d, device, "q_weight"),
+        _weight(k_weight, d, device, "k_weight"), float(eps), q_out.data_ptr(), q_to, k_to_at, k_to, to_stream)
+    if status:
+        _check(status)
+    return q_out, (None if k is None else k_out)
+
+
+def kv8_norm_rope_write(q, k, v, positions, slots, rope: RopeTable, k_cache, v_cache, k_scale, v_scale, q_weight=None,
+                        k_weight=None, eps: float = 1e-6, interleaved: bool = False, min_scale: float = 0.0, q_out=None,
+                        stream=None):
+    """qk_norm_rope and kv8_write in one pass: the queries [T, query heads, D] are normed, rotated and returned (q_out may
+    be q), the keys and values [T, kv heads, D] go into slots [T] of the cache, the keys normed and rotated before."""
+    shape, scales = k_cache.shape, k_scale.shape
+    if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES or len(shape) != 4 or v_cache.shape != shape \
+            or k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or v_scale.shape != scales \
+            or (scales != shape[1:2] and scales != shape[:3]) or not k_cache.is_contiguous() \
+            or not v_cache.is_contiguous() or not k_scale.is_contiguous() or not v_scale.is_contiguous():
+        raise _cache_refused(k_cache, v_cache, k_scale, v_scale)
+    n, h, page, d = shape
+    q_shape = q.shape
+    if len(q_shape) != 3:
+        raise ValueError("q must be bf16 [T, query heads, D of the cache]")
+    T, hq, _ = q_shape
+    if positions.dtype is not _I32 or positions.shape != (T,) or not positions.is_contiguous():
+        raise _vector_refused("positions [T]")
+    if slots.dtype is not _I32 or slots.shape != (T,) or not slots.is_contiguous():
+        raise _vector_refused("slots [T]")
+    turns, magnitude = rope
+    if turns.dtype is not _I64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise _rope_refused()
+    if q_out is None:
+        with _on(stream):
+            q_out = torch.empty(T, hq, d, dtype=_BF16, device=q.device)
+    q_stride, q_to = _row_stride(q, T, hq, d, "q"), _row_stride(q_out, T, hq, d, "q_out")
+    k_stride, v_stride = _row_stride(k, T, h, d, "k"), _row_stride(v, T, h, d, "v")
+    device = k_cache.get_device()
+    if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                          == q.get_device() == k.get_device() == v.get_device() == q_out.get_device()
+                          == positions.get_device() == slots.get_device() == turns.get_device()) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, k, v, q_out, positions, slots, turns)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    status = (_lib or _load()).kv8_norm_rope_write(
+        q.data_ptr(), q_stride, hq, k.data_ptr(), k_stride, v.data_ptr(), v_stride, h, T, d, positions.data_ptr(),
+        slots.data_ptr(), turns.data_ptr(), 2 * turns.numel(), magnitude, 1 if interleaved else 0,
+        _weight(q_weight, d, device, "q_weight"), _weight(k_weight, d, device, "k_weight"), float(eps), n, page,
+        len(scales) == 3, float(min_scale), q_out.data_ptr(), q_to, k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), to_stream)
+    if status:
+        _check(status)
+    return q_out
+
+
+# ---- page tables
+def _table(page_table, rows):
+    """(row stride, pages of a row) of an int32 [rows or any number, max pages] table whose rows may lie apart."""
+    if page_table.dtype is not _I32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [sequences, max pages]")
+    have, most = page_table.shape
+    row, one = page_table.stride()
+    if (rows is not None and have != rows) or (one != 1 and most > 1):
+        raise ValueError("page_table must be int32 [sequences, max pages], each sequence's pages contiguous")
+    return (row if have > 1 else most), most
+
+
+def _vectors(n, **vectors):
+    for what, t in vectors.items():
+        if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous int32 vector [{n}]")
+
+
+def _pages_device(ws, *tensors):
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    device = ws.get_device()
+    if device < 0 or any(t.get_device() != device for t in tensors) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(ws, *tensors)
+    return device
+
+
+def kv_pages_extend(lens, new_lens, page_table, free_pages, free_count, page_size: int, capacity: int, out: PageStep = None,
+                    ws=None, stream=None) -> PageStep:
+    """Gives each sequence's new tokens (new_lens [B], behind lens [B]) pages off the stack free_pages [num pages], of
+    which free_count [1] are there, and enters them in page_table [B, max pages]; all int32, on the GPU. Returns
+    PageStep(starts [B + 1], and for up to `capacity` tokens seqs, positions, seen and slots, lens [B]); padding tokens
+    have the slot -1. A sequence that cannot have all of its pages gets none (see kv_pages_extend in
+    include/w4a8_moe.h). out.lens may be lens."""
+    if lens.dim() != 1 or free_pages.dim() != 1:
+        raise _vector_refused("lens and free_pages each")
+    B = lens.shape[0]
+    row, most = _table(page_table, B)
+    num_pages = free_pages.shape[0]
+    _vectors(B, lens=lens, new_lens=new_lens)
+    _vectors(num_pages, free_pages=free_pages)
+    _vectors(1, free_count=free_count)
+    capacity = int(capacity)
+    if out is None or ws is None:
+        with _on(stream):
+            if out is None:
+                c = max(capacity, 0)
+                out = PageStep(*torch.empty(2 * B + 1 + 4 * c, dtype=_I32, device=lens.device).split([B + 1, c, c, c, c, B]))
+            ws = ws if ws is not None else _ws(256, lens.device)
+    starts, seqs, positions, seen, slots, lens_out = out
+    _vectors(B + 1, starts=starts)
+    _vectors(capacity, seqs=seqs, positions=positions, seen=seen, slots=slots)
+    _vectors(B, lens_out=lens_out)
+    device = _pages_device(ws, lens, new_lens, page_table, free_pages, free_count, *out)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    status = (_lib or _load()).kv_pages_extend(
+        lens.data_ptr(), new_lens.data_ptr(), B, page_table.data_ptr(), row, most, int(page_size), free_pages.data_ptr(),
+        free_count.data_ptr(), num_pages, capacity, starts.data_ptr(), seqs.data_ptr(), positions.data_ptr(),
+        seen.data_ptr(), slots.data_ptr(), lens_out.data_ptr(), ws.data_ptr(), ws.nbytes, to_stream)
+    if status:
+        _check(status)
+    return out
+
+
+def kv_pages_truncate(lens, keep_lens, page_table, free_pages, free_count, page_size: int, out=None, ws=None, stream=None):
+    """Gives the pages behind each sequence's first keep_lens [B] of lens [B] tokens back to the stack (0: the sequence is
+    finished). Returns the lengths now, [B] (out, which may be lens or keep_lens)."""
+    if lens.dim() != 1 or free_pages.dim() != 1:
+        raise _vector_refused("lens and free_pages each")
+    B = lens.shape[0]
+    row, most = _table(page_table, B)
+    num_pages = free_pages.shape[0]
+    if out is None or ws is None:
+        with _on(stream):
+            out = out if out is not None else torch.empty(B, dtype=_I32, device=lens.device)
+            ws = ws if ws is not None else _ws(256, lens.device)
+    _vectors(B, lens=lens, keep_lens=keep_lens, out=out)
+    _vectors(num_pages, free_pages=free_pages)
+    _vectors(1, free_count=free_count)
+    device = _pages_device(ws, lens, keep_lens, page_table, free_pages, free_count, out)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    status = (_lib or _load()).kv_pages_truncate(
+        lens.data_ptr(), keep_lens.data_ptr(), B, page_table.data_ptr(), row, most, int(page_size), free_pages.data_ptr(),
+        free_count.data_ptr(), num_pages, out.data_ptr(), ws.data_ptr(), ws.nbytes, to_stream)
+    if status:
+        _check(status)
+    return out
+
+
+# ---- the cache of 4 bits
+_U8 = torch.uint8
+
+
+def _cache4(k_cache, v_cache, k_scale, v_scale):
+    """The shape of a 4-bit cache, [pages, kv heads, page size, D]."""
+    shape = k_cache.shape
+    if k_cache.dtype is not _U8 or v_cache.dtype is not _U8 or len(shape) != 4 or v_cache.shape != shape \
+            or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous uint8 [pages, kv heads, page size, D / 2]")
+    n, h, page, half = shape
+    scales = (n, h, page, 2)
+    if k_scale.dtype is not _BF16 or v_scale.dtype is not _BF16 or k_scale.shape != scales or v_scale.shape != scales \
+            or not (k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("k_scale and v_scale must be contiguous bf16 [pages, kv heads, page size, 2]")
+    return n, h, page, 2 * half
+
+
+def kv4_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
+    """Quantize bf16 keys and values [T, kv heads, D] (rows may lie apart) to 4 bits into slots [T] (int32; out of range:
+    skipped) of the cache: codes uint8 [pages, kv heads, page size, D / 2], and with each row its step and least value,
+    bf16 [pages, kv heads, page size, 2]."""
+    n, h, page, d = _cache4(k_cache, v_cache, k_scale, v_scale)
+    if slots.dtype is not _I32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise _vector_refused("slots")
+    T = slots.shape[0]
+    k_stride, v_stride = _row_stride(k, T, h, d, "k"), _row_stride(v, T, h, d, "v")
+    device = k_cache.get_device()
+    if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                          == k.get_device() == v.get_device() == slots.get_device()) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, k, v, slots)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    status = (_lib or _load()).kv4_write(
+        k.data_ptr(), v.data_ptr(), T, k_stride, v_stride, slots.data_ptr(), h, d, n, page, k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), to_stream)
+    if status:
+        _check(status)
+
+
+def kv4_read(k_cache, v_cache, k_scale, v_scale, slots, k_out=None, v_out=None, stream=None):
+    """The 4-bit cache's slots [T] (int32; out of range: zeros) as bf16 keys and values, each [T, kv heads, D]."""
+    n, h, page, d = _cache4(k_cache, v_cache, k_scale, v_scale)
+    if slots.dtype is not _I32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise _vector_refused("slots")
+    T = slots.shape[0]
+    if k_out is None or v_out is None:
+        with _on(stream):
+            k_out = k_out if k_out is not None else torch.empty(T, h, d, dtype=_BF16, device=k_cache.device)
+            v_out = v_out if v_out is not None else torch.empty(T, h, d, dtype=_BF16, device=k_cache.device)
+    k_stride, v_stride = _row_stride(k_out, T, h, d, "k_out"), _row_stride(v_out, T, h, d, "v_out")
+    device = k_cache.get_device()
+    if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                          == slots.get_device() == k_out.get_device() == v_out.get_device()) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    status = (_lib or _load()).kv4_read(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), T, h, d, n,
+        page, k_out.data_ptr(), k_stride, v_out.data_ptr(), v_stride, to_stream)
+    if status:
+        _check(status)
+    return k_out, v_out
+
+
+def kv4_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, seqs=None, sm_scale=None,
+                  logit_cap: float = 0.0, out=None, lse=None, ws=None, stream=None):
+    """Decode attention of bf16 q [T, query heads, D] over the 4-bit cache: token t sees the first lens[t] keys of sequence
+    seqs[t] (None: sequence t), whose pages are page_table [sequences, max pages]; int32. Returns (bf16 out
+    [T, query heads, D], fp32 lse [T, query heads] or None). Pass `lse` (a tensor, or True to allocate one) to receive it.
+    sm_scale defaults to D ** -0.5; logit_cap 0 is no cap."""
+    n, h, page, d = _cache4(k_cache, v_cache, k_scale, v_scale)
+    q_shape = q.shape
+    if len(q_shape) != 3:
+        raise ValueError("q must be bf16 [T, query heads, D of the cache]")
+    T, hq, _ = q_shape
+    q_stride = _row_stride(q, T, hq, d, "q")
+    row, most = _table(page_table, None)
+    have = page_table.shape[0]
+    if lens.dtype is not _I32 or lens.shape != (T,) or not lens.is_contiguous():
+        raise _vector_refused("lens [T]")
+    if seqs is None:
+        if have != T:
+            raise ValueError("page_table must have a row for each token where seqs is None")
+    elif seqs.dtype is not _I32 or seqs.shape != (T,) or not seqs.is_contiguous():
+        raise _vector_refused("seqs [T]")
+    if lse is False:
+        lse = None
+    if out is None or lse is True or ws is None:
+        with _on(stream):
+            out = out if out is not None else torch.empty(T, hq, d, dtype=_BF16, device=q.device)
+            lse = torch.empty(T, hq, dtype=_F32, device=q.device) if lse is True else lse
+            ws = ws if ws is not None else _ws(kv4_attention_workspace_size(T, hq, h, d, most, page), q.device)
+    if out.dtype is not _BF16 or out.shape != q_shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous bf16 [T, query heads, D]")
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (T, hq) or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [T, query heads]")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    device = k_cache.get_device()
+    if device < 0 or not (device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                          == q.get_device() == page_table.get_device() == lens.get_device() == out.get_device()
+                          == ws.get_device()) \
+            or (seqs is not None and seqs.get_device() != device) or (lse is not None and lse.get_device() != device) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(k_cache, v_cache, k_scale, v_scale, q, page_table, lens, out, ws,
+                               *(t for t in (seqs, lse) if t is not None))
+    to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    status = (_lib or _load()).kv4_attention(
+        q.data_ptr(), q_stride, T, hq, h, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), n, page, page_table.data_ptr(), row, have, most, None if seqs is None else seqs.data_ptr(),
+        lens.data_ptr(), d ** -0.5 if sm_scale is None else float(sm_scale), float(logit_cap), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, to_stream)
     if status:
         _check(status)
     return out, lse

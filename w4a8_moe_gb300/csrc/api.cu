@@ -2,13 +2,17 @@
 // encoding and kernel launches. Declarations and contracts: include/w4a8_moe.h.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
 #include "../../include/w4a8_moe.h"
 #include "internal.h"
+#include "kv4.cuh"
 #include "kv8.cuh"
+#include "pages.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace w4a8 {
 
@@ -286,6 +290,35 @@ static size_t kv8_ws(int B, int Hq, int Hkv, int D, int prefix_len, Kv8Ws* w, vo
     return c.off;
 }
 
+// ---- norm and rotation of queries and keys
+static bool rope_dims_ok(int D, int rot)
+{
+    return D >= 16 && D <= kRopeMostD && D % 16 == 0 && rot >= 16 && rot <= D && rot % 16 == 0;
+}
+static bool rope_row_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0; }
+static bool rope_values_ok(float magnitude, int interleaved, float eps)
+{
+    return std::isfinite(magnitude) && (interleaved == 0 || interleaved == 1) && std::isfinite(eps) && eps >= 0.0f;
+}
+
+// ---- page tables
+static bool pages_ok(int B, int64_t table_stride, int max_pages, int page_size, int num_pages)
+{
+    return B >= 1 && B <= kPagesMostSeqs && max_pages >= 1 && table_stride >= max_pages && num_pages >= 1 &&
+           kv8_page_shift(page_size) >= 0 && static_cast<int64_t>(max_pages) * page_size < (static_cast<int64_t>(1) << 31) &&
+           static_cast<int64_t>(num_pages) * page_size < (static_cast<int64_t>(1) << 31);
+}
+static PagePool page_pool(const int32_t* table, int64_t stride, int max_pages, int page_size, int32_t* stack,
+                          int32_t* count, int num_pages, void* ws)
+{
+    PagePool p;
+    p.table = const_cast<int32_t*>(table), p.stride = stride, p.max_pages = max_pages;
+    p.stack = stack, p.count = count, p.num_pages = num_pages, p.page_shift = kv8_page_shift(page_size);
+    p.err = static_cast<uint32_t*>(ws);
+    p.ticket = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 128);
+    return p;
+}
+
 }  // namespace w4a8
 
 using namespace w4a8;
@@ -304,6 +337,7 @@ const char* w4a8_status_string(int status)
     case W4A8_ERR_LAUNCH: return "W4A8_ERR_LAUNCH: CUDA launch or driver call failed";
     case W4A8_ERR_TIMEOUT: return "W4A8_ERR_TIMEOUT: a kernel gave up on a bounded wait";
     case W4A8_ERR_INDEX: return "W4A8_ERR_INDEX: a page index or length read on the device was out of range";
+    case W4A8_ERR_PAGES: return "W4A8_ERR_PAGES: the pool of pages ran out";
     default: return "W4A8: unknown status";
     }
 }
@@ -821,6 +855,266 @@ int kv8_prefix_attention(const uint16_t* q_bf16, int64_t q_stride, int B, int Hq
                                                                                                  : W4A8_ERR_LAUNCH;
 }
 
+int rope_table(int rotary_dim, const double* inv_freq, double base, int scaling, double factor, double original_len,
+               double low, double high, uint64_t* turns, float* magnitude)
+{
+    if (!turns || !magnitude)
+        return W4A8_ERR_NULL;
+    const int R = rotary_dim, n = R / 2;
+    if (!rope_dims_ok(kRopeMostD, R) || scaling < 0 || scaling > 4)
+        return W4A8_ERR_SHAPE;
+    const double two_pi = 6.283185307179586476925;
+    if (inv_freq) {
+        for (int i = 0; i < n; ++i)
+            if (!(std::fabs(inv_freq[i]) <= two_pi))
+                return W4A8_ERR_SHAPE;
+    } else if (!(base > 1.0) || !std::isfinite(base) || (scaling && (!(factor >= 1.0) || !std::isfinite(factor))) ||
+               (scaling >= 3 && (!(original_len >= 1.0) || !std::isfinite(original_len) || !(low > 0.0) ||
+                                 !(low < high) || !std::isfinite(high)))) {
+        return W4A8_ERR_SHAPE;
+    }
+    *magnitude = 1.0f;
+    double first = 0.0, last = 0.0;   // scaling 3: the ramp's ends
+    if (!inv_freq && scaling == 2)
+        base *= std::pow(factor, R / (R - 2.0));
+    if (!inv_freq && scaling == 3) {
+        const double per = R / (2.0 * std::log(base));
+        first = std::max(std::floor(per * std::log(original_len / (high * two_pi))), 0.0);
+        last = std::min(std::ceil(per * std::log(original_len / (low * two_pi))), R - 1.0);
+        if (last == first)
+            last += 0.001;   // a step
+        *magnitude = static_cast<float>(0.1 * std::log(factor) + 1.0);
+    }
+    for (int i = 0; i < n; ++i) {
+        double f = inv_freq ? inv_freq[i] : std::pow(base, -2.0 * i / R);
+        if (!inv_freq && scaling == 1) {
+            f /= factor;
+        } else if (!inv_freq && scaling == 3) {
+            const double ramp = std::min(std::max((i - first) / (last - first), 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        } else if (!inv_freq && scaling == 4) {
+            const double keep = std::min(std::max((original_len * f / two_pi - low) / (high - low), 0.0), 1.0);
+            f = f / factor * (1.0 - keep) + f * keep;
+        }
+        const double turn = std::fabs(f) / two_pi;   // 0..1
+        const uint64_t u = turn < 1.0 ? static_cast<uint64_t>(std::ldexp(turn, 64)) : 0;
+        turns[i] = f < 0.0 ? 0 - u : u;
+    }
+    return W4A8_OK;
+}
+
+int qk_norm_rope(const uint16_t* q_bf16, int64_t q_stride, int Hq, const uint16_t* k_bf16, int64_t k_stride, int Hkv,
+                 int T, int D, const int32_t* positions, const uint64_t* turns, int rotary_dim, float magnitude,
+                 int interleaved, const uint16_t* q_weight, const uint16_t* k_weight, float eps, uint16_t* q_out,
+                 int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride, void* stream)
+{
+    if (!q_bf16 || !q_out || !positions || !turns || (Hkv > 0 && (!k_bf16 || !k_out)))
+        return W4A8_ERR_NULL;
+    const int64_t q_row = static_cast<int64_t>(Hq) * D, k_row = static_cast<int64_t>(Hkv) * D;
+    if (T < 1 || Hq < 1 || Hkv < 0 || static_cast<int64_t>(Hq) + Hkv > 65535 || !rope_dims_ok(D, rotary_dim) ||
+        !rope_row_ok(q_stride, q_row) || !rope_row_ok(q_out_stride, q_row) ||
+        (Hkv > 0 && (!rope_row_ok(k_stride, k_row) || !rope_row_ok(k_out_stride, k_row))) ||
+        !rope_values_ok(magnitude, interleaved, eps))
+        return W4A8_ERR_SHAPE;
+    if (!aligned16(q_bf16) || !aligned16(q_out) || !aligned16(k_bf16) || !aligned16(k_out) || !aligned16(turns) ||
+        !aligned16(q_weight) || !aligned16(k_weight) || !aligned4(positions))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    Rope a = {};
+    a.q = q_bf16, a.k = k_bf16, a.q_stride = q_stride, a.k_stride = k_stride;
+    a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D, a.rot = rotary_dim;
+    a.positions = positions, a.turns = turns, a.magnitude = magnitude, a.interleaved = interleaved;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.eps = eps;
+    a.q_out = q_out, a.k_out = k_out, a.q_out_stride = q_out_stride, a.k_out_stride = k_out_stride;
+    return launch_rope(a, false, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK : W4A8_ERR_LAUNCH;
+}
+
+int kv8_norm_rope_write(const uint16_t* q_bf16, int64_t q_stride, int Hq, const uint16_t* k_bf16, int64_t k_stride,
+                        const uint16_t* v_bf16, int64_t v_stride, int Hkv, int T, int D, const int32_t* positions,
+                        const int32_t* slots, const uint64_t* turns, int rotary_dim, float magnitude, int interleaved,
+                        const uint16_t* q_weight, const uint16_t* k_weight, float eps, int num_pages, int page_size,
+                        int scale_mode, float min_scale, uint16_t* q_out, int64_t q_out_stride, uint8_t* k_cache,
+                        uint8_t* v_cache, float* k_scale, float* v_scale, void* stream)
+{
+    if (!q_bf16 || !k_bf16 || !v_bf16 || !positions || !slots || !turns || !q_out || !k_cache || !v_cache || !k_scale ||
+        !v_scale)
+        return W4A8_ERR_NULL;
+    const int64_t q_row = static_cast<int64_t>(Hq) * D;
+    if (Hq < 1 || !kv8_cache_ok(Hkv, D, num_pages, page_size, scale_mode) || static_cast<int64_t>(Hq) + 2 * Hkv > 65535 ||
+        !kv8_rows_ok(T, Hkv, D, k_stride, v_stride) || !rope_dims_ok(D, rotary_dim) || !rope_row_ok(q_stride, q_row) ||
+        !rope_row_ok(q_out_stride, q_row) || !rope_values_ok(magnitude, interleaved, eps) || !std::isfinite(min_scale) ||
+        min_scale < 0.0f)
+        return W4A8_ERR_SHAPE;
+    if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(q_out) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(turns) || !aligned16(q_weight) || !aligned16(k_weight) ||
+        !aligned4(positions) || !aligned4(slots) || !aligned4(k_scale) || !aligned4(v_scale))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    Rope a = {};
+    a.q = q_bf16, a.k = k_bf16, a.v = v_bf16, a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D, a.rot = rotary_dim;
+    a.positions = positions, a.turns = turns, a.magnitude = magnitude, a.interleaved = interleaved;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.eps = eps;
+    a.q_out = q_out, a.q_out_stride = q_out_stride;
+    a.slots = slots, a.k_cache = k_cache, a.v_cache = v_cache, a.k_scale = k_scale, a.v_scale = v_scale;
+    a.num_slots = num_pages * page_size, a.page_shift = kv8_page_shift(page_size), a.per_token = scale_mode;
+    a.min_scale = min_scale;
+    return launch_rope(a, true, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK : W4A8_ERR_LAUNCH;
+}
+
+size_t kv_pages_workspace_size(void) { return kHeader; }
+
+int kv_pages_extend(const int32_t* lens, const int32_t* new_lens, int B, int32_t* page_table, int64_t table_stride,
+                    int max_pages, int page_size, int32_t* free_pages, int32_t* free_count, int num_pages, int capacity,
+                    int32_t* starts, int32_t* seqs, int32_t* positions, int32_t* seen, int32_t* slots, int32_t* lens_out,
+                    void* ws, size_t ws_bytes, void* stream)
+{
+    const void* ptrs[] = {lens, new_lens, page_table, free_pages, free_count, starts, seqs, positions, seen, slots, lens_out};
+    for (const void* p : ptrs)
+        if (!p)
+            return W4A8_ERR_NULL;
+    if (!pages_ok(B, table_stride, max_pages, page_size, num_pages) || capacity < 1 || capacity >= 1 << 30)
+        return W4A8_ERR_SHAPE;
+    for (const void* p : ptrs)
+        if (!aligned4(p))
+            return W4A8_ERR_ALIGN;
+    if (!ws || ws_bytes < kv_pages_workspace_size())
+        return W4A8_ERR_WORKSPACE;
+    if (!aligned16(ws))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    const PagesExtend a{page_pool(page_table, table_stride, max_pages, page_size, free_pages, free_count, num_pages, ws),
+                        B, capacity, lens, new_lens, starts, seqs, positions, seen, slots, lens_out};
+    return launch_pages_extend(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK : W4A8_ERR_LAUNCH;
+}
+
+int kv_pages_truncate(const int32_t* lens, const int32_t* keep_lens, int B, const int32_t* page_table,
+                      int64_t table_stride, int max_pages, int page_size, int32_t* free_pages, int32_t* free_count,
+                      int num_pages, int32_t* lens_out, void* ws, size_t ws_bytes, void* stream)
+{
+    const void* ptrs[] = {lens, keep_lens, page_table, free_pages, free_count, lens_out};
+    for (const void* p : ptrs)
+        if (!p)
+            return W4A8_ERR_NULL;
+    if (!pages_ok(B, table_stride, max_pages, page_size, num_pages))
+        return W4A8_ERR_SHAPE;
+    for (const void* p : ptrs)
+        if (!aligned4(p))
+            return W4A8_ERR_ALIGN;
+    if (!ws || ws_bytes < kv_pages_workspace_size())
+        return W4A8_ERR_WORKSPACE;
+    if (!aligned16(ws))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    const PagesTruncate a{page_pool(page_table, table_stride, max_pages, page_size, free_pages, free_count, num_pages, ws),
+                          B, lens, keep_lens, lens_out};
+    return launch_pages_truncate(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK : W4A8_ERR_LAUNCH;
+}
+
+int kv4_write(const uint16_t* k_bf16, const uint16_t* v_bf16, int T, int64_t k_stride, int64_t v_stride,
+              const int32_t* slots, int Hkv, int D, int num_pages, int page_size, uint8_t* k_cache, uint8_t* v_cache,
+              uint16_t* k_scale, uint16_t* v_scale, void* stream)
+{
+    if (!k_bf16 || !v_bf16 || !slots || !k_cache || !v_cache || !k_scale || !v_scale)
+        return W4A8_ERR_NULL;
+    if (!kv8_cache_ok(Hkv, D, num_pages, page_size, 1) || !kv8_rows_ok(T, Hkv, D, k_stride, v_stride))
+        return W4A8_ERR_SHAPE;
+    const void* ptrs[] = {k_bf16, v_bf16, k_cache, v_cache, k_scale, v_scale};
+    for (const void* p : ptrs)
+        if (!aligned16(p))
+            return W4A8_ERR_ALIGN;
+    if (!aligned4(slots))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    const Kv8Rows a{T, Hkv, D, num_pages * page_size, kv8_page_shift(page_size), 1, 0.0f, k_stride, v_stride};
+    return launch_kv4_write(a, k_bf16, v_bf16, slots, k_cache, v_cache, reinterpret_cast<uint32_t*>(k_scale),
+                            reinterpret_cast<uint32_t*>(v_scale), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? W4A8_OK
+               : W4A8_ERR_LAUNCH;
+}
+
+int kv4_read(const uint8_t* k_cache, const uint8_t* v_cache, const uint16_t* k_scale, const uint16_t* v_scale,
+             const int32_t* slots, int T, int Hkv, int D, int num_pages, int page_size, uint16_t* k_bf16,
+             int64_t k_stride, uint16_t* v_bf16, int64_t v_stride, void* stream)
+{
+    if (!k_bf16 || !v_bf16 || !slots || !k_cache || !v_cache || !k_scale || !v_scale)
+        return W4A8_ERR_NULL;
+    if (!kv8_cache_ok(Hkv, D, num_pages, page_size, 1) || !kv8_rows_ok(T, Hkv, D, k_stride, v_stride))
+        return W4A8_ERR_SHAPE;
+    const void* ptrs[] = {k_bf16, v_bf16, k_cache, v_cache, k_scale, v_scale};
+    for (const void* p : ptrs)
+        if (!aligned16(p))
+            return W4A8_ERR_ALIGN;
+    if (!aligned4(slots))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    const Kv8Rows a{T, Hkv, D, num_pages * page_size, kv8_page_shift(page_size), 1, 0.0f, k_stride, v_stride};
+    return launch_kv4_read(a, k_cache, v_cache, reinterpret_cast<const uint32_t*>(k_scale),
+                           reinterpret_cast<const uint32_t*>(v_scale), slots, k_bf16, v_bf16,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? W4A8_OK
+               : W4A8_ERR_LAUNCH;
+}
+
+size_t kv4_attention_workspace_size(int T, int Hq, int Hkv, int D, int max_pages, int page_size)
+{
+    return kv8_prefix_attention_workspace_size(T, Hq, Hkv, D, 0, max_pages, page_size);
+}
+
+int kv4_attention(const uint16_t* q_bf16, int64_t q_stride, int T, int Hq, int Hkv, int D, const uint8_t* k_cache,
+                  const uint8_t* v_cache, const uint16_t* k_scale, const uint16_t* v_scale, int num_pages, int page_size,
+                  const int32_t* page_table, int64_t table_stride, int num_seqs, int max_pages, const int32_t* seqs,
+                  const int32_t* lens, float sm_scale, float logit_cap, uint16_t* out_bf16, float* lse, void* ws,
+                  size_t ws_bytes, void* stream)
+{
+    if (!q_bf16 || !k_cache || !v_cache || !k_scale || !v_scale || !out_bf16 || (max_pages > 0 && (!page_table || !lens)))
+        return W4A8_ERR_NULL;
+    if (!kv8_cache_ok(Hkv, D, num_pages, page_size, 1) || !kv8_attn_ok(T, Hq, Hkv, D, 0, max_pages, page_size) ||
+        q_stride < static_cast<int64_t>(Hq) * D || q_stride % 8 != 0 || table_stride < max_pages ||
+        (max_pages > 0 && num_seqs < (seqs ? 1 : T)) || !std::isfinite(sm_scale) || !std::isfinite(logit_cap) ||
+        logit_cap < 0.0f)
+        return W4A8_ERR_SHAPE;
+    const void* ptrs[] = {q_bf16, k_cache, v_cache, k_scale, v_scale, out_bf16};
+    for (const void* p : ptrs)
+        if (!aligned16(p))
+            return W4A8_ERR_ALIGN;
+    if (!aligned4(page_table) || !aligned4(seqs) || !aligned4(lens) || !aligned4(lse))
+        return W4A8_ERR_ALIGN;
+    Kv8Ws w;
+    if (!ws || ws_bytes < kv8_ws(T, Hq, Hkv, D, 0, &w, ws))
+        return W4A8_ERR_WORKSPACE;
+    if (!aligned16(ws))
+        return W4A8_ERR_ALIGN;
+    int sms;
+    if (int st = current_device(&sms))
+        return st;
+    Kv4Attn a = {};
+    a.q = q_bf16, a.q_stride = q_stride;
+    a.B = T, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;
+    a.k_cache = k_cache, a.v_cache = v_cache;
+    a.k_scale = reinterpret_cast<const float*>(k_scale), a.v_scale = reinterpret_cast<const float*>(v_scale);
+    a.num_pages = num_pages, a.page_shift = kv8_page_shift(page_size);
+    a.page_table = page_table, a.table_stride = table_stride, a.max_pages = max_pages, a.lens = lens;
+    a.seqs = seqs, a.num_seqs = num_seqs;
+    a.sm_scale = sm_scale, a.cap = logit_cap;
+    a.tiles = w.tiles, a.part_o = w.part_o, a.part_ml = w.part_ml, a.cum = w.cum;
+    a.err = static_cast<uint32_t*>(ws);
+    a.out = out_bf16, a.lse = lse;
+    return launch_kv4_attn(a, D, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK : W4A8_ERR_LAUNCH;
+}
+
 int w4a8_device_error(void* ws, int* code_out, void* stream)
 {
     if (!ws || !code_out)
@@ -830,7 +1124,8 @@ int w4a8_device_error(void* ws, int* code_out, void* stream)
     if (cudaMemcpyAsync(&word, ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaMemsetAsync(ws, 0, sizeof(word), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
         return W4A8_ERR_LAUNCH;
-    *code_out = (word & kErrBitTimeout) ? W4A8_ERR_TIMEOUT : (word & kErrBitIndex) ? W4A8_ERR_INDEX : W4A8_OK;
+    *code_out = (word & kErrBitTimeout) ? W4A8_ERR_TIMEOUT : (word & kErrBitIndex) ? W4A8_ERR_INDEX
+                : (word & kErrBitPages) ? W4A8_ERR_PAGES : W4A8_OK;
     return W4A8_OK;
 }
 

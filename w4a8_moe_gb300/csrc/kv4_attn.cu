@@ -1,0 +1,492 @@
+// Decode attention over the key/value cache of 4 bits.
+//
+// "ROCm: enable trillion-parameter MoE models with INT4-FP8 single node",
+// config.json (48 query and 8 key/value heads): the attention of kv8_attn.cu for a
+// cache of the weights' width.
+//
+// A key is k_j = s_j c_j + m_j with codes c_j in 0..15, a value v_j = t_j d_j + n_j:
+//   x_j = sm_scale * (s_j (q . c_j) + m_j sum(q))       (cap > 0: cap * tanh(x_j / cap))
+//   out = (sum_j (e^{x_j} t_j) d_j + sum_j e^{x_j} n_j) / sum_j e^{x_j}
+// so the matrix products run over the codes, and the least values are one number a
+// key. The split between warps, the pieces and their join are those of the FP8 cache.
+#include <math.h>
+
+#include "internal.h"
+#include "kv4.cuh"
+#include "kv_split.cuh"
+
+namespace w4a8 {
+
+namespace {
+
+constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
+constexpr int kUnitShift = 5;
+constexpr int kUnit = 1 << kUnitShift;   // keys
+constexpr int kSub = kUnit / 16;         // of them in one product
+constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
+
+// A unit as its warp meets it, found by one lane for each of 32 units ahead.
+struct __align__(8) Unit {
+    int64_t row[2];   // cache rows (page, head, offset) of its first and its seventeenth key
+    int pair;
+    int live_last;    // keys that exist (1..32), and 256 where the pair ends
+};
+
+template <int D>
+struct Ring {   // one warp's shared memory
+    static constexpr int kStages = 2;             // units in flight
+    static constexpr int kCodes = kUnit * D / 2;  // bytes of K or V codes of a unit
+    static constexpr int kStage = 2 * kCodes + 2 * kUnit * 4;   // K, V, their scales
+    static constexpr int desc = kStages * kStage;
+    static constexpr int bars = desc + kDescs * static_cast<int>(sizeof(Unit));
+    static constexpr int total = (bars + kStages * 8 + 127) / 128 * 128;   // bulk copies want 16 bytes
+};
+
+__device__ __forceinline__ int64_t page_row(const Kv4Attn& a, const int32_t* pages, int h, int key)
+{
+    const int idx = key >> a.page_shift;
+    int page = idx < a.max_pages ? __ldg(pages + idx) : -1;
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
+        set_error(a.err, kErrBitIndex);
+        page = 0;
+    }
+    return cache_row(a.page_shift, a.Hkv, (static_cast<int64_t>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1)),
+                     h);
+}
+__device__ __forceinline__ Unit find_unit(const Kv4Attn& a, const Line& line, const int* cum, int64_t u)
+{
+    int lo = 0, hi = a.B;   // the last b with cum[b] * hr <= u
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int64_t>(cum[mid]) * line.hr <= u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const unsigned n = cum[lo + 1] - cum[lo];
+    const int64_t in = u - static_cast<int64_t>(cum[lo]) * line.hr;
+    int j, k;
+    if (in <= 0xFFFFFFFFll) {
+        j = static_cast<int>(static_cast<uint32_t>(in) / n);
+        k = static_cast<int>(static_cast<uint32_t>(in) - j * n);
+    } else {
+        j = static_cast<int>(in / n);
+        k = static_cast<int>(in - static_cast<int64_t>(j) * n);
+    }
+    int seq = lo;
+    if (a.seqs) {
+        seq = __ldg(a.seqs + lo);
+        if (static_cast<unsigned>(seq) >= static_cast<unsigned>(a.num_seqs)) {
+            set_error(a.err, kErrBitIndex);
+            seq = 0;
+        }
+    }
+    const int h = j / a.tiles, key0 = k << kUnitShift, len = seq_len(a, lo);
+    const int32_t* pages = a.page_table + seq * a.table_stride;
+    Unit x;
+    x.pair = lo * line.hr + j;
+    x.row[0] = page_row(a, pages, h, key0);
+    // a page of 16 ends inside the unit, and the next may not exist
+    x.row[1] = a.page_shift >= kUnitShift ? x.row[0] + 16 : len - key0 > 16 ? page_row(a, pages, h, key0 + 16) : x.row[0];
+    x.live_last = min(len - key0, kUnit) | (k == static_cast<int>(n) - 1 ? 256 : 0);
+    return x;
+}
+
+}  // namespace
+
+// Fragments. An f16 whose bits are 0000 0000 0000 cccc is the subnormal number
+// c 2^-24, and one with the code four bits up is c 2^-20; the tensor cores take
+// subnormals as they are, so codes become operands by a mask, two to a register,
+// without any conversion. The powers of two are taken out again where it costs
+// nothing: of a key's codes in the queries that meet them (2^14 or 2^10 times the
+// query, whose largest element stands in [1, 2)), of a value's in the result.
+//   word of 8 codes: & 000F000F -> codes 0, 4; & 00F000F0 -> 1, 5; shifted by 8 -> 2, 6 and 3, 7
+// Which d a fragment register stands for is free as long as q and o use the same
+// order. Both products have the rows as their N: S^T = K Q^T with 16 keys as M and
+// O^T = V^T P^T with D as M. A thread reads, of K's keys g and g + 8, chunk c of
+// their D codes, and of V's keys 2c, 2c + 1, 2c + 8, 2c + 9 (the pairs of an operand
+// register), chunk g. Two rows of D 128 cover the banks once, so neighbours are
+// swapped in every other pair of keys, which spreads V's reads over both halves.
+template <int D, int NT, int PER_SM>
+__global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __grid_constant__ Kv4Attn a)
+{
+    using S = Ring<D>;
+    constexpr int kStages = S::kStages;
+    constexpr int R = 8 * NT;      // rows of a tile
+    constexpr int KS = D / 16;     // k-steps of Q K^T = m-tiles of O^T
+    constexpr int WK = D / 32;     // words of a thread's chunk of a key: 8 codes each
+    constexpr int WV = D / 64;     // and of a value
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* cum = reinterpret_cast<int*>(smem + kWarps * S::total);   // [B + 1]
+    __shared__ int warp_sum[kWarps];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int swap_g = g ^ ((g >> 1) & 1), swap_c = c & 1;   // where the neighbours' swap puts a key
+    grid_dep_wait();
+    grid_dep_launch();     // the join reads the lengths only until this kernel has ended
+    const int total = sum_units<kWarps>(a, cum, warp_sum);
+    const uint32_t ring = smem_u32(smem) + warp * S::total;
+    if (lane < kStages)
+        mbar_init(ring + S::bars + lane * 8, 1);
+    fence_mbar_init();
+    __syncthreads();
+
+    const Line line = make_line(a, total);
+    // few units: one warp on each SM before a second
+    const int me = warp * gridDim.x + blockIdx.x;
+    const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
+    const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
+    Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
+
+    // unit i of this warp into its ring slot; batches of 32 descriptors ahead of it
+    auto issue = [&](int i) {
+        if (i >= units)
+            return;
+        if (i % 32 == 0) {
+            if (i + lane < units)
+                descs[(i + lane) % kDescs] = find_unit(a, line, cum, u_begin + i + lane);
+            __syncwarp();
+        }
+        if (lane == 0) {
+            const Unit& x = descs[i % kDescs];
+            const uint32_t dst = ring + (i % kStages) * S::kStage, bar = ring + S::bars + (i % kStages) * 8;
+            mbar_arrive_expect_tx(bar, S::kStage);
+            const int n = a.page_shift >= kUnitShift ? 1 : 2, rows = kUnit / n;
+            for (int p = 0; p < n; ++p) {
+                const int64_t row = x.row[p];
+                const uint32_t to = dst + p * rows * (D / 2), sc = dst + 2 * S::kCodes + p * rows * 4;
+                bulk_load(to, a.k_cache + row * (D / 2), rows * (D / 2), bar);
+                bulk_load(to + S::kCodes, a.v_cache + row * (D / 2), rows * (D / 2), bar);
+                bulk_load(sc, a.k_scale + row, rows * 4, bar);
+                bulk_load(sc + kUnit * 4, a.v_scale + row, rows * 4, bar);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+        issue(i);
+
+    uint32_t qb[KS][NT][2];
+    float qs[NT][2], qm[NT][2], o[KS][NT][4], m[NT][2], l[NT][2], ln[NT][2];
+    int rows = 0;
+    bool fresh = true;
+    for (int i = 0; i < units; ++i) {
+        const int pair = descs[i % kDescs].pair, live_last = descs[i % kDescs].live_last;
+        const int live = live_last & 255;
+        if (fresh) {
+            // ---- a new piece. Queries: f16 fragments of q * 2^-e, e from the row's
+            // largest element, times the powers above. bf16 has 8 significant bits,
+            // so only elements below 2^-27 of the largest lose anything, 2^-35 of it.
+            const int b = pair / line.hr, j = pair % line.hr;
+            const int h = j / a.tiles, row0 = (j % a.tiles) * R;
+            rows = min(R, a.group - row0);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int r = row0 + t * 8 + g;
+                uint4 raw[D / 32];
+                if (t * 8 + g < rows) {
+                    const uint16_t* src = a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + r) * D + c * (D / 4);
+#pragma unroll
+                    for (int w = 0; w < WK; ++w)
+                        raw[w] = __ldg(reinterpret_cast<const uint4*>(src) + w);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < WK; ++w)
+                        raw[w] = make_uint4(0, 0, 0, 0);
+                }
+                uint32_t top = 0;
+#pragma unroll
+                for (int w = 0; w < WK; ++w) {
+                    const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top = max(top, max((x[e] >> 16) & 0x7FFFu, x[e] & 0x7FFFu));
+                }
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const int ex = static_cast<int>(top >> 7);
+                const int e = top == 0 || ex == 255 ? 0 : max(ex, 1) - 127;
+                const float down = ldexpf(1.0f, -e);
+                float sum = 0.0f;   // of q * 2^-e
+#pragma unroll
+                for (int w = 0; w < WK; ++w) {
+                    const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+                    float y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        y[k] = __uint_as_float(k & 1 ? x[k / 2] & 0xFFFF0000u : x[k / 2] << 16) * down;
+                        sum += y[k];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float f = k & 1 ? 0x1p10f : 0x1p14f;
+                        qb[2 * w + (k >> 1)][t][k & 1] = pack_f16(y[k] * f, y[k + 4] * f);
+                    }
+                }
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                float f = ldexpf(a.sm_scale, e);
+                f = a.cap > 0.0f ? f / a.cap * (2.0f * kLog2e) : f * kLog2e;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {   // of the rows 2c, 2c + 1
+                    qs[t][y] = __shfl_sync(0xFFFFFFFFu, f, c * 8 + y * 4);
+                    qm[t][y] = __shfl_sync(0xFFFFFFFFu, f * sum, c * 8 + y * 4);
+                    m[t][y] = kLowest;
+                    l[t][y] = 0.0f;
+                    ln[t][y] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        o[j][t][k] = 0.0f;
+            fresh = false;
+        }
+
+        // ---- the unit's codes into registers, and its slot to the next copy
+        const uint32_t at = ring + (i % kStages) * S::kStage;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(ring + S::bars + (i % kStages) * 8, (i / kStages) & 1))) {
+            set_error(a.err, kErrBitTimeout);
+            for (int j = i + 1; j < min(i + kStages, units); ++j)   // copies in flight end before the warp does
+                mbar_wait(ring + S::bars + (j % kStages) * 8, (j / kStages) & 1);
+            break;
+        }
+        uint32_t xk[kSub][2][WK], xv[kSub][4][WV];
+        float ks[kSub][2], km[kSub][2], vs[kSub][2], vm[kSub][2];   // of the keys g, g + 8
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int key = u * 16 + x * 8 + swap_g;
+                if (D == 128) {
+                    const uint4 w = lds128(at + key * (D / 2) + c * 16);
+                    xk[u][x][0] = w.x, xk[u][x][1] = w.y, xk[u][x][WK - 2] = w.z, xk[u][x][WK - 1] = w.w;
+                } else {
+                    const uint2 w = lds64(at + key * (D / 2) + c * 8);
+                    xk[u][x][0] = w.x, xk[u][x][1] = w.y;
+                }
+                const uint32_t pk = __float_as_uint(lds32(at + 2 * S::kCodes + key * 4));
+                const uint32_t pv = __float_as_uint(lds32(at + 2 * S::kCodes + (kUnit + key) * 4));
+                ks[u][x] = __uint_as_float(pk << 16), km[u][x] = __uint_as_float(pk & 0xFFFF0000u);
+                vs[u][x] = __uint_as_float(pv << 16), vm[u][x] = __uint_as_float(pv & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int key = u * 16 + (k >> 1) * 8 + c * 2 + ((k & 1) ^ swap_c);
+                if (D == 128) {
+                    const uint2 w = lds64(at + S::kCodes + key * (D / 2) + g * 8);
+                    xv[u][k][0] = w.x, xv[u][k][WV - 1] = w.y;
+                } else {
+                    xv[u][k][0] = __float_as_uint(lds32(at + S::kCodes + key * (D / 2) + g * 4));
+                }
+            }
+        }
+        if (live < kUnit) {   // what lies behind the last key may be no number
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (u * 16 + x * 8 + swap_g >= live)
+                        ks[u][x] = km[u][x] = vs[u][x] = vm[u][x] = 0.0f;
+        }
+        __syncwarp();
+        issue(i + kStages);
+
+        // ---- S^T = K Q^T: s[u][t][2 x + y] is key g + 8 x, row 8 t + 2c + y
+        float s[kSub][NT][4];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[u][t][k] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WK; ++w)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t w0 = half ? xk[u][0][w] >> 8 : xk[u][0][w], w1 = half ? xk[u][1][w] >> 8 : xk[u][1][w];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        mma_f16(s[u][t], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u,
+                                qb[2 * w + half][t][0], qb[2 * w + half][t][1]);
+                }
+        }
+        // ---- scores in log2 units (cap * tanh(y) = cap * (1 - 2 / (1 + e^{2y})), qs
+        // and qm holding 2 log2(e) / cap); keys past the end are -inf. The product
+        // is 2^-10 of q 2^-e . c.
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float x = fmaf(s[u][t][k] * 1024.0f * qs[t][k & 1], ks[u][k >> 1], km[u][k >> 1] * qm[t][k & 1]);
+                    if (a.cap > 0.0f)
+                        x = fmaf(-2.0f * kLog2e * a.cap, rcp(1.0f + ex2(x)), kLog2e * a.cap);
+                    s[u][t][k] = x;
+                }
+        if (live < kUnit) {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[u][t][k] = u * 16 + (k >> 1) * 8 + swap_g < live ? s[u][t][k] : -INFINITY;
+        }
+        // ---- weights under the reference as it stands; where one, times the size of
+        // its value, would come near f16's end the reference is raised and they are
+        // taken again. (The size: the larger of the step and the least value, so that
+        // neither product of the weight leaves the range.)
+        float p[kSub][NT][4];
+        auto size = [&](int u, int x) { return fmaxf(fabsf(vs[u][x]), fabsf(vm[u][x])); };
+        auto weigh = [&]() {
+            float top = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float z = fmaxf(size(u, x), kLeastScale);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            p[u][t][2 * x + y] = ex2(s[u][t][2 * x + y] - m[t][y]);
+                            top = fmaxf(top, p[u][t][2 * x + y] * z);
+                        }
+                }
+            return top;
+        };
+        if (__any_sync(0xFFFFFFFFu, weigh() > kMostWeight)) {
+            float lift[kSub][2];   // log2 of the values' sizes
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    lift[u][x] = fmaxf(log2f(size(u, x)), kLeastScaleLog2);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+                        top = fmaxf(top, fmaxf(s[u][t][y] + lift[u][0], s[u][t][2 + y] + lift[u][1]));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+                    const float to = fmaxf(m[t][y], top - kWeightTop);
+                    const float f = ex2(m[t][y] - to);
+                    m[t][y] = to;
+                    l[t][y] *= f;
+                    ln[t][y] *= f;
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) {
+                        o[j][t][y] *= f;
+                        o[j][t][2 + y] *= f;
+                    }
+                }
+            weigh();
+        }
+        // ---- P^T and O^T += V^T P^T
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float p0 = p[u][t][2 * x], p1 = p[u][t][2 * x + 1];
+                    l[t][0] += p0;
+                    l[t][1] += p1;
+                    ln[t][0] = fmaf(p0, vm[u][x], ln[t][0]);
+                    ln[t][1] = fmaf(p1, vm[u][x], ln[t][1]);
+                    pb[t][x] = transpose8(pack_f16(p0 * vs[u][x], p1 * vs[u][x]));
+                }
+#pragma unroll
+            for (int w = 0; w < WV; ++w)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t sel = q < 2 ? 0x5410u : 0x7632u;
+                    uint32_t x0 = prmt(xv[u][0][w], xv[u][1][w], sel), x1 = prmt(xv[u][2][w], xv[u][3][w], sel);
+                    if (q & 1)
+                        x0 >>= 8, x1 >>= 8;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        mma_f16(o[4 * w + q][t], x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u,
+                                pb[t][0], pb[t][1]);
+                }
+        }
+
+        // ---- the piece ends with its pair or with the warp's units
+        if ((live_last & 256) || i + 1 == units) {
+            const int64_t slot = static_cast<int64_t>(pair) + me;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+                        l[t][y] += __shfl_xor_sync(0xFFFFFFFFu, l[t][y], x);
+                        ln[t][y] += __shfl_xor_sync(0xFFFFFFFFu, ln[t][y], x);
+                    }
+                    if (g == 0 && t * 8 + c * 2 + y < rows)
+                        a.part_ml[slot * R + t * 8 + c * 2 + y] = make_float2(m[t][y], l[t][y]);
+                }
+                float* dst = a.part_o + (slot * R + t * 8 + c * 2) * D + g * (D / 8);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (t * 8 + c * 2 + e < rows) {
+#pragma unroll
+                        for (int j = 0; j < KS; j += 2)   // values 2j and 2j + 1 of the chunk: rows g and g + 8
+                            *reinterpret_cast<float4*>(dst + e * D + 2 * j) =
+                                make_float4(fmaf(o[j][t][e], 0x1p24f, ln[t][e]), fmaf(o[j][t][2 + e], 0x1p20f, ln[t][e]),
+                                            fmaf(o[j + 1][t][e], 0x1p24f, ln[t][e]),
+                                            fmaf(o[j + 1][t][2 + e], 0x1p20f, ln[t][e]));
+                    }
+            }
+            fresh = true;
+        }
+    }
+}
+
+static int ring_smem(int D, int B) { return kWarps * (D == 128 ? Ring<128>::total : Ring<64>::total) + (B + 1) * 4; }
+
+template <int D, int NT, int PER_SM>
+static cudaError_t launch_pieces(const Kv4Attn& a, cudaStream_t s)
+{
+    const int smem = ring_smem(D, a.B);
+    auto kern = kv4_attn_kernel<D, NT, PER_SM>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch_dependent(kern, dim3(a.warps / kWarps), dim3(kWarps * 32), smem, s, a);
+}
+
+cudaError_t launch_kv4_attn(const Kv4Attn& in, int D, int num_sms, cudaStream_t s)
+{
+    Kv4Attn a = in;
+    const int R = kv8_attn_row_tile(a.group);
+    a.unit_shift = kUnitShift;
+    const int64_t pairs = static_cast<int64_t>(a.Hkv) * a.B * a.tiles;
+    const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
+    const int blocks = min(R == 8 ? 4 : D == 64 ? 3 : 2, fit);
+    a.warps = min(num_sms * blocks * kWarps, kKv8MaxWarps / kWarps * kWarps);
+    a.free_warps = a.warps;
+    a.spread = static_cast<int>(min(max(min(8 * pairs, int64_t{2048}), int64_t{1536}), 128 * pairs));
+    cudaError_t e = cudaSuccess;
+    if (a.max_pages)
+        e = D == 128 ? (R == 8 ? launch_pieces<128, 1, 4>(a, s) : launch_pieces<128, 2, 2>(a, s))
+                     : (R == 8 ? launch_pieces<64, 1, 4>(a, s) : launch_pieces<64, 2, 3>(a, s));
+    if (e != cudaSuccess)
+        return e;
+    return launch_kv_join(a, Kv8Prefix{}, D, num_sms, s);
+}
+
+}  // namespace w4a8

@@ -37,44 +37,11 @@ __device__ __forceinline__ RowAt row_at(const Kv8Rows& a, const int32_t* __restr
     r.slot = r.live ? __ldg(slots + r.t) : -1;
     return r;
 }
-__device__ __forceinline__ int64_t cache_row(const Kv8Rows& a, int64_t slot, int h)
+__device__ __forceinline__ void encode_bf16(const uint4 (&raw)[2], float top, float s, uint2 (&c)[2])
 {
-    const int64_t page = slot >> a.page_shift;
-    const int64_t off = slot & ((1 << a.page_shift) - 1);
-    return ((page * a.Hkv + h) << a.page_shift) + off;
-}
-
-// E4M3(x / s) of 16 values, the quotient rounded to fp32 first. A division of
-// every value would be most of the call's arithmetic; here it is q = x r with
-// r = 1 / s correctly rounded, then q + (q s - x) (-r) by two fused multiply-adds,
-// which is the correctly rounded quotient where nothing under- or overflows
-// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990). With 2^-60 <= s < 2^60 and finite values below 2^60 s that
-// holds for every quotient above 2^-11, and smaller ones have the code 0 either
-// way; other rows divide. The residual is taken with that sign so that a zero
-// keeps its own: q s - x is +0 for x = -0, and +0 (-r) + (-0) is -0.
-__device__ __forceinline__ void encode16(const uint4 (&raw)[2], float top, float s, uint2 (&c)[2])
-{
-    const float r = __frcp_rn(s);
-    const bool plain = s >= 8.6736174e-19f && s < 1.1529215e18f && top < s * 1.1529215e18f;
-    const F2 r2(-r, -r), s2(s, s);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float lo = __uint_as_float(u[j] << 16), hi = __uint_as_float(u[j] & 0xFFFF0000u);
-            if (plain) {
-                const F2 x(-lo, -hi), q = mul2(x, r2);
-                const F2 t = fma2(fma2(q, s2, x), r2, q);
-                e[j] = cvt_e4m3x2(t.hi(), t.lo());
-            } else {
-                e[j] = cvt_e4m3x2(__fdiv_rn(hi, s), __fdiv_rn(lo, s));
-            }
-        }
-        c[i] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
-    }
+    float x[16];
+    unpack16(raw, x);
+    encode16(x, top, s, c);
 }
 
 // The largest magnitude of 16 bf16 values, as bits: not finite from 0x7F80 on.
@@ -142,7 +109,7 @@ __global__ void __launch_bounds__(kRowThreads) kv8_write_kernel(const __grid_con
             raw[y][i] = r.live ? __ldg(reinterpret_cast<const uint4*>(src) + i * L + lane) : make_uint4(0, 0, 0, 0);
     }
     const bool ok = r.live && r.slot >= 0 && r.slot < a.num_slots;
-    const int64_t at = ok ? cache_row(a, r.slot, r.h) : 0;
+    const int64_t at = ok ? cache_row(a.page_shift, a.Hkv, r.slot, r.h) : 0;
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         float* scale = y ? v_scale : k_scale;
@@ -166,7 +133,7 @@ __global__ void __launch_bounds__(kRowThreads) kv8_write_kernel(const __grid_con
         }
         if (ok) {
             uint2 c[2];
-            encode16(raw[y], __uint_as_float(top << 16), s, c);
+            encode_bf16(raw[y], __uint_as_float(top << 16), s, c);
             uint2* dst = reinterpret_cast<uint2*>((y ? v_cache : k_cache) + at * D);
             dst[lane] = c[0];
             dst[L + lane] = c[1];
@@ -196,7 +163,7 @@ __global__ void __launch_bounds__(kRowThreads) kv8_read_kernel(const __grid_cons
     uint2 raw[2][2] = {{make_uint2(0, 0), make_uint2(0, 0)}, {make_uint2(0, 0), make_uint2(0, 0)}};
     float s[2] = {0.0f, 0.0f};
     if (r.slot >= 0 && r.slot < a.num_slots) {
-        const int64_t at = cache_row(a, r.slot, r.h);
+        const int64_t at = cache_row(a.page_shift, a.Hkv, r.slot, r.h);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const uint2* src = reinterpret_cast<const uint2*>((y ? v_cache : k_cache) + at * D);

@@ -5,9 +5,12 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ptx.cuh"
+
 namespace w4a8 {
 
 constexpr uint32_t kErrBitIndex = 2u;  // a page index or a length was out of range
+constexpr uint32_t kErrBitPages = 4u;  // a pool of pages ran out
 
 // ---- cache: E4M3 codes [num_pages, Hkv, page_size, D], page_size = 1 << page_shift.
 struct Kv8Rows {            // arguments of the write and the read
@@ -25,7 +28,8 @@ cudaError_t launch_kv8_read(const Kv8Rows& a, const uint8_t* k_cache, const uint
 
 // ---- attention
 constexpr int kKv8MaxBatch = 4096;  // the split's prefix sums live in shared memory
-constexpr int kKv8Unit = 16;        // keys per unit of the split (a unit never crosses a page)
+constexpr int kKv8UnitShift = 4;    // keys per unit of the split (a unit never crosses a page)
+constexpr int kKv8Unit = 1 << kKv8UnitShift;
 constexpr int kKv8MaxWarps = 152 * 16;   // warps the units are divided over, at most
 
 struct Kv8Attn {
@@ -51,6 +55,7 @@ struct Kv8Attn {
     uint32_t* err;
     uint16_t* out;
     float* lse;
+    int unit_shift;     // log2 of the keys of a unit
     int warps;          // that the units go to
     int free_warps;     // of them those that need not wait for the tiled prefix
     int spread;         // warps up to which the units are spread by twos
@@ -77,6 +82,8 @@ cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int p
 bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);
 int kv8_attn_row_tile(int group);
 void kv8_attn_layout(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms, int* blocks_per_sm, int* warps_a_row);
+// Adds up the pieces that a kernel over `a`'s split has left.
+cudaError_t launch_kv_join(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_kv8_attn(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s);
 
 // Two E4M3 codes (low byte first) to two f16 values: exact for every code.
@@ -174,6 +181,60 @@ __device__ __forceinline__ float rcp(float x)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// ---- rows of the cache
+__device__ __forceinline__ int64_t cache_row(int page_shift, int Hkv, int64_t slot, int h)
+{
+    const int64_t page = slot >> page_shift;
+    const int64_t off = slot & ((1 << page_shift) - 1);
+    return ((page * Hkv + h) << page_shift) + off;
+}
+
+// 16 bf16 values as fp32.
+__device__ __forceinline__ void unpack16(const uint4 (&raw)[2], float (&x)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[i * 8 + 2 * j] = __uint_as_float(u[j] << 16);
+            x[i * 8 + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+    }
+}
+
+// E4M3(x / s) of 16 values, the quotient rounded to fp32 first; no |x| is above
+// top. A division of every value would be most of a call's arithmetic; here it is
+// q = x r with r = 1 / s correctly rounded, then q + (q s - x) (-r) by two fused
+// multiply-adds, which is the correctly rounded quotient where nothing under- or
+// overflows (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990). With 2^-60 <= s < 2^60 and values below 2^60 s
+// that holds for every quotient above 2^-11, and smaller ones have the code 0
+// either way; other rows divide. The residual is taken with that sign so that a
+// zero keeps its own: q s - x is +0 for x = -0, and +0 (-r) + (-0) is -0.
+__device__ __forceinline__ void encode16(const float (&x)[16], float top, float s, uint2 (&c)[2])
+{
+    const float r = __frcp_rn(s);
+    const bool plain = s >= 8.6736174e-19f && s < 1.1529215e18f && top < s * 1.1529215e18f;
+    const F2 r2(-r, -r), s2(s, s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float lo = x[i * 8 + 2 * j], hi = x[i * 8 + 2 * j + 1];
+            if (plain) {
+                const F2 x(-lo, -hi), q = mul2(x, r2);
+                const F2 t = fma2(fma2(q, s2, x), r2, q);
+                e[j] = cvt_e4m3x2(t.hi(), t.lo());
+            } else {
+                e[j] = cvt_e4m3x2(__fdiv_rn(hi, s), __fdiv_rn(lo, s));
+            }
+        }
+        c[i] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+    }
 }
 
 }  // namespace w4a8

@@ -1,0 +1,276 @@
+// Page tables of the key/value cache kept on the GPU: the pages and slots of a
+// step's new tokens from the sequences' lengths, and the way back.
+//
+// "ROCm: enable trillion-parameter MoE models with INT4-FP8 single node",
+// config.json (kv_cache_scheme): the cache whose pages these are. The pages have no
+// counterpart for the tables themselves, which a serving program there keeps on the host.
+//
+// Free pages stand on a stack. Sequence b, with len_b tokens and add_b new ones,
+// needs n_b = ceil((len_b + add_b) / page) - ceil(len_b / page) pages; in the order
+// of b they are taken off the top, so the j-th page taken is stack[count - 1 - j]
+// and everything follows from two prefix sums over the sequences. Every block adds
+// these up for itself (4096 sequences: 16 values a thread), then the blocks share
+// the tokens and the new table entries between them; who a token or a page belongs
+// to is found by bisection. Nothing that one block writes does another one read but
+// the lengths and the count, which the last block to have read them writes.
+#include "internal.h"
+#include "kv8.cuh"
+#include "pages.cuh"
+#include "ptx.cuh"
+
+namespace w4a8 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItems = 4;   // tokens of a thread
+
+// The last i of [0, n) with sums[i] <= x (sums rises from 0 and n >= 1).
+__device__ __forceinline__ int owner(const int* sums, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// What stands before each thread of the block: exclusive prefix sums of two values,
+// which stop growing at their limits (sums of natural numbers cut off that way
+// still associate).
+__device__ __forceinline__ void block_before(unsigned& x, unsigned& y, unsigned most_x, unsigned most_y)
+{
+    __shared__ unsigned sx[kThreads / 32], sy[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned dx = __shfl_up_sync(0xFFFFFFFFu, x, o), dy = __shfl_up_sync(0xFFFFFFFFu, y, o);
+        if (lane >= o) {
+            x = min(x + dx, most_x);
+            y = min(y + dy, most_y);
+        }
+    }
+    if (lane == 31)
+        sx[warp] = x, sy[warp] = y;
+    __syncthreads();
+    x = __shfl_up_sync(0xFFFFFFFFu, x, 1);
+    y = __shfl_up_sync(0xFFFFFFFFu, y, 1);
+    if (lane == 0)
+        x = y = 0;
+    for (int w = 0; w < warp; ++w) {
+        x = min(x + sx[w], most_x);
+        y = min(y + sy[w], most_y);
+    }
+}
+
+__device__ __forceinline__ int pages_of(int tokens, int shift)   // tokens >= 0
+{
+    return static_cast<int>((static_cast<unsigned>(tokens) + (1u << shift) - 1) >> shift);
+}
+__device__ __forceinline__ int free_pages(const PagePool& p)
+{
+    const int n = *p.count;
+    if (n < 0 || n > p.num_pages)
+        set_error(p.err, kErrBitIndex);
+    return min(max(n, 0), p.num_pages);
+}
+// Whether this block is the last of the grid to come here; all threads agree.
+__device__ __forceinline__ bool last_block(uint32_t* ticket)
+{
+    __shared__ bool last;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = gridDim.x == 1 || atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
+    __syncthreads();
+    return last;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads) pages_extend_kernel(const __grid_constant__ PagesExtend a)
+{
+    extern __shared__ int smem[];
+    int* starts = smem;               // [B + 1] tokens before each sequence, T + 1 at most
+    int* ahead = smem + a.B + 1;      // [B + 1] pages that those before it need, num_pages + 1 at most
+    int* have = ahead + a.B + 1;      // [B] its tokens; less than 0 (the complement) where it gets no pages
+    __shared__ int taken;
+    const int tid = threadIdx.x, shift = a.p.page_shift;
+    if (tid == 0)
+        taken = 0;
+    grid_dep_wait();
+    const int count = free_pages(a.p);
+    const int64_t most_tokens = static_cast<int64_t>(a.p.max_pages) << shift;
+
+    // ---- the sums: a thread takes `per` sequences in a row
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    const unsigned most_x = static_cast<unsigned>(a.T) + 1, most_y = static_cast<unsigned>(a.p.num_pages) + 1;
+    unsigned x = 0, y = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+        const int len = a.lens[b], add = max(a.add[b], 0);
+        const bool ok = len >= 0 && a.add[b] >= 0 && static_cast<int64_t>(len) + add <= most_tokens;
+        bad |= !ok;
+        have[b] = ok ? len : ~max(len, 0);
+        starts[b + 1] = add;
+        ahead[b + 1] = ok ? pages_of(len + add, shift) - pages_of(len, shift) : 0;
+        x = min(x + add, most_x);
+        y = min(y + ahead[b + 1], most_y);
+    }
+    block_before(x, y, most_x, most_y);
+    if (tid == 0)
+        starts[0] = 0, ahead[0] = 0;
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int need = ahead[b + 1];
+        x = min(x + static_cast<unsigned>(starts[b + 1]), most_x);
+        y = min(y + static_cast<unsigned>(need), most_y);
+        starts[b + 1] = static_cast<int>(x);
+        ahead[b + 1] = static_cast<int>(y);
+        const bool room = x <= static_cast<unsigned>(a.T), there = need == 0 || y <= static_cast<unsigned>(count);
+        if (!room && blockIdx.x == 0)
+            bad = true;
+        if (!there && blockIdx.x == 0)
+            set_error(a.p.err, kErrBitPages);
+        if (!(room && there) && have[b] >= 0)
+            have[b] = ~have[b];
+        if (need && have[b] >= 0)
+            mine = static_cast<int>(y);
+    }
+    if (bad && blockIdx.x == 0)
+        set_error(a.p.err, kErrBitIndex);
+    if (mine)
+        atomicMax(&taken, mine);   // those that get pages are the first of those that need some
+    const bool last = last_block(a.p.ticket);
+
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= a.B; b += kThreads)
+            a.starts[b] = min(starts[b], a.T);
+    // ---- the new entries of the tables
+    const int step = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
+    for (int j = first; j < taken; j += step) {
+        const int b = owner(ahead, a.B, j);
+        const int64_t at = pages_of(have[b], shift) + j - ahead[b];
+        a.p.table[b * a.p.stride + at] = a.p.stack[count - 1 - j];
+    }
+    // ---- the tokens
+    const int total = min(starts[a.B], a.T);
+    for (int t = first; t < a.T; t += step) {
+        int seq = -1, pos = 0, seen = 0, slot = -1;
+        if (t < total) {
+            seq = owner(starts, a.B, t);
+            const int len = have[seq];
+            pos = static_cast<int>(static_cast<unsigned>(len < 0 ? ~len : len) + static_cast<unsigned>(t - starts[seq]));
+            seen = len < 0 ? 0 : pos + 1;
+            if (len >= 0) {
+                const int at = pos >> shift, used = pages_of(len, shift);
+                const int page = at < used ? a.p.table[seq * a.p.stride + at]
+                                           : a.p.stack[count - 1 - (ahead[seq] + at - used)];
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.p.num_pages))
+                    slot = (page << shift) + (pos & ((1 << shift) - 1));
+                else
+                    set_error(a.p.err, kErrBitIndex);
+            }
+        }
+        a.seqs[t] = seq;
+        a.positions[t] = pos;
+        a.seen[t] = seen;
+        a.slots[t] = slot;
+    }
+    if (last) {   // every block has read the lengths and the count
+        for (int b = tid; b < a.B; b += kThreads) {
+            const int len = have[b];
+            a.lens_out[b] = len >= 0 ? len + (starts[b + 1] - starts[b]) : a.lens[b];
+        }
+        if (tid == 0)
+            *a.p.count = count - taken;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) pages_truncate_kernel(const __grid_constant__ PagesTruncate a)
+{
+    extern __shared__ int smem[];
+    int* ahead = smem;             // [B + 1] pages that those before it give back, num_pages + 1 at most
+    int* kept = smem + a.B + 1;    // [B] tokens
+    const int tid = threadIdx.x, shift = a.p.page_shift;
+    grid_dep_wait();
+    const int count = free_pages(a.p);
+    const int64_t most_tokens = static_cast<int64_t>(a.p.max_pages) << shift;
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    const unsigned most = static_cast<unsigned>(a.p.num_pages) + 1;
+    unsigned x = 0, unused = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+        const int len = a.lens[b], keep = a.keep[b];
+        const bool ok = keep >= 0 && keep <= len && len <= most_tokens;
+        bad |= !ok;
+        kept[b] = ok ? keep : len;
+        ahead[b + 1] = ok ? pages_of(len, shift) - pages_of(keep, shift) : 0;
+        x = min(x + ahead[b + 1], most);
+    }
+    block_before(x, unused, most, most);
+    if (tid == 0)
+        ahead[0] = 0;
+    for (int b = b0; b < b1; ++b) {
+        x = min(x + static_cast<unsigned>(ahead[b + 1]), most);
+        ahead[b + 1] = static_cast<int>(x);
+    }
+    const bool last = last_block(a.p.ticket);
+    // more pages than the stack has room for: somebody's length is wrong, and nothing goes back
+    const int given = ahead[a.B];
+    const bool fits = given <= a.p.num_pages - count;
+    if ((bad || !fits) && blockIdx.x == 0)
+        set_error(a.p.err, kErrBitIndex);
+    if (fits) {
+        for (int j = blockIdx.x * kThreads + tid; j < given; j += gridDim.x * kThreads) {
+            const int b = owner(ahead, a.B, j);
+            const int64_t at = pages_of(kept[b], shift) + j - ahead[b];
+            const int page = a.p.table[b * a.p.stride + at];
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.p.num_pages))
+                set_error(a.p.err, kErrBitIndex);
+            // in reverse: what an extension took comes to lie as it lay
+            a.p.stack[count + given - 1 - j] = page;
+        }
+    }
+    if (last) {
+        for (int b = tid; b < a.B; b += kThreads)
+            a.lens_out[b] = fits ? kept[b] : a.lens[b];
+        if (tid == 0 && fits)
+            *a.p.count = count + given;
+    }
+}
+
+static unsigned blocks_for(int64_t items, int num_sms)
+{
+    const int64_t n = (items + kThreads * kItems - 1) / (kThreads * kItems);
+    return static_cast<unsigned>(n < 1 ? 1 : n > num_sms ? num_sms : n);
+}
+
+template <class A>
+static cudaError_t launch(void (*kern)(A), const A& a, unsigned blocks, int smem, cudaStream_t s)
+{
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch_dependent(kern, dim3(blocks), dim3(kThreads), smem, s, a);
+}
+
+cudaError_t launch_pages_extend(const PagesExtend& a, int num_sms, cudaStream_t s)
+{
+    return launch(pages_extend_kernel, a, blocks_for(a.T, num_sms), (3 * a.B + 2) * 4, s);
+}
+
+cudaError_t launch_pages_truncate(const PagesTruncate& a, int num_sms, cudaStream_t s)
+{
+    // how many pages go back only the device knows: the most that it could be
+    const int64_t most = static_cast<int64_t>(a.B) * a.p.max_pages;
+    return launch(pages_truncate_kernel, a, blocks_for(most < a.p.num_pages ? most : a.p.num_pages, num_sms),
+                  (2 * a.B + 1) * 4, s);
+}
+
+}  // namespace w4a8

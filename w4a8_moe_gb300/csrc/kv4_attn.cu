@@ -126,8 +126,9 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     grid_dep_launch();     // the join reads the lengths only until this kernel has ended
     const int total = sum_units<kWarps>(a, cum, warp_sum);
     const uint32_t ring = smem_u32(smem) + warp * S::total;
+    const int copies = a.page_shift >= kUnitShift ? 4 : 8, copy_keys = 4 * kUnit / copies;   // of a unit, see below
     if (lane < kStages)
-        mbar_init(ring + S::bars + lane * 8, 1);
+        mbar_init(ring + S::bars + lane * 8, copies);
     fence_mbar_init();
     __syncthreads();
 
@@ -138,6 +139,13 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
     Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
 
+    // lane 0 copies codes of keys, 1 of values, 2 and 3 their scales, 4 to 7 those of
+    // the second page where pages are half a unit
+    const uint32_t copy_row = lane & 2 ? 4 : D / 2, copy_bytes = copy_keys * copy_row;
+    const uint32_t copy_to = ring + (lane & 2 ? 2 * S::kCodes + (lane & 1) * kUnit * 4 : (lane & 1) * S::kCodes) +
+                             (lane >> 2) * copy_bytes;
+    const uint8_t* copy_from = lane & 2 ? reinterpret_cast<const uint8_t*>(lane & 1 ? a.v_scale : a.k_scale)
+                                        : lane & 1 ? a.v_cache : a.k_cache;
     // unit i of this warp into its ring slot; batches of 32 descriptors ahead of it
     auto issue = [&](int i) {
         if (i >= units)
@@ -147,19 +155,11 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                 descs[(i + lane) % kDescs] = find_unit(a, line, cum, u_begin + i + lane);
             __syncwarp();
         }
-        if (lane == 0) {
-            const Unit& x = descs[i % kDescs];
-            const uint32_t dst = ring + (i % kStages) * S::kStage, bar = ring + S::bars + (i % kStages) * 8;
-            mbar_arrive_expect_tx(bar, S::kStage);
-            const int n = a.page_shift >= kUnitShift ? 1 : 2, rows = kUnit / n;
-            for (int p = 0; p < n; ++p) {
-                const int64_t row = x.row[p];
-                const uint32_t to = dst + p * rows * (D / 2), sc = dst + 2 * S::kCodes + p * rows * 4;
-                bulk_load(to, a.k_cache + row * (D / 2), rows * (D / 2), bar);
-                bulk_load(to + S::kCodes, a.v_cache + row * (D / 2), rows * (D / 2), bar);
-                bulk_load(sc, a.k_scale + row, rows * 4, bar);
-                bulk_load(sc + kUnit * 4, a.v_scale + row, rows * 4, bar);
-            }
+        if (lane < copies) {   // one instruction for all of the unit's copies
+            const uint32_t bar = ring + S::bars + (i % kStages) * 8;
+            mbar_arrive_expect_tx(bar, copy_bytes);
+            bulk_load(copy_to + (i % kStages) * S::kStage, copy_from + descs[i % kDescs].row[lane >> 2] * copy_row, copy_bytes,
+                      bar);
         }
     };
 #pragma unroll
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
         issue(i);
 
     uint32_t qb[KS][NT][2];
-    float qs[NT][2], qm[NT][2], o[KS][NT][4], m[NT][2], l[NT][2], ln[NT][2];
+    float qs[NT][2], qm[NT][2], o[KS][NT][4], m[NT][2];
+    F2 l2[NT], ln2[NT];   // sums of the weights, and of weights times least values, of rows 2c and 2c + 1
     int rows = 0;
     bool fresh = true;
     for (int i = 0; i < units; ++i) {
@@ -232,9 +233,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                     qs[t][y] = __shfl_sync(0xFFFFFFFFu, f, c * 8 + y * 4);
                     qm[t][y] = __shfl_sync(0xFFFFFFFFu, f * sum, c * 8 + y * 4);
                     m[t][y] = kLowest;
-                    l[t][y] = 0.0f;
-                    ln[t][y] = 0.0f;
                 }
+                l2[t] = ln2[t] = F2(0.0f, 0.0f);
             }
 #pragma unroll
             for (int j = 0; j < KS; ++j)
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                 mbar_wait(ring + S::bars + (j % kStages) * 8, (j / kStages) & 1);
             break;
         }
-        uint32_t xk[kSub][2][WK], xv[kSub][4][WV];
+        uint32_t xk[kSub][2][WK];
         float ks[kSub][2], km[kSub][2], vs[kSub][2], vm[kSub][2];   // of the keys g, g + 8
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
@@ -273,16 +273,6 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                 ks[u][x] = __uint_as_float(pk << 16), km[u][x] = __uint_as_float(pk & 0xFFFF0000u);
                 vs[u][x] = __uint_as_float(pv << 16), vm[u][x] = __uint_as_float(pv & 0xFFFF0000u);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int key = u * 16 + (k >> 1) * 8 + c * 2 + ((k & 1) ^ swap_c);
-                if (D == 128) {
-                    const uint2 w = lds64(at + S::kCodes + key * (D / 2) + g * 8);
-                    xv[u][k][0] = w.x, xv[u][k][WV - 1] = w.y;
-                } else {
-                    xv[u][k][0] = __float_as_uint(lds32(at + S::kCodes + key * (D / 2) + g * 4));
-                }
-            }
         }
         if (live < kUnit) {   // what lies behind the last key may be no number
 #pragma unroll
@@ -292,8 +282,6 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                     if (u * 16 + x * 8 + swap_g >= live)
                         ks[u][x] = km[u][x] = vs[u][x] = vm[u][x] = 0.0f;
         }
-        __syncwarp();
-        issue(i + kStages);
 
         // ---- S^T = K Q^T: s[u][t][2 x + y] is key g + 8 x, row 8 t + 2c + y
         float s[kSub][NT][4];
@@ -323,12 +311,21 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float x = fmaf(s[u][t][k] * 1024.0f * qs[t][k & 1], ks[u][k >> 1], km[u][k >> 1] * qm[t][k & 1]);
-                    if (a.cap > 0.0f)
-                        x = fmaf(-2.0f * kLog2e * a.cap, rcp(1.0f + ex2(x)), kLog2e * a.cap);
-                    s[u][t][k] = x;
+                for (int x = 0; x < 2; ++x) {   // (rows in pairs: one instruction for both)
+                    const F2 qc = mul2(mul2(F2(s[u][t][2 * x], s[u][t][2 * x + 1]), F2(1024.0f, 1024.0f)),
+                                       F2(qs[t][0], qs[t][1]));
+                    const F2 y = fma2(qc, F2(ks[u][x], ks[u][x]), mul2(F2(km[u][x], km[u][x]), F2(qm[t][0], qm[t][1])));
+                    s[u][t][2 * x] = y.lo(), s[u][t][2 * x + 1] = y.hi();
                 }
+        if (a.cap > 0.0f) {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[u][t][k] = fmaf(-2.0f * kLog2e * a.cap, rcp(1.0f + ex2(s[u][t][k])), kLog2e * a.cap);
+        }
         if (live < kUnit) {
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
@@ -351,13 +348,15 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float z = fmaxf(size(u, x), kLeastScale);
+                    float most = 0.0f;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            p[u][t][2 * x + y] = ex2(s[u][t][2 * x + y] - m[t][y]);
-                            top = fmaxf(top, p[u][t][2 * x + y] * z);
-                        }
+                    for (int t = 0; t < NT; ++t) {
+                        const F2 y = add2(F2(s[u][t][2 * x], s[u][t][2 * x + 1]), F2(-m[t][0], -m[t][1]));
+                        p[u][t][2 * x] = ex2(y.lo());
+                        p[u][t][2 * x + 1] = ex2(y.hi());
+                        most = fmaxf(most, fmaxf(p[u][t][2 * x], p[u][t][2 * x + 1]));
+                    }
+                    top = fmaxf(top, most * z);
                 }
             return top;
         };
@@ -369,7 +368,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                 for (int x = 0; x < 2; ++x)
                     lift[u][x] = fmaxf(log2f(size(u, x)), kLeastScaleLog2);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                float f[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     float top = -INFINITY;
@@ -380,18 +380,39 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                     for (int x = 4; x < 32; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
                     const float to = fmaxf(m[t][y], top - kWeightTop);
-                    const float f = ex2(m[t][y] - to);
+                    f[y] = ex2(m[t][y] - to);
                     m[t][y] = to;
-                    l[t][y] *= f;
-                    ln[t][y] *= f;
 #pragma unroll
                     for (int j = 0; j < KS; ++j) {
-                        o[j][t][y] *= f;
-                        o[j][t][2 + y] *= f;
+                        o[j][t][y] *= f[y];
+                        o[j][t][2 + y] *= f[y];
                     }
                 }
+                l2[t] = mul2(l2[t], F2(f[0], f[1]));
+                ln2[t] = mul2(ln2[t], F2(f[0], f[1]));
+            }
             weigh();
         }
+        // ---- the values' codes, only now: registers that hold them while the scores
+        // are made are missing there (180 us with them before, 166 us so, 64 sequences
+        // of 8192-16384 keys); and the slot to the next copy
+        uint32_t xv[kSub][4][WV];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int key = u * 16 + (k >> 1) * 8 + c * 2 + ((k & 1) ^ swap_c);
+                if (D == 128) {
+                    const uint2 w = lds64(at + S::kCodes + key * (D / 2) + g * 8);
+                    xv[u][k][0] = w.x, xv[u][k][WV - 1] = w.y;
+                } else {
+                    xv[u][k][0] = __float_as_uint(lds32(at + S::kCodes + key * (D / 2) + g * 4));
+                }
+            }
+        }
+        __syncwarp();
+        issue(i + kStages);
+
         // ---- P^T and O^T += V^T P^T
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
@@ -400,12 +421,10 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float p0 = p[u][t][2 * x], p1 = p[u][t][2 * x + 1];
-                    l[t][0] += p0;
-                    l[t][1] += p1;
-                    ln[t][0] = fmaf(p0, vm[u][x], ln[t][0]);
-                    ln[t][1] = fmaf(p1, vm[u][x], ln[t][1]);
-                    pb[t][x] = transpose8(pack_f16(p0 * vs[u][x], p1 * vs[u][x]));
+                    const F2 weight(p[u][t][2 * x], p[u][t][2 * x + 1]), scaled = mul2(weight, F2(vs[u][x], vs[u][x]));
+                    l2[t] = add2(l2[t], weight);
+                    ln2[t] = fma2(weight, F2(vm[u][x], vm[u][x]), ln2[t]);
+                    pb[t][x] = transpose8(pack_f16(scaled.lo(), scaled.hi()));
                 }
 #pragma unroll
             for (int w = 0; w < WV; ++w)
@@ -427,15 +446,16 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
             const int64_t slot = static_cast<int64_t>(pair) + me;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                float l[2] = {l2[t].lo(), l2[t].hi()}, ln[2] = {ln2[t].lo(), ln2[t].hi()};
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) {
-                        l[t][y] += __shfl_xor_sync(0xFFFFFFFFu, l[t][y], x);
-                        ln[t][y] += __shfl_xor_sync(0xFFFFFFFFu, ln[t][y], x);
+                        l[y] += __shfl_xor_sync(0xFFFFFFFFu, l[y], x);
+                        ln[y] += __shfl_xor_sync(0xFFFFFFFFu, ln[y], x);
                     }
                     if (g == 0 && t * 8 + c * 2 + y < rows)
-                        a.part_ml[slot * R + t * 8 + c * 2 + y] = make_float2(m[t][y], l[t][y]);
+                        a.part_ml[slot * R + t * 8 + c * 2 + y] = make_float2(m[t][y], l[y]);
                 }
                 float* dst = a.part_o + (slot * R + t * 8 + c * 2) * D + g * (D / 8);
 #pragma unroll
@@ -444,9 +464,9 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
 #pragma unroll
                         for (int j = 0; j < KS; j += 2)   // values 2j and 2j + 1 of the chunk: rows g and g + 8
                             *reinterpret_cast<float4*>(dst + e * D + 2 * j) =
-                                make_float4(fmaf(o[j][t][e], 0x1p24f, ln[t][e]), fmaf(o[j][t][2 + e], 0x1p20f, ln[t][e]),
-                                            fmaf(o[j + 1][t][e], 0x1p24f, ln[t][e]),
-                                            fmaf(o[j + 1][t][2 + e], 0x1p20f, ln[t][e]));
+                                make_float4(fmaf(o[j][t][e], 0x1p24f, ln[e]), fmaf(o[j][t][2 + e], 0x1p20f, ln[e]),
+                                            fmaf(o[j + 1][t][e], 0x1p24f, ln[e]),
+                                            fmaf(o[j + 1][t][2 + e], 0x1p20f, ln[e]));
                     }
             }
             fresh = true;

@@ -153,6 +153,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t at)
 // Two fp32 operations in one instruction.
 struct F2 {
     uint64_t v;
+    F2() = default;
     __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
     __device__ __forceinline__ explicit F2(uint64_t x) : v(x) {}
     __device__ __forceinline__ float lo() const { return __uint_as_float(static_cast<uint32_t>(v)); }

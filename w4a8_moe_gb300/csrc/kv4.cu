@@ -19,8 +19,9 @@ namespace {
 
 constexpr int kRowThreads = 128;
 
-// A row's keys and values, D of each; D / 16 lanes share it, 16 values of both a
-// lane: 32 bytes of bf16 and 8 bytes of codes, whole sectors for the warp.
+// A row's keys and values, D of each; D / 16 lanes share it, a lane taking 8 values
+// (16 bytes of bf16, 4 of codes) out of each half of both, so that every load and
+// store of a warp covers whole 32-byte sectors.
 struct RowAt {
     int t, h;
     bool live;
@@ -43,40 +44,71 @@ __device__ __forceinline__ RowAt row_at(const Kv8Rows& a, const int32_t* __restr
 // rounded to fp32 each. The quotient is q = d r with r = 1 / s correctly rounded and
 // one correction, q + (d - q s) r, which rounds like the division where nothing
 // under- or overflows (Markstein 1990, as in the FP8 cache's encoder): 2^-60 <= s <
-// 2^60, and |d| <= 15.06 s for every value of the row; differences below 2^-11 s have
-// the code 0 either way. Other rows divide halves, which cannot overflow.
+// 2^60, and 0 <= d <= 15.06 s for every value of a row, as s is at most 2^-8 off;
+// differences below 2^-11 s have the code 0 either way. Such a quotient rounds to 0..15
+// by itself, and added to 1.5 * 2^23 it does so into the sum's lowest bits, where codes
+// are put together by multiplying by 16. Other rows divide halves, which cannot
+// overflow.
 __device__ __forceinline__ uint2 encode_row16(const float (&x)[16], bool finite, float m, float s)
 {
-    uint32_t c[16];
+    uint32_t w[2];
     const bool plain = finite && s >= 8.6736174e-19f && s < 1.1529215e18f && fabsf(m) < 1.1529215e18f;
     if (plain) {
         const float r = __frcp_rn(s);
-        const F2 r2(r, r), s2(-s, -s), m2(-m, -m);
+        const F2 r2(r, r), s2(-s, -s), m2(-m, -m), round2(12582912.0f, 12582912.0f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const F2 d = add2(F2(x[2 * j], x[2 * j + 1]), m2), q = mul2(d, r2);
-            const F2 y = fma2(fma2(q, s2, d), r2, q);
-            c[2 * j] = static_cast<uint32_t>(min(max(__float2int_rn(y.lo()), 0), 15));
-            c[2 * j + 1] = static_cast<uint32_t>(min(max(__float2int_rn(y.hi()), 0), 15));
+        for (int i = 0; i < 2; ++i) {
+            uint32_t sum = 0;
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {
+                const F2 d = add2(F2(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]), m2), q = mul2(d, r2);
+                const F2 y = add2(fma2(fma2(q, s2, d), r2, q), round2);
+                sum = sum * 256 + __float_as_uint(y.hi()) * 16 + __float_as_uint(y.lo());
+            }
+            w[i] = sum - 0x4B400000u * 0x11111111u;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            c[j] = s > 0.0f ? static_cast<uint32_t>(
-                                  min(max(__float2int_rn(__fdiv_rn(0.5f * x[j] - 0.5f * m, 0.5f * s)), 0), 15))
-                            : 0;
-    }
-    uint32_t w[2] = {0, 0};
+        for (int i = 0; i < 2; ++i) {
+            w[i] = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        w[j / 8] |= c[j] << (4 * (j % 8));
+            for (int j = 0; j < 8; ++j) {
+                const float y = __fdiv_rn(0.5f * x[8 * i + j] - 0.5f * m, 0.5f * s);
+                w[i] |= s > 0.0f ? static_cast<uint32_t>(min(max(__float2int_rn(y), 0), 15)) << (4 * j) : 0;
+            }
+        }
+    }
     return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)   // NaN where one of them is
+{
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+}
+// The largest value of a row (high half) and the largest of its negatives (low half),
+// 16 values here and those of the other lanes; NaN where a value is.
+template <int L>
+__device__ __forceinline__ uint32_t bounds(const uint4 (&raw)[2])
+{
+    const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+    uint32_t hi = u[0], lo = u[0] ^ 0x80008000u;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        hi = max_bf16x2(hi, u[i]);
+        lo = max_bf16x2(lo, u[i] ^ 0x80008000u);
+    }
+    uint32_t r = max_bf16x2(prmt(lo, hi, 0x5410), prmt(lo, hi, 0x7632));
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+        r = max_bf16x2(r, __shfl_xor_sync(0xFFFFFFFFu, r, o));
+    return r;
 }
 
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const __grid_constant__ Kv8Rows a,
+__global__ void __launch_bounds__(kRowThreads, 12) kv4_write_kernel(const __grid_constant__ Kv8Rows a,
                                                                 const uint16_t* __restrict__ k,
                                                                 const uint16_t* __restrict__ v,
                                                                 const int32_t* __restrict__ slots,
@@ -95,7 +127,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const __grid_con
         const uint16_t* src = (y ? v + r.t * a.v_stride : k + r.t * a.k_stride) + static_cast<int64_t>(r.h) * D;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            raw[y][i] = r.live ? __ldg(reinterpret_cast<const uint4*>(src) + lane * 2 + i) : make_uint4(0, 0, 0, 0);
+            raw[y][i] = r.live ? __ldg(reinterpret_cast<const uint4*>(src) + i * L + lane) : make_uint4(0, 0, 0, 0);
     }
     const bool ok = r.live && r.slot >= 0 && r.slot < a.num_slots;
     const int64_t at = ok ? cache_row(a.page_shift, a.Hkv, r.slot, r.h) : 0;
@@ -103,29 +135,24 @@ __global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const __grid_con
     for (int y = 0; y < 2; ++y) {
         float x[16];
         unpack16(raw[y], x);
-        // over the finite values; a NaN anywhere leaves the row without numbers
-        float lo = INFINITY, hi = -INFINITY, odd = 0.0f;   // odd: NaN where a value is not finite
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            lo = fminf(lo, x[i]);
-            hi = fmaxf(hi, x[i]);
-            odd += 0.0f * x[i];
-        }
-        const bool finite = odd == 0.0f;
+        const uint32_t ends = bounds<L>(raw[y]);
+        float lo = -__uint_as_float(ends << 16), hi = __uint_as_float(ends & 0xFFFF0000u), odd = 0.0f;
+        const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;   // all of the row
         if (__any_sync(0xFFFFFFFFu, !finite)) {
-            lo = INFINITY, hi = -INFINITY, odd = 0.0f;
+            // over the finite values; a NaN anywhere leaves the row without numbers
+            lo = INFINITY, hi = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (fabsf(x[i]) < INFINITY)
                     lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
                 odd = isnan(x[i]) ? x[i] : odd;
             }
-        }
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-            odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
+            for (int o = L / 2; o > 0; o >>= 1) {
+                lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+                hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+                odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
+            }
         }
         if (hi < lo)   // nothing finite
             lo = hi = 0.0f;
@@ -134,9 +161,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const __grid_con
         if (isnan(odd))
             s_bits = m_bits = 0x7FC0u;
         if (ok) {
-            uint8_t* dst = (y ? v_cache : k_cache) + at * (D / 2);
-            *(reinterpret_cast<uint2*>(dst) + lane) =
-                isnan(odd) ? make_uint2(0, 0) : encode_row16(x, finite, lo, bf16_bits_to_float(s_bits));
+            uint32_t* dst = reinterpret_cast<uint32_t*>((y ? v_cache : k_cache) + at * (D / 2));
+            const uint2 c = isnan(odd) ? make_uint2(0, 0) : encode_row16(x, finite, lo, bf16_bits_to_float(s_bits));
+            dst[lane] = c.x;
+            dst[L + lane] = c.y;
             if (lane == 0)
                 (y ? v_scale : k_scale)[at] = s_bits | (static_cast<uint32_t>(m_bits) << 16);
         }
@@ -159,13 +187,14 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const __grid_cons
     if (!r.live)
         return;
     const int lane = threadIdx.x % L;
-    uint2 raw[2] = {make_uint2(0, 0), make_uint2(0, 0)};
-    uint32_t pair[2] = {0, 0};
+    uint32_t raw[2][2] = {{0, 0}, {0, 0}}, pair[2] = {0, 0};
     if (r.slot >= 0 && r.slot < a.num_slots) {
         const int64_t at = cache_row(a.page_shift, a.Hkv, r.slot, r.h);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            raw[y] = __ldg(reinterpret_cast<const uint2*>((y ? v_cache : k_cache) + at * (D / 2)) + lane);
+            const uint32_t* src = reinterpret_cast<const uint32_t*>((y ? v_cache : k_cache) + at * (D / 2));
+            raw[y][0] = __ldg(src + lane);
+            raw[y][1] = __ldg(src + L + lane);
             pair[y] = __ldg((y ? v_scale : k_scale) + at);
         }
     }
@@ -175,16 +204,18 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const __grid_cons
         uint16_t* dst = (y ? v + r.t * a.v_stride : k + r.t * a.k_stride) + static_cast<int64_t>(r.h) * D;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t w = i ? raw[y].y : raw[y].x;
+            const uint32_t w = raw[y][i];
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float x0 = fmaf(static_cast<float>((w >> (8 * j)) & 15u), s, m);
-                const float x1 = fmaf(static_cast<float>((w >> (8 * j + 4)) & 15u), s, m);
-                o[j] = static_cast<uint32_t>(float_to_bf16_bits(x0)) |
-                       (static_cast<uint32_t>(float_to_bf16_bits(x1)) << 16);
+                // 2^23 + c has c in its lowest bits
+                const F2 c = add2(F2(__uint_as_float(0x4B000000u | ((w >> (8 * j)) & 15u)),
+                                     __uint_as_float(0x4B000000u | ((w >> (8 * j + 4)) & 15u))),
+                                  F2(-8388608.0f, -8388608.0f));
+                const F2 v = fma2(c, F2(s, s), F2(m, m));
+                o[j] = pack_bf16(v.lo(), v.hi());
             }
-            *(reinterpret_cast<uint4*>(dst) + lane * 2 + i) = make_uint4(o[0], o[1], o[2], o[3]);
+            *(reinterpret_cast<uint4*>(dst) + i * L + lane) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }

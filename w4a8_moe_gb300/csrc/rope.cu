@@ -16,15 +16,11 @@ namespace w4a8 {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kMostTokens = 4;   // of a block
 
 __device__ __forceinline__ uint4 pack8(const float* x)
 {
-    uint32_t u[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        u[j] = static_cast<uint32_t>(float_to_bf16_bits(x[2 * j])) |
-               (static_cast<uint32_t>(float_to_bf16_bits(x[2 * j + 1])) << 16);
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
 template <int L>
@@ -55,164 +51,192 @@ __device__ __forceinline__ float row_max(float x)
 // position, modulo 2^64, is the exact fraction of the turn that the position comes
 // to, whatever its size, where an fp32 angle would be off by 2^-24 of all its
 // turns (a tenth of a radian at a position of a million). Its upper 32 bits go
-// through sincospif. That is some 40 instructions a pair, the largest part of a
-// row's arithmetic, so a group of lanes keeps its 8 sines and cosines for several
-// heads of its token.
+// through sincospif. That is some 40 instructions a pair, a third of a row's
+// arithmetic, so a block makes the sines and cosines of its tokens once, in shared
+// memory, while its first rows are on their way.
 template <int L, bool INTER, bool CACHE>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Rope a)
 {
+    constexpr int G = kThreads / L;   // rows at once
+    // [2][D] the norms' weights (queries', keys'), then [tokens][2][rot / 2] cosines, sines
+    extern __shared__ __align__(16) float shared[];
+    float* table = shared + 2 * a.D;
+    __shared__ int64_t slot_of[kMostTokens];
     grid_dep_wait();
-    const int lane = threadIdx.x % L;
-    const int t = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    const int lane = threadIdx.x % L, group = threadIdx.x / L;
+    const int t0 = blockIdx.x * a.tokens, tokens = min(a.tokens, a.T - t0);
     const int n_q = a.Hq, n_k = a.Hq + a.Hkv, n = CACHE ? n_k + a.Hkv : n_k;
-    const int r0 = blockIdx.y * a.slice, r1 = min(r0 + a.slice, n);
-    const bool live = t < a.T && lane * 16 < a.D;
-    const bool turning = live && lane * 16 < a.rot;
+    const int first = blockIdx.y * a.slice, rows = min(a.slice, n - first);   // of each token
+    const bool mine = lane * 16 < a.D, turning = lane * 16 < a.rot;
     // the lane's two runs of 8 values
     const int at0 = !INTER && turning ? lane * 8 : lane * 16;
     const int at1 = !INTER && turning ? lane * 8 + a.rot / 2 : lane * 16 + 8;
 
-    auto load = [&](int r, uint4(&raw)[2]) {
-        raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-        if (live && r < r1) {
+    // the group's next row: token (of the block's; from `tokens` on there is none) and r
+    int next_token = 0, next_r = group;
+    uint4 next[2];
+    auto fetch = [&]() {
+        while (next_r >= rows) {
+            next_r -= rows;
+            ++next_token;
+        }
+        next[0] = next[1] = make_uint4(0, 0, 0, 0);
+        if (mine && next_token < tokens) {
+            const int r = first + next_r;
+            const int64_t t = t0 + next_token;
             const uint16_t* src = r < n_q   ? a.q + t * a.q_stride + static_cast<int64_t>(r) * a.D
                                   : r < n_k ? a.k + t * a.k_stride + static_cast<int64_t>(r - n_q) * a.D
                                             : a.v + t * a.v_stride + static_cast<int64_t>(r - n_k) * a.D;
-            raw[0] = *reinterpret_cast<const uint4*>(src + at0);
-            raw[1] = *reinterpret_cast<const uint4*>(src + at1);
+            next[0] = *reinterpret_cast<const uint4*>(src + at0);
+            next[1] = *reinterpret_cast<const uint4*>(src + at1);
         }
     };
-    uint4 next[2];
-    load(r0, next);
+    fetch();
 
-    int64_t slot = -1;
-    if (CACHE && t < a.T)
-        slot = __ldg(a.slots + t);
-    float cs[8], sn[8];
-    if (r0 < n_k && turning) {
-        const int64_t pos = __ldg(a.positions + t);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const ulonglong2 f = __ldg(reinterpret_cast<const ulonglong2*>(a.turns + lane * 8 + j));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint64_t turn = static_cast<uint64_t>(pos) * (e ? f.y : f.x);
-                sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[j + e], &cs[j + e]);
-                sn[j + e] *= a.magnitude;
-                cs[j + e] *= a.magnitude;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            cs[j] = 1.0f, sn[j] = 0.0f;
+    const int half = a.rot / 2;
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int token = i / half, j = i - token * half;
+        const int64_t pos = __ldg(a.positions + t0 + token);
+        const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(a.turns + j);
+        float s, c;
+        sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
+        table[token * a.rot + j] = c * a.magnitude;
+        table[token * a.rot + half + j] = s * a.magnitude;
     }
+    const bool norms = a.q_weight || a.k_weight;
+    if (norms)
+        for (int i = threadIdx.x; i < a.D; i += kThreads) {
+            shared[i] = a.q_weight ? bf16_bits_to_float(__ldg(a.q_weight + i)) : 1.0f;
+            shared[a.D + i] = a.k_weight ? bf16_bits_to_float(__ldg(a.k_weight + i)) : 1.0f;
+        }
+    if (CACHE && threadIdx.x < tokens)
+        slot_of[threadIdx.x] = __ldg(a.slots + t0 + threadIdx.x);
+    __syncthreads();
 
-    const uint16_t* weight_of = nullptr;
-    float w[16];
-    for (int r = r0; r < r1; ++r) {
+    for (int left = tokens * rows; left > 0; left -= G) {
         float x[16];
         unpack16(next, x);
-        load(r + 1, next);
-        const uint16_t* weight = r < n_q ? a.q_weight : r < n_k ? a.k_weight : nullptr;
-        if (weight) {
-            if (weight != weight_of) {
-                weight_of = weight;
-                uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (live) {
-                    raw[0] = __ldg(reinterpret_cast<const uint4*>(weight + at0));
-                    raw[1] = __ldg(reinterpret_cast<const uint4*>(weight + at1));
+        const int token = next_token, r = first + next_r;
+        const bool there = token < tokens, live = mine && there;
+        next_r += G;
+        fetch();
+        if (norms) {
+            F2 sum2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+                sum2 = fma2(F2(x[j], x[j + 1]), F2(x[j], x[j + 1]), sum2);
+            const float sum = row_sum<L>(sum2.lo() + sum2.hi());
+            if (live && (r < n_q ? a.q_weight : r < n_k ? a.k_weight : nullptr)) {
+                const float f = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+                const float* w = shared + (r < n_q ? 0 : a.D);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 w4 = *reinterpret_cast<const float4*>(w + (j < 8 ? at0 + j : at1 + j - 8));
+                    const F2 y0 = mul2(mul2(F2(x[j], x[j + 1]), F2(f, f)), F2(w4.x, w4.y));
+                    const F2 y1 = mul2(mul2(F2(x[j + 2], x[j + 3]), F2(f, f)), F2(w4.z, w4.w));
+                    x[j] = y0.lo(), x[j + 1] = y0.hi(), x[j + 2] = y1.lo(), x[j + 3] = y1.hi();
                 }
-                unpack16(raw, w);
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                sum = fmaf(x[i], x[i], sum);
-            sum = row_sum<L>(sum);
-            const float f = rsqrtf(sum / static_cast<float>(a.D) + a.eps);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                x[i] = x[i] * f * w[i];
-        }
-        if (turning && r < n_k) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i0 = INTER ? 2 * j : j, i1 = INTER ? 2 * j + 1 : j + 8;
-                const float lo = x[i0], hi = x[i1];
-                x[i0] = fmaf(lo, cs[j], -hi * sn[j]);
-                x[i1] = fmaf(hi, cs[j], lo * sn[j]);
             }
         }
-        if (!CACHE || r < n_q) {
-            if (live) {
-                uint16_t* dst = r < n_q ? a.q_out + t * a.q_out_stride + static_cast<int64_t>(r) * a.D
-                                        : a.k_out + t * a.k_out_stride + static_cast<int64_t>(r - n_q) * a.D;
-                *reinterpret_cast<uint4*>(dst + at0) = pack8(x);
-                *reinterpret_cast<uint4*>(dst + at1) = pack8(x + 8);
+        if (turning && r < n_k && there) {
+            const float* cosines = table + token * a.rot + lane * 8;
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {   // four pairs
+                const float4 c4 = *reinterpret_cast<const float4*>(cosines + j);
+                const float4 s4 = *reinterpret_cast<const float4*>(cosines + half + j);
+                const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+                if (INTER) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float lo = x[2 * (j + i)], hi = x[2 * (j + i) + 1];
+                        x[2 * (j + i)] = fmaf(lo, c[i], -hi * s[i]);
+                        x[2 * (j + i) + 1] = fmaf(hi, c[i], lo * s[i]);
+                    }
+                } else {   // (the pairs' first values are neighbours, and their second ones)
+#pragma unroll
+                    for (int i = j; i < j + 4; i += 2) {
+                        const F2 lo(x[i], x[i + 1]), hi(x[8 + i], x[9 + i]);
+                        const F2 cc(c[i - j], c[i - j + 1]), ss(s[i - j], s[i - j + 1]);
+                        const F2 y0 = fma2(mul2(hi, ss), F2(-1.0f, -1.0f), mul2(lo, cc)), y1 = fma2(lo, ss, mul2(hi, cc));
+                        x[i] = y0.lo(), x[i + 1] = y0.hi(), x[8 + i] = y1.lo(), x[9 + i] = y1.hi();
+                    }
+                }
             }
+        }
+        if (live && (!CACHE || r < n_q)) {
+            const int64_t t = t0 + token;
+            uint16_t* dst = r < n_q ? a.q_out + t * a.q_out_stride + static_cast<int64_t>(r) * a.D
+                                    : a.k_out + t * a.k_out_stride + static_cast<int64_t>(r - n_q) * a.D;
+            *reinterpret_cast<uint4*>(dst + at0) = pack8(x);
+            *reinterpret_cast<uint4*>(dst + at1) = pack8(x + 8);
+        }
+        if (!CACHE || !__any_sync(0xFFFFFFFFu, r >= n_q))
             continue;
-        }
         // ---- into the cache, as kv8_write does with bf16 rows
-        const bool is_k = r < n_k;
-        const int h = is_k ? r - n_q : r - n_k;
-        const bool ok = live && slot >= 0 && slot < a.num_slots;
-        const int64_t row = ok ? cache_row(a.page_shift, a.Hkv, slot, h) : 0;
-        float* scale = is_k ? a.k_scale : a.v_scale;
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            top = fmaxf(top, fabsf(x[i]));   // (passes over NaN)
-        float s;
+        for (int j = 0; j < 16; ++j)
+            top = fmaxf(top, fabsf(x[j]));   // (passes over NaN)
+        float finite = 0.0f;
         if (a.per_token) {
             top = row_max<L>(top);
-            float finite = top;
+            finite = top;
             if (__any_sync(0xFFFFFFFFu, top > 3.4028235e38f)) {
                 finite = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    finite = fmaxf(finite, fabsf(x[i]) <= 3.4028235e38f ? fabsf(x[i]) : 0.0f);
+                for (int j = 0; j < 16; ++j)
+                    finite = fmaxf(finite, fabsf(x[j]) <= 3.4028235e38f ? fabsf(x[j]) : 0.0f);
                 finite = row_max<L>(finite);
             }
-            s = fmaxf(__fdiv_rn(finite, 448.0f), a.min_scale);
-            s = s == 0.0f ? 1.0f : s;
-        } else {
-            s = __ldg(scale + h);
         }
-        if (ok) {
+        const int64_t slot = live ? slot_of[token] : -1;
+        if (r >= n_q && slot >= 0 && slot < a.num_slots) {
+            const bool is_k = r < n_k;
+            const int h = is_k ? r - n_q : r - n_k;
+            const int64_t at = cache_row(a.page_shift, a.Hkv, slot, h);
+            float* scale = is_k ? a.k_scale : a.v_scale;
+            float s;
+            if (a.per_token) {
+                s = fmaxf(__fdiv_rn(finite, 448.0f), a.min_scale);
+                s = s == 0.0f ? 1.0f : s;
+                if (lane == 0)
+                    scale[at] = s;
+            } else {
+                s = __ldg(scale + h);
+            }
             uint2 c[2];
             encode16(x, top, s, c);
-            uint8_t* dst = (is_k ? a.k_cache : a.v_cache) + row * a.D;
+            uint8_t* dst = (is_k ? a.k_cache : a.v_cache) + at * a.D;
             *reinterpret_cast<uint2*>(dst + at0) = c[0];
             *reinterpret_cast<uint2*>(dst + at1) = c[1];
-            if (a.per_token && lane == 0)
-                scale[row] = s;
         }
     }
 }
 
 template <int L, bool CACHE>
-static cudaError_t launch(const Rope& a, cudaStream_t s)
+static cudaError_t launch(Rope a, int num_sms, cudaStream_t s)
 {
-    const int rows = a.Hq + (CACHE ? 2 : 1) * a.Hkv, tokens = kThreads / L;
-    const dim3 grid((a.T + tokens - 1) / tokens, (rows + a.slice - 1) / a.slice);
+    constexpr int G = kThreads / L;
+    a.inv_d = 1.0f / static_cast<float>(a.D);
+    const int rows = a.Hq + (CACHE ? 2 : 1) * a.Hkv;
+    // A block for one token, or for several where they are many (angles are made once
+    // a block and 16 blocks an SM keep it busy); few tokens are spread over the SMs by
+    // their rows.
+    const int64_t passes = static_cast<int64_t>(a.T) * ((rows + G - 1) / G), each = static_cast<int64_t>(num_sms) * 16;
+    a.tokens = static_cast<int>(min(max(passes / each, int64_t{1}), int64_t{kMostTokens}));
+    a.slice = passes < each ? G : rows;
+    const dim3 grid((a.T + a.tokens - 1) / a.tokens, (rows + a.slice - 1) / a.slice);
     return launch_dependent(a.interleaved ? rope_kernel<L, true, CACHE> : rope_kernel<L, false, CACHE>, grid,
-                            dim3(kThreads), 0, s, a);
+                            dim3(kThreads), (2 * a.D + a.tokens * a.rot) * static_cast<int>(sizeof(float)), s, a);
 }
 
-cudaError_t launch_rope(Rope a, bool to_cache, int num_sms, cudaStream_t s)
+cudaError_t launch_rope(const Rope& a, bool to_cache, int num_sms, cudaStream_t s)
 {
-    const int L = a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
-    const int64_t rows = a.Hq + (to_cache ? 2 : 1) * a.Hkv;
-    // rows that a group of lanes takes: one until the GPU is full of groups, then up to 8
-    const int64_t lanes = rows * a.T * L;
-    a.slice = static_cast<int>(min(max(lanes / (static_cast<int64_t>(num_sms) * 1024), int64_t{1}), int64_t{8}));
-    a.slice = static_cast<int>(rows / max(rows / a.slice, int64_t{1}));
-    if ((rows + a.slice - 1) / a.slice > 65535)
-        a.slice = static_cast<int>((rows + 65534) / 65535);
     if (to_cache)
-        return L == 4 ? launch<4, true>(a, s) : launch<8, true>(a, s);
-    return L == 4 ? launch<4, false>(a, s) : L == 8 ? launch<8, false>(a, s) : launch<16, false>(a, s);
+        return a.D <= 64 ? launch<4, true>(a, num_sms, s) : launch<8, true>(a, num_sms, s);
+    return a.D <= 64    ? launch<4, false>(a, num_sms, s)
+           : a.D <= 128 ? launch<8, false>(a, num_sms, s)
+                        : launch<16, false>(a, num_sms, s);
 }
 
 }  // namespace w4a8

@@ -21,7 +21,7 @@ struct Rope {
     int interleaved;
     const uint16_t* q_weight;   // bf16 [D], null: no norm
     const uint16_t* k_weight;
-    float eps;
+    float eps, inv_d;   // 1 / D
     uint16_t* q_out;
     uint16_t* k_out;   // null where a cache is written
     int64_t q_out_stride, k_out_stride;
@@ -33,9 +33,9 @@ struct Rope {
     float* v_scale;
     int num_slots, page_shift, per_token;
     float min_scale;
-    int slice;   // rows (heads of one token) that a group of lanes takes one after another
+    int tokens, slice;   // tokens of a block, rows (heads) of each
 };
 // Where `to_cache` is set the keys and values go into the cache, else the keys to k_out.
-cudaError_t launch_rope(Rope a, bool to_cache, int num_sms, cudaStream_t s);
+cudaError_t launch_rope(const Rope& a, bool to_cache, int num_sms, cudaStream_t s);
 
 }  // namespace w4a8

@@ -692,15 +692,15 @@ def kv8_norm_rope_write(q, k, v, positions, slots, rope: RopeTable, k_cache, v_c
 
 
 # ---- page tables
-def _table(page_table, rows):
-    """(row stride, pages of a row) of an int32 [rows or any number, max pages] table whose rows may lie apart."""
+def _table(page_table):
+    """(rows, pages of a row, row stride) of an int32 [sequences, max pages] table whose rows may lie apart."""
     if page_table.dtype is not _I32 or page_table.dim() != 2:
         raise ValueError("page_table must be int32 [sequences, max pages]")
     have, most = page_table.shape
     row, one = page_table.stride()
-    if (rows is not None and have != rows) or (one != 1 and most > 1):
+    if one != 1 and most > 1:
         raise ValueError("page_table must be int32 [sequences, max pages], each sequence's pages contiguous")
-    return (row if have > 1 else most), most
+    return have, most, (row if have > 1 else most)
 
 
 def _vectors(n, **vectors):
@@ -709,14 +709,21 @@ def _vectors(n, **vectors):
             raise ValueError(f"{what} must be a contiguous int32 vector [{n}]")
 
 
-def _pages_device(ws, *tensors):
+def _pool_refused(B, lens, other, what, have, free_pages, free_count, ws):
+    if lens.dtype is not _I32 or lens.dim() != 1 or not lens.is_contiguous():
+        return _vector_refused("lens")
+    if free_pages.dtype is not _I32 or free_pages.dim() != 1 or not free_pages.is_contiguous():
+        return _vector_refused("free_pages")
+    if have != B:
+        return ValueError("page_table must have a row for each sequence")
     if not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    device = ws.get_device()
-    if device < 0 or any(t.get_device() != device for t in tensors) \
-            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
-        raise _devices_refused(ws, *tensors)
-    return device
+        return ValueError("ws must be contiguous")
+    try:
+        _vectors(B, **{what: other})
+        _vectors(1, free_count=free_count)
+    except ValueError as e:
+        return e
+    return None
 
 
 def kv_pages_extend(lens, new_lens, page_table, free_pages, free_count, page_size: int, capacity: int, out: PageStep = None,
@@ -726,31 +733,43 @@ def kv_pages_extend(lens, new_lens, page_table, free_pages, free_count, page_siz
     PageStep(starts [B + 1], and for up to `capacity` tokens seqs, positions, seen and slots, lens [B]); padding tokens
     have the slot -1. A sequence that cannot have all of its pages gets none (see kv_pages_extend in
     include/w4a8_moe.h). out.lens may be lens."""
-    if lens.dim() != 1 or free_pages.dim() != 1:
-        raise _vector_refused("lens and free_pages each")
-    B = lens.shape[0]
-    row, most = _table(page_table, B)
-    num_pages = free_pages.shape[0]
-    _vectors(B, lens=lens, new_lens=new_lens)
-    _vectors(num_pages, free_pages=free_pages)
-    _vectors(1, free_count=free_count)
-    capacity = int(capacity)
-    if out is None or ws is None:
+    B, capacity = lens.numel(), int(capacity)
+    n = (B,)
+    have, most, row = _table(page_table)
+    if ws is None:
         with _on(stream):
-            if out is None:
-                c = max(capacity, 0)
-                out = PageStep(*torch.empty(2 * B + 1 + 4 * c, dtype=_I32, device=lens.device).split([B + 1, c, c, c, c, B]))
-            ws = ws if ws is not None else _ws(256, lens.device)
-    starts, seqs, positions, seen, slots, lens_out = out
-    _vectors(B + 1, starts=starts)
-    _vectors(capacity, seqs=seqs, positions=positions, seen=seen, slots=slots)
-    _vectors(B, lens_out=lens_out)
-    device = _pages_device(ws, lens, new_lens, page_table, free_pages, free_count, *out)
+            ws = _ws(256, lens.device)
+    if lens.dtype is not _I32 or lens.shape != n or not lens.is_contiguous() or new_lens.dtype is not _I32 \
+            or new_lens.shape != n or not new_lens.is_contiguous() or have != B or free_pages.dtype is not _I32 \
+            or free_pages.dim() != 1 or not free_pages.is_contiguous() or free_count.dtype is not _I32 \
+            or free_count.shape != (1,) or not ws.is_contiguous():
+        raise _pool_refused(B, lens, new_lens, "new_lens", have, free_pages, free_count, ws)
+    device = lens.get_device()
+    if device < 0 or not (device == new_lens.get_device() == page_table.get_device() == free_pages.get_device()
+                          == free_count.get_device() == ws.get_device()) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(lens, new_lens, page_table, free_pages, free_count, ws)
     to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
+    if out is None:
+        if capacity < 0:
+            raise ValueError("capacity must be positive")
+        with _on(stream):
+            buf = torch.empty(2 * B + 1 + 4 * capacity, dtype=_I32, device=lens.device)
+        out = PageStep(*buf.split_with_sizes((B + 1, capacity, capacity, capacity, capacity, B)))
+        at, step = buf.data_ptr(), 4 * capacity
+        tokens = at + 4 * (B + 1)
+        to = at, tokens, tokens + step, tokens + 2 * step, tokens + 3 * step, tokens + 4 * step
+    else:
+        starts, seqs, positions, seen, slots, lens_out = out
+        _vectors(B + 1, starts=starts)
+        _vectors(capacity, seqs=seqs, positions=positions, seen=seen, slots=slots)
+        _vectors(B, lens_out=lens_out)
+        if not all(t.get_device() == device for t in out):
+            raise _devices_refused(lens, *out)
+        to = [t.data_ptr() for t in out]
     status = (_lib or _load()).kv_pages_extend(
         lens.data_ptr(), new_lens.data_ptr(), B, page_table.data_ptr(), row, most, int(page_size), free_pages.data_ptr(),
-        free_count.data_ptr(), num_pages, capacity, starts.data_ptr(), seqs.data_ptr(), positions.data_ptr(),
-        seen.data_ptr(), slots.data_ptr(), lens_out.data_ptr(), ws.data_ptr(), ws.nbytes, to_stream)
+        free_count.data_ptr(), free_pages.numel(), capacity, *to, ws.data_ptr(), ws.nbytes, to_stream)
     if status:
         _check(status)
     return out
@@ -759,23 +778,29 @@ def kv_pages_extend(lens, new_lens, page_table, free_pages, free_count, page_siz
 def kv_pages_truncate(lens, keep_lens, page_table, free_pages, free_count, page_size: int, out=None, ws=None, stream=None):
     """Gives the pages behind each sequence's first keep_lens [B] of lens [B] tokens back to the stack (0: the sequence is
     finished). Returns the lengths now, [B] (out, which may be lens or keep_lens)."""
-    if lens.dim() != 1 or free_pages.dim() != 1:
-        raise _vector_refused("lens and free_pages each")
-    B = lens.shape[0]
-    row, most = _table(page_table, B)
-    num_pages = free_pages.shape[0]
+    B = lens.numel()
+    n = (B,)
+    have, most, row = _table(page_table)
     if out is None or ws is None:
         with _on(stream):
             out = out if out is not None else torch.empty(B, dtype=_I32, device=lens.device)
             ws = ws if ws is not None else _ws(256, lens.device)
-    _vectors(B, lens=lens, keep_lens=keep_lens, out=out)
-    _vectors(num_pages, free_pages=free_pages)
-    _vectors(1, free_count=free_count)
-    device = _pages_device(ws, lens, keep_lens, page_table, free_pages, free_count, out)
+    if lens.dtype is not _I32 or lens.shape != n or not lens.is_contiguous() or keep_lens.dtype is not _I32 \
+            or keep_lens.shape != n or not keep_lens.is_contiguous() or have != B or free_pages.dtype is not _I32 \
+            or free_pages.dim() != 1 or not free_pages.is_contiguous() or free_count.dtype is not _I32 \
+            or free_count.shape != (1,) or not ws.is_contiguous():
+        raise _pool_refused(B, lens, keep_lens, "keep_lens", have, free_pages, free_count, ws)
+    if out.dtype is not _I32 or out.shape != n or not out.is_contiguous():
+        raise _vector_refused("out")
+    device = lens.get_device()
+    if device < 0 or not (device == keep_lens.get_device() == page_table.get_device() == free_pages.get_device()
+                          == free_count.get_device() == ws.get_device() == out.get_device()) \
+            or ((_gpus or _count_gpus()) != 1 and device != _current_device()):
+        raise _devices_refused(lens, keep_lens, page_table, free_pages, free_count, ws, out)
     to_stream = _raw_stream(device) if stream is None else _handle(stream, device)
     status = (_lib or _load()).kv_pages_truncate(
         lens.data_ptr(), keep_lens.data_ptr(), B, page_table.data_ptr(), row, most, int(page_size), free_pages.data_ptr(),
-        free_count.data_ptr(), num_pages, out.data_ptr(), ws.data_ptr(), ws.nbytes, to_stream)
+        free_count.data_ptr(), free_pages.numel(), out.data_ptr(), ws.data_ptr(), ws.nbytes, to_stream)
     if status:
         _check(status)
     return out
@@ -858,8 +883,7 @@ def kv4_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, seqs=
         raise ValueError("q must be bf16 [T, query heads, D of the cache]")
     T, hq, _ = q_shape
     q_stride = _row_stride(q, T, hq, d, "q")
-    row, most = _table(page_table, None)
-    have = page_table.shape[0]
+    have, most, row = _table(page_table)
     if lens.dtype is not _I32 or lens.shape != (T,) or not lens.is_contiguous():
         raise _vector_refused("lens [T]")
     if seqs is None:

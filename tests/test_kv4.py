@@ -294,10 +294,53 @@ def test_attention_several_tokens_of_a_sequence(lib, hq, hkv, d, page, drafts):
     assert bool((out[empty] == 0).all()) and bool((lse[empty] == -torch.inf).all())
 
 
+@pytest.mark.parametrize("hq,hkv,d,page", [(8, 8, 64, 32), (12, 4, 128, 16), (32, 8, 128, 64), (16, 4, 64, 16), (48, 8, 64, 16),
+                                           (14, 2, 128, 32), (8, 1, 128, 16), (18, 2, 64, 64)])
+def test_attention_runs_of_tokens(lib, hq, hkv, d, page):
+    """Runs of neighbours of one sequence, of every length: shorter and longer than what a tile of rows holds, the same
+    sequence in several runs, lengths in any order within a run, tokens without keys inside one; few and many sequences."""
+    for rows, seed in ((6, 0), (60, 1)):
+        b = Batch([(53 * i) % 400 + 20 for i in range(rows)], hq, hkv, d, page, seed=seed + hq)
+        full = b.lens_list
+        rng = np.random.default_rng(seed)
+        seqs, lens = [], []
+        for run in (1, 2, 3, 5, 8, 16, 17, 33, 1, 2, 4):
+            i = int(rng.integers(0, min(rows, 6)))
+            seqs += [i] * run
+            some = full[i] - np.arange(run)[::-1] if run % 2 else rng.integers(0, full[i] + 1, run)
+            lens += [max(int(n), 0) for n in some]
+        b.seqs_list, b.lens_list = seqs, lens
+        b.seqs = torch.tensor(seqs, dtype=torch.int32, device="cuda")
+        b.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        b.q = (torch.randn(len(seqs), hq, d, generator=gen, device="cuda") * 1.5).to(torch.bfloat16)
+        b.check(*b.run(lib))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (6, 1, 128), (8, 2, 128)])
+def test_attention_a_token_does_not_see_what_is_behind_it(lib, hq, hkv, d):
+    """Keys and values that are no numbers, behind a token's last key but before its neighbour's, leave it as it was."""
+    b = Batch([100, 70, 33], hq, hkv, d, 16, seed=41, drafts=4)
+    clean = b.run(lib)
+    for which in ("ks", "vs"):
+        for bad in (float("nan"), float("inf")):
+            keep = getattr(b, which).clone()
+            for i, n in enumerate((100, 70, 33)):   # the last draft's own key
+                getattr(b, which)[int(b.table[i, (n - 1) // 16]), :, (n - 1) % 16] = bad
+            out, lse = b.run(lib)
+            last = torch.arange(12) % 4 == 3
+            assert torch.equal(out[~last], clean[0][~last]) and torch.equal(lse[~last], clean[1][~last])
+            if bad != bad:   # (a score of minus infinity is a weight of zero)
+                assert bool(torch.isnan(out[last]).any(-1).all())
+            getattr(b, which).copy_(keep)
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (3, 1, 128)])
 def test_attention_largest_batch(lib, hq, hkv, d):
     """4096 tokens, the most a call takes (every 37th checked)."""
     b = Batch([(i * 7) % 70 for i in range(4096)], hq, hkv, d, 16, seed=20)
+    b.check(*b.run(lib), every=37)
+    b = Batch([(i * 7) % 70 for i in range(1024)], hq, hkv, d, 16, seed=20, drafts=4)
     b.check(*b.run(lib), every=37)
 
 

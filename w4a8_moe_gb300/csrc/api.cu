@@ -301,6 +301,24 @@ static bool rope_values_ok(float magnitude, int interleaved, float eps)
     return std::isfinite(magnitude) && (interleaved == 0 || interleaved == 1) && std::isfinite(eps) && eps >= 0.0f;
 }
 
+// ---- 4-bit cache
+struct Kv4Ws {
+    float* part_o;
+    float2* part_ml;
+    int *cum, *lead;
+};
+static size_t kv4_ws(int T, int Hq, int Hkv, int D, Kv4Ws* w, void* ws)
+{
+    Carver c(ws);
+    const int group = Hq / Hkv, R = kv8_attn_row_tile(group);
+    const size_t rows = (static_cast<size_t>(T) * Hkv * ((group + R - 1) / R) + kKv8MaxWarps) * R;
+    w->part_o = c.take<float>(rows * D * 4);
+    w->part_ml = c.take<float2>(rows * 8);
+    w->cum = c.take<int>((static_cast<size_t>(T) + 1) * 4);
+    w->lead = c.take<int>(static_cast<size_t>(T) * 4);
+    return c.off;
+}
+
 // ---- page tables
 static bool pages_ok(int B, int64_t table_stride, int max_pages, int page_size, int num_pages)
 {
@@ -1070,7 +1088,10 @@ int kv4_read(const uint8_t* k_cache, const uint8_t* v_cache, const uint16_t* k_s
 
 size_t kv4_attention_workspace_size(int T, int Hq, int Hkv, int D, int max_pages, int page_size)
 {
-    return kv8_prefix_attention_workspace_size(T, Hq, Hkv, D, 0, max_pages, page_size);
+    if (!kv8_attn_ok(T, Hq, Hkv, D, 0, max_pages, page_size))
+        return 0;
+    Kv4Ws w;
+    return kv4_ws(T, Hq, Hkv, D, &w, nullptr);
 }
 
 int kv4_attention(const uint16_t* q_bf16, int64_t q_stride, int T, int Hq, int Hkv, int D, const uint8_t* k_cache,
@@ -1092,8 +1113,8 @@ int kv4_attention(const uint16_t* q_bf16, int64_t q_stride, int T, int Hq, int H
             return W4A8_ERR_ALIGN;
     if (!aligned4(page_table) || !aligned4(seqs) || !aligned4(lens) || !aligned4(lse))
         return W4A8_ERR_ALIGN;
-    Kv8Ws w;
-    if (!ws || ws_bytes < kv8_ws(T, Hq, Hkv, D, 0, &w, ws))
+    Kv4Ws w;
+    if (!ws || ws_bytes < kv4_ws(T, Hq, Hkv, D, &w, ws))
         return W4A8_ERR_WORKSPACE;
     if (!aligned16(ws))
         return W4A8_ERR_ALIGN;
@@ -1109,7 +1130,7 @@ int kv4_attention(const uint16_t* q_bf16, int64_t q_stride, int T, int Hq, int H
     a.page_table = page_table, a.table_stride = table_stride, a.max_pages = max_pages, a.lens = lens;
     a.seqs = seqs, a.num_seqs = num_seqs;
     a.sm_scale = sm_scale, a.cap = logit_cap;
-    a.tiles = w.tiles, a.part_o = w.part_o, a.part_ml = w.part_ml, a.cum = w.cum;
+    a.part_o = w.part_o, a.part_ml = w.part_ml, a.cum = w.cum, a.lead = w.lead;
     a.err = static_cast<uint32_t*>(ws);
     a.out = out_bf16, a.lse = lse;
     return launch_kv4_attn(a, D, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK : W4A8_ERR_LAUNCH;

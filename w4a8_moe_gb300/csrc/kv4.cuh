@@ -22,6 +22,7 @@ cudaError_t launch_kv4_read(const Kv8Rows& a, const uint8_t* k_cache, const uint
 struct Kv4Attn : Kv8Attn {
     const int32_t* seqs;
     int num_seqs;
+    int per_tile;   // tokens of a sequence that a tile of rows holds
 };
 cudaError_t launch_kv4_attn(const Kv4Attn& a, int D, int num_sms, cudaStream_t s);
 

@@ -26,10 +26,12 @@ constexpr int kSub = kUnit / 16;         // of them in one product
 constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
 
 // A unit as its warp meets it, found by one lane for each of 32 units ahead.
-struct __align__(8) Unit {
+struct __align__(16) Unit {
     int64_t row[2];   // cache rows (page, head, offset) of its first and its seventeenth key
     int pair;
-    int live_last;    // keys that exist (1..32), and 256 where the pair ends
+    int live_last;    // keys that exist (1..32), 256 where the pair ends, 512 where a token does not see all of them
+    int key0;
+    int tokens;       // that the pair's rows belong to
 };
 
 template <int D>
@@ -53,6 +55,75 @@ __device__ __forceinline__ int64_t page_row(const Kv4Attn& a, const int32_t* pag
     return cache_row(a.page_shift, a.Hkv, (static_cast<int64_t>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1)),
                      h);
 }
+// Several tokens of a sequence share a tile of rows where they are neighbours in the
+// batch: each run of tokens with one sequence is cut into tiles of up to per_tile
+// tokens, and the first of a tile stands for it in the line. Prefix sums of the tiles'
+// units as sum_units has them (0 for the others), and, from block 0, whose tile each
+// token is in.
+template <int WARPS>
+__device__ __forceinline__ int sum_tiles(const Kv4Attn& a, int* cum, int* warp_sum)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ int warp_start[WARPS];
+    int carry = 0, carry_start = 0;
+    for (int b0 = 0; b0 < a.B; b0 += WARPS * 32) {
+        const int b = b0 + tid;
+        const int seq = b < a.B ? __ldg(a.seqs + b) : 0;
+        // where the token's run starts: the last boundary up to it
+        int start = b < a.B && (b == 0 || __ldg(a.seqs + b - 1) != seq) ? b : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+            start = max(start, __shfl_up_sync(0xFFFFFFFFu, start, min(o, lane)));
+        if (lane == 31)
+            warp_start[warp] = start;
+        __syncthreads();
+        start = max(start, carry_start);
+        for (int w = 0; w < warp; ++w)
+            start = max(start, warp_start[w]);
+        for (int w = 0; w < WARPS; ++w)
+            carry_start = max(carry_start, warp_start[w]);
+        const int in_tile = (b - start) % a.per_tile;
+        int n = 0;
+        if (b < a.B) {
+            if (blockIdx.x == 0) {
+                a.lead[b] = b - in_tile;
+                if (static_cast<unsigned>(__ldg(a.lens + b)) > static_cast<unsigned>(a.max_pages << a.page_shift))
+                    set_error(a.err, kErrBitIndex);
+            }
+            if (in_tile == 0)
+                for (int j = 0; j < a.per_tile && b + j < a.B && __ldg(a.seqs + b + j) == seq; ++j)
+                    n = max(n, seq_units(a, b + j));
+        }
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            s += lane >= o ? t : 0;
+        }
+        if (lane == 31)
+            warp_sum[warp] = s;
+        __syncthreads();
+        int base = carry;
+        for (int w = 0; w < warp; ++w)
+            base += warp_sum[w];
+        if (b < a.B) {
+            cum[b] = base + s - n;
+            if (blockIdx.x == 0)
+                a.cum[b] = base + s - n;
+        }
+        for (int w = 0; w < WARPS; ++w)
+            carry += warp_sum[w];
+        __syncthreads();
+    }
+    if (tid == 0) {
+        cum[a.B] = carry;
+        if (blockIdx.x == 0)
+            a.cum[a.B] = carry;
+    }
+    return carry;
+}
+
+template <bool MULTI>
 __device__ __forceinline__ Unit find_unit(const Kv4Attn& a, const Line& line, const int* cum, int64_t u)
 {
     int lo = 0, hi = a.B;   // the last b with cum[b] * hr <= u
@@ -81,14 +152,22 @@ __device__ __forceinline__ Unit find_unit(const Kv4Attn& a, const Line& line, co
             seq = 0;
         }
     }
-    const int h = j / a.tiles, key0 = k << kUnitShift, len = seq_len(a, lo);
+    const int h = j / a.tiles, key0 = k << kUnitShift;
     const int32_t* pages = a.page_table + seq * a.table_stride;
     Unit x;
+    x.key0 = key0;
+    x.tokens = 1;
+    int len = seq_len(a, lo), least = len;
+    if (MULTI)
+        for (; x.tokens < a.per_tile && lo + x.tokens < a.B && __ldg(a.seqs + lo + x.tokens) == __ldg(a.seqs + lo); ++x.tokens) {
+            const int other = seq_len(a, lo + x.tokens);
+            len = max(len, other), least = min(least, other);
+        }
     x.pair = lo * line.hr + j;
     x.row[0] = page_row(a, pages, h, key0);
     // a page of 16 ends inside the unit, and the next may not exist
     x.row[1] = a.page_shift >= kUnitShift ? x.row[0] + 16 : len - key0 > 16 ? page_row(a, pages, h, key0 + 16) : x.row[0];
-    x.live_last = min(len - key0, kUnit) | (k == static_cast<int>(n) - 1 ? 256 : 0);
+    x.live_last = min(len - key0, kUnit) | (k == static_cast<int>(n) - 1 ? 256 : 0) | (least - key0 < kUnit ? 512 : 0);
     return x;
 }
 
@@ -107,7 +186,7 @@ __device__ __forceinline__ Unit find_unit(const Kv4Attn& a, const Line& line, co
 // their D codes, and of V's keys 2c, 2c + 1, 2c + 8, 2c + 9 (the pairs of an operand
 // register), chunk g. Two rows of D 128 cover the banks once, so neighbours are
 // swapped in every other pair of keys, which spreads V's reads over both halves.
-template <int D, int NT, int PER_SM>
+template <int D, int NT, bool MULTI, int PER_SM>
 __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __grid_constant__ Kv4Attn a)
 {
     using S = Ring<D>;
@@ -124,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     const int swap_g = g ^ ((g >> 1) & 1), swap_c = c & 1;   // where the neighbours' swap puts a key
     grid_dep_wait();
     grid_dep_launch();     // the join reads the lengths only until this kernel has ended
-    const int total = sum_units<kWarps>(a, cum, warp_sum);
+    const int total = MULTI ? sum_tiles<kWarps>(a, cum, warp_sum) : sum_units<kWarps>(a, cum, warp_sum);
     const uint32_t ring = smem_u32(smem) + warp * S::total;
     const int copies = a.page_shift >= kUnitShift ? 4 : 8, copy_keys = 4 * kUnit / copies;   // of a unit, see below
     if (lane < kStages)
@@ -152,7 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
             return;
         if (i % 32 == 0) {
             if (i + lane < units)
-                descs[(i + lane) % kDescs] = find_unit(a, line, cum, u_begin + i + lane);
+                descs[(i + lane) % kDescs] = find_unit<MULTI>(a, line, cum, u_begin + i + lane);
             __syncwarp();
         }
         if (lane < copies) {   // one instruction for all of the unit's copies
@@ -169,7 +248,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     uint32_t qb[KS][NT][2];
     float qs[NT][2], qm[NT][2], o[KS][NT][4], m[NT][2];
     F2 l2[NT], ln2[NT];   // sums of the weights, and of weights times least values, of rows 2c and 2c + 1
-    int rows = 0;
+    int rows = 0, sees[NT][2];   // MULTI: keys that rows 2c and 2c + 1 see
     bool fresh = true;
     for (int i = 0; i < units; ++i) {
         const int pair = descs[i % kDescs].pair, live_last = descs[i % kDescs].live_last;
@@ -179,14 +258,16 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
             // largest element, times the powers above. bf16 has 8 significant bits,
             // so only elements below 2^-27 of the largest lose anything, 2^-35 of it.
             const int b = pair / line.hr, j = pair % line.hr;
-            const int h = j / a.tiles, row0 = (j % a.tiles) * R;
-            rows = min(R, a.group - row0);
+            const int h = j / a.tiles, row0 = (j % a.tiles) * R;   // (MULTI: one tile)
+            rows = MULTI ? descs[i % kDescs].tokens * a.group : min(R, a.group - row0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int r = row0 + t * 8 + g;
                 uint4 raw[D / 32];
                 if (t * 8 + g < rows) {
-                    const uint16_t* src = a.q + b * a.q_stride + static_cast<int64_t>(h * a.group + r) * D + c * (D / 4);
+                    const int token = MULTI ? r / a.group : 0;
+                    const uint16_t* src = a.q + (b + token) * a.q_stride +
+                                          static_cast<int64_t>(h * a.group + r - token * a.group) * D + c * (D / 4);
 #pragma unroll
                     for (int w = 0; w < WK; ++w)
                         raw[w] = __ldg(reinterpret_cast<const uint4*>(src) + w);
@@ -233,6 +314,10 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                     qs[t][y] = __shfl_sync(0xFFFFFFFFu, f, c * 8 + y * 4);
                     qm[t][y] = __shfl_sync(0xFFFFFFFFu, f * sum, c * 8 + y * 4);
                     m[t][y] = kLowest;
+                    if (MULTI) {
+                        const int token = (t * 8 + 2 * c + y) / a.group;
+                        sees[t][y] = t * 8 + 2 * c + y < rows ? seq_len(a, b + token) : 0;
+                    }
                 }
                 l2[t] = ln2[t] = F2(0.0f, 0.0f);
             }
@@ -326,14 +411,16 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
                     for (int k = 0; k < 4; ++k)
                         s[u][t][k] = fmaf(-2.0f * kLog2e * a.cap, rcp(1.0f + ex2(s[u][t][k])), kLog2e * a.cap);
         }
-        if (live < kUnit) {
+        if (live_last & 512) {
+            const int key0 = descs[i % kDescs].key0;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        s[u][t][k] = u * 16 + (k >> 1) * 8 + swap_g < live ? s[u][t][k] : -INFINITY;
+                        s[u][t][k] = u * 16 + (k >> 1) * 8 + swap_g < (MULTI ? sees[t][k & 1] - key0 : live) ? s[u][t][k]
+                                                                                                         : -INFINITY;
         }
         // ---- weights under the reference as it stands; where one, times the size of
         // its value, would come near f16's end the reference is raised and they are
@@ -421,9 +508,16 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const F2 weight(p[u][t][2 * x], p[u][t][2 * x + 1]), scaled = mul2(weight, F2(vs[u][x], vs[u][x]));
+                    const F2 weight(p[u][t][2 * x], p[u][t][2 * x + 1]);
+                    F2 scaled = mul2(weight, F2(vs[u][x], vs[u][x]));
+                    F2 least = fma2(weight, F2(vm[u][x], vm[u][x]), ln2[t]);
+                    if (MULTI && (live_last & 512)) {   // what a row does not see may be no number
+                        const bool y0 = s[u][t][2 * x] != -INFINITY, y1 = s[u][t][2 * x + 1] != -INFINITY;
+                        scaled = F2(y0 ? scaled.lo() : 0.0f, y1 ? scaled.hi() : 0.0f);
+                        least = F2(y0 ? least.lo() : ln2[t].lo(), y1 ? least.hi() : ln2[t].hi());
+                    }
                     l2[t] = add2(l2[t], weight);
-                    ln2[t] = fma2(weight, F2(vm[u][x], vm[u][x]), ln2[t]);
+                    ln2[t] = least;
                     pb[t][x] = transpose8(pack_f16(scaled.lo(), scaled.hi()));
                 }
 #pragma unroll
@@ -476,11 +570,11 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
 
 static int ring_smem(int D, int B) { return kWarps * (D == 128 ? Ring<128>::total : Ring<64>::total) + (B + 1) * 4; }
 
-template <int D, int NT, int PER_SM>
+template <int D, int NT, bool MULTI, int PER_SM>
 static cudaError_t launch_pieces(const Kv4Attn& a, cudaStream_t s)
 {
     const int smem = ring_smem(D, a.B);
-    auto kern = kv4_attn_kernel<D, NT, PER_SM>;
+    auto kern = kv4_attn_kernel<D, NT, MULTI, PER_SM>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
@@ -488,11 +582,21 @@ static cudaError_t launch_pieces(const Kv4Attn& a, cudaStream_t s)
     }
     return launch_dependent(kern, dim3(a.warps / kWarps), dim3(kWarps * 32), smem, s, a);
 }
-
+// Tokens of a sequence that share a tile: as many as 8 rows hold, where the sequences
+// are given apart (`seqs`); the codes of a unit are taken apart once for all of them.
+// (16 sequences of 2000-4000 keys, 5 tokens each, us with a tile for each token / so:
+// 32 query and 8 kv heads 60 / 48, 8 and 8 56 / 27. Two tokens of a larger group in 16
+// rows would not pay: 16 rows cost 1.74 times what 8 do, as they leave room for half
+// the warps; 48 query and 8 kv heads 58.9 / 57.5 with that, and it would be slower for
+// an odd number of tokens.)
 cudaError_t launch_kv4_attn(const Kv4Attn& in, int D, int num_sms, cudaStream_t s)
 {
     Kv4Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
+    a.tiles = (a.group + R - 1) / R;
+    a.per_tile = a.seqs && a.max_pages ? max(8 / a.group, 1) : 1;
+    if (a.per_tile == 1)
+        a.lead = nullptr;
     a.unit_shift = kUnitShift;
     const int64_t pairs = static_cast<int64_t>(a.Hkv) * a.B * a.tiles;
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
@@ -502,11 +606,12 @@ cudaError_t launch_kv4_attn(const Kv4Attn& in, int D, int num_sms, cudaStream_t 
     a.spread = static_cast<int>(min(max(min(8 * pairs, int64_t{2048}), int64_t{1536}), 128 * pairs));
     cudaError_t e = cudaSuccess;
     if (a.max_pages)
-        e = D == 128 ? (R == 8 ? launch_pieces<128, 1, 4>(a, s) : launch_pieces<128, 2, 2>(a, s))
-                     : (R == 8 ? launch_pieces<64, 1, 4>(a, s) : launch_pieces<64, 2, 3>(a, s));
+        e = R == 16            ? (D == 128 ? launch_pieces<128, 2, false, 2>(a, s) : launch_pieces<64, 2, false, 3>(a, s))
+            : a.per_tile == 1 ? (D == 128 ? launch_pieces<128, 1, false, 4>(a, s) : launch_pieces<64, 1, false, 4>(a, s))
+                              : (D == 128 ? launch_pieces<128, 1, true, 4>(a, s) : launch_pieces<64, 1, true, 4>(a, s));
     if (e != cudaSuccess)
         return e;
-    return launch_kv_join(a, Kv8Prefix{}, D, num_sms, s);
+    return launch_kv_join(a, Kv8Prefix{}, R, D, num_sms, s);
 }
 
 }  // namespace w4a8

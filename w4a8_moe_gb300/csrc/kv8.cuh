@@ -62,6 +62,7 @@ struct Kv8Attn {
     float free_us;      // that the others wait, about
     int beside;         // a tiled prefix runs beside
     int* cum;           // [B + 1] prefix sums of the sequences' units, left for the join
+    int* lead;          // [B] the row of the batch in whose tile each one is, or null: its own
 };
 // The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key
 // tiles); part_* [split][kv head][row] as above.
@@ -82,8 +83,8 @@ cudaError_t launch_kv8_prefix(const Kv8Attn& a, const Kv8Prefix& p, int D, int p
 bool kv8_prefix_tiled(int Hkv, int rows, int prefix_len);
 int kv8_attn_row_tile(int group);
 void kv8_attn_layout(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms, int* blocks_per_sm, int* warps_a_row);
-// Adds up the pieces that a kernel over `a`'s split has left.
-cudaError_t launch_kv_join(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms, cudaStream_t s);
+// Adds up the pieces, of R rows, that a kernel over `a`'s split has left.
+cudaError_t launch_kv_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_kv8_attn(const Kv8Attn& a, const Kv8Prefix& p, int D, int per_token, int num_sms, cudaStream_t s);
 
 // Two E4M3 codes (low byte first) to two f16 values: exact for every code.

@@ -483,8 +483,8 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     const int b = there ? head / a.Hq : 0, qh = there ? head - b * a.Hq : 0, h = qh / a.group, gi = qh - h * a.group;
     // units before the sequence's and all of them: a short sum over the lengths
     // while the kernel before is still at work, else what it left
-    const bool sum_here = a.B <= kJoinSums;
-    int before = 0, units = 0, all = 0;
+    const bool sum_here = a.B <= kJoinSums && !a.lead;
+    int before = 0, units = 0, all = 0, tile = b;   // (the batch row that has the tile)
     if (sum_here) {
         for (int i = lane; i < a.B; i += L) {
             const int n = seq_units(a, i);
@@ -501,8 +501,9 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     } else {
         grid_dep_wait();
         if (a.max_pages) {
-            before = a.cum[b];
-            units = a.cum[b + 1] - before;
+            tile = a.lead ? a.lead[b] : b;
+            before = a.cum[tile];
+            units = a.cum[tile + 1] - before;
             all = a.cum[a.B];
         }
     }
@@ -522,11 +523,11 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     }
     n2 = n1;
     if (units) {
-        const int j = h * a.tiles + gi / R;
+        const int in_tile = (b - tile) * a.group + gi, j = h * a.tiles + in_tile / R;
         const int64_t first = line.own + static_cast<int64_t>(before) * line.hr + static_cast<int64_t>(j) * units;
         const int w = warp_of(line, first);
         n2 += warp_of(line, first + units - 1) - w + 1;
-        at_own = static_cast<int64_t>(line.pairs_p + b * line.hr + j + w - n1) * R + gi % R;
+        at_own = static_cast<int64_t>(line.pairs_p + tile * line.hr + j + w - n1) * R + in_tile % R;
     }
     n2 = there ? n2 : 0;
     if (sum_here)
@@ -726,9 +727,8 @@ static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int 
                             dim3(kJoinCta * 32), 0, s, a, p, R);
 }
 
-cudaError_t launch_kv_join(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms, cudaStream_t s)
+cudaError_t launch_kv_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int D, int num_sms, cudaStream_t s)
 {
-    const int R = kv8_attn_row_tile(a.group);
     return D == 128 ? launch_join<128>(a, p, R, num_sms, s) : launch_join<64>(a, p, R, num_sms, s);
 }
 
@@ -801,7 +801,7 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
         if (e != cudaSuccess)
             return e;
     }
-    return launch_kv_join(a, p, D, num_sms, s);
+    return launch_kv_join(a, p, R, D, num_sms, s);
 }
 
 }  // namespace w4a8

@@ -71,20 +71,27 @@ __device__ __forceinline__ int pages_of(int tokens, int shift)   // tokens >= 0
 {
     return static_cast<int>((static_cast<unsigned>(tokens) + (1u << shift) - 1) >> shift);
 }
-__device__ __forceinline__ int free_pages(const PagePool& p)
+// The pages on the stack, read by one thread for the block (a barrier has to follow).
+__device__ __forceinline__ void read_count(const PagePool& p, int* count)
 {
-    const int n = *p.count;
-    if (n < 0 || n > p.num_pages)
-        set_error(p.err, kErrBitIndex);
-    return min(max(n, 0), p.num_pages);
+    if (threadIdx.x == 0) {
+        const int n = *p.count;
+        if (n < 0 || n > p.num_pages)
+            set_error(p.err, kErrBitIndex);
+        *count = min(max(n, 0), p.num_pages);
+    }
 }
-// Whether this block is the last of the grid to come here; all threads agree.
+// Whether this block is the last of the grid to come here; all threads agree. What
+// the others have read into shared memory before, they have read.
 __device__ __forceinline__ bool last_block(uint32_t* ticket)
 {
     __shared__ bool last;
     __syncthreads();
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
+        __threadfence();
         last = gridDim.x == 1 || atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
+        __threadfence();
+    }
     __syncthreads();
     return last;
 }
@@ -97,12 +104,12 @@ __global__ void __launch_bounds__(kThreads) pages_extend_kernel(const __grid_con
     int* starts = smem;               // [B + 1] tokens before each sequence, T + 1 at most
     int* ahead = smem + a.B + 1;      // [B + 1] pages that those before it need, num_pages + 1 at most
     int* have = ahead + a.B + 1;      // [B] its tokens; less than 0 (the complement) where it gets no pages
-    __shared__ int taken;
+    __shared__ int taken, count;
     const int tid = threadIdx.x, shift = a.p.page_shift;
     if (tid == 0)
         taken = 0;
     grid_dep_wait();
-    const int count = free_pages(a.p);
+    read_count(a.p, &count);
     const int64_t most_tokens = static_cast<int64_t>(a.p.max_pages) << shift;
 
     // ---- the sums: a thread takes `per` sequences in a row
@@ -195,9 +202,10 @@ __global__ void __launch_bounds__(kThreads) pages_truncate_kernel(const __grid_c
     extern __shared__ int smem[];
     int* ahead = smem;             // [B + 1] pages that those before it give back, num_pages + 1 at most
     int* kept = smem + a.B + 1;    // [B] tokens
+    __shared__ int count;
     const int tid = threadIdx.x, shift = a.p.page_shift;
     grid_dep_wait();
-    const int count = free_pages(a.p);
+    read_count(a.p, &count);
     const int64_t most_tokens = static_cast<int64_t>(a.p.max_pages) << shift;
     const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     const unsigned most = static_cast<unsigned>(a.p.num_pages) + 1;

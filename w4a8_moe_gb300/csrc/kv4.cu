@@ -107,6 +107,10 @@ __device__ __forceinline__ uint32_t bounds(const uint4 (&raw)[2])
 
 }  // namespace
 
+// 32768 tokens of 8 heads of 128 (172 MB): 34.3 us, 5.0 TB/s or 74 % of a copy's rate;
+// the arithmetic of 16 codes, some 200 instructions a lane, bounds it as much as memory
+// does (with a conversion and two bounds for each code 35.5 us, 12 blocks an SM 34.3 / as
+// many as registers would leave, 10, 35.5). 256 tokens take 2.7 us.
 template <int D>
 __global__ void __launch_bounds__(kRowThreads, 12) kv4_write_kernel(const __grid_constant__ Kv8Rows a,
                                                                 const uint16_t* __restrict__ k,
@@ -171,7 +175,9 @@ __global__ void __launch_bounds__(kRowThreads, 12) kv4_write_kernel(const __grid
     }
 }
 
-// x = bf16(c s + m); rows whose slot is out of range are zero.
+// x = bf16(c s + m); rows whose slot is out of range are zero. Bound by memory: the same
+// 32768 tokens 30.2 us, 5.7 TB/s, 83 % of a copy's rate (37.6 us with 16 values in a row
+// to a lane, whose stores cover half sectors).
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const __grid_constant__ Kv8Rows a,
                                                                const uint8_t* __restrict__ k_cache,

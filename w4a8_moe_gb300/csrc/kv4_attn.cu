@@ -173,6 +173,13 @@ __device__ __forceinline__ Unit find_unit(const Kv4Attn& a, const Line& line, co
 
 }  // namespace
 
+// Bound by instructions and memory alike: 64 sequences of 8192-16384 keys, 32 query and
+// 8 kv heads (857 MB) take 157 us, 5.4 TB/s or 80 % of a copy's rate, with the units'
+// arithmetic left out 129 us; a unit is 500 instructions of a warp, 176 of them the
+// masks below (integer instructions, which go at half the rate), 32 matrix products.
+// Short sequences are bound by the chain lengths -> page -> codes -> result -> join,
+// some 7 us.
+//
 // Fragments. An f16 whose bits are 0000 0000 0000 cccc is the subnormal number
 // c 2^-24, and one with the code four bits up is c 2^-20; the tensor cores take
 // subnormals as they are, so codes become operands by a mask, two to a register,

@@ -13,6 +13,9 @@
 // the tokens and the new table entries between them; who a token or a page belongs
 // to is found by bisection. Nothing that one block writes does another one read but
 // the lengths and the count, which the last block to have read them writes.
+//
+// Bound by latency: lengths, sums, page, slot one after another. 256 sequences' step
+// takes 3.4 us, and as much to take back; 1024 sequences with 102912 tokens 5.4 us.
 #include "internal.h"
 #include "kv8.cuh"
 #include "pages.cuh"

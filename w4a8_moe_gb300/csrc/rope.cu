@@ -42,6 +42,11 @@ __device__ __forceinline__ float row_max(float x)
 
 }  // namespace
 
+// Bound by memory: 32768 tokens of 32 + 8 heads of 128 with norms (671 MB) take 103
+// us, 6.5 TB/s or 96 % of a copy's rate, 8192 of them 30.3 us, 82 % (a launch and the
+// first rows' way are 4 us of it); 32768 tokens of 48 query and 8 kv heads into the
+// cache (1009 MB) 161 us, 92 %. 32 tokens take 2.1 us, into the cache 2.6.
+//
 // L lanes share a row (one head of one token), 16 values each, in two runs of 8:
 // a rotating lane has both halves of 8 pairs, so nothing is exchanged but the sum
 // of squares (and the largest value of a row that finds its own scale), every
@@ -53,14 +58,17 @@ __device__ __forceinline__ float row_max(float x)
 // turns (a tenth of a radian at a position of a million). Its upper 32 bits go
 // through sincospif. That is some 40 instructions a pair, a third of a row's
 // arithmetic, so a block makes the sines and cosines of its tokens once, in shared
-// memory, while its first rows are on their way.
+// memory, while its first rows are on their way (made by each group of lanes for its
+// own heads: 37.5 us for the 8192 tokens). Shared memory holds what a lane reads in one
+// instruction as the lanes lie, so that none of its reads conflict (43.4 us with norms
+// and interleaved pairs before). One block a range of tokens for as long as the kernel
+// runs, without new blocks, was slower: 188 us into the cache.
 template <int L, bool INTER, bool CACHE>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Rope a)
 {
     constexpr int G = kThreads / L;   // rows at once
-    // [2][D] the norms' weights (queries', keys'), then [tokens][2][rot / 2] cosines, sines
-    extern __shared__ __align__(16) float shared[];
-    float* table = shared + 2 * a.D;
+    extern __shared__ __align__(16) float table[];   // [tokens][2][rot / 2] cosines, sines, in fours of the lanes
+    __shared__ uint4 weights[2][2][L];               // of the norms: queries' and keys', a lane's two runs
     __shared__ int64_t slot_of[kMostTokens];
     grid_dep_wait();
     const int lane = threadIdx.x % L, group = threadIdx.x / L;
@@ -100,15 +108,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(a.turns + j);
         float s, c;
         sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
-        table[token * a.rot + j] = c * a.magnitude;
-        table[token * a.rot + half + j] = s * a.magnitude;
+        float* to = table + token * a.rot + (j / 4 % 2) * (half / 2) + j / 8 * 4 + j % 4;
+        to[0] = c * a.magnitude;
+        to[half] = s * a.magnitude;
     }
     const bool norms = a.q_weight || a.k_weight;
-    if (norms)
-        for (int i = threadIdx.x; i < a.D; i += kThreads) {
-            shared[i] = a.q_weight ? bf16_bits_to_float(__ldg(a.q_weight + i)) : 1.0f;
-            shared[a.D + i] = a.k_weight ? bf16_bits_to_float(__ldg(a.k_weight + i)) : 1.0f;
+    if (threadIdx.x < 2 * L) {   // the lanes of the first groups load their runs of the queries' and the keys' weights
+        const uint16_t* weight = threadIdx.x < L ? a.q_weight : a.k_weight;
+        if (weight && mine) {
+            weights[threadIdx.x / L][0][lane] = __ldg(reinterpret_cast<const uint4*>(weight + at0));
+            weights[threadIdx.x / L][1][lane] = __ldg(reinterpret_cast<const uint4*>(weight + at1));
         }
+    }
     if (CACHE && threadIdx.x < tokens)
         slot_of[threadIdx.x] = __ldg(a.slots + t0 + threadIdx.x);
     __syncthreads();
@@ -128,22 +139,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             const float sum = row_sum<L>(sum2.lo() + sum2.hi());
             if (live && (r < n_q ? a.q_weight : r < n_k ? a.k_weight : nullptr)) {
                 const float f = rsqrtf(fmaf(sum, a.inv_d, a.eps));
-                const float* w = shared + (r < n_q ? 0 : a.D);
+                const uint4 raw[2] = {weights[r < n_q ? 0 : 1][0][lane], weights[r < n_q ? 0 : 1][1][lane]};
+                float w[16];
+                unpack16(raw, w);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 w4 = *reinterpret_cast<const float4*>(w + (j < 8 ? at0 + j : at1 + j - 8));
-                    const F2 y0 = mul2(mul2(F2(x[j], x[j + 1]), F2(f, f)), F2(w4.x, w4.y));
-                    const F2 y1 = mul2(mul2(F2(x[j + 2], x[j + 3]), F2(f, f)), F2(w4.z, w4.w));
-                    x[j] = y0.lo(), x[j + 1] = y0.hi(), x[j + 2] = y1.lo(), x[j + 3] = y1.hi();
+                for (int j = 0; j < 16; j += 2) {
+                    const F2 y = mul2(mul2(F2(x[j], x[j + 1]), F2(f, f)), F2(w[j], w[j + 1]));
+                    x[j] = y.lo(), x[j + 1] = y.hi();
                 }
             }
         }
         if (turning && r < n_k && there) {
-            const float* cosines = table + token * a.rot + lane * 8;
+            const float* cosines = table + token * a.rot + lane * 4;
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {   // four pairs
-                const float4 c4 = *reinterpret_cast<const float4*>(cosines + j);
-                const float4 s4 = *reinterpret_cast<const float4*>(cosines + half + j);
+                const float4 c4 = *reinterpret_cast<const float4*>(cosines + j / 4 * (half / 2));
+                const float4 s4 = *reinterpret_cast<const float4*>(cosines + j / 4 * (half / 2) + half);
                 const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
                 if (INTER) {
 #pragma unroll
@@ -227,7 +238,7 @@ static cudaError_t launch(Rope a, int num_sms, cudaStream_t s)
     a.slice = passes < each ? G : rows;
     const dim3 grid((a.T + a.tokens - 1) / a.tokens, (rows + a.slice - 1) / a.slice);
     return launch_dependent(a.interleaved ? rope_kernel<L, true, CACHE> : rope_kernel<L, false, CACHE>, grid,
-                            dim3(kThreads), (2 * a.D + a.tokens * a.rot) * static_cast<int>(sizeof(float)), s, a);
+                            dim3(kThreads), a.tokens * a.rot * static_cast<int>(sizeof(float)), s, a);
 }
 
 cudaError_t launch_rope(const Rope& a, bool to_cache, int num_sms, cudaStream_t s)

@@ -40,8 +40,7 @@ struct Ring {   // one warp's shared memory
     static constexpr int kCodes = kUnit * D / 2;  // bytes of K or V codes of a unit
     static constexpr int kStage = 2 * kCodes + 2 * kUnit * 4;   // K, V, their scales
     static constexpr int desc = kStages * kStage;
-    static constexpr int bars = desc + kDescs * static_cast<int>(sizeof(Unit));
-    static constexpr int total = (bars + kStages * 8 + 127) / 128 * 128;   // bulk copies want 16 bytes
+    static constexpr int total = (desc + kDescs * static_cast<int>(sizeof(Unit)) + 127) / 128 * 128;
 };
 
 __device__ __forceinline__ int64_t page_row(const Kv4Attn& a, const int32_t* pages, int h, int key)
@@ -171,6 +170,11 @@ __device__ __forceinline__ Unit find_unit(const Kv4Attn& a, const Line& line, co
     return x;
 }
 
+__device__ __forceinline__ void copy16(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
 }  // namespace
 
 // Bound by instructions and memory alike: 64 sequences of 8192-16384 keys, 32 query and
@@ -191,8 +195,9 @@ __device__ __forceinline__ Unit find_unit(const Kv4Attn& a, const Line& line, co
 // order. Both products have the rows as their N: S^T = K Q^T with 16 keys as M and
 // O^T = V^T P^T with D as M. A thread reads, of K's keys g and g + 8, chunk c of
 // their D codes, and of V's keys 2c, 2c + 1, 2c + 8, 2c + 9 (the pairs of an operand
-// register), chunk g. Two rows of D 128 cover the banks once, so neighbours are
-// swapped in every other pair of keys, which spreads V's reads over both halves.
+// register), chunk g. So that these reads meet no bank twice, the upper four of eight
+// keys are taken in the order 5 4 7 6, and rows of D 128, two of which cover the banks,
+// have the halves of every other two exchanged.
 template <int D, int NT, bool MULTI, int PER_SM>
 __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __grid_constant__ Kv4Attn a)
 {
@@ -207,15 +212,11 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     __shared__ int warp_sum[kWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int swap_g = g ^ ((g >> 1) & 1), swap_c = c & 1;   // where the neighbours' swap puts a key
+    const int swap_g = g ^ (g >> 2), swap_c = c >> 1;   // keys in the order 0 1 2 3 5 4 7 6 (see above)
     grid_dep_wait();
     grid_dep_launch();     // the join reads the lengths only until this kernel has ended
     const int total = MULTI ? sum_tiles<kWarps>(a, cum, warp_sum) : sum_units<kWarps>(a, cum, warp_sum);
     const uint32_t ring = smem_u32(smem) + warp * S::total;
-    const int copies = a.page_shift >= kUnitShift ? 4 : 8, copy_keys = 4 * kUnit / copies;   // of a unit, see below
-    if (lane < kStages)
-        mbar_init(ring + S::bars + lane * 8, copies);
-    fence_mbar_init();
     __syncthreads();
 
     const Line line = make_line(a, total);
@@ -225,28 +226,31 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
     Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
 
-    // lane 0 copies codes of keys, 1 of values, 2 and 3 their scales, 4 to 7 those of
-    // the second page where pages are half a unit
-    const uint32_t copy_row = lane & 2 ? 4 : D / 2, copy_bytes = copy_keys * copy_row;
-    const uint32_t copy_to = ring + (lane & 2 ? 2 * S::kCodes + (lane & 1) * kUnit * 4 : (lane & 1) * S::kCodes) +
-                             (lane >> 2) * copy_bytes;
-    const uint8_t* copy_from = lane & 2 ? reinterpret_cast<const uint8_t*>(lane & 1 ? a.v_scale : a.k_scale)
-                                        : lane & 1 ? a.v_cache : a.k_cache;
-    // unit i of this warp into its ring slot; batches of 32 descriptors ahead of it
+    // unit i of this warp into its ring slot; batches of 32 descriptors ahead of it.
+    // (Every call is one group of copies, empty behind the last unit.)
     auto issue = [&](int i) {
-        if (i >= units)
-            return;
-        if (i % 32 == 0) {
-            if (i + lane < units)
-                descs[(i + lane) % kDescs] = find_unit<MULTI>(a, line, cum, u_begin + i + lane);
-            __syncwarp();
+        if (i < units) {
+            if (i % 32 == 0) {
+                if (i + lane < units)
+                    descs[(i + lane) % kDescs] = find_unit<MULTI>(a, line, cum, u_begin + i + lane);
+                __syncwarp();
+            }
+            const Unit& x = descs[i % kDescs];
+            const uint32_t stage = ring + (i % kStages) * S::kStage;
+            const uint32_t to = stage + (D == 128 ? lane ^ (lane >> 2 & 2) : lane) * 16;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {   // 16 keys
+                const int64_t from = x.row[p] * (D / 2) + lane * 16;
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    copy16(to + p * 8 * D + j * 512, a.k_cache + from + j * 512);
+                    copy16(to + S::kCodes + p * 8 * D + j * 512, a.v_cache + from + j * 512);
+                }
+            }
+            if (lane < 16)   // four pairs of numbers of a key or a value each
+                copy16(stage + 2 * S::kCodes + lane * 16, (lane & 8 ? a.v_scale : a.k_scale) + x.row[(lane >> 2) & 1] + (lane & 3) * 4);
         }
-        if (lane < copies) {   // one instruction for all of the unit's copies
-            const uint32_t bar = ring + S::bars + (i % kStages) * 8;
-            mbar_arrive_expect_tx(bar, copy_bytes);
-            bulk_load(copy_to + (i % kStages) * S::kStage, copy_from + descs[i % kDescs].row[lane >> 2] * copy_row, copy_bytes,
-                      bar);
-        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
@@ -340,12 +344,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
 
         // ---- the unit's codes into registers, and its slot to the next copy
         const uint32_t at = ring + (i % kStages) * S::kStage;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(ring + S::bars + (i % kStages) * 8, (i / kStages) & 1))) {
-            set_error(a.err, kErrBitTimeout);
-            for (int j = i + 1; j < min(i + kStages, units); ++j)   // copies in flight end before the warp does
-                mbar_wait(ring + S::bars + (j % kStages) * 8, (j / kStages) & 1);
-            break;
-        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();   // the other lanes' copies too
         uint32_t xk[kSub][2][WK];
         float ks[kSub][2], km[kSub][2], vs[kSub][2], vm[kSub][2];   // of the keys g, g + 8
 #pragma unroll
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
             for (int x = 0; x < 2; ++x) {
                 const int key = u * 16 + x * 8 + swap_g;
                 if (D == 128) {
-                    const uint4 w = lds128(at + key * (D / 2) + c * 16);
+                    const uint4 w = lds128(at + key * (D / 2) + (c ^ (swap_g & 2)) * 16);
                     xk[u][x][0] = w.x, xk[u][x][1] = w.y, xk[u][x][WK - 2] = w.z, xk[u][x][WK - 1] = w.w;
                 } else {
                     const uint2 w = lds64(at + key * (D / 2) + c * 8);
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
             for (int k = 0; k < 4; ++k) {
                 const int key = u * 16 + (k >> 1) * 8 + c * 2 + ((k & 1) ^ swap_c);
                 if (D == 128) {
-                    const uint2 w = lds64(at + S::kCodes + key * (D / 2) + g * 8);
+                    const uint2 w = lds64(at + S::kCodes + key * (D / 2) + (g * 8 ^ (c & 1) * 32));
                     xv[u][k][0] = w.x, xv[u][k][WV - 1] = w.y;
                 } else {
                     xv[u][k][0] = __float_as_uint(lds32(at + S::kCodes + key * (D / 2) + g * 4));

@@ -605,3 +605,45 @@ def test_python_checks_raise_before_a_launch(lib):
             lib.kv4_read(b.k, b.v, b.ks, scale, slots)
     with pytest.raises(ValueError):
         lib.kv4_read(b.k, b.v.cpu(), b.ks, b.vs, slots)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 8, 64), (48, 8, 64)])
+def test_attention_very_many_units(lib, hq, hkv, d):
+    """So many keys that the shares go by the blocks' places: right, the same bits every time, the workspace's counters
+    left at zero, and larger and smaller calls in turn on one workspace."""
+    b = Batch([5000 + 331 * i % 3000 for i in range(40)], hq, hkv, d, 64, seed=50)
+    few = Batch([300, 20, 7], hq, hkv, d, 64, seed=51)
+    ws = torch.zeros(lib.kv4_attention_workspace_size(40, hq, hkv, d, 1, 64), dtype=torch.uint8, device="cuda")
+    first, small = b.run(lib, ws=ws), few.run(lib, ws=ws)
+    b.check(*first, every=7)
+    few.check(*small)
+    assert bool((ws[:256] == 0).all())
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(60):
+        for x, want in ((b, first), (few, small)):
+            got = x.run(lib, ws=ws)
+            differ += (got[0] != want[0]).sum() + (got[1] != want[1]).sum()
+    assert int(differ) == 0 and lib.w4a8_device_error(ws) == 0
+    # beside other work on the GPU: blocks come to other places
+    side = torch.cuda.Stream()
+    m = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            m = torch.relu(m) + 0.5
+        got = b.run(lib, ws=ws)
+        differ += (got[0] != first[0]).sum() + (got[1] != first[1]).sum()
+    torch.cuda.synchronize()
+    assert int(differ) == 0 and lib.w4a8_device_error(ws) == 0 and bool((ws[:256] == 0).all())
+
+
+def test_attention_header_that_is_not_zero_is_reported(lib):
+    """Counters that a call did not leave behind: the call ends, and says so."""
+    b = Batch([7000] * 40, 32, 8, 128, 64, seed=52)
+    ws = torch.zeros(lib.kv4_attention_workspace_size(40, 32, 8, 128, 1, 64), dtype=torch.uint8, device="cuda")
+    want = b.run(lib, ws=ws)
+    ws[64:80] = 0x7F
+    b.run(lib, ws=ws)
+    assert lib.w4a8_device_error(ws) == W4A8_ERR_INDEX
+    got = b.run(lib, ws=ws)   # the call has put them right
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and lib.w4a8_device_error(ws) == 0

@@ -1131,7 +1131,7 @@ int kv4_attention(const uint16_t* q_bf16, int64_t q_stride, int T, int Hq, int H
     a.seqs = seqs, a.num_seqs = num_seqs;
     a.sm_scale = sm_scale, a.cap = logit_cap;
     a.part_o = w.part_o, a.part_ml = w.part_ml, a.cum = w.cum, a.lead = w.lead;
-    a.err = static_cast<uint32_t*>(ws);
+    a.err = static_cast<uint32_t*>(ws), a.tickets = a.err + 16;
     a.out = out_bf16, a.lse = lse;
     return launch_kv4_attn(a, D, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A8_OK : W4A8_ERR_LAUNCH;
 }

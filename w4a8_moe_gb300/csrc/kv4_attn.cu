@@ -178,8 +178,8 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from)
 }  // namespace
 
 // Bound by instructions and memory alike: 64 sequences of 8192-16384 keys, 32 query and
-// 8 kv heads (857 MB) take 157 us, 5.4 TB/s or 80 % of a copy's rate, with the units'
-// arithmetic left out 129 us; a unit is 500 instructions of a warp, 176 of them the
+// 8 kv heads (857 MB) take 141 us, 6.1 TB/s or 90 % of a copy's rate, with the units'
+// arithmetic left out 129 us; a unit is 477 instructions of a warp, 176 of them the
 // masks below (integer instructions, which go at half the rate), 32 matrix products.
 // Short sequences are bound by the chain lengths -> page -> codes -> result -> join,
 // some 7 us.
@@ -220,10 +220,32 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     __syncthreads();
 
     const Line line = make_line(a, total);
-    // few units: one warp on each SM before a second
-    const int me = warp * gridDim.x + blockIdx.x;
-    const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
-    const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
+    // Few units: one warp on each SM before a second. Very many: a block takes one of the
+    // shares for its place on the SM, and where those are gone one of another place's
+    // (which block does a share changes no result). There are as many shares as blocks,
+    // so one is found, unless the workspace's header was not zero.
+    int place = 0, block = blockIdx.x;
+    const int sms = gridDim.x / line.places;
+    if (line.places > 1) {
+        __shared__ int mine;
+        if (tid == 0) {
+            unsigned slot;
+            asm volatile("mov.u32 %0, %warpid;" : "=r"(slot));
+            int p = min(static_cast<int>(slot) / kWarps, line.places - 1), tries = 0;
+            unsigned ticket;
+            while ((ticket = atomicAdd(a.tickets + p, 1u)) >= static_cast<unsigned>(sms) && ++tries < line.places)
+                p = p + 1 < line.places ? p + 1 : 0;
+            if (tries == line.places)
+                set_error(a.err, kErrBitIndex);
+            mine = tries == line.places ? blockIdx.x : p * sms + ticket;
+        }
+        __syncthreads();
+        place = mine / sms;
+        block = mine - place * sms;
+    }
+    const int me = (place * kWarps + warp) * sms + block;
+    const int64_t u_begin = me < line.n ? warp_begin<true>(a, line, me) : 0;
+    const int units = me < line.n ? static_cast<int>(warp_begin<true>(a, line, me + 1) - u_begin) : 0;
     Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
 
     // unit i of this warp into its ring slot; batches of 32 descriptors ahead of it.
@@ -610,6 +632,14 @@ cudaError_t launch_kv4_attn(const Kv4Attn& in, int D, int num_sms, cudaStream_t 
     const int blocks = min(R == 8 ? 4 : D == 64 ? 3 : 2, fit);
     a.warps = min(num_sms * blocks * kWarps, kKv8MaxWarps / kWarps * kWarps);
     a.free_warps = a.warps;
+    // Shares by place where four blocks fit an SM (two or three, of 16 rows, gain nothing).
+    // us with equal shares / proportions of 170:140:118:100 / 200:160:130:100 /
+    // 250:190:140:100: 64 sequences of 8192-16384 keys of D 128 153 / 146 / 143 / 148, 256
+    // of 500-1000 55.9 / 54.4 / 54.1 / 55.7, 32 of 4096-8192 of D 64 35.9 / 34.7 / 35.5 / 36.8.
+    const int weights[2][4] = {{170, 140, 118, 100}, {200, 160, 130, 100}};
+    a.places = blocks == 4 && a.warps == num_sms * blocks * kWarps ? blocks : 1;
+    for (int i = 0; i < 4; ++i)
+        a.place_weight[i] = weights[D == 128][i];
     a.spread = static_cast<int>(min(max(min(8 * pairs, int64_t{2048}), int64_t{1536}), 128 * pairs));
     cudaError_t e = cudaSuccess;
     if (a.max_pages)

@@ -56,6 +56,9 @@ struct Kv8Attn {
     uint16_t* out;
     float* lse;
     int unit_shift;     // log2 of the keys of a unit
+    int places;         // blocks that an SM holds, where the shares may go by them (else 0 or 1)
+    int place_weight[4];   // their proportions
+    uint32_t* tickets;     // [4] shares of each place that are taken; zero between calls
     int warps;          // that the units go to
     int free_warps;     // of them those that need not wait for the tiled prefix
     int spread;         // warps up to which the units are spread by twos

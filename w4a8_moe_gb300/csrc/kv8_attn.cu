@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
     int me = block < first ? warp * first + block : line.n1 + (block - first) * kWarps + warp;
     if (block < first && me >= line.n1)
         me = line.n;
-    const int64_t u_begin = me < line.n ? warp_begin(line, me) : 0;
-    const int units = me < line.n ? static_cast<int>(warp_begin(line, me + 1) - u_begin) : 0;
+    const int64_t u_begin = me < line.n ? warp_begin(a, line, me) : 0;
+    const int units = me < line.n ? static_cast<int>(warp_begin(a, line, me + 1) - u_begin) : 0;
     Unit* descs = reinterpret_cast<Unit*>(smem + warp * S::total + S::desc);
 
     // unit i of this warp into its ring slot; batches of 32 descriptors ahead of it
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
 // others do, and each takes few registers.
 constexpr int kJoinCta = 4;      // warps of a CTA where a row has one or less
 constexpr int kJoinSums = 128;   // sequences up to which a warp sums their units itself
-template <int D, int W>
+template <int D, int W, bool PLACES>   // PLACES: shares by the blocks' places (Line::places)
 __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
                                                                          const __grid_constant__ Kv8Prefix p, int R)
 {
@@ -517,21 +517,23 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     if (a.ptiles) {
         const int pair = h * a.ptiles + row / R;
         const int64_t first = static_cast<int64_t>(pair) * line.up;
-        const int w = warp_of(line, first);
-        n1 += warp_of(line, first + line.up - 1) - w + 1;
+        const int w = warp_of(a, line, first);
+        n1 += warp_of(a, line, first + line.up - 1) - w + 1;
         at_pre = static_cast<int64_t>(pair + w - n0) * R + row % R;
     }
     n2 = n1;
     if (units) {
         const int in_tile = (b - tile) * a.group + gi, j = h * a.tiles + in_tile / R;
         const int64_t first = line.own + static_cast<int64_t>(before) * line.hr + static_cast<int64_t>(j) * units;
-        const int w = warp_of(line, first);
-        n2 += warp_of(line, first + units - 1) - w + 1;
+        const int w = warp_of<PLACES>(a, line, first);
+        n2 += warp_of<PLACES>(a, line, first + units - 1) - w + 1;
         at_own = static_cast<int64_t>(line.pairs_p + tile * line.hr + j + w - n1) * R + in_tile % R;
     }
     n2 = there ? n2 : 0;
     if (sum_here)
         grid_dep_wait();
+    if (PLACES && blockIdx.x == 0 && tid < 4)
+        a.tickets[tid] = 0;
     // Lane i of a row finds piece first_piece + S i and its weight; then every
     // lane reads its values of all of them. Nothing that is read waits for
     // anything but the kernel before. (Both halves of a warp go round together.)
@@ -713,23 +715,25 @@ static int join_warps(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms)
     return heads > 18 * num_sms ? 0 : 1;
 }
 
-template <int D>
+template <int D, bool PLACES>
 static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
 {
     const int heads = a.B * a.Hq, warps = join_warps(a, p, D, num_sms);
     if (warps > 1)
-        return launch_dependent(warps == 8   ? kv8_join_kernel<D, 8>
-                                : warps == 4 ? kv8_join_kernel<D, 4>
-                                             : kv8_join_kernel<D, 2>,
+        return launch_dependent(warps == 8   ? kv8_join_kernel<D, 8, PLACES>
+                                : warps == 4 ? kv8_join_kernel<D, 4, PLACES>
+                                             : kv8_join_kernel<D, 2, PLACES>,
                                 dim3(heads), dim3(warps * 32), 0, s, a, p, R);
     const int rows = kJoinCta * (warps ? 1 : 2);   // of a CTA
-    return launch_dependent(warps ? kv8_join_kernel<D, 1> : kv8_join_kernel<D, 0>, dim3((heads + rows - 1) / rows),
-                            dim3(kJoinCta * 32), 0, s, a, p, R);
+    return launch_dependent(warps ? kv8_join_kernel<D, 1, PLACES> : kv8_join_kernel<D, 0, PLACES>,
+                            dim3((heads + rows - 1) / rows), dim3(kJoinCta * 32), 0, s, a, p, R);
 }
 
 cudaError_t launch_kv_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int D, int num_sms, cudaStream_t s)
 {
-    return D == 128 ? launch_join<128>(a, p, R, num_sms, s) : launch_join<64>(a, p, R, num_sms, s);
+    if (a.places > 1)
+        return D == 128 ? launch_join<128, true>(a, p, R, num_sms, s) : launch_join<64, true>(a, p, R, num_sms, s);
+    return D == 128 ? launch_join<128, false>(a, p, R, num_sms, s) : launch_join<64, false>(a, p, R, num_sms, s);
 }
 
 // Whether the tensor-core kernel takes the prefix. It costs a third launch and

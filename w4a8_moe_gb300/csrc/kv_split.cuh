@@ -7,6 +7,7 @@
 namespace w4a8 {
 
 constexpr float kMostWeight = 0x1p15f;   // 2^kWeightMost
+constexpr int kPlaceUnits = 8;   // units of a warp from which on shares may go by its block's place
 constexpr float kLowest = -3.4028235e38f;   // the reference of a row without keys
 
 // D[16x8] += A[16x16] B[16x8], f16 operands, fp32 accumulators.
@@ -57,6 +58,7 @@ struct Line {
     int pairs_p;    // prefix pairs
     int64_t own;    // first unit of the sequences' pairs
     int hr;         // pairs of a sequence
+    int places;     // shares by the blocks' places on their SM (1: equal shares)
 };
 __device__ __forceinline__ int seq_len(const Kv8Attn& a, int b)
 {
@@ -102,7 +104,22 @@ __device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
     }
     l.n1 = warps_for(l.U1, a.spread, a.free_warps);
     l.n = l.n1 + (late > 0 ? warps_for(l.U - l.U1, a.spread, late) : 0);
+    l.places = a.places > 1 && l.U >= kPlaceUnits * static_cast<int64_t>(a.warps) ? a.places : 1;
     return l;
+}
+// An SM's schedulers let the warps of its first block go before those of its second
+// and so on. With equal shares the last ones end much later, and alone: 64 sequences
+// of 8192-16384 keys of 4 bits, the four blocks' warps after 100, 113, 129 and 145 us,
+// the memory being busy for the first 100 and half idle then. Where units are many the
+// shares therefore go by the block's place, in the proportions of
+// Kv8Attn::place_weight: the n / places warps of each place stand together in the line.
+__device__ __forceinline__ int64_t weight_before(const Kv8Attn& a, const Line& l, int w)   // of w warps
+{
+    const int per = l.n / l.places, place = min(w / per, l.places - 1);
+    int64_t sum = static_cast<int64_t>(w - place * per) * a.place_weight[place];
+    for (int p = 0; p < place; ++p)
+        sum += static_cast<int64_t>(per) * a.place_weight[p];
+    return sum;
 }
 // (32-bit division where the numbers allow it: warps are fewer than 2^12.)
 __device__ __forceinline__ int64_t share(int64_t units, int i, int n)
@@ -116,12 +133,24 @@ __device__ __forceinline__ int share_of(int64_t units, int64_t u, int n)
                                               static_cast<uint32_t>(units))
                            : static_cast<int>(((u + 1) * n - 1) / units);
 }
-__device__ __forceinline__ int64_t warp_begin(const Line& l, int w)
+template <bool PLACES = false>
+__device__ __forceinline__ int64_t warp_begin(const Kv8Attn& a, const Line& l, int w)
 {
+    if (PLACES && l.places > 1)
+        return l.U * weight_before(a, l, w) / weight_before(a, l, l.n);
     return w < l.n1 ? share(l.U1, w, l.n1) : l.U1 + (l.n > l.n1 ? share(l.U - l.U1, w - l.n1, l.n - l.n1) : 0);
 }
-__device__ __forceinline__ int warp_of(const Line& l, int64_t u)
+template <bool PLACES = false>
+__device__ __forceinline__ int warp_of(const Kv8Attn& a, const Line& l, int64_t u)
 {
+    if (PLACES && l.places > 1) {   // the last w whose begin, rounded down, is u or less
+        const int per = l.n / l.places;
+        int64_t rest = ((u + 1) * weight_before(a, l, l.n) - 1) / l.U;
+        int place = 0;
+        for (; place < l.places - 1 && rest >= static_cast<int64_t>(per) * a.place_weight[place]; ++place)
+            rest -= static_cast<int64_t>(per) * a.place_weight[place];
+        return place * per + static_cast<int>(min(rest / a.place_weight[place], static_cast<int64_t>(per - 1)));
+    }
     return u < l.U1 ? share_of(l.U1, u, l.n1) : l.n1 + share_of(l.U - l.U1, u - l.U1, l.n - l.n1);
 }
 

@@ -23,6 +23,17 @@ __device__ __forceinline__ uint4 pack8(const float* x)
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
+// Cosine and sine of turn / 2^32 turns. The nearest quarter is taken off in whole
+// numbers, so that what is left (an eighth at most) keeps all of a float's digits.
+__device__ __forceinline__ float2 cos_sin(uint32_t turn)
+{
+    const uint32_t quarter = (turn + (1u << 29)) >> 30;
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(turn - (quarter << 30))) * 0x1p-31f, &s, &c);
+    const float x = quarter & 1 ? -s : c, y = quarter & 1 ? c : s;
+    return quarter & 2 ? make_float2(-x, -y) : make_float2(x, y);
+}
+
 template <int L>
 __device__ __forceinline__ float row_sum(float x)
 {
@@ -55,8 +66,8 @@ __device__ __forceinline__ float row_max(float x)
 // The angle. A table holds f_i / 2 pi as 64-bit fractions of a turn; times the
 // position, modulo 2^64, is the exact fraction of the turn that the position comes
 // to, whatever its size, where an fp32 angle would be off by 2^-24 of all its
-// turns (a tenth of a radian at a position of a million). Its upper 32 bits go
-// through sincospif. That is some 40 instructions a pair, a third of a row's
+// turns (a tenth of a radian at a position of a million). The nearest quarter is taken
+// off its upper 32 bits, the rest goes through sincospif. That is some 40 instructions a pair, a third of a row's
 // arithmetic, so a block makes the sines and cosines of its tokens once, in shared
 // memory, while its first rows are on their way (made by each group of lanes for its
 // own heads: 37.5 us for the 8192 tokens). Shared memory holds what a lane reads in one
@@ -106,11 +117,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const int token = i / half, j = i - token * half;
         const int64_t pos = __ldg(a.positions + t0 + token);
         const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(a.turns + j);
-        float s, c;
-        sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
+        const float2 cs = cos_sin(static_cast<uint32_t>(turn >> 32));
         float* to = table + token * a.rot + (j / 4 % 2) * (half / 2) + j / 8 * 4 + j % 4;
-        to[0] = c * a.magnitude;
-        to[half] = s * a.magnitude;
+        to[0] = cs.x * a.magnitude;
+        to[half] = cs.y * a.magnitude;
     }
     const bool norms = a.q_weight || a.k_weight;
     if (threadIdx.x < 2 * L) {   // the lanes of the first groups load their runs of the queries' and the keys' weights
@@ -138,7 +148,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                 sum2 = fma2(F2(x[j], x[j + 1]), F2(x[j], x[j + 1]), sum2);
             const float sum = row_sum<L>(sum2.lo() + sum2.hi());
             if (live && (r < n_q ? a.q_weight : r < n_k ? a.k_weight : nullptr)) {
-                const float f = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+                const float mean = fmaf(sum, a.inv_d, a.eps);
+                float f = rsqrtf(mean);   // two units off at most: a Newton step takes it to half of one
+                if (mean >= 0x1p-100f && mean < 0x1p120f)
+                    f = fmaf(0.5f * f, fmaf(-mean * f, f, 1.0f), f);
                 const uint4 raw[2] = {weights[r < n_q ? 0 : 1][0][lane], weights[r < n_q ? 0 : 1][1][lane]};
                 float w[16];
                 unpack16(raw, w);
@@ -168,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     for (int i = j; i < j + 4; i += 2) {
                         const F2 lo(x[i], x[i + 1]), hi(x[8 + i], x[9 + i]);
                         const F2 cc(c[i - j], c[i - j + 1]), ss(s[i - j], s[i - j + 1]);
-                        const F2 y0 = fma2(mul2(hi, ss), F2(-1.0f, -1.0f), mul2(lo, cc)), y1 = fma2(lo, ss, mul2(hi, cc));
+                            const F2 y0 = fma2(hi, mul2(ss, F2(-1.0f, -1.0f)), mul2(lo, cc)), y1 = fma2(lo, ss, mul2(hi, cc));
                         x[i] = y0.lo(), x[i + 1] = y0.hi(), x[8 + i] = y1.lo(), x[9 + i] = y1.hi();
                     }
                 }

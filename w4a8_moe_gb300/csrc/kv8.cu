@@ -37,11 +37,18 @@ __device__ __forceinline__ RowAt row_at(const Kv8Rows& a, const int32_t* __restr
     r.slot = r.live ? __ldg(slots + r.t) : -1;
     return r;
 }
-__device__ __forceinline__ void encode_bf16(const uint4 (&raw)[2], float top, float s, uint2 (&c)[2])
+__device__ __forceinline__ void encode16(const uint4 (&raw)[2], float top, float s, uint2 (&c)[2])
 {
-    float x[16];
-    unpack16(raw, x);
-    encode16(x, top, s, c);
+    const Encoder encode(top, s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            e[j] = encode.two(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
+        c[i] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+    }
 }
 
 // The largest magnitude of 16 bf16 values, as bits: not finite from 0x7F80 on.
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kRowThreads) kv8_write_kernel(const __grid_con
         }
         if (ok) {
             uint2 c[2];
-            encode_bf16(raw[y], __uint_as_float(top << 16), s, c);
+            encode16(raw[y], __uint_as_float(top << 16), s, c);
             uint2* dst = reinterpret_cast<uint2*>((y ? v_cache : k_cache) + at * D);
             dst[lane] = c[0];
             dst[L + lane] = c[1];

@@ -58,7 +58,7 @@ struct Kv8Attn {
     int unit_shift;     // log2 of the keys of a unit
     int places;         // blocks that an SM holds, where the shares may go by them (else 0 or 1)
     int place_weight[4];   // their proportions
-    uint32_t* tickets;     // [4] shares of each place that are taken; zero between calls
+    uint32_t* tickets;     // [4] shares of each place that are taken, zero between calls; null but for the 4-bit cache
     int warps;          // that the units go to
     int free_warps;     // of them those that need not wait for the tiled prefix
     int spread;         // warps up to which the units are spread by twos
@@ -216,36 +216,35 @@ __device__ __forceinline__ void unpack16(const uint4 (&raw)[2], float (&x)[16])
     }
 }
 
-// E4M3(x / s) of 16 values, the quotient rounded to fp32 first; no |x| is above
-// top. A division of every value would be most of a call's arithmetic; here it is
-// q = x r with r = 1 / s correctly rounded, then q + (q s - x) (-r) by two fused
+// E4M3(x / s) of the values of a row, the quotient rounded to fp32 first; no |x| is
+// above top. A division of every value would be most of a call's arithmetic; here it
+// is q = x r with r = 1 / s correctly rounded, then q + (q s - x) (-r) by two fused
 // multiply-adds, which is the correctly rounded quotient where nothing under- or
 // overflows (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990). With 2^-60 <= s < 2^60 and values below 2^60 s
-// that holds for every quotient above 2^-11, and smaller ones have the code 0
-// either way; other rows divide. The residual is taken with that sign so that a
-// zero keeps its own: q s - x is +0 for x = -0, and +0 (-r) + (-0) is -0.
-__device__ __forceinline__ void encode16(const float (&x)[16], float top, float s, uint2 (&c)[2])
-{
-    const float r = __frcp_rn(s);
-    const bool plain = s >= 8.6736174e-19f && s < 1.1529215e18f && top < s * 1.1529215e18f;
-    const F2 r2(-r, -r), s2(s, s);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float lo = x[i * 8 + 2 * j], hi = x[i * 8 + 2 * j + 1];
-            if (plain) {
-                const F2 x(-lo, -hi), q = mul2(x, r2);
-                const F2 t = fma2(fma2(q, s2, x), r2, q);
-                e[j] = cvt_e4m3x2(t.hi(), t.lo());
-            } else {
-                e[j] = cvt_e4m3x2(__fdiv_rn(hi, s), __fdiv_rn(lo, s));
-            }
-        }
-        c[i] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+// System/6000 processor", 1990). With 2^-60 <= s < 2^60 and values below 2^60 s that
+// holds for every quotient above 2^-11, and smaller ones have the code 0 either way;
+// other rows divide. The residual is taken with that sign so that a zero keeps its
+// own: q s - x is +0 for x = -0, and +0 (-r) + (-0) is -0.
+struct Encoder {
+    float s;
+    bool plain;
+    F2 r2, s2;
+    __device__ __forceinline__ Encoder(float top, float scale)
+    {
+        const float r = __frcp_rn(scale);
+        s = scale;
+        plain = s >= 8.6736174e-19f && s < 1.1529215e18f && top < s * 1.1529215e18f;
+        r2 = F2(-r, -r), s2 = F2(s, s);
     }
-}
+    __device__ __forceinline__ uint32_t two(float lo, float hi) const   // codes of two values
+    {
+        if (plain) {
+            const F2 x(-lo, -hi), q = mul2(x, r2);
+            const F2 t = fma2(fma2(q, s2, x), r2, q);
+            return cvt_e4m3x2(t.hi(), t.lo());
+        }
+        return cvt_e4m3x2(__fdiv_rn(hi, s), __fdiv_rn(lo, s));
+    }
+};
 
 }  // namespace w4a8

@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
 // others do, and each takes few registers.
 constexpr int kJoinCta = 4;      // warps of a CTA where a row has one or less
 constexpr int kJoinSums = 128;   // sequences up to which a warp sums their units itself
-template <int D, int W, bool PLACES>   // PLACES: shares by the blocks' places (Line::places)
+template <int D, int W, bool BITS4>   // BITS4: tiles of several tokens, shares by the blocks' places
 __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
                                                                          const __grid_constant__ Kv8Prefix p, int R)
 {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     const int b = there ? head / a.Hq : 0, qh = there ? head - b * a.Hq : 0, h = qh / a.group, gi = qh - h * a.group;
     // units before the sequence's and all of them: a short sum over the lengths
     // while the kernel before is still at work, else what it left
-    const bool sum_here = a.B <= kJoinSums && !a.lead;
+    const bool sum_here = a.B <= kJoinSums && !(BITS4 && a.lead);
     int before = 0, units = 0, all = 0, tile = b;   // (the batch row that has the tile)
     if (sum_here) {
         for (int i = lane; i < a.B; i += L) {
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     } else {
         grid_dep_wait();
         if (a.max_pages) {
-            tile = a.lead ? a.lead[b] : b;
+            tile = BITS4 && a.lead ? a.lead[b] : b;
             before = a.cum[tile];
             units = a.cum[tile + 1] - before;
             all = a.cum[a.B];
@@ -525,14 +525,14 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     if (units) {
         const int in_tile = (b - tile) * a.group + gi, j = h * a.tiles + in_tile / R;
         const int64_t first = line.own + static_cast<int64_t>(before) * line.hr + static_cast<int64_t>(j) * units;
-        const int w = warp_of<PLACES>(a, line, first);
-        n2 += warp_of<PLACES>(a, line, first + units - 1) - w + 1;
+        const int w = warp_of<BITS4>(a, line, first);
+        n2 += warp_of<BITS4>(a, line, first + units - 1) - w + 1;
         at_own = static_cast<int64_t>(line.pairs_p + tile * line.hr + j + w - n1) * R + in_tile % R;
     }
     n2 = there ? n2 : 0;
     if (sum_here)
         grid_dep_wait();
-    if (PLACES && blockIdx.x == 0 && tid < 4)
+    if (BITS4 && blockIdx.x == 0 && tid < 4)
         a.tickets[tid] = 0;
     // Lane i of a row finds piece first_piece + S i and its weight; then every
     // lane reads its values of all of them. Nothing that is read waits for
@@ -715,23 +715,23 @@ static int join_warps(const Kv8Attn& a, const Kv8Prefix& p, int D, int num_sms)
     return heads > 18 * num_sms ? 0 : 1;
 }
 
-template <int D, bool PLACES>
+template <int D, bool BITS4>
 static cudaError_t launch_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int num_sms, cudaStream_t s)
 {
     const int heads = a.B * a.Hq, warps = join_warps(a, p, D, num_sms);
     if (warps > 1)
-        return launch_dependent(warps == 8   ? kv8_join_kernel<D, 8, PLACES>
-                                : warps == 4 ? kv8_join_kernel<D, 4, PLACES>
-                                             : kv8_join_kernel<D, 2, PLACES>,
+        return launch_dependent(warps == 8   ? kv8_join_kernel<D, 8, BITS4>
+                                : warps == 4 ? kv8_join_kernel<D, 4, BITS4>
+                                             : kv8_join_kernel<D, 2, BITS4>,
                                 dim3(heads), dim3(warps * 32), 0, s, a, p, R);
     const int rows = kJoinCta * (warps ? 1 : 2);   // of a CTA
-    return launch_dependent(warps ? kv8_join_kernel<D, 1, PLACES> : kv8_join_kernel<D, 0, PLACES>,
+    return launch_dependent(warps ? kv8_join_kernel<D, 1, BITS4> : kv8_join_kernel<D, 0, BITS4>,
                             dim3((heads + rows - 1) / rows), dim3(kJoinCta * 32), 0, s, a, p, R);
 }
 
 cudaError_t launch_kv_join(const Kv8Attn& a, const Kv8Prefix& p, int R, int D, int num_sms, cudaStream_t s)
 {
-    if (a.places > 1)
+    if (a.tickets)
         return D == 128 ? launch_join<128, true>(a, p, R, num_sms, s) : launch_join<64, true>(a, p, R, num_sms, s);
     return D == 128 ? launch_join<128, false>(a, p, R, num_sms, s) : launch_join<64, false>(a, p, R, num_sms, s);
 }

@@ -228,11 +228,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             } else {
                 s = __ldg(scale + h);
             }
-            uint2 c[2];
-            encode16(x, top, s, c);
+            const Encoder encode(top, s);
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                c[j] = encode.two(x[4 * j], x[4 * j + 1]) | (encode.two(x[4 * j + 2], x[4 * j + 3]) << 16);
             uint8_t* dst = (is_k ? a.k_cache : a.v_cache) + at * a.D;
-            *reinterpret_cast<uint2*>(dst + at0) = c[0];
-            *reinterpret_cast<uint2*>(dst + at1) = c[1];
+            *reinterpret_cast<uint2*>(dst + at0) = make_uint2(c[0], c[1]);
+            *reinterpret_cast<uint2*>(dst + at1) = make_uint2(c[2], c[3]);
         }
     }
 }

@@ -502,7 +502,8 @@ int rope_table(int rotary_dim, const double* inv_freq, double base, int scaling,
  *   interleaved 0: pairs (i, i + R/2), 1: pairs (2i, 2i + 1), i < R/2; the other
  *        D - R values of a head are not rotated.
  *   q_weight, k_weight [D] bf16 : x -> x / sqrt(mean(x^2) + eps) * w over the D
- *        values of a head, before the rotation; NULL: no norm.
+ *        values of a head, before the rotation; NULL: no norm. (The sum of squares is
+ *        held in fp32: values from 2^60 on leave it. A row of zeros needs eps > 0.)
  *   q_out, k_out bf16 : out, the same shapes; each may be its own input (same
  *        pointer and stride), else they must not overlap the inputs.
  *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin), all of it in fp32,

@@ -299,12 +299,13 @@ def test_attention_several_tokens_of_a_sequence(lib, hq, hkv, d, page, drafts):
 def test_attention_runs_of_tokens(lib, hq, hkv, d, page):
     """Runs of neighbours of one sequence, of every length: shorter and longer than what a tile of rows holds, the same
     sequence in several runs, lengths in any order within a run, tokens without keys inside one; few and many sequences."""
-    for rows, seed in ((6, 0), (60, 1)):
+    for rows, seed, runs in ((6, 0, (1, 2, 3, 5, 8, 16, 17, 33, 1, 2, 4)), (60, 1, (1, 2, 3, 5, 8, 16, 17, 33, 1, 2, 4)),
+                             (40, 2, (100, 61, 200, 1, 7, 140, 3))):   # (across 128 tokens, which a block sums at once)
         b = Batch([(53 * i) % 400 + 20 for i in range(rows)], hq, hkv, d, page, seed=seed + hq)
         full = b.lens_list
         rng = np.random.default_rng(seed)
         seqs, lens = [], []
-        for run in (1, 2, 3, 5, 8, 16, 17, 33, 1, 2, 4):
+        for run in runs:
             i = int(rng.integers(0, min(rows, 6)))
             seqs += [i] * run
             some = full[i] - np.arange(run)[::-1] if run % 2 else rng.integers(0, full[i] + 1, run)
@@ -314,7 +315,7 @@ def test_attention_runs_of_tokens(lib, hq, hkv, d, page):
         b.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
         gen = torch.Generator(device="cuda").manual_seed(seed)
         b.q = (torch.randn(len(seqs), hq, d, generator=gen, device="cuda") * 1.5).to(torch.bfloat16)
-        b.check(*b.run(lib))
+        b.check(*b.run(lib), every=1 if len(seqs) < 100 else 5)
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (6, 1, 128), (8, 2, 128)])

@@ -92,12 +92,13 @@ template <int L>
 __device__ __forceinline__ uint32_t bounds(const uint4 (&raw)[2])
 {
     const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
-    uint32_t hi = u[0], lo = u[0] ^ 0x80008000u;
+    uint32_t hi = u[0], lo = u[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
         hi = max_bf16x2(hi, u[i]);
-        lo = max_bf16x2(lo, u[i] ^ 0x80008000u);
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(u[i]));
     }
+    lo ^= 0x80008000u;
     uint32_t r = max_bf16x2(prmt(lo, hi, 0x5410), prmt(lo, hi, 0x7632));
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1)

@@ -90,9 +90,11 @@ __device__ __forceinline__ bool last_block(uint32_t* ticket)
 {
     __shared__ bool last;
     __syncthreads();
+    if (gridDim.x == 1)
+        return true;
     if (threadIdx.x == 0) {
         __threadfence();
-        last = gridDim.x == 1 || atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
+        last = atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
         __threadfence();
     }
     __syncthreads();

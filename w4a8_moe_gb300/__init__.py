@@ -755,7 +755,8 @@ def kv_pages_extend(lens, new_lens, page_table, free_pages, free_count, page_siz
             raise ValueError("capacity must be positive")
         with _on(stream):
             buf = torch.empty(2 * B + 1 + 4 * capacity, dtype=_I32, device=lens.device)
-        out = PageStep(*buf.split_with_sizes((B + 1, capacity, capacity, capacity, capacity, B)))
+        # (whole numbers: no views that a gradient would have to know of, which take longer to make and to free)
+        out = PageStep(*buf.unsafe_split_with_sizes((B + 1, capacity, capacity, capacity, capacity, B)))
         at, step = buf.data_ptr(), 4 * capacity
         tokens = at + 4 * (B + 1)
         to = at, tokens, tokens + step, tokens + 2 * step, tokens + 3 * step, tokens + 4 * step

@@ -537,6 +537,25 @@ def test_another_stream(lib):
         assert torch.equal(o, want[0]) and torch.equal(z, want[1])
 
 
+def test_two_calls_at_once(lib):
+    """Two calls on two streams, each with its workspace, large and small: each gives the bits it gives alone."""
+    a, b = Batch([6000] * 40, 32, 8, 128, 64, seed=61), Batch([200, 7000, 3], 8, 2, 64, 16, seed=62, drafts=2)
+    ws = [torch.zeros(lib.kv4_attention_workspace_size(n, hq, hkv, d, 1, 16), dtype=torch.uint8, device="cuda")
+          for n, hq, hkv, d in ((40, 32, 8, 128), (6, 8, 2, 64))]
+    want = [x.run(lib, ws=w) for x, w in zip((a, b), ws)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    differ = [torch.zeros((), dtype=torch.int64, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got = x.run(lib, ws=ws[i])
+                differ[i] += (got[0] != want[i][0]).sum() + (got[1] != want[i][1]).sum()
+    torch.cuda.synchronize()
+    assert [int(x) for x in differ] == [0, 0] and all(lib.w4a8_device_error(w) == 0 for w in ws)
+
+
 def test_graph_capture_with_growing_lengths(lib):
     """A captured step (write, attention, reading back) follows the lengths and pages that stand in device memory."""
     b = Batch([5, 60, 33], 12, 2, 128, 16, seed=17)

@@ -641,14 +641,24 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     if (!there)
         return;
     const bool empty = sum == 0.0f;
+    // Of very many rows one division each, not one a value (1024 sequences of 10-100 keys
+    // of 4 bits 55.2 -> 53.4 us; few rows of D 64 were slower so, 24.4 -> 27.4).
+    constexpr bool kOnce = BITS4 && W == 0 && D == 128;
+    if (kOnce) {
+        const float f = empty ? 0.0f : __frcp_rn(sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            acc[i] = empty ? 0.0f : acc[i] * f;
+    }
     uint16_t* dst = a.out + static_cast<int64_t>(head) * D;
 #pragma unroll
     for (int i = 0; i < V; i += F) {
         uint32_t r[F / 2];
 #pragma unroll
         for (int j = 0; j < F; j += 2)
-            r[j / 2] = static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[i + j] / sum)) |
-                       (static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[i + j + 1] / sum)) << 16);
+            r[j / 2] = kOnce ? pack_bf16(acc[i + j], acc[i + j + 1])
+                             : static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[i + j] / sum)) |
+                                   (static_cast<uint32_t>(float_to_bf16_bits(empty ? 0.0f : acc[i + j + 1] / sum)) << 16);
         uint16_t* x = dst + (i / F * L + lane) * F;
         if (F == 4)
             *reinterpret_cast<uint2*>(x) = make_uint2(r[0], r[F / 2 - 1]);

@@ -20,7 +20,7 @@ namespace w4a8 {
 namespace {
 
 constexpr int kWarps = 4;    // per CTA; they share nothing but the prefix sums
-constexpr int kUnitShift = 5;
+constexpr int kUnitShift = kKv4UnitShift;
 constexpr int kUnit = 1 << kUnitShift;   // keys
 constexpr int kSub = kUnit / 16;         // of them in one product
 constexpr int kDescs = 64;   // unit descriptors held per warp (two batches of 32)
@@ -67,7 +67,7 @@ __device__ __forceinline__ int sum_lengths(const Kv8Attn& a, int* cum, int* warp
     int n = 0;
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
-        n += seq_units(a, b);
+        n += seq_units(a, b, kUnitShift);
         if (blockIdx.x == 0 && a.max_pages &&
             static_cast<unsigned>(__ldg(a.lens + b)) > static_cast<unsigned>(a.max_pages << a.page_shift))
             set_error(a.err, kErrBitIndex);
@@ -90,7 +90,7 @@ __device__ __forceinline__ int sum_lengths(const Kv8Attn& a, int* cum, int* warp
         cum[b] = base;
         if (blockIdx.x == 0)
             a.cum[b] = base;
-        base += seq_units(a, b);
+        base += seq_units(a, b, kUnitShift);
     }
     if (tid == 0) {
         cum[a.B] = total;
@@ -137,7 +137,7 @@ __device__ __forceinline__ int sum_tiles(const Kv4Attn& a, int* cum, int* warp_s
             }
             if (in_tile == 0)
                 for (int j = 0; j < a.per_tile && b + j < a.B && __ldg(a.seqs + b + j) == seq; ++j)
-                    n = max(n, seq_units(a, b + j));
+                    n = max(n, seq_units(a, b + j, kUnitShift));
         }
         int s = n;
 #pragma unroll
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
     const uint32_t ring = smem_u32(smem) + warp * S::total;
     __syncthreads();
 
-    const Line line = make_line(a, total);
+    const Line line = make_line(a, total, kUnitShift);
     // Few units: one warp on each SM before a second. Very many: a block takes one of the
     // shares for its place on the SM, and where those are gone one of another place's
     // (which block does a share changes no result). There are as many shares as blocks,

@@ -30,6 +30,7 @@ cudaError_t launch_kv8_read(const Kv8Rows& a, const uint8_t* k_cache, const uint
 constexpr int kKv8MaxBatch = 4096;  // the split's prefix sums live in shared memory
 constexpr int kKv8UnitShift = 4;    // keys per unit of the split (a unit never crosses a page)
 constexpr int kKv8Unit = 1 << kKv8UnitShift;
+constexpr int kKv4UnitShift = 5;    // of the 4-bit cache
 constexpr int kKv8MaxWarps = 152 * 16;   // warps the units are divided over, at most
 
 struct Kv8Attn {
@@ -55,7 +56,7 @@ struct Kv8Attn {
     uint32_t* err;
     uint16_t* out;
     float* lse;
-    int unit_shift;     // log2 of the keys of a unit
+    int unit_shift;     // log2 of the keys of a unit, for the host
     int places;         // blocks that an SM holds, where the shares may go by them (else 0 or 1)
     int place_weight[4];   // their proportions
     uint32_t* tickets;     // [4] shares of each place that are taken, zero between calls; null but for the 4-bit cache

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
     fence_mbar_init();
     __syncthreads();
 
-    const Line line = make_line(a, carry);
+    const Line line = make_line(a, carry, kKv8UnitShift);
     // few units: one warp on each SM before a second; the first CTAs run first, and
     // the late ones go on from the last warp of theirs that has a share
     const int first = a.free_warps / kWarps, block = static_cast<int>(blockIdx.x);
@@ -476,6 +476,7 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     constexpr int L = W ? 32 : 16;                  // lanes of a row
     constexpr int V = D / L, F = V >= 4 ? 4 : 2;    // values of a lane, in groups of F that stand L F apart
     constexpr int S = W ? W : 1;                    // strides over the pieces
+    constexpr int kUnitShift = BITS4 ? kKv4UnitShift : kKv8UnitShift;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid % L;
     const int head = W > 1 ? blockIdx.x : blockIdx.x * (kJoinCta * 32 / L) + tid / L;   // b * Hq + query head
     const int first_piece = W > 1 ? warp : 0;
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     int before = 0, units = 0, all = 0, tile = b;   // (the batch row that has the tile)
     if (sum_here) {
         for (int i = lane; i < a.B; i += L) {
-            const int n = seq_units(a, i);
+            const int n = seq_units(a, i, kUnitShift);
             all += n;
             before += i < b ? n : 0;
             units += i == b ? n : 0;
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
             all = a.cum[a.B];
         }
     }
-    const Line line = make_line(a, all);
+    const Line line = make_line(a, all, kUnitShift);
 
     // the row's pieces: [0, n0) of the tiled prefix, [n0, n1) of the untiled one, [n1, n2) of its own keys
     const int row = b * a.group + gi;

@@ -64,9 +64,9 @@ __device__ __forceinline__ int seq_len(const Kv8Attn& a, int b)
 {
     return a.max_pages ? min(max(__ldg(a.lens + b), 0), a.max_pages << a.page_shift) : 0;
 }
-__device__ __forceinline__ int seq_units(const Kv8Attn& a, int b)
+__device__ __forceinline__ int seq_units(const Kv8Attn& a, int b, int unit_shift)
 {
-    return static_cast<int>((static_cast<unsigned>(seq_len(a, b)) + (1u << a.unit_shift) - 1) >> a.unit_shift);
+    return static_cast<int>((static_cast<unsigned>(seq_len(a, b)) + (1u << unit_shift) - 1) >> unit_shift);
 }
 // Warps for so many units. Two units are in flight at once, so a second pair of
 // them costs a warp another latency (one sequence of 8 heads and 64 keys: 8.4 us
@@ -78,12 +78,12 @@ __host__ __device__ __forceinline__ int warps_for(int64_t units, int spread, int
     const int u = units < 1 << 16 ? static_cast<int>(units) : 1 << 16;
     return min(max(min((u + 1) >> 1, spread), u >> 2), most);
 }
-__device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total)
+__device__ __forceinline__ Line make_line(const Kv8Attn& a, int64_t seq_total, int unit_shift)
 {
     Line l;
     l.hr = a.Hkv * a.tiles;
     l.pairs_p = a.Hkv * a.ptiles;
-    l.up = (a.prefix_len + (1 << a.unit_shift) - 1) >> a.unit_shift;
+    l.up = (a.prefix_len + (1 << unit_shift) - 1) >> unit_shift;
     l.own = static_cast<int64_t>(l.pairs_p) * l.up;
     l.U = l.own + seq_total * l.hr;
     l.U1 = l.U;
@@ -164,7 +164,7 @@ __device__ __forceinline__ int sum_units(const Kv8Attn& a, int* cum, int* warp_s
     int carry = 0;
     for (int b0 = 0; b0 < a.B; b0 += WARPS * 32) {
         const int b = b0 + tid;
-        const int n = b < a.B ? seq_units(a, b) : 0;
+        const int n = b < a.B ? seq_units(a, b, kKv8UnitShift) : 0;
         if (blockIdx.x == 0 && b < a.B && a.max_pages &&
             static_cast<unsigned>(__ldg(a.lens + b)) > static_cast<unsigned>(a.max_pages << a.page_shift))
             set_error(a.err, kErrBitIndex);

@@ -142,6 +142,21 @@ def test_extend_and_truncate(lib, batch, page, longest, new, pad, in_place):
         state = (after, *state[1:])
 
 
+@pytest.mark.parametrize("batch", range(4084, 4097))
+def test_largest_batches(lib, batch):
+    """Their sums take a block's shared memory past the 48 KB that need no asking for."""
+    p = Pool([b % 17 for b in range(batch)], 16, 3, spare=batch, seed=batch)
+    state = p.gpu()
+    ws = workspace(lib)
+    new = [b % 3 for b in range(batch)]
+    step = extend_and_compare(lib, p, state, new, sum(new) + 1, ws)
+    keep = [n // 2 for n in p.lens]
+    after = lib.kv_pages_truncate(step.lens, torch.tensor(keep, dtype=I32, device="cuda"), *state[1:], 16, ws=ws)
+    p.truncate(keep)
+    same_pool(p, *state[1:], after)
+    assert lib.w4a8_device_error(ws) == 0
+
+
 def test_truncating_what_was_extended_restores_the_stack(lib):
     p = Pool([3, 0, 64, 65, 200], 16, 40, spare=30)
     lens, table, stack, count = p.gpu()

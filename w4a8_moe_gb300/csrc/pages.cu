@@ -265,7 +265,7 @@ static unsigned blocks_for(int64_t items, int num_sms)
 template <class A>
 static cudaError_t launch(void (*kern)(A), const A& a, unsigned blocks, int smem, cudaStream_t s)
 {
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {   // with what the kernel holds besides, 48 KB need to be asked for
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;

@@ -345,6 +345,13 @@ def test_attention_largest_batch(lib, hq, hkv, d):
     b.check(*b.run(lib), every=37)
 
 
+def test_attention_shared_memory_at_its_default_limit(lib):
+    """Batches whose prefix sums take a block's shared memory past the 48 KB that need no asking for."""
+    for batch in range(1524, 1540):
+        b = Batch([i % 5 for i in range(batch)], 1, 1, 128, 16, seed=batch)
+        b.check(*b.run(lib), every=211)
+
+
 @pytest.mark.parametrize("batch,hq,hkv,d,own,extra,page", [
     (1, 16, 1, 128, 9000, 1, 64),     # many pieces a row, joined by eight warps
     (3, 8, 8, 64, 5000, 1, 16),

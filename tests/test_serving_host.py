@@ -165,6 +165,20 @@ def test_table_by_pairs_and_by_wavelength():
         assert g == pytest.approx(f * keep + f / 8 * (1 - keep), rel=1e-10)
 
 
+def test_table_by_pairs_where_no_pair_is_between():
+    """All pairs turn more than `high` times over the original length, or all of them less than `low` times."""
+    for rot, base, length, low, high, ratio in ((64, 2.0, 4.0e5, 1.0, 32.0, 1), (16, 10.0, 1.0e9, 1.0, 32.0, 1),
+                                                (64, 10000.0, 4.0, 1.0, 32.0, 8), (16, 100.0, 64.0, 900.0, 1000.0, 8),
+                                                (128, 1.5, 2.0, 1.0, 32.0, 8)):
+        plain = radians(pkg.rope_table(rot, base=base, device="cpu"))
+        over = [length * f / (2 * math.pi) for f in plain]
+        assert min(over) > high if ratio == 1 else max(over) < low
+        got = radians(pkg.rope_table(rot, base=base, scaling="yarn", factor=8.0, original_len=length, low=low, high=high,
+                                     device="cpu"))
+        for f, g in zip(plain, got):
+            assert f / g == pytest.approx(ratio, rel=1e-12)
+
+
 def test_table_of_own_frequencies():
     own = [1.0, -0.25, 0.0, 6.25, -6.25, 1e-12, 2 * math.pi, 0.5]
     for got, x in zip(radians(pkg.rope_table(16, inv_freq=own, device="cpu")), own):

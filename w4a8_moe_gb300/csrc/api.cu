@@ -899,8 +899,10 @@ int rope_table(int rotary_dim, const double* inv_freq, double base, int scaling,
         const double per = R / (2.0 * std::log(base));
         first = std::max(std::floor(per * std::log(original_len / (high * two_pi))), 0.0);
         last = std::min(std::ceil(per * std::log(original_len / (low * two_pi))), R - 1.0);
-        if (last == first)
-            last += 0.001;   // a step
+        if (last < 0.0)   // even the first pair turns less than `low` times
+            first = last - 1.0;
+        else if (last <= first)   // a step, behind all pairs where the last one still turns more than `high` times
+            last = first + 0.001;
         *magnitude = static_cast<float>(0.1 * std::log(factor) + 1.0);
     }
     for (int i = 0; i < n; ++i) {

@@ -252,7 +252,7 @@ static cudaError_t launch(Rope a, int num_sms, cudaStream_t s)
     const int64_t passes = static_cast<int64_t>(a.T) * ((rows + G - 1) / G), each = static_cast<int64_t>(num_sms) * 16;
     a.tokens = static_cast<int>(min(max(passes / each, int64_t{1}), int64_t{kMostTokens}));
     a.slice = passes < each ? G : rows;
-    const dim3 grid((a.T + a.tokens - 1) / a.tokens, (rows + a.slice - 1) / a.slice);
+    const dim3 grid((a.T - 1) / a.tokens + 1, (rows + a.slice - 1) / a.slice);
     return launch_dependent(a.interleaved ? rope_kernel<L, true, CACHE> : rope_kernel<L, false, CACHE>, grid,
                             dim3(kThreads), a.tokens * a.rot * static_cast<int>(sizeof(float)), s, a);
 }

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     for (int i = j; i < j + 4; i += 2) {
                         const F2 lo(x[i], x[i + 1]), hi(x[8 + i], x[9 + i]);
                         const F2 cc(c[i - j], c[i - j + 1]), ss(s[i - j], s[i - j + 1]);
-                            const F2 y0 = fma2(hi, mul2(ss, F2(-1.0f, -1.0f)), mul2(lo, cc)), y1 = fma2(lo, ss, mul2(hi, cc));
+                        const F2 y0 = fma2(hi, mul2(ss, F2(-1.0f, -1.0f)), mul2(lo, cc)), y1 = fma2(lo, ss, mul2(hi, cc));
                         x[i] = y0.lo(), x[i + 1] = y0.hi(), x[8 + i] = y1.lo(), x[9 + i] = y1.hi();
                     }
                 }

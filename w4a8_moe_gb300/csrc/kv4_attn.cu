@@ -676,7 +676,12 @@ cudaError_t launch_kv4_attn(const Kv4Attn& in, int D, int num_sms, cudaStream_t 
     a.unit_shift = kUnitShift;
     const int64_t pairs = static_cast<int64_t>(a.Hkv) * a.B * a.tiles;
     const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
-    const int blocks = min(R == 8 ? 4 : D == 64 ? 3 : 2, fit);
+    // 16 rows of D 64 by two until the tables allow many units (16 query and 1 kv heads, us
+    // at two / three: 24 sequences of up to 5001 keys with 4 drafts each, 15000 units, 22.6 /
+    // 24.4; 96 of 1000-3000 17.4 / 18.3, 8 of 16000 13.6 / 15.0; 64 of 8000, 16000 units,
+    // 23.6 / 23.1, 256 of 4000, 32000 units, 37.2 / 34.9).
+    const int64_t units = pairs * ((static_cast<int64_t>(a.max_pages) << a.page_shift) >> kUnitShift);
+    const int blocks = min(R == 8 ? 4 : D == 64 && units >= 20000 ? 3 : 2, fit);
     a.warps = min(num_sms * blocks * kWarps, kKv8MaxWarps / kWarps * kWarps);
     a.free_warps = a.warps;
     // Shares by place where four blocks fit an SM (two or three, of 16 rows, gain nothing).

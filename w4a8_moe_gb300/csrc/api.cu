@@ -149,8 +149,8 @@ struct MoeWs {
     uint8_t* hq;
     unsigned long long* s0h;
     float* ypart;
-    float* hf;             // dynamic intermediate scale only
-    unsigned int* hmax;    // header word at byte 64 (dynamic only)
+    float* hf;             // dynamic intermediate scale only, and the next
+    unsigned int* hmax;    // max|h| of a call (not in the header: it stays behind)
     int* done;             // [256] per-expert progress counters (one-launch forward)
     uint8_t* wq8;          // prefill: the weights unpacked once per call
     int* sync;             // prefill: the down GEMM's pacing counters
@@ -168,7 +168,7 @@ static size_t moe_ws(int T, int H, int I, int E, int k, MoeWs* w, void* ws, bool
     w->done = c.take<int>(256 * 4);
     w->wq8 = c.take<uint8_t>(moe_unpack_once(T) ? static_cast<size_t>(E) * 3 * I * H : 0);
     w->sync = c.take<int>(moe_unpack_once(T) ? static_cast<size_t>(kMoeSyncInts) * 4 : 0);
-    w->hmax = ws ? reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + 64) : nullptr;
+    w->hmax = c.take<unsigned int>(dynamic ? 4 : 0);
     return c.off;
 }
 

@@ -1,0 +1,81 @@
+"""Calls from several host threads at once whose kernels need different amounts of shared memory: every one of them is
+launched, and gives what it gives alone."""
+import sys
+import threading
+
+import pytest
+import torch
+
+from helpers import ensure_built
+from test_kv4 import Batch as Batch4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ensure_built()
+    import w4a8_moe_gb300 as pkg
+    return pkg
+
+
+class Recorder:
+    """The library, with the arguments of every call that went to it."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        f = getattr(self.real, name)
+
+        def call(*args):
+            self.calls.append((f, args))
+            return f(*args)
+        return call
+
+
+def at_once(lib, monkeypatch, calls, outputs, times=4000):
+    """Makes each of `calls` on a stream of its own, then all of them again and again from a thread each, straight through
+    the C entry points; what they wrote has to be what they wrote alone."""
+    recorder = Recorder(lib._load())
+    monkeypatch.setattr(lib, "_lib", recorder)
+    made = []
+    for call in calls:
+        recorder.calls = []
+        call(torch.cuda.Stream())
+        made.append([c for c in recorder.calls if c[1] and not c[0].__name__.endswith("size")])
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in outputs]
+    refused, gate = [], threading.Barrier(len(made))
+
+    def work(own):
+        gate.wait()
+        for _ in range(times):
+            refused.extend(s for s in [f(*args) for f, args in own] if s)
+
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(own,)) for own in made]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(before)
+    torch.cuda.synchronize()
+    assert not refused, (len(refused), refused[0])
+    assert all(torch.equal(x, y) for x, y in zip(outputs, want))
+
+
+@pytest.mark.parametrize("hq,hkv,drafts", [(1, 1, 1), (1, 1, 4), (16, 1, 1)])
+def test_attention_over_4_bits(lib, monkeypatch, hq, hkv, drafts):
+    calls, outputs = [], []
+    for tokens in (4096, 2000, 4096, 3000):
+        b = Batch4([i % 5 for i in range(tokens // drafts)], hq, hkv, 128, 16, seed=81, drafts=drafts)
+        ws = torch.zeros(lib.kv4_attention_workspace_size(tokens, hq, hkv, 128, 1, 16), dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty_like(b.q), torch.empty(tokens, hq, device="cuda")
+        calls.append(lambda s, b=b, ws=ws, out=out, lse=lse: b.run(lib, ws=ws, out=out, lse=lse, stream=s))
+        outputs += [out, lse]
+    at_once(lib, monkeypatch, calls, outputs)

@@ -11,6 +11,8 @@ from test_kv4 import Batch as Batch4
 
 pytestmark = pytest.mark.gpu
 
+I32 = torch.int32
+
 
 @pytest.fixture(scope="module")
 def lib():
@@ -78,4 +80,20 @@ def test_attention_over_4_bits(lib, monkeypatch, hq, hkv, drafts):
         out, lse = torch.empty_like(b.q), torch.empty(tokens, hq, device="cuda")
         calls.append(lambda s, b=b, ws=ws, out=out, lse=lse: b.run(lib, ws=ws, out=out, lse=lse, stream=s))
         outputs += [out, lse]
+    at_once(lib, monkeypatch, calls, outputs)
+
+
+def test_page_tables(lib, monkeypatch):
+    """No pages move (all tokens fit their last page), so that every call finds what the first one found."""
+    calls, outputs = [], []
+    for batch in (4096, 4050, 4096, 4020):
+        lens = torch.tensor([1 + b % 13 for b in range(batch)], dtype=I32, device="cuda")
+        new = torch.tensor([b % 3 for b in range(batch)], dtype=I32, device="cuda")
+        pool = (torch.arange(batch, dtype=I32, device="cuda").view(batch, 1), torch.arange(batch, dtype=I32, device="cuda"),
+                torch.zeros(1, dtype=I32, device="cuda"), 16)
+        ws = torch.zeros(lib.kv_pages_workspace_size(), dtype=torch.uint8, device="cuda")
+        step = lib.PageStep(*[torch.empty(n, dtype=I32, device="cuda") for n in [batch + 1] + [2 * batch] * 4 + [batch]])
+        calls.append(lambda s, a=(lens, new, *pool), step=step, ws=ws, batch=batch:
+                     lib.kv_pages_extend(*a, 2 * batch, out=step, ws=ws, stream=s))
+        outputs += step
     at_once(lib, monkeypatch, calls, outputs)

@@ -263,19 +263,25 @@ static unsigned blocks_for(int64_t items, int num_sms)
 }
 
 template <class A>
-static cudaError_t launch(void (*kern)(A), const A& a, unsigned blocks, int smem, cudaStream_t s)
+static cudaError_t launch(void (*kern)(A), const A& a, unsigned blocks, int ints, int most_ints, cudaStream_t s)
 {
-    if (smem > 47 * 1024) {   // with what the kernel holds besides, 48 KB need to be asked for
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // More than 48 KB, with what the kernel holds besides, have to be asked for: always
+    // the most that a call can need, as another thread's call may be between here and its launch.
+    if (ints * 4 > 47 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_ints * 4);
         if (e != cudaSuccess)
             return e;
     }
-    return launch_dependent(kern, dim3(blocks), dim3(kThreads), smem, s, a);
+    return launch_dependent(kern, dim3(blocks), dim3(kThreads), ints * 4, s, a);
 }
+
+// Integers that the kernels' arrays of a call of B sequences take.
+static int extend_ints(int B) { return 3 * B + 2; }
+static int truncate_ints(int B) { return 2 * B + 1; }
 
 cudaError_t launch_pages_extend(const PagesExtend& a, int num_sms, cudaStream_t s)
 {
-    return launch(pages_extend_kernel, a, blocks_for(a.T, num_sms), (3 * a.B + 2) * 4, s);
+    return launch(pages_extend_kernel, a, blocks_for(a.T, num_sms), extend_ints(a.B), extend_ints(kPagesMostSeqs), s);
 }
 
 cudaError_t launch_pages_truncate(const PagesTruncate& a, int num_sms, cudaStream_t s)
@@ -283,7 +289,7 @@ cudaError_t launch_pages_truncate(const PagesTruncate& a, int num_sms, cudaStrea
     // how many pages go back only the device knows: the most that it could be
     const int64_t most = static_cast<int64_t>(a.B) * a.p.max_pages;
     return launch(pages_truncate_kernel, a, blocks_for(most < a.p.num_pages ? most : a.p.num_pages, num_sms),
-                  (2 * a.B + 1) * 4, s);
+                  truncate_ints(a.B), truncate_ints(kPagesMostSeqs), s);
 }
 
 }  // namespace w4a8

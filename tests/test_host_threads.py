@@ -1,13 +1,15 @@
 """Calls from several host threads at once whose kernels need different amounts of shared memory: every one of them is
 launched, and gives what it gives alone."""
+import subprocess
 import sys
 import threading
 
 import pytest
 import torch
 
-from helpers import ensure_built
+from helpers import ROOT, ensure_built
 from test_kv4 import Batch as Batch4
+from test_kv8 import Batch as Batch8
 
 pytestmark = pytest.mark.gpu
 
@@ -83,6 +85,19 @@ def test_attention_over_4_bits(lib, monkeypatch, hq, hkv, drafts):
     at_once(lib, monkeypatch, calls, outputs)
 
 
+@pytest.mark.parametrize("hq,hkv,mode", [(1, 1, 0), (16, 1, 1)])
+def test_attention_over_8_bits(lib, monkeypatch, hq, hkv, mode):
+    calls, outputs = [], []
+    for batch in (4096, 2900, 4096, 3500):
+        b = Batch8([i % 5 for i in range(batch)], 0, hq, hkv, 128, 16, mode, seed=82)
+        ws = torch.zeros(lib.kv8_prefix_attention_workspace_size(batch, hq, hkv, 128, 0, 10, 16), dtype=torch.uint8,
+                         device="cuda")
+        out, lse = torch.empty_like(b.q), torch.empty(batch, hq, device="cuda")
+        calls.append(lambda s, b=b, ws=ws, out=out, lse=lse: b.run(lib, ws=ws, out=out, lse=lse, stream=s))
+        outputs += [out, lse]
+    at_once(lib, monkeypatch, calls, outputs)
+
+
 def test_page_tables(lib, monkeypatch):
     """No pages move (all tokens fit their last page), so that every call finds what the first one found."""
     calls, outputs = [], []
@@ -97,3 +112,24 @@ def test_page_tables(lib, monkeypatch):
                      lib.kv_pages_extend(*a, 2 * batch, out=step, ws=ws, stream=s))
         outputs += step
     at_once(lib, monkeypatch, calls, outputs)
+
+
+CHILD = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import torch
+import w4a8_moe_gb300 as lib
+from test_kv8 import Batch
+for batch in range(2678, 2692):
+    b = Batch([i % 5 for i in range(batch)], 0, {hq}, 1, 128, 16, {mode}, seed=batch)
+    b.check(*b.run(lib), every=211)
+print("all right")
+"""
+
+
+@pytest.mark.parametrize("hq,mode", [(1, 0), (1, 1), (16, 0), (16, 1)])
+def test_attention_over_8_bits_at_the_shared_memory_that_needs_no_asking(lib, hq, mode):
+    """In a process of its own: a larger batch before would have asked for more already."""
+    r = subprocess.run([sys.executable, "-c", CHILD.format(root=ROOT, hq=hq, mode=mode)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "all right" in r.stdout, r.stderr[-2000:]

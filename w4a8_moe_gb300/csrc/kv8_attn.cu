@@ -677,8 +677,11 @@ static cudaError_t launch_pieces(const Kv8Attn& a, cudaStream_t s)
 {
     const int smem = ring_smem(D, a.B);
     auto kern = kv8_attn_kernel<D, NT, TOK, PER_SM>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // More than 48 KB, with what the kernel holds besides, have to be asked for: always
+    // the most that a call can need, as another thread's call may be between here and its launch.
+    if (smem > 47 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_smem(D, kKv8MaxBatch));
         if (e != cudaSuccess)
             return e;
     }

@@ -23,13 +23,16 @@ __device__ __forceinline__ uint4 pack8(const float* x)
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Cosine and sine of turn / 2^32 turns. The nearest quarter is taken off in whole
-// numbers, so that what is left (an eighth at most) keeps all of a float's digits.
-__device__ __forceinline__ float2 cos_sin(uint32_t turn)
+// Cosine and sine of turn / 2^64 turns. The nearest quarter is taken off in whole
+// numbers and the rest (an eighth at most) converted once, so that however near an
+// angle is to a quarter's end its sine there keeps all of a float's digits. (The upper
+// 32 bits alone are off by 2^-32 of a turn, which is 0.4 % of the first position's sine
+// of a pair that turns by 210 of them.)
+__device__ __forceinline__ float2 cos_sin(uint64_t turn)
 {
-    const uint32_t quarter = (turn + (1u << 29)) >> 30;
+    const uint32_t quarter = static_cast<uint32_t>((turn + (uint64_t{1} << 61)) >> 62);
     float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(turn - (quarter << 30))) * 0x1p-31f, &s, &c);
+    sincospif(__ll2float_rn(static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62))) * 0x1p-63f, &s, &c);
     const float x = quarter & 1 ? -s : c, y = quarter & 1 ? c : s;
     return quarter & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
@@ -67,7 +70,7 @@ __device__ __forceinline__ float row_max(float x)
 // position, modulo 2^64, is the exact fraction of the turn that the position comes
 // to, whatever its size, where an fp32 angle would be off by 2^-24 of all its
 // turns (a tenth of a radian at a position of a million). The nearest quarter is taken
-// off its upper 32 bits, the rest goes through sincospif. That is some 40 instructions a pair, a third of a row's
+// off it, the rest goes through sincospif. That is dozens of instructions a pair, a third of a row's
 // arithmetic, so a block makes the sines and cosines of its tokens once, in shared
 // memory, while its first rows are on their way (made by each group of lanes for its
 // own heads: 37.5 us for the 8192 tokens). Shared memory holds what a lane reads in one
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const int token = i / half, j = i - token * half;
         const int64_t pos = __ldg(a.positions + t0 + token);
         const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(a.turns + j);
-        const float2 cs = cos_sin(static_cast<uint32_t>(turn >> 32));
+        const float2 cs = cos_sin(turn);
         float* to = table + token * a.rot + (j / 4 % 2) * (half / 2) + j / 8 * 4 + j % 4;
         to[0] = cs.x * a.magnitude;
         to[half] = cs.y * a.magnitude;

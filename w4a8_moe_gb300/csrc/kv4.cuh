@@ -17,11 +17,8 @@ cudaError_t launch_kv4_read(const Kv8Rows& a, const uint8_t* k_cache, const uint
                             const uint32_t* v_scale, const int32_t* slots, uint16_t* k, uint16_t* v, cudaStream_t s);
 
 // Decode attention: the rows of the batch are query tokens, each with its own
-// length (`lens`), and `seqs` says whose page table a token reads (null: its own).
-// The scale pointers of the base are those of the pairs above.
+// length (`lens`). The scale pointers of the base are those of the pairs above.
 struct Kv4Attn : Kv8Attn {
-    const int32_t* seqs;
-    int num_seqs;
     int per_tile;   // tokens of a sequence that a tile of rows holds
 };
 cudaError_t launch_kv4_attn(const Kv4Attn& a, int D, int num_sms, cudaStream_t s);

@@ -541,8 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    // (from 2^27 on a float's steps are larger than kWeightTop)
-                    const float to = fmaxf(m[t][y], fabsf(top) < 0x1p27f ? top - kWeightTop : top);
+                    const float to = fmaxf(m[t][y], reference(top));
                     f[y] = ex2(m[t][y] - to);
                     m[t][y] = to;
 #pragma unroll

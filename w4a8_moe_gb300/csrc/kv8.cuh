@@ -67,6 +67,9 @@ struct Kv8Attn {
     int beside;         // a tiled prefix runs beside
     int* cum;           // [B + 1] prefix sums of the sequences' units, left for the join
     int* lead;          // [B] the row of the batch in whose tile each one is, or null: its own
+    const int32_t* seqs;   // [B] whose page table a row of the batch reads (null: its own)
+    int num_seqs;
+    int per_token;      // scales for each token and head (else for each head; not for 4 bits)
 };
 // The prefix on the tensor cores: CTAs of (kv head, 256 rows, a range of key
 // tiles); part_* [split][kv head][row] as above.
@@ -127,6 +130,18 @@ constexpr float kWeightMost = 15.0f;
 // most, added up over the keys of a piece.
 constexpr float kLeastScale = 0x1p-92f;
 constexpr float kLeastScaleLog2 = -92.0f;
+
+// From these scores (log2) on a float's steps, 8 and more, leave no room for
+// kWeightTop or a scale's size beside a score. A row with such a score gets kWild for
+// its reference, under which all other weights are 0, and the join computes it from
+// the definition (wild_row), which costs the ordinary ones nothing.
+constexpr float kEnormous = 0x1p26f;
+constexpr float kWild = 0x1p127f;
+// The reference for a largest score of `top`, in the log2 of a weight times its value's size.
+__device__ __forceinline__ float reference(float top)
+{
+    return fabsf(top) >= kEnormous && top > -INFINITY ? kWild : top - kWeightTop;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    const float to = fmaxf(m[t][y], top - kWeightTop);
+                    const float to = fmaxf(m[t][y], reference(top));
                     const float f = ex2(m[t][y] - to);
                     m[t][y] = to;
                     l[t][y] *= f;
@@ -462,6 +462,73 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
     grid_dep_wait();   // the join after this kernel also reads what the one before it wrote
 }
 
+// Row `head` (b * Hq + query head) from the definition in 64 bits, by L lanes of a
+// warp: one whose scores are enormous (see reference). It goes over all keys for each C
+// values of a lane, a few million keys a second: such rows are rare and have to be
+// right, and the ordinary ones' registers are not to pay for them.
+template <int D, bool BITS4, int L>
+__device__ __noinline__ void wild_row(const Kv8Attn& a, int head)
+{
+    constexpr int C = 2;
+    const unsigned mask = L == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16);
+    const int lane = threadIdx.x % L, b = head / a.Hq, qh = head - b * a.Hq, h = qh / a.group;
+    int seq = b;
+    if (a.seqs) {
+        seq = __ldg(a.seqs + b);
+        seq = static_cast<unsigned>(seq) < static_cast<unsigned>(a.num_seqs) ? seq : 0;
+    }
+    const uint16_t* q = a.q + b * a.q_stride + static_cast<int64_t>(qh) * D;
+    const int64_t keys = static_cast<int64_t>(a.prefix_len) + seq_len(a, b);
+    // value d of a cache row: a code times its scale, or times its step and on its least value
+    auto value = [&](const uint8_t* cache, const float* scale, int64_t at, int d) -> double {
+        if (BITS4) {
+            const uint32_t pair = __float_as_uint(__ldg(scale + at));
+            const int code = (__ldg(cache + at * (D / 2) + d / 2) >> (d % 2 * 4)) & 15;
+            return static_cast<double>(code) * __uint_as_float(pair << 16) + __uint_as_float(pair & 0xFFFF0000u);
+        }
+        float code;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}"
+            : "=f"(code) : "r"(e4m3x2_to_f16x2(__ldg(cache + at * D + d))));
+        return static_cast<double>(code) * __ldg(scale + (a.per_token ? at : h));
+    };
+#pragma unroll 1
+    for (int d0 = lane; d0 < D; d0 += C * L) {
+        double acc[C] = {}, sum = 0.0, ref = -1.7e308;
+#pragma unroll 1
+        for (int64_t j = 0; j < keys; ++j) {
+            const bool first = j < a.prefix_len;
+            const int key = static_cast<int>(first ? j : j - a.prefix_len);
+            int page = __ldg((first ? a.prefix_pages : a.page_table + seq * a.table_stride) + (key >> a.page_shift));
+            page = static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages) ? page : 0;
+            const int64_t at = cache_row(a.page_shift, a.Hkv,
+                                         (static_cast<int64_t>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1)), h);
+            double score = 0.0;
+#pragma unroll 1
+            for (int d = lane; d < D; d += L)
+                score += bf16_bits_to_float(q[d]) * value(a.k_cache, a.k_scale, at, d);
+#pragma unroll 1
+            for (int o = L / 2; o > 0; o >>= 1)
+                score += __shfl_xor_sync(mask, score, o);
+            score *= a.sm_scale;
+            if (a.cap > 0.0f)
+                score = a.cap * tanh(score / a.cap);
+            score *= 1.4426950408889634;   // log2(e)
+            const double to = score > ref ? score : ref;
+            const double f = ex2(static_cast<float>(ref - to)), weight = ex2(static_cast<float>(score - to));
+            ref = to;
+            sum = sum * f + weight;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                acc[i] = acc[i] * f + weight * value(a.v_cache, a.v_scale, at, d0 + i * L);
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            a.out[static_cast<int64_t>(head) * D + d0 + i * L] = float_to_bf16_bits(static_cast<float>(acc[i] / sum));
+        if (a.lse && d0 == 0)
+            a.lse[head] = static_cast<float>((ref + log2(sum)) * 0.6931471805599453);
+    }
+}
+
 // Adds up the pieces of a (sequence, query head): W warps take them in turn, or,
 // where there are very many rows, half a warp (W = 0). The fewer rows, the more
 // warps take one: with few rows each has many pieces, and only their number hides
@@ -469,8 +536,10 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
 // others do, and each takes few registers.
 constexpr int kJoinCta = 4;      // warps of a CTA where a row has one or less
 constexpr int kJoinSums = 128;   // sequences up to which a warp sums their units itself
+// (7 blocks an SM of half a warp a row: left to itself the compiler takes fewer registers
+// since it has wild_row to call, 256 sequences of 500-1000 keys of 4 bits 54.6 us / 53.3 so.)
 template <int D, int W, bool BITS4>   // BITS4: tiles of several tokens, shares by the blocks' places
-__global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
+__global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32, W ? 0 : 7) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
                                                                          const __grid_constant__ Kv8Prefix p, int R)
 {
     constexpr int L = W ? 32 : 16;                  // lanes of a row
@@ -641,6 +710,10 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32) kv8_join_kernel(c
     }
     if (!there)
         return;
+    if (top >= kEnormous) {   // kWild
+        wild_row<D, BITS4, L>(a, head);
+        return;
+    }
     const bool empty = sum == 0.0f;
     // Of very many rows one division each, not one a value (1024 sequences of 10-100 keys
     // of 4 bits 55.2 -> 53.4 us; few rows of D 64 were slower so, 24.4 -> 27.4).
@@ -801,6 +874,7 @@ cudaError_t launch_kv8_attn(const Kv8Attn& in, const Kv8Prefix& p, int D, int pe
 {
     Kv8Attn a = in;
     const int R = kv8_attn_row_tile(a.group);
+    a.per_token = per_token;
     const bool two = lay_out(a, p, D, num_sms) == 2;
     cudaError_t e;
     if (p.splits) {

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             // the reference raised where the largest weight asks for it (kWeightMost;
             // the whole warp goes through its accumulators together),
             auto raise = [&](int i, float best) {
-                const float next = fmaxf(m, best - kWeightTop);
+                const float next = fmaxf(m, reference(best));
                 const float f = next == -INFINITY ? 1.0f : ex2(m - next);
                 m = next;
                 enormous = __any_sync(0xFFFFFFFFu, m > -INFINITY && fabsf(m) > kFused);

@@ -551,9 +551,9 @@ int kv8_norm_rope_write(const uint16_t* q_bf16, int64_t q_stride, int Hq, const 
  *        in, the pages of the tokens that are there; out, those of the new tokens
  *        as well. Other entries are left as they are.
  *   free_pages [num_pages] i32, free_count [1] i32 (device): the stack of pages that
- *        nobody has, its top at free_pages[free_count - 1]. In the order of the
- *        sequences, and of each one's tokens, pages are taken off the top;
- *        free_count, out, is what is left.
+ *        nobody has, its top at free_pages[free_count - 1]; what lies behind is
+ *        unspecified. In the order of the sequences, and of each one's tokens, pages
+ *        are taken off the top; free_count, out, is what is left.
  *   capacity: tokens that the outputs have room for.
  *   starts [B + 1] i32, out: the first token of each sequence; starts[B] their number
  *        (at most capacity).
@@ -587,9 +587,10 @@ int kv_pages_extend(const int32_t* lens, const int32_t* new_lens, int B, int32_t
  *
  *   lens, keep_lens, lens_out [B] i32: lens_out = keep_lens; may be either input.
  *   Other arguments as of kv_pages_extend.
- *   A sequence with keep_lens outside [0, lens] or lens above max_pages * page_size
- *   keeps all; if the pages do not fit the stack nothing goes back at all and every
- *   lens_out is lens; a page number out of range goes back as it is: W4A8_ERR_INDEX each.
+ *   A sequence with keep_lens outside [0, lens], with lens above max_pages * page_size
+ *   or with a page number out of range behind its first keep_lens tokens keeps all; if the
+ *   pages do not fit the stack nothing goes back at all and every lens_out is lens:
+ *   W4A8_ERR_INDEX each.
  */
 int kv_pages_truncate(const int32_t* lens, const int32_t* keep_lens, int B, const int32_t* page_table,
                       int64_t table_stride, int max_pages, int page_size, int32_t* free_pages, int32_t* free_count,

@@ -12,7 +12,8 @@
 // these up for itself (4096 sequences: 16 values a thread), then the blocks share
 // the tokens and the new table entries between them; who a token or a page belongs
 // to is found by bisection. Nothing that one block writes does another one read but
-// the lengths and the count, which the last block to have read them writes.
+// the lengths and the count, which the last block to have read them writes (and, where a
+// table is broken, the pages given back, which that block writes once more).
 //
 // Bound by latency: lengths, sums, page, slot one after another. 256 sequences' step
 // takes 3.4 us, and as much to take back; 1024 sequences with 102912 tokens 5.4 us.
@@ -85,8 +86,9 @@ __device__ __forceinline__ void read_count(const PagePool& p, int* count)
     }
 }
 // Whether this block is the last of the grid to come here; all threads agree. What
-// the others have read into shared memory before, they have read.
-__device__ __forceinline__ bool last_block(uint32_t* ticket)
+// the others have read into shared memory before, they have read. `flag`, which the
+// block's threads may have raised before, is in the last block whether any block's was.
+__device__ __forceinline__ bool last_block(uint32_t* ticket, int* flag)
 {
     __shared__ bool last;
     __syncthreads();
@@ -94,7 +96,12 @@ __device__ __forceinline__ bool last_block(uint32_t* ticket)
         return true;
     if (threadIdx.x == 0) {
         __threadfence();
-        last = atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
+        const uint32_t seen = atomicAdd(ticket, *flag ? 0x10001u : 1u);   // blocks, and above them those with the flag
+        last = (seen & 0xFFFFu) == gridDim.x - 1;
+        if (last) {
+            *ticket = 0;
+            *flag |= seen >> 16;
+        }
         __threadfence();
     }
     __syncthreads();
@@ -109,10 +116,10 @@ __global__ void __launch_bounds__(kThreads) pages_extend_kernel(const __grid_con
     int* starts = smem;               // [B + 1] tokens before each sequence, T + 1 at most
     int* ahead = smem + a.B + 1;      // [B + 1] pages that those before it need, num_pages + 1 at most
     int* have = ahead + a.B + 1;      // [B] its tokens; less than 0 (the complement) where it gets no pages
-    __shared__ int taken, count;
+    __shared__ int taken, count, none;
     const int tid = threadIdx.x, shift = a.p.page_shift;
     if (tid == 0)
-        taken = 0;
+        taken = none = 0;
     grid_dep_wait();
     read_count(a.p, &count);
     const int64_t most_tokens = static_cast<int64_t>(a.p.max_pages) << shift;
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) pages_extend_kernel(const __grid_con
         set_error(a.p.err, kErrBitIndex);
     if (mine)
         atomicMax(&taken, mine);   // those that get pages are the first of those that need some
-    const bool last = last_block(a.p.ticket);
+    const bool last = last_block(a.p.ticket, &none);
 
     if (blockIdx.x == 0)
         for (int b = tid; b <= a.B; b += kThreads)
@@ -207,8 +214,10 @@ __global__ void __launch_bounds__(kThreads) pages_truncate_kernel(const __grid_c
     extern __shared__ int smem[];
     int* ahead = smem;             // [B + 1] pages that those before it give back, num_pages + 1 at most
     int* kept = smem + a.B + 1;    // [B] tokens
-    __shared__ int count;
+    __shared__ int count, broken;  // broken: a page number out of range was met
     const int tid = threadIdx.x, shift = a.p.page_shift;
+    if (tid == 0)
+        broken = 0;
     grid_dep_wait();
     read_count(a.p, &count);
     const int64_t most_tokens = static_cast<int64_t>(a.p.max_pages) << shift;
@@ -231,10 +240,10 @@ __global__ void __launch_bounds__(kThreads) pages_truncate_kernel(const __grid_c
         x = min(x + static_cast<unsigned>(ahead[b + 1]), most);
         ahead[b + 1] = static_cast<int>(x);
     }
-    const bool last = last_block(a.p.ticket);
+    __syncthreads();
     // more pages than the stack has room for: somebody's length is wrong, and nothing goes back
-    const int given = ahead[a.B];
-    const bool fits = given <= a.p.num_pages - count;
+    int given = ahead[a.B];
+    bool fits = given <= a.p.num_pages - count;
     if ((bad || !fits) && blockIdx.x == 0)
         set_error(a.p.err, kErrBitIndex);
     if (fits) {
@@ -242,18 +251,49 @@ __global__ void __launch_bounds__(kThreads) pages_truncate_kernel(const __grid_c
             const int b = owner(ahead, a.B, j);
             const int64_t at = pages_of(kept[b], shift) + j - ahead[b];
             const int page = a.p.table[b * a.p.stride + at];
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.p.num_pages))
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.p.num_pages)) {
                 set_error(a.p.err, kErrBitIndex);
+                broken = 1;
+            }
             // in reverse: what an extension took comes to lie as it lay
             a.p.stack[count + given - 1 - j] = page;
         }
     }
-    if (last) {
-        for (int b = tid; b < a.B; b += kThreads)
-            a.lens_out[b] = fits ? kept[b] : a.lens[b];
-        if (tid == 0 && fits)
-            *a.p.count = count + given;
+    // the last block to have done its part writes the lengths and the count, which all have read
+    if (!last_block(a.p.ticket, &broken))
+        return;
+    if (broken || !fits) {
+        // Sequences with a page number out of range among those to go keep all, so that no
+        // such number comes to the stack; the others' pages are written again, by this block.
+        for (int b = 0; b < a.B; ++b) {
+            const int len = a.lens[b], end = kept[b] < len ? pages_of(len, shift) : 0;
+            bool mine = false;
+            for (int i = end ? pages_of(kept[b], shift) + tid : 0; i < end; i += kThreads)
+                mine |= static_cast<unsigned>(a.p.table[b * a.p.stride + i]) >= static_cast<unsigned>(a.p.num_pages);
+            if (end && __syncthreads_or(mine) && tid == 0)
+                kept[b] = len;
+        }
+        __syncthreads();
+        x = unused = 0;
+        for (int b = b0; b < b1; ++b)
+            x = min(x + (kept[b] < a.lens[b] ? pages_of(a.lens[b], shift) - pages_of(kept[b], shift) : 0), most);
+        block_before(x, unused, most, most);
+        for (int b = b0; b < b1; ++b) {
+            x = min(x + (kept[b] < a.lens[b] ? pages_of(a.lens[b], shift) - pages_of(kept[b], shift) : 0), most);
+            ahead[b + 1] = static_cast<int>(x);
+        }
+        __syncthreads();
+        given = ahead[a.B];
+        fits = given <= a.p.num_pages - count;
+        for (int j = tid; fits && j < given; j += kThreads) {
+            const int b = owner(ahead, a.B, j);
+            a.p.stack[count + given - 1 - j] = a.p.table[b * a.p.stride + pages_of(kept[b], shift) + j - ahead[b]];
+        }
     }
+    for (int b = tid; b < a.B; b += kThreads)
+        a.lens_out[b] = fits ? kept[b] : a.lens[b];
+    if (tid == 0 && fits)
+        *a.p.count = count + given;
 }
 
 static unsigned blocks_for(int64_t items, int num_sms)

@@ -677,7 +677,9 @@ cudaError_t launch_kv4_attn(const Kv4Attn& in, int D, int num_sms, cudaStream_t 
         a.lead = nullptr;
     a.unit_shift = kUnitShift;
     const int64_t pairs = static_cast<int64_t>(a.Hkv) * a.B * a.tiles;
-    const int fit = 228 * 1024 / (ring_smem(D, a.B) + 1024);   // CTAs an SM holds: by registers, by shared memory
+    // CTAs an SM holds: by registers, by shared memory (128 bytes of static arrays, 1 KB of
+    // the system's, steps of 128)
+    const int fit = 228 * 1024 / ((ring_smem(D, a.B) + 127) / 128 * 128 + 128 + 1024);
     // 16 rows of D 64 by two until the tables allow many units (16 query and 1 kv heads, us
     // at two / three: 24 sequences of up to 5001 keys with 4 drafts each, 15000 units, 22.6 /
     // 24.4; 96 of 1000-3000 17.4 / 18.3, 8 of 16000 13.6 / 15.0; 64 of 8000, 16000 units,

@@ -680,12 +680,15 @@ cudaError_t launch_kv4_attn(const Kv4Attn& in, int D, int num_sms, cudaStream_t 
     // CTAs an SM holds: by registers, by shared memory (128 bytes of static arrays, 1 KB of
     // the system's, steps of 128)
     const int fit = 228 * 1024 / ((ring_smem(D, a.B) + 127) / 128 * 128 + 128 + 1024);
-    // 16 rows of D 64 by two until the tables allow many units (16 query and 1 kv heads, us
-    // at two / three: 24 sequences of up to 5001 keys with 4 drafts each, 15000 units, 22.6 /
-    // 24.4; 96 of 1000-3000 17.4 / 18.3, 8 of 16000 13.6 / 15.0; 64 of 8000, 16000 units,
-    // 23.6 / 23.1, 256 of 4000, 32000 units, 37.2 / 34.9).
+    // 16 rows of D 64 by two blocks until the tables allow 105 units an SM (16000 here). 16
+    // query and 1 kv heads, us at two / three: 24 sequences of up to 5001 keys with 4 drafts
+    // each, 15000 units, 21.6 / 23.6; 96 of 1000-3000, 9000, 17.6 / 18.3; 8 of 16000, 4000,
+    // 13.8 / 15.1; 64 of 8000, 16000, 24.1 / 23.5; 128 of 4000, 16000, 24.7 / 23.6; 256 of
+    // 4000, 32000, 37.5 / 35.2. Only the device knows the lengths: where all are as long as
+    // the table three would win from 12000 on (48 of 8000 21.2 / 19.8), where the tables are
+    // much wider than the lengths two would longer (128 of 0-5000, 20000 units, 21.6 / 21.9).
     const int64_t units = pairs * ((static_cast<int64_t>(a.max_pages) << a.page_shift) >> kUnitShift);
-    const int blocks = min(R == 8 ? 4 : D == 64 && units >= 20000 ? 3 : 2, fit);
+    const int blocks = min(R == 8 ? 4 : D == 64 && units >= 105 * static_cast<int64_t>(num_sms) ? 3 : 2, fit);
     a.warps = min(num_sms * blocks * kWarps, kKv8MaxWarps / kWarps * kWarps);
     a.free_warps = a.warps;
     // Shares by place where four blocks fit an SM (two or three, of 16 rows, gain nothing).

@@ -224,7 +224,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from)
 }  // namespace
 
 // Bound by instructions and memory alike: 64 sequences of 8192-16384 keys, 32 query and
-// 8 kv heads (857 MB) take 141 us, 6.1 TB/s or 90 % of a copy's rate, with the units'
+// 8 kv heads (857 MB) take 143 us, 6.0 TB/s or 88 % of a copy's rate, with the units'
 // arithmetic left out 129 us; a unit is 477 instructions of a warp, 176 of them the
 // masks below (integer instructions, which go at half the rate), 32 matrix products.
 // Short sequences are bound by the chain lengths -> page -> codes -> result -> join,
@@ -575,7 +575,10 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv4_attn_kernel(const __g
         __syncwarp();
         issue(i + kStages);
 
-        // ---- P^T and O^T += V^T P^T
+        // ---- P^T and O^T += V^T P^T. A weight times its value's step is rounded to f16
+        // (2^-11; a second operand for the rest would double these matrix products, and the
+        // outputs' error against 64 bits, most of it bf16's own rounding, is 5-11 % larger
+        // for it); the sum of the weights and their products with least values stay in fp32.
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
             uint32_t pb[NT][2];

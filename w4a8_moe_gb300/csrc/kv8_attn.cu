@@ -716,7 +716,8 @@ __global__ void __launch_bounds__((W > 1 ? W : kJoinCta) * 32, W ? 0 : 7) kv8_jo
     }
     const bool empty = sum == 0.0f;
     // Of very many rows one division each, not one a value (1024 sequences of 10-100 keys
-    // of 4 bits 55.2 -> 53.4 us; few rows of D 64 were slower so, 24.4 -> 27.4).
+    // of 4 bits 55.2 -> 53.4 us; few rows of D 64 were slower so, 24.4 -> 27.4): two fp32
+    // roundings in place of one, 2^-23 of a value before bf16's 2^-9.
     constexpr bool kOnce = BITS4 && W == 0 && D == 128;
     if (kOnce) {
         const float f = empty ? 0.0f : __frcp_rn(sum);

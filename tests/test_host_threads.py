@@ -38,7 +38,7 @@ class Recorder:
         return call
 
 
-def at_once(lib, monkeypatch, calls, outputs, times=4000):
+def at_once(lib, monkeypatch, calls, outputs, times=1500):
     """Makes each of `calls` on a stream of its own, then all of them again and again from a thread each, straight through
     the C entry points; what they wrote has to be what they wrote alone."""
     recorder = Recorder(lib._load())

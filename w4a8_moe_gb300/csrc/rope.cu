@@ -59,7 +59,7 @@ __device__ __forceinline__ float row_max(float x)
 // Bound by memory: 32768 tokens of 32 + 8 heads of 128 with norms (671 MB) take 103
 // us, 6.5 TB/s or 96 % of a copy's rate, 8192 of them 30.3 us, 82 % (a launch and the
 // first rows' way are 4 us of it); 32768 tokens of 48 query and 8 kv heads into the
-// cache (1009 MB) 161 us, 92 %. 32 tokens take 2.1 us, into the cache 2.6.
+// cache (1009 MB) 164 us, 91 %. 32 tokens take 2.1 us, into the cache 2.6.
 //
 // L lanes share a row (one head of one token), 16 values each, in two runs of 8:
 // a rotating lane has both halves of 8 pairs, so nothing is exchanged but the sum

@@ -422,8 +422,8 @@ int kv8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scal
  *   largest one. With scale_mode 1 that is the weight times its value's scale, off
  *   by 2^-11 of itself and 2^-27 of the largest such product among the keys whose
  *   values are not all zero (scales below 2^-92 lose more). A row (a query head of a
- *   sequence) with a score of 2^26 log 2 (4.6e7) or more in size is computed in 64 bits
- *   instead, at a few million keys a second. A sequence without any key
+ *   sequence) with a score of 2^26 log 2 (4.6e7) or more in size is computed key by key
+ *   instead, which takes many times as long. A sequence without any key
  *   has out = 0 and lse = -infinity. lse may be NULL. Cache bytes behind the
  *   last token of a page have no influence. The same call gives the same bits.
  *   Several query tokens of one sequence are several rows that share its pages,
@@ -652,7 +652,7 @@ int kv4_read(const uint8_t* k_cache, const uint8_t* v_cache, const uint16_t* k_s
  *   rounded to f16, relative to a running reference: off by 2^-11 of itself and 2^-32 of
  *   the largest product of a weight with max(step, |least value|); where it meets least
  *   values it stays in fp32. A row (a query head of a token) with a score of 2^26 log 2
- *   (4.6e7) or more in size is computed in 64 bits instead, at a few million keys a second.
+ *   (4.6e7) or more in size is computed key by key instead, which takes many times as long.
  *   A token without keys has out = 0 and lse = -infinity. lse may be NULL. What lies
  *   behind the last key of a page has no influence. The same call gives the same bits.
  *   Requires 1 <= T <= 4096, Hq a multiple of Hkv, Hq <= 65535, max_pages >= 0,

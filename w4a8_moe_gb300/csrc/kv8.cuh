@@ -132,9 +132,9 @@ constexpr float kLeastScale = 0x1p-92f;
 constexpr float kLeastScaleLog2 = -92.0f;
 
 // From these scores (log2) on a float's steps, 8 and more, leave no room for
-// kWeightTop or a scale's size beside a score. A row with such a score gets kWild for
-// its reference, under which all other weights are 0, and the join computes it from
-// the definition (wild_row), which costs the ordinary ones nothing.
+// kWeightTop or a value's size beside a score. A row with such a score gets kWild for
+// its reference, under which all weights are 0, and the join computes it from the
+// definition (wild_row), which costs the ordinary ones nothing.
 constexpr float kEnormous = 0x1p26f;
 constexpr float kWild = 0x1p127f;
 // The reference for a largest score of `top`, in the log2 of a weight times its value's size.

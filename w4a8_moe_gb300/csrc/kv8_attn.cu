@@ -462,14 +462,17 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) kv8_attn_kernel(const __g
     grid_dep_wait();   // the join after this kernel also reads what the one before it wrote
 }
 
-// Row `head` (b * Hq + query head) from the definition in 64 bits, by L lanes of a
-// warp: one whose scores are enormous (see reference). It goes over all keys for each C
-// values of a lane, a few million keys a second: such rows are rare and have to be
-// right, and the ordinary ones' registers are not to pay for them.
+// Row `head` (b * Hq + query head) from the definition, by L lanes of a warp: one whose
+// scores are enormous (see reference). A lane takes every L-th key: its products with
+// the query, both as they are but for a power of two, are added up in fp32, and what
+// follows is in 64 bits. Then all of them add the values of the keys that weigh
+// anything, a few dimensions each. All rows of 64 sequences over 8192 tokens, 48 query
+// and 8 kv heads, take 31 ms, ordinary ones 0.03 (a lane a dimension, key after key in
+// 64 bits: 476 ms); 64 of 8000 keys of 4 bits, 32 and 8 heads, 2.8 ms (100).
 template <int D, bool BITS4, int L>
 __device__ __noinline__ void wild_row(const Kv8Attn& a, int head)
 {
-    constexpr int C = 2;
+    constexpr int V = D / L;   // values of a lane: lane, lane + L, ...
     const unsigned mask = L == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16);
     const int lane = threadIdx.x % L, b = head / a.Hq, qh = head - b * a.Hq, h = qh / a.group;
     int seq = b;
@@ -478,55 +481,88 @@ __device__ __noinline__ void wild_row(const Kv8Attn& a, int head)
         seq = static_cast<unsigned>(seq) < static_cast<unsigned>(a.num_seqs) ? seq : 0;
     }
     const uint16_t* q = a.q + b * a.q_stride + static_cast<int64_t>(qh) * D;
-    const int64_t keys = static_cast<int64_t>(a.prefix_len) + seq_len(a, b);
-    // value d of a cache row: a code times its scale, or times its step and on its least value
-    auto value = [&](const uint8_t* cache, const float* scale, int64_t at, int d) -> double {
-        if (BITS4) {
-            const uint32_t pair = __float_as_uint(__ldg(scale + at));
-            const int code = (__ldg(cache + at * (D / 2) + d / 2) >> (d % 2 * 4)) & 15;
-            return static_cast<double>(code) * __uint_as_float(pair << 16) + __uint_as_float(pair & 0xFFFF0000u);
-        }
-        float code;
+    uint32_t top = 0;
+#pragma unroll 1
+    for (int d = lane; d < D; d += L)
+        top = max(top, q[d] & 0x7FFFu);
+#pragma unroll 1
+    for (int o = L / 2; o > 0; o >>= 1)
+        top = max(top, __shfl_xor_sync(mask, top, o));
+    const int e = top >> 7 == 255 ? 0 : max(static_cast<int>(top >> 7), 1) - 127;
+    const float down = ldexpf(1.0f, -e);   // takes the query's largest element to [1, 2)
+    const double factor = ldexp(static_cast<double>(a.sm_scale), e);
+    auto code = [](const uint8_t* row, int d) -> float {   // number d of a row of codes
+        if (BITS4)
+            return static_cast<float>((__ldg(row + d / 2) >> (d % 2 * 4)) & 15);
+        float x;
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}"
-            : "=f"(code) : "r"(e4m3x2_to_f16x2(__ldg(cache + at * D + d))));
-        return static_cast<double>(code) * __ldg(scale + (a.per_token ? at : h));
+            : "=f"(x) : "r"(e4m3x2_to_f16x2(__ldg(row + d))));
+        return x;
     };
+    constexpr int kRow = BITS4 ? D / 2 : D;   // bytes
+    auto step = [&](const float* scale, int64_t at) {
+        return BITS4 ? __uint_as_float(__float_as_uint(__ldg(scale + at)) << 16) : __ldg(scale + (a.per_token ? at : h));
+    };
+    auto least = [&](const float* scale, int64_t at) {
+        return BITS4 ? __uint_as_float(__float_as_uint(__ldg(scale + at)) & 0xFFFF0000u) : 0.0f;
+    };
+
+    double acc[V] = {}, sum = 0.0, ref = -1.7e308;   // (the sum of the lane's own keys)
+    const int64_t keys = static_cast<int64_t>(a.prefix_len) + seq_len(a, b);
 #pragma unroll 1
-    for (int d0 = lane; d0 < D; d0 += C * L) {
-        double acc[C] = {}, sum = 0.0, ref = -1.7e308;
-#pragma unroll 1
-        for (int64_t j = 0; j < keys; ++j) {
+    for (int64_t j0 = 0; j0 < keys; j0 += L) {
+        const int64_t j = j0 + lane;
+        int64_t at = 0;
+        double score = -INFINITY;
+        bool odd = false;   // a value that is no number shows even where it weighs nothing
+        if (j < keys) {
             const bool first = j < a.prefix_len;
             const int key = static_cast<int>(first ? j : j - a.prefix_len);
             int page = __ldg((first ? a.prefix_pages : a.page_table + seq * a.table_stride) + (key >> a.page_shift));
             page = static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages) ? page : 0;
-            const int64_t at = cache_row(a.page_shift, a.Hkv,
-                                         (static_cast<int64_t>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1)), h);
-            double score = 0.0;
-#pragma unroll 1
-            for (int d = lane; d < D; d += L)
-                score += bf16_bits_to_float(q[d]) * value(a.k_cache, a.k_scale, at, d);
-#pragma unroll 1
-            for (int o = L / 2; o > 0; o >>= 1)
-                score += __shfl_xor_sync(mask, score, o);
-            score *= a.sm_scale;
+            at = cache_row(a.page_shift, a.Hkv, (static_cast<int64_t>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1)), h);
+            float dot = 0.0f, all = 0.0f;
+#pragma unroll 8
+            for (int d = 0; d < D; ++d) {
+                const float x = bf16_bits_to_float(q[d]) * down;
+                dot = fmaf(x, code(a.k_cache + at * kRow, d), dot);
+                all += x;
+                odd |= !BITS4 && (__ldg(a.v_cache + at * kRow + d) & 0x7F) == 0x7F;
+            }
+            score = (static_cast<double>(dot) * step(a.k_scale, at) + static_cast<double>(all) * least(a.k_scale, at)) * factor;
             if (a.cap > 0.0f)
                 score = a.cap * tanh(score / a.cap);
             score *= 1.4426950408889634;   // log2(e)
-            const double to = score > ref ? score : ref;
-            const double f = ex2(static_cast<float>(ref - to)), weight = ex2(static_cast<float>(score - to));
-            ref = to;
-            sum = sum * f + weight;
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                acc[i] = acc[i] * f + weight * value(a.v_cache, a.v_scale, at, d0 + i * L);
+            odd |= !(fabsf(step(a.v_scale, at)) + fabsf(least(a.v_scale, at)) < INFINITY);
         }
+        double to = score > ref ? score : ref;
+#pragma unroll 1
+        for (int o = L / 2; o > 0; o >>= 1)
+            to = fmax(to, __shfl_xor_sync(mask, to, o));
+        const double f = ex2(static_cast<float>(ref - to)), weight = ex2(static_cast<float>(score - to));
+        ref = to;
+        sum = sum * f + weight;
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            a.out[static_cast<int64_t>(head) * D + d0 + i * L] = float_to_bf16_bits(static_cast<float>(acc[i] / sum));
-        if (a.lse && d0 == 0)
-            a.lse[head] = static_cast<float>((ref + log2(sum)) * 0.6931471805599453);
+        for (int i = 0; i < V; ++i)
+            acc[i] *= f;
+#pragma unroll 1
+        for (unsigned left = __ballot_sync(mask, weight > 0.0 || odd) & mask; left; left &= left - 1) {
+            const int from = (__ffs(left) - 1) % L;
+            const int64_t row = __shfl_sync(mask, at, from, L);
+            const double w = __shfl_sync(mask, weight, from, L), s = step(a.v_scale, row), m = least(a.v_scale, row);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                acc[i] += w * (code(a.v_cache + row * kRow, lane + i * L) * s + m);
+        }
     }
+#pragma unroll 1
+    for (int o = L / 2; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(mask, sum, o);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        a.out[static_cast<int64_t>(head) * D + lane + i * L] = float_to_bf16_bits(static_cast<float>(acc[i] / sum));
+    if (a.lse && lane == 0)
+        a.lse[head] = static_cast<float>((ref + log2(sum)) * 0.6931471805599453);
 }
 
 // Adds up the pieces of a (sequence, query head): W warps take them in turn, or,

@@ -130,11 +130,12 @@ def test_several_tokens_of_4_bits(lib, hq, hkv, d, power):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("rows", [2, 300])
-def test_ordinary_rows_beside_one(lib, bits, rows):
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [2, 20, 50, 100, 300])   # 8, 4, 2, 1 and half a warp to join a row
+def test_ordinary_rows_beside_one(lib, bits, d, rows):
     """One query head of one sequence with such scores, NaN among another's: all others keep their bits."""
     lens = [60 + i % 50 for i in range(rows)]
-    b = Batch4(lens, 12, 2, 128, 16, seed=44) if bits == 4 else Batch8(lens, 40, 12, 2, 128, 16, 1, seed=44)
+    b = Batch4(lens, 12, 2, d, 16, seed=44) if bits == 4 else Batch8(lens, 40, 12, 2, d, 16, 1, seed=44)
     plain, plain_lse = b.run(lib)
     b.q[1, 4] = (b.q[1, 4].double() * 2.0 ** 40).to(torch.bfloat16)
     b.q[0, 11, 5] = float("nan")
@@ -145,6 +146,17 @@ def test_ordinary_rows_beside_one(lib, bits, rows):
     assert torch.equal(out[same], plain[same]) and torch.equal(lse[same], plain_lse[same])
     assert bool(torch.isnan(out[0, 11]).all()) and bool(torch.isfinite(out[0, :11].float()).all())
     assert bool(torch.isfinite(out[1].float()).all()) and bool((lse[1, 4].abs() > 1e9).all())
+    if bits == 4:
+        kc, kst, kl, vc, vst, vl = b.keys(1)
+        k, v = kc * kst + kl, vc * vst + vl
+    else:
+        k, v = b.keys(1)
+    s = (b.q[1, 4].double() @ k[0].T) * b.scale
+    best, second = s.topk(2).values.tolist()
+    assert best - second > 1e6 * max(1.0, abs(best) * 2.0 ** -40)   # (so that the best key has all of the weight)
+    want = v[0, s.argmax()]
+    assert bool(((out[1, 4].double() - want).abs() <= want.abs() * 2.0 ** -8 + v[0].abs().amax() * 2.0 ** -20).all())
+    assert abs(float(lse[1, 4]) - best) <= abs(best) * 2.0 ** -20
     again = b.run(lib)
     assert torch.equal(again[0].view(torch.int16), out.view(torch.int16)) and torch.equal(again[1][1:], lse[1:])
 
